@@ -87,6 +87,7 @@ typedef enum {
 #define PA_DEVERR_TIMEOUT      0x8u  /* a bounded barrier wait gave up */
 #define PA_DEVERR_QUERY_RANGE  0x10u /* chunked prefill: q_start out of order or range */
 #define PA_DEVERR_GROUP        0x20u /* grouped decode: bad group bounds, or members' shared blocks differ */
+#define PA_DEVERR_TREE         0x40u /* drafted tree: a parent or a path element out of order or range */
 
 /* Shape of a paged KV cache. */
 typedef struct {
@@ -126,6 +127,47 @@ pa_status pa_cache_write(const void* k, const void* v, int32_t in_dtype,
                          const int64_t* slot_mapping, int64_t num_tokens,
                          void* k_cache, void* v_cache, float* k_scale, float* v_scale,
                          const pa_cache_desc* desc, void* stream);
+
+/*
+ * pa_rope_cache_write -- rotary positions of this step's queries and keys,
+ * fused with pa_cache_write: q is rotated into q_out, k is rotated and stored
+ * with v at slot_mapping.  [LLM-INF] 2.2 (pages hold the generated tokens'
+ * K/V); the pages are silent on rotary positions.
+ *
+ * The first rot_dim dims of every head are rotated in pairs (x1, x2), the
+ * others pass.  With angle = positions[t] * inv_freq[i] (radians) and
+ * c, s = factor * cos, factor * sin of it, pair i becomes
+ *     (x1 c - x2 s, x1 s + x2 c)        in float32, rounded once to the
+ * destination's type.  Pair i is dims (i, i + rot_dim / 2), or dims
+ * (2 i, 2 i + 1) when interleaved.  Scaled rotary variants are a matter of
+ * inv_freq and factor.
+ *
+ * q            device, token t's row [num_q_heads][head_dim] at q + t *
+ *              q_stride elements of in_dtype, likewise k and v
+ *              ([num_kv_heads][head_dim]): views of one packed projection
+ *              need no copy.  Strides are at least a row and a multiple of 16
+ *              bytes.  num_q_heads = 0: no queries (q, q_out may be NULL).
+ * in_dtype     F16, BF16 or F32, as pa_cache_write.
+ * positions    device int64 [num_tokens], any value (the angle is formed
+ *              modulo one turn in 64-bit fixed point, so far positions lose
+ *              nothing).
+ * inv_freq     device double [rot_dim / 2].
+ * rot_dim      a multiple of 16 in 16 .. head_dim.
+ * factor       host, finite (1, or the attention factor of a scaled variant).
+ * slot_mapping, caches, scales  as pa_cache_write; FP8 / INT8 codes are those
+ *              of the rotated float32 key (and of v).  A token whose slot is
+ *              negative stores nothing (its q is still rotated); a slot past
+ *              the pool likewise, flagged PA_DEVERR_SLOT_RANGE.
+ * q_out        device, rows at q_out_stride, in q_out_dtype = in_dtype (F16,
+ *              BF16 or F32 for F32 inputs).  May be q itself (same stride and
+ *              type); other overlaps are not allowed.
+ */
+pa_status pa_rope_cache_write(const void* q, const void* k, const void* v, int32_t in_dtype, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, const int64_t* positions,
+                              const double* inv_freq, int32_t rot_dim, int32_t interleaved, float factor,
+                              const int64_t* slot_mapping, int64_t num_tokens, int32_t num_q_heads, void* q_out,
+                              int32_t q_out_dtype, int64_t q_out_stride, void* k_cache, void* v_cache,
+                              float* k_scale, float* v_scale, const pa_cache_desc* desc, void* stream);
 
 /*
  * pa_decode_workspace_size -- bytes of device workspace pa_decode needs for
@@ -474,6 +516,116 @@ pa_status pa_chunked_prefill(const void* q, int32_t q_dtype, const int32_t* q_st
                              void* workspace, size_t workspace_bytes,
                              int32_t split_tokens, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Drafted trees ([LLM-INF] 6.1: the target model verifies the draft tokens in
+ * one pass; the pages draft a chain, here several continuations at once).  A
+ * sequence's tree is the last n_b = q_start[b+1] - q_start[b] tokens of its
+ * context: node 0 the current token, every other node below an earlier one.
+ * One step: append n_b slots per sequence (pa_append_tokens),
+ * pa_rope_cache_write with the nodes' positions (context + depth),
+ * pa_tree_attention in every layer, the model's pick after every node,
+ * pa_tree_accept once, pa_tree_commit in every layer, and pa_truncate_seq to
+ * the new length.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * pa_tree_mask -- the mask rows and depths of one tree from its parents (host
+ * only).  parents: int32 [n], parents[i] in -1 .. i - 1 (-1: a root).  mask:
+ * int64 [n][mask_words] out, bit j % 64 of word j / 64 of row i set when j is i
+ * or an ancestor of i; mask_words >= ceil(n / 64).  depths: int32 [n] out (a
+ * root has 0), may be NULL.  PA_ERR_INVALID on a bad argument.
+ */
+pa_status pa_tree_mask(const int32_t* parents, int32_t n, int32_t mask_words, int64_t* mask, int32_t* depths);
+
+/*
+ * pa_tree_attention_workspace_size -- bytes of device workspace
+ * pa_tree_attention needs on the current device (0 on an invalid argument).
+ * It does not grow with the batch or the context.
+ */
+size_t pa_tree_attention_workspace_size(int32_t num_q_heads, int32_t max_q_len, const pa_cache_desc* desc);
+
+/*
+ * pa_tree_attention -- paged attention of a tree's nodes: node i of sequence b
+ * sees the keys 0 .. L_b - n_b - 1 of the context before the tree, and the
+ * key of node j (position L_b - n_b + j) when bit j of its mask row is set:
+ *     out[q_start[b]+i][h] = sum_t softmax_t(scale * q[q_start[b]+i][h] . K_t) V_t
+ * over the keys it sees, kv head g = h / G.  A row that sees no key is zero.
+ * The nodes' K/V are in the cache already.  A node's K/V row reaches only the
+ * rows that see it, whatever it holds (infinities and NaN included).
+ *
+ * q, q_start, k_scale, v_scale, block_tables, context_lens, max_context_len,
+ * out          as pa_chunked_prefill; any number of query heads per kv head.
+ *              n_b > L_b is flagged PA_DEVERR_CONTEXT_LEN; the nodes before
+ *              the cached ones have no key then.
+ * max_q_len    host upper bound on n_b (<= 65535); longer sequences are
+ *              skipped and flagged PA_DEVERR_QUERY_RANGE.
+ * tree_mask    device int64 [num_tokens][mask_words], the rows packed as q's
+ *              tokens are (pa_tree_mask builds them); any bits are allowed,
+ *              those from n_b on are not read as keys.
+ * mask_words   at least ceil(max_q_len / 64).
+ * scale        finite; of either sign.
+ * workspace    device, >= pa_tree_attention_workspace_size bytes, 16-byte
+ *              aligned; scratch.  Calls that may run at the same time need
+ *              one each.
+ * Deterministic: the same inputs give the same bits on the same device.
+ *
+ * Work: one persistent CTA per SM streams an equal share of the batch's
+ * 128-key chunks (planned on the device from context_lens) and multiplies on
+ * tcgen05 tensor cores, 128 or 256 (node, head) rows at a time; items that
+ * span CTAs are merged by a second kernel.
+ */
+pa_status pa_tree_attention(const void* q, int32_t q_dtype, const int32_t* q_start, int32_t num_tokens,
+                            int32_t max_q_len, const int64_t* tree_mask, int32_t mask_words,
+                            const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                            const int32_t* block_tables, int32_t max_blocks_per_seq,
+                            const int32_t* context_lens, int32_t max_context_len, int32_t B, int32_t num_q_heads,
+                            float scale, void* out, int32_t out_dtype, const pa_cache_desc* desc, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/*
+ * pa_tree_accept -- the accepted path of every sequence's tree.  Node 0 is
+ * accepted; after an accepted node i comes its lowest child c with
+ * draft_tokens[c] == target_tokens[i], up to max_path nodes.
+ *
+ * draft_tokens  device int64 [num_tokens]: the nodes' own tokens.
+ * target_tokens device int64 [num_tokens]: the token the model picked after
+ *               each node.
+ * parents       device int32 [num_tokens]: each node's parent, an earlier
+ *               node's index within the sequence, or -1 (never accepted,
+ *               except node 0, whose entry is not read).  Others are treated
+ *               as -1 and flagged PA_DEVERR_TREE.
+ * path          device int32 [B][max_path] out: accepted nodes, ascending,
+ *               padded with -1.  path_len: device int32 [B] out (0 for n_b =
+ *               0).  next_token: device int64 [B] out: the model's pick after
+ *               the last accepted node (-1 for n_b = 0).
+ * A sequence whose q_start is out of order or range counts as n_b = 0 and is
+ * flagged PA_DEVERR_QUERY_RANGE.
+ */
+pa_status pa_tree_accept(const int64_t* draft_tokens, const int64_t* target_tokens, const int32_t* parents,
+                         const int32_t* q_start, int32_t num_tokens, int32_t B, int32_t max_path, int32_t* path,
+                         int32_t* path_len, int64_t* next_token, void* stream);
+
+/*
+ * pa_tree_commit -- move the accepted nodes' K/V rows (and 1-byte caches'
+ * scales) together: element i of sequence b's path moves from position
+ * L_b - n_b + path[b][i] to L_b - n_b + i, in place.  The rows behind the
+ * path keep what they hold.
+ *
+ * path, path_len as pa_tree_accept gives them: ascending, path[b][i] in
+ *              i .. n_b - 1, path_len[b] <= min(max_path, n_b).
+ * new_lens     device int32 [B] out, may be NULL: L_b - n_b + path_len[b].
+ *              Must not overlap context_lens.
+ * A sequence with a path, length or block id out of order or range moves
+ * nothing, keeps L_b in new_lens and is flagged (PA_DEVERR_TREE,
+ * PA_DEVERR_CONTEXT_LEN, PA_DEVERR_QUERY_RANGE, PA_DEVERR_BLOCK_RANGE).  The
+ * blocks written must not be shared between sequences (pa_append_tokens has
+ * copied them).
+ */
+pa_status pa_tree_commit(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                         const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+                         const int32_t* q_start, const int32_t* path, int32_t max_path, const int32_t* path_len,
+                         int32_t B, int32_t* new_lens, const pa_cache_desc* desc, void* stream);
+
 /*
  * pa_decode_static_ws -- pa_decode that allocates nothing.  The pages have no
  * counterpart: this entry point exists for callers of this library that
@@ -615,6 +767,11 @@ pa_status pa_free_seqs(pa_alloc* a, const uint64_t* ids, int32_t n);
  * refcounts, so the next pa_append_slots copies a shared partial block
  * ([LLM-INF] 2.2 copy-on-write for beam search).  All or nothing. */
 pa_status pa_reselect(pa_alloc* a, const uint64_t* ids, const int32_t* parent_idx, int32_t n);
+
+/* Shorten a sequence to its first num_tokens tokens (0 .. its token count):
+ * the blocks behind them are released in logical order.  Drops the rejected
+ * nodes of a drafted tree after pa_tree_commit. */
+pa_status pa_truncate_seq(pa_alloc* a, uint64_t seq_id, int64_t num_tokens);
 
 /* Release a sequence: refcount - 1 per block, freed at 0. */
 pa_status pa_free_seq(pa_alloc* a, uint64_t seq_id);

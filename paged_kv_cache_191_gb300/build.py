@@ -21,8 +21,8 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE,
           "--expt-relaxed-constexpr"]
 SOURCES = ["decode.cu", "decode_static.cu", "prefill.cu", "cache_ops.cu", "api.cpp", "allocator.cpp", "scheduler.cpp",
-           "serve.cpp", "segments.cpp"]
-HEADERS = ["device_common.cuh", "pa_internal.h", "kv_map.h"]
+           "serve.cpp", "segments.cpp", "tree.cu", "tree_step.cu", "tree.cpp"]
+HEADERS = ["device_common.cuh", "tcgen05.cuh", "cache_rows.cuh", "pa_internal.h", "kv_map.h"]
 
 
 def nvcc():

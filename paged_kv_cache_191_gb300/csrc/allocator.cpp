@@ -321,6 +321,21 @@ pa_status pa_reselect(pa_alloc* a, const uint64_t* ids, const int32_t* parent_id
   return pa::ok();
 }
 
+pa_status pa_truncate_seq(pa_alloc* a, uint64_t seq_id, int64_t num_tokens) {
+  if (!a) return pa::fail(PA_ERR_INVALID, "pa_truncate_seq: null handle");
+  auto it = a->seqs.find(seq_id);
+  if (it == a->seqs.end()) return pa::fail(PA_ERR_NOT_FOUND, "pa_truncate_seq: unknown sequence");
+  pa_alloc::Seq& s = it->second;
+  if (num_tokens < 0 || num_tokens > s.ntok)
+    return pa::fail(PA_ERR_INVALID, "pa_truncate_seq: %lld tokens of %lld", static_cast<long long>(num_tokens),
+                    static_cast<long long>(s.ntok));
+  const size_t keep = static_cast<size_t>((num_tokens + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE);
+  for (size_t i = keep; i < s.blocks.size(); ++i) a->release(s.blocks[i]);
+  s.blocks.resize(keep);
+  s.ntok = num_tokens;
+  return pa::ok();
+}
+
 pa_status pa_free_seq(pa_alloc* a, uint64_t seq_id) {
   if (!a) return pa::fail(PA_ERR_INVALID, "pa_free_seq: null handle");
   auto it = a->seqs.find(seq_id);

@@ -37,7 +37,7 @@ pa_status fail(pa_status st, const char* fmt, ...) {
   return st;
 }
 
-static pa_status check_desc(const pa_cache_desc* d, const char* fn) {
+pa_status check_desc(const pa_cache_desc* d, const char* fn) {
   if (!d) return fail(PA_ERR_INVALID, "%s: desc is NULL", fn);
   if (d->block_size != PA_BLOCK_SIZE)
     return fail(PA_ERR_UNSUPPORTED, "%s: block_size must be 16", fn);
@@ -52,7 +52,7 @@ static pa_status check_desc(const pa_cache_desc* d, const char* fn) {
   return PA_OK;
 }
 
-static int sm_count() {
+int sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
@@ -758,14 +758,18 @@ pa_status pa_swap_blocks(void* dst_k, void* dst_v, float* dst_k_scale, float* ds
 
 pa_status pa_device_errors(uint32_t* flags, int32_t clear) {
   if (!flags) return fail(PA_ERR_INVALID, "pa_device_errors: flags is NULL");
-  uint32_t a = 0, b = 0, c = 0;
+  uint32_t a = 0, b = 0, c = 0, t = 0, s = 0;
   pa_status st = pa::read_errors_decode(&a, clear != 0);
   if (st != PA_OK) return st;
   st = pa::read_errors_cache_ops(&b, clear != 0);
   if (st != PA_OK) return st;
   st = pa::read_errors_prefill(&c, clear != 0);
   if (st != PA_OK) return st;
-  *flags = a | b | c;
+  st = pa::read_errors_tree(&t, clear != 0);
+  if (st != PA_OK) return st;
+  st = pa::read_errors_tree_step(&s, clear != 0);
+  if (st != PA_OK) return st;
+  *flags = a | b | c | t | s;
   return PA_OK;
 }
 

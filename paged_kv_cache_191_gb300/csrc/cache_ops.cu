@@ -18,6 +18,7 @@
 // swap ("LLM推理引擎深度实战" 3.2, preemption by moving a request's pages to CPU
 // memory and back) is the same copy between two pools, one of them in
 // page-locked host memory that the kernel addresses directly.
+#include "cache_rows.cuh"
 #include "device_common.cuh"
 #include "pa_internal.h"
 
@@ -27,30 +28,6 @@ namespace {
 __device__ uint32_t g_cache_err;
 
 constexpr int kWriteThreads = 256;
-
-// 8 consecutive input values as float, from f16 / bf16 / f32 storage.
-template <int IN>
-__device__ __forceinline__ void load8(const void* base, size_t idx, float (&x)[8]) {
-  if constexpr (IN == PA_DTYPE_F32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + idx);
-    const float4 a = p[0], b = p[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  } else {
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + idx);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float2 f;
-      if constexpr (IN == PA_DTYPE_F16)
-        f = dev::unpack2<__half>(w[i]);
-      else
-        f = dev::unpack2<__nv_bfloat16>(w[i]);
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    }
-  }
-}
 
 // 16-bit cache: copy (same dtype, exact) or round from f32.
 template <int IN, int KV>
@@ -81,7 +58,7 @@ __global__ void __launch_bounds__(kWriteThreads)
       out = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(isv ? v : k) + src);
     } else {
       float x[8];
-      load8<IN>(isv ? v : k, src, x);
+      dev::load8<IN>(isv ? v : k, src, x);
       uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -94,33 +71,6 @@ __global__ void __launch_bounds__(kWriteThreads)
     }
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(isv ? vc : kc) + dst) = out;
   }
-}
-
-__device__ __forceinline__ float block_max(float x, float* red) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-  const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
-  if (l == 0) red[w] = x;
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    float y = threadIdx.x < (blockDim.x >> 5) ? red[threadIdx.x] : 0.f;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
-    if (threadIdx.x == 0) red[32] = y;
-  }
-  __syncthreads();
-  return red[32];
-}
-
-// One code of a quantised cache from a float already divided by the scale:
-// E4M3 round-to-nearest-even saturating to finite, or INT8 round-to-nearest-
-// even (the scale makes |x| <= 127 up to its own rounding; clamped).
-template <bool INT8>
-__device__ __forceinline__ uint32_t encode_q8(float x) {
-  if constexpr (INT8)
-    return static_cast<uint32_t>(static_cast<uint8_t>(static_cast<int8_t>(max(-127, min(127, __float2int_rn(x))))));
-  else
-    return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
 }
 
 // Quantised cache (E4M3 or INT8): per-token amax -> scale -> codes, for K then V.
@@ -150,20 +100,20 @@ __global__ void __launch_bounds__(kWriteThreads)
     float amax = 0.f;
     for (int j = threadIdx.x; j < nvec; j += blockDim.x) {
       float x[8];
-      load8<IN>(src, static_cast<size_t>(t) * Hkv * D + static_cast<size_t>(j) * 8, x);
+      dev::load8<IN>(src, static_cast<size_t>(t) * Hkv * D + static_cast<size_t>(j) * 8, x);
 #pragma unroll
       for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
     }
-    amax = block_max(amax, red);
+    amax = dev::block_max(amax, red);
     const float scale = amax > 0.f ? __fdiv_rn(amax, INT8 ? 127.0f : 448.0f) : 1.0f;
     for (int j = threadIdx.x; j < nvec; j += blockDim.x) {
       const int h = j / vpr, c = j - h * vpr;
       float x[8];
-      load8<IN>(src, (static_cast<size_t>(t) * Hkv + h) * D + c * 8, x);
+      dev::load8<IN>(src, (static_cast<size_t>(t) * Hkv + h) * D + c * 8, x);
       uint32_t lo = 0, hi = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint32_t code = encode_q8<INT8>(__fdiv_rn(x[e], scale));
+        const uint32_t code = dev::encode_q8<INT8>(__fdiv_rn(x[e], scale));
         if (e < 4)
           lo |= code << (8 * e);
         else

@@ -154,6 +154,75 @@ struct PrefillLaunch {
 };
 pa_status launch_prefill(const PrefillLaunch& a, void* stream);
 
+// Arguments of the tree attention launch after host validation.
+struct TreeLaunch {
+  const void* q;
+  int32_t q_dtype;
+  const int32_t* q_start;
+  const int64_t* mask;
+  int32_t words;
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale;  // FP8 / INT8 caches, else null
+  const float* v_scale;
+  const int32_t* block_tables;
+  int32_t max_blocks;
+  const int32_t* context_lens;
+  int32_t max_context_len, max_q_len;
+  int32_t B, T, Hq, Hkv, D, num_blocks, kv_dtype;
+  float scale;
+  void* out;
+  int32_t out_dtype;
+  void* workspace;
+  int32_t tiles;  // 128-row tiles of an item (1 or 2)
+  int32_t n_cta;  // persistent CTAs: one per SM
+};
+pa_status launch_tree(const TreeLaunch& a, void* stream);
+
+// Arguments of the rotary cache write after host validation.
+struct RopeLaunch {
+  const void* q;  // may be null with Hq = 0
+  const void* k;
+  const void* v;
+  int32_t in_dtype;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;  // elements between tokens
+  const int64_t* positions;
+  const double* inv_freq;
+  int32_t rot_dim, interleaved;
+  float factor;
+  const int64_t* slots;
+  int64_t T;
+  int32_t Hq;
+  void* q_out;
+  int32_t q_out_dtype;
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+};
+pa_status launch_rope_write(const RopeLaunch& a, const pa_cache_desc* d, void* stream);
+
+pa_status launch_tree_accept(const int64_t* draft, const int64_t* target, const int32_t* parents,
+                             const int32_t* q_start, int32_t T, int32_t B, int32_t max_path, int32_t* path,
+                             int32_t* path_len, int64_t* next_token, void* stream);
+
+struct CommitLaunch {
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* block_tables;
+  int32_t max_blocks;
+  const int32_t* context_lens;
+  const int32_t* q_start;
+  const int32_t* path;
+  int32_t max_path;
+  const int32_t* path_len;
+  int32_t B;
+  int32_t* new_lens;
+};
+pa_status launch_tree_commit(const CommitLaunch& a, const pa_cache_desc* d, void* stream);
+
 pa_status launch_cache_write(const void* k, const void* v, int32_t in_dtype,
                              const int64_t* slots, int64_t T, void* k_cache, void* v_cache,
                              float* k_scale, float* v_scale, const pa_cache_desc* d,
@@ -194,5 +263,12 @@ bool current_context_id(unsigned long long* id);
 pa_status read_errors_decode(uint32_t* flags, bool clear);
 pa_status read_errors_cache_ops(uint32_t* flags, bool clear);
 pa_status read_errors_prefill(uint32_t* flags, bool clear);
+pa_status read_errors_tree(uint32_t* flags, bool clear);
+pa_status read_errors_tree_step(uint32_t* flags, bool clear);
+
+// Host checks shared by the entry points: a valid, built cache shape; the
+// current device's SM count (148 where there is none to ask).
+pa_status check_desc(const pa_cache_desc* d, const char* fn);
+int sm_count();
 
 }  // namespace pa

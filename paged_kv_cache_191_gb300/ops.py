@@ -21,6 +21,7 @@ BLOCK_SIZE = 16
 DEVERR_SLOT_RANGE, DEVERR_BLOCK_RANGE, DEVERR_CONTEXT_LEN, DEVERR_TIMEOUT = 1, 2, 4, 8
 DEVERR_QUERY_RANGE = 16
 DEVERR_GROUP = 32
+DEVERR_TREE = 64
 
 _TORCH_DT = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32,
              torch.uint8: FP8_E4M3, torch.float8_e4m3fn: FP8_E4M3, torch.int8: INT8}
@@ -73,6 +74,16 @@ SIGNATURES = {
     "pa_last_error": (C.c_char_p, []),
     "pa_version": (_I32, []),
     "pa_cache_write": (C.c_int, [_P, _P, _I32, _P, _I64, _P, _P, _P, _P, C.POINTER(CacheDesc), _P]),
+    "pa_rope_cache_write": (C.c_int, [_P, _P, _P, _I32, _I64, _I64, _I64, _P, _P, _I32, _I32, _F, _P, _I64, _I32,
+                                      _P, _I32, _I64, _P, _P, _P, _P, C.POINTER(CacheDesc), _P]),
+    "pa_tree_mask": (C.c_int, [_P, _I32, _I32, _P, _P]),
+    "pa_tree_attention_workspace_size": (C.c_size_t, [_I32, _I32, C.POINTER(CacheDesc)]),
+    "pa_tree_attention": (C.c_int, [_P, _I32, _P, _I32, _I32, _P, _I32, _P, _P, _P, _P, _P, _I32, _P, _I32, _I32,
+                                    _I32, _F, _P, _I32, C.POINTER(CacheDesc), _P, C.c_size_t, _P]),
+    "pa_tree_accept": (C.c_int, [_P, _P, _P, _P, _I32, _I32, _I32, _P, _P, _P, _P]),
+    "pa_tree_commit": (C.c_int, [_P, _P, _P, _P, _P, _I32, _P, _P, _P, _I32, _P, _I32, _P, C.POINTER(CacheDesc),
+                                 _P]),
+    "pa_truncate_seq": (C.c_int, [_P, _U64, _I64]),
     "pa_decode_workspace_size": (C.c_size_t, [_I32, _I32, _I32, C.POINTER(CacheDesc), _I32]),
     "pa_decode_plan_info": (C.c_int, [_I32, _I32, _I32, C.POINTER(CacheDesc), _I32, _I32P, _I32P, _I32P]),
     "pa_chunked_prefill_plan_info": (C.c_int, [_I32, _I32, _I32, _I32, _I32, C.POINTER(CacheDesc), _I32,
@@ -211,6 +222,266 @@ def cache_write(k, v, slot_mapping, k_cache, v_cache, k_scale=None, v_scale=None
     _check(lib().pa_cache_write(_ptr(k), _ptr(v), _TORCH_DT[k.dtype], _ptr(slot_mapping), T,
                                 _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
                                 C.byref(desc), _stream(stream)), "pa_cache_write")
+
+
+def _same_device(*named):
+    """All the tensors (None allowed) are CUDA tensors of one device, whose
+    index is returned."""
+    dev = None
+    for t, n in named:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError(f"{n} must be a CUDA tensor")
+        d = t.get_device()
+        if dev is None:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"{n} is on another device")
+    if dev != torch.cuda.current_device():
+        raise ValueError("the tensors are not on the current device")
+    return dev
+
+
+def _dense(*named):
+    for t, n in named:
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous")
+
+
+def _scales(k_scale, v_scale, k_cache):
+    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if t is not None and (t.dtype != torch.float32 or t.shape != (k_cache.shape[0], BLOCK_SIZE)):
+            raise ValueError(f"{n} must be float32 [num_blocks, 16]")
+
+
+def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_context=4096, beta_fast=32.0,
+                     beta_slow=1.0, device=None):
+    """(inv_freq, factor) for rope_cache_write: float64 [rot_dim / 2] angles
+    per position, and the factor on cosine and sine.
+
+    scaling None: base ** (-2 i / rot_dim).  "linear": positions divided by
+    `factor`.  "ntk": the base grown so that the slowest pair turns `factor`
+    times slower.  "yarn": pairs that turn more than beta_fast times within
+    original_context are kept, those that turn less than beta_slow times slow
+    down by `factor`, with a linear ramp over the pairs between; cosine and
+    sine are multiplied by 0.1 ln(factor) + 1."""
+    import math
+    if rot_dim <= 0 or rot_dim % 16:
+        raise ValueError("rot_dim must be a positive multiple of 16")
+    if base <= 1.0 or factor < 1.0:
+        raise ValueError("base must be above 1 and factor at least 1")
+    i = torch.arange(rot_dim // 2, dtype=torch.float64)
+    if scaling == "ntk":
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    f = base ** (-2.0 * i / rot_dim)
+    attention = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        pair = lambda turns: rot_dim * math.log(original_context / (turns * 2 * math.pi)) / (2 * math.log(base))  # noqa: E731
+        lo, hi = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), rot_dim - 1)
+        ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+        f = f / factor * ramp + f * (1.0 - ramp)
+        attention = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return f.to(device) if device is not None else f, attention
+
+
+def _rows(t, name, heads_dim):
+    """Token stride of [T, H, D] rows whose last two dims are dense."""
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != heads_dim):
+        raise ValueError(f"{name} must be [T, heads, head_dim] with dense heads")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def rope_cache_write(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, interleaved=False, factor=1.0,
+                     q_out=None, k_scale=None, v_scale=None, out_dtype=None, stream=None):
+    """Rotate q [T, Hq, D] and k [T, Hkv, D] by positions [T] (int64), store k
+    and v at slot_mapping [T] (int64; < 0 stores nothing); returns the rotated
+    q (q_out, a new tensor, or None when q is None).
+
+    inv_freq: float64 [rot_dim / 2] on the device, factor: rope_frequencies.
+    q, k and v may be views of one packed projection (only their heads and
+    dims have to be dense).  q_out may be q itself."""
+    _same_device((q, "q"), (k, "k"), (v, "v"), (positions, "positions"), (inv_freq, "inv_freq"),
+                 (slot_mapping, "slot_mapping"), (k_cache, "k_cache"), (v_cache, "v_cache"), (q_out, "q_out"),
+                 (k_scale, "k_scale"), (v_scale, "v_scale"))
+    _dense((positions, "positions"), (inv_freq, "inv_freq"), (slot_mapping, "slot_mapping"), (k_cache, "k_cache"),
+           (v_cache, "v_cache"), (k_scale, "k_scale"), (v_scale, "v_scale"))
+    desc = cache_desc(k_cache)
+    D = desc.head_dim
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache differ")
+    _scales(k_scale, v_scale, k_cache)
+    ks, vs = _rows(k, "k", D), _rows(v, "v", D)
+    T = k.shape[0]
+    if k.shape != (T, desc.num_kv_heads, D) or v.shape != k.shape:
+        raise ValueError("k, v must be [T, num_kv_heads, head_dim]")
+    if k.dtype != v.dtype or k.dtype not in (torch.float16, torch.bfloat16, torch.float32):
+        raise ValueError("q, k, v must share dtype f16 / bf16 / f32")
+    if positions.dtype != torch.int64 or positions.numel() != T:
+        raise ValueError("positions must be int64 [T]")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T:
+        raise ValueError("slot_mapping must be int64 [T]")
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be float64 [rot_dim / 2]")
+    Hq, qs, os_ = 0, 0, 0
+    odt = k.dtype
+    if q is not None:
+        qs, Hq = _rows(q, "q", D), q.shape[1]
+        if q.shape[0] != T or q.shape[2] != D or q.dtype != k.dtype:
+            raise ValueError("q must be [T, num_q_heads, head_dim] in k's dtype")
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=out_dtype or q.dtype, device=q.device)
+        elif q_out.shape != q.shape or q_out.dtype not in (torch.float16, torch.bfloat16, torch.float32):
+            raise ValueError("q_out must be [T, num_q_heads, head_dim] in f16 / bf16 / f32")
+        os_, odt = _rows(q_out, "q_out", D), q_out.dtype
+    _check(lib().pa_rope_cache_write(_ptr(q), _ptr(k), _ptr(v), _TORCH_DT[k.dtype], qs, ks, vs, _ptr(positions),
+                                     _ptr(inv_freq), 2 * inv_freq.shape[0], 1 if interleaved else 0, float(factor),
+                                     _ptr(slot_mapping), T, Hq, _ptr(q_out), _TORCH_DT[odt], os_, _ptr(k_cache),
+                                     _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), C.byref(desc), _stream(stream)),
+           "pa_rope_cache_write")
+    return q_out if q is not None else None
+
+
+def tree_mask(parents, q_start=None):
+    """Host helper for tree_attention: (mask int64 [T, words], depths int32
+    [T]) of the trees whose packed parents (int [T], within the sequence, -1: a
+    root) start at q_start (int [B + 1]; None: one tree).  words is
+    ceil(largest tree / 64)."""
+    import numpy as np
+    par = np.ascontiguousarray(parents, dtype=np.int32)
+    qs = np.asarray([0, len(par)] if q_start is None else q_start, dtype=np.int64)
+    sizes = np.diff(qs)
+    if par.ndim != 1 or len(qs) < 1 or qs[0] != 0 or (sizes < 0).any() or qs[-1] != len(par):
+        raise ValueError("q_start must run from 0 to the number of nodes")
+    words = max(1, -(-int(sizes.max(initial=0)) // 64))
+    mask = np.zeros((len(par), words), dtype=np.int64)
+    depths = np.zeros(len(par), dtype=np.int32)
+    at = lambda a, i: C.c_void_p(a.ctypes.data + i * a.strides[0])  # noqa: E731
+    for i, n in zip(qs[:-1].tolist(), sizes.tolist()):
+        if n:
+            _check(lib().pa_tree_mask(at(par, i), n, words, at(mask, i), at(depths, i)), "pa_tree_mask")
+    return mask, depths
+
+
+def tree_attention_workspace_size(num_q_heads, max_q_len, k_cache):
+    return int(lib().pa_tree_attention_workspace_size(num_q_heads, int(max_q_len), C.byref(cache_desc(k_cache))))
+
+
+def tree_attention(q, q_start, tree_mask, k_cache, v_cache, block_tables, context_lens, max_context_len, max_q_len,
+                   scale, out=None, out_dtype=None, workspace=None, stream=None, k_scale=None, v_scale=None):
+    """Paged attention of drafted trees: the last q_start[b+1] - q_start[b]
+    tokens of sequence b's context are its nodes; node i sees the context
+    before the tree and the nodes whose bits its row of tree_mask (int64
+    [T, words], ops.tree_mask) sets.  q: [T, Hq, D] packed; returns out
+    [T, Hq, D] (q dtype, or out_dtype)."""
+    _same_device((q, "q"), (q_start, "q_start"), (tree_mask, "tree_mask"), (k_cache, "k_cache"),
+                 (v_cache, "v_cache"), (block_tables, "block_tables"), (context_lens, "context_lens"), (out, "out"),
+                 (workspace, "workspace"), (k_scale, "k_scale"), (v_scale, "v_scale"))
+    _dense((q, "q"), (q_start, "q_start"), (tree_mask, "tree_mask"), (k_cache, "k_cache"), (v_cache, "v_cache"),
+           (block_tables, "block_tables"), (context_lens, "context_lens"), (out, "out"), (workspace, "workspace"),
+           (k_scale, "k_scale"), (v_scale, "v_scale"))
+    desc = cache_desc(k_cache)
+    T, Hq, D = q.shape
+    B = context_lens.numel()
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache differ")
+    _scales(k_scale, v_scale, k_cache)
+    if D != desc.head_dim:
+        raise ValueError("q head_dim differs from the cache")
+    if q_start.dtype != torch.int32 or q_start.numel() != B + 1:
+        raise ValueError("q_start must be int32 [B + 1]")
+    if tree_mask.dtype != torch.int64 or tree_mask.dim() != 2 or tree_mask.shape[0] != T:
+        raise ValueError("tree_mask must be int64 [T, words]")
+    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("block_tables must be int32 [B, max_blocks]")
+    if context_lens.dtype != torch.int32:
+        raise ValueError("context_lens must be int32 [B]")
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=out_dtype or q.dtype, device=q.device)
+    elif out.shape != (T, Hq, D):
+        raise ValueError("out must be [T, Hq, D]")
+    L = lib()
+    if workspace is None:
+        workspace = torch.empty(int(L.pa_tree_attention_workspace_size(Hq, int(max_q_len), C.byref(desc))),
+                                dtype=torch.uint8, device=q.device)
+    _check(L.pa_tree_attention(_ptr(q), _dtype(q, "q"), _ptr(q_start), T, int(max_q_len), _ptr(tree_mask),
+                               tree_mask.shape[1], _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                               _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), int(max_context_len),
+                               B, Hq, float(scale), _ptr(out), _dtype(out, "out"), C.byref(desc), _ptr(workspace),
+                               workspace.numel() * workspace.element_size(), _stream(stream)), "pa_tree_attention")
+    return out
+
+
+def _dtype(t, name):
+    dt = _TORCH_DT.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{name}: unsupported dtype {t.dtype}")
+    return dt
+
+
+def tree_accept(draft_tokens, target_tokens, parents, q_start, max_path, stream=None):
+    """Accepted path of every tree: (path int32 [B, max_path] padded with -1,
+    path_len int32 [B], next_token int64 [B]).  draft_tokens, target_tokens
+    int64 [T]: the nodes' tokens and the model's pick after each; parents
+    int32 [T]; q_start int32 [B + 1]."""
+    _same_device((draft_tokens, "draft_tokens"), (target_tokens, "target_tokens"), (parents, "parents"),
+                 (q_start, "q_start"))
+    _dense((draft_tokens, "draft_tokens"), (target_tokens, "target_tokens"), (parents, "parents"),
+           (q_start, "q_start"))
+    T, B = draft_tokens.numel(), q_start.numel() - 1
+    if draft_tokens.dtype != torch.int64 or target_tokens.dtype != torch.int64 or target_tokens.numel() != T:
+        raise ValueError("draft_tokens and target_tokens must be int64 [T]")
+    if parents.dtype != torch.int32 or parents.numel() != T:
+        raise ValueError("parents must be int32 [T]")
+    if q_start.dtype != torch.int32 or B < 0:
+        raise ValueError("q_start must be int32 [B + 1]")
+    dev = q_start.device
+    path = torch.empty((B, max_path), dtype=torch.int32, device=dev)
+    path_len = torch.empty((B,), dtype=torch.int32, device=dev)
+    token = torch.empty((B,), dtype=torch.int64, device=dev)
+    _check(lib().pa_tree_accept(_ptr(draft_tokens), _ptr(target_tokens), _ptr(parents), _ptr(q_start), T, B,
+                                int(max_path), _ptr(path), _ptr(path_len), _ptr(token), _stream(stream)),
+           "pa_tree_accept")
+    return path, path_len, token
+
+
+def tree_commit(k_cache, v_cache, block_tables, context_lens, q_start, path, path_len, k_scale=None, v_scale=None,
+                new_lens=None, stream=None):
+    """Move the accepted nodes' cache rows together, in place: path element i
+    of sequence b goes to the i-th position of its tree.  Returns the new
+    context lengths (int32 [B])."""
+    _same_device((k_cache, "k_cache"), (v_cache, "v_cache"), (block_tables, "block_tables"),
+                 (context_lens, "context_lens"), (q_start, "q_start"), (path, "path"), (path_len, "path_len"),
+                 (k_scale, "k_scale"), (v_scale, "v_scale"), (new_lens, "new_lens"))
+    _dense((k_cache, "k_cache"), (v_cache, "v_cache"), (block_tables, "block_tables"),
+           (context_lens, "context_lens"), (q_start, "q_start"), (path, "path"), (path_len, "path_len"),
+           (k_scale, "k_scale"), (v_scale, "v_scale"), (new_lens, "new_lens"))
+    desc = cache_desc(k_cache)
+    B = context_lens.numel()
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache differ")
+    _scales(k_scale, v_scale, k_cache)
+    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("block_tables must be int32 [B, max_blocks]")
+    if context_lens.dtype != torch.int32 or path_len.dtype != torch.int32 or path_len.numel() != B:
+        raise ValueError("context_lens and path_len must be int32 [B]")
+    if q_start.dtype != torch.int32 or q_start.numel() != B + 1:
+        raise ValueError("q_start must be int32 [B + 1]")
+    if path.dtype != torch.int32 or path.dim() != 2 or path.shape[0] != B:
+        raise ValueError("path must be int32 [B, max_path]")
+    if new_lens is None:
+        new_lens = torch.empty((B,), dtype=torch.int32, device=context_lens.device)
+    elif new_lens.dtype != torch.int32 or new_lens.numel() != B:
+        raise ValueError("new_lens must be int32 [B]")
+    _check(lib().pa_tree_commit(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_tables),
+                                block_tables.shape[1], _ptr(context_lens), _ptr(q_start), _ptr(path), path.shape[1],
+                                _ptr(path_len), B, _ptr(new_lens), C.byref(desc), _stream(stream)),
+           "pa_tree_commit")
+    return new_lens
 
 
 def decode_plan_info(B, num_q_heads, max_context_len, k_cache, split_tokens=0):
@@ -672,6 +943,10 @@ class BlockAllocator:
         n = len(ids)
         A = (C.c_uint64 * max(n, 1))(*ids)
         _check(lib().pa_free_seqs(self._h, A, n), "pa_free_seqs")
+
+    def truncate_seq(self, seq_id, num_tokens):
+        """Keep the first num_tokens tokens; the blocks behind them are released."""
+        _check(lib().pa_truncate_seq(self._h, seq_id, num_tokens), "pa_truncate_seq")
 
     def free_seq(self, seq_id):
         _check(lib().pa_free_seq(self._h, seq_id), "pa_free_seq")
