@@ -554,7 +554,7 @@ size_t pa_tree_attention_workspace_size(int32_t num_q_heads, int32_t max_q_len, 
  * rows that see it, whatever it holds (infinities and NaN included).
  *
  * q, q_start, k_scale, v_scale, block_tables, context_lens, max_context_len,
- * out          as pa_chunked_prefill; any number of query heads per kv head.
+ * out          as pa_chunked_prefill; up to 128 query heads per kv head.
  *              n_b > L_b is flagged PA_DEVERR_CONTEXT_LEN; the nodes before
  *              the cached ones have no key then.
  * max_q_len    host upper bound on n_b (<= 65535); longer sequences are

@@ -174,7 +174,6 @@ struct TreeLaunch {
   void* out;
   int32_t out_dtype;
   void* workspace;
-  int32_t tiles;  // 128-row tiles of an item (1 or 2)
   int32_t n_cta;  // persistent CTAs: one per SM
 };
 pa_status launch_tree(const TreeLaunch& a, void* stream);

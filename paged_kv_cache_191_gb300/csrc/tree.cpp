@@ -11,12 +11,12 @@ namespace {
 
 bool mis(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
 
-// Rows of an item: two 128-row tiles when a sequence can have more than one
-// tile's worth of (node, head) rows per kv head.
-int32_t tree_tiles(int32_t max_q_len, int32_t num_q_heads, const pa_cache_desc* d) {
-  return static_cast<int64_t>(max_q_len) * (num_q_heads / d->num_kv_heads) > 128 ? 2 : 1;
+// Rows a node takes in a tile: its heads per kv head, up to a power of two.
+int32_t node_rows(int32_t num_q_heads, const pa_cache_desc* d) {
+  int32_t r = 1;
+  while (r < num_q_heads / d->num_kv_heads) r *= 2;
+  return r;
 }
-
 pa_status check_tree(int32_t T, int32_t num_q_heads, int32_t max_q_len, const pa_cache_desc* desc) {
   pa_status st = pa::check_desc(desc, "pa_tree_attention");
   if (st != PA_OK) return st;
@@ -26,14 +26,16 @@ pa_status check_tree(int32_t T, int32_t num_q_heads, int32_t max_q_len, const pa
   if (max_q_len > 65535) return fail(PA_ERR_UNSUPPORTED, "pa_tree_attention: max_q_len above 65535");
   if (num_q_heads % desc->num_kv_heads)
     return fail(PA_ERR_INVALID, "pa_tree_attention: num_q_heads must be a multiple of num_kv_heads");
-  if (static_cast<int64_t>(max_q_len) * (num_q_heads / desc->num_kv_heads) > INT32_MAX)
-    return fail(PA_ERR_UNSUPPORTED, "pa_tree_attention: too many rows per kv head");
+  if (num_q_heads / desc->num_kv_heads > 128)
+    return fail(PA_ERR_UNSUPPORTED, "pa_tree_attention: more than 128 query heads per kv head");
   return PA_OK;
 }
 
-size_t tree_workspace(int32_t max_q_len, int32_t num_q_heads, const pa_cache_desc* d) {
-  const size_t rows = static_cast<size_t>(2) * pa::sm_count() * 128 * tree_tiles(max_q_len, num_q_heads, d);
-  return (rows * (d->head_dim + 2) * sizeof(float) + 255) & ~static_cast<size_t>(255);
+// Per CTA two sets of 128 partial rows (o, m, l) and 32 bytes on the item it
+// leaves unfinished.
+size_t tree_workspace(const pa_cache_desc* d) {
+  const size_t ctas = static_cast<size_t>(pa::sm_count());
+  return (ctas * (2 * 128 * (d->head_dim + 2) * sizeof(float) + 32) + 255) & ~static_cast<size_t>(255);
 }
 
 }  // namespace
@@ -116,7 +118,7 @@ pa_status pa_rope_cache_write(const void* q, const void* k, const void* v, int32
 
 size_t pa_tree_attention_workspace_size(int32_t num_q_heads, int32_t max_q_len, const pa_cache_desc* desc) {
   if (check_tree(0, num_q_heads, max_q_len, desc) != PA_OK) return 0;
-  return tree_workspace(max_q_len, num_q_heads, desc);
+  return tree_workspace(desc);
 }
 
 pa_status pa_tree_attention(const void* q, int32_t q_dtype, const int32_t* q_start, int32_t num_tokens,
@@ -148,15 +150,14 @@ pa_status pa_tree_attention(const void* q, int32_t q_dtype, const int32_t* q_sta
   if (mis(q, 16) || mis(k_cache, 16) || mis(v_cache, 16) || mis(out, 16) || mis(tree_mask, 8) || mis(q_start, 4) ||
       mis(block_tables, 4) || mis(context_lens, 4))
     return fail(PA_ERR_INVALID, "%s: misaligned pointer", fn);
-  const int32_t tiles = tree_tiles(max_q_len, num_q_heads, desc);
   // units of work (128-key chunks of every item) are counted in 32 bits
-  const int64_t G = num_q_heads / desc->num_kv_heads, chunks = static_cast<int64_t>(max_context_len) / 128 + 1;
-  const int64_t items = static_cast<int64_t>(num_tokens) * G / (128 * tiles) + B;
+  const int64_t G = node_rows(num_q_heads, desc), chunks = static_cast<int64_t>(max_context_len) / 128 + 1;
+  const int64_t items = static_cast<int64_t>(num_tokens) * G / 128 + B;
   if (items * desc->num_kv_heads > INT32_MAX / 2 / chunks)
     return fail(PA_ERR_UNSUPPORTED, "%s: more than 2^30 chunks of work", fn);
-  if (static_cast<int64_t>(num_tokens) * num_q_heads > static_cast<int64_t>(INT32_MAX) * 8)
+  if (static_cast<int64_t>(num_tokens) * num_q_heads > INT32_MAX)
     return fail(PA_ERR_UNSUPPORTED, "%s: too many query rows for one grid", fn);
-  const size_t need = tree_workspace(max_q_len, num_q_heads, desc);
+  const size_t need = tree_workspace(desc);
   if (!workspace || !pa::aligned16(workspace) || workspace_bytes < need)
     return fail(PA_ERR_INVALID, "%s: workspace NULL, misaligned or %zu of %zu bytes", fn, workspace_bytes, need);
   pa::TreeLaunch a;
@@ -185,7 +186,6 @@ pa_status pa_tree_attention(const void* q, int32_t q_dtype, const int32_t* q_sta
   a.out = out;
   a.out_dtype = out_dtype;
   a.workspace = workspace;
-  a.tiles = tiles;
   a.n_cta = pa::sm_count();
   return pa::launch_tree(a, stream);
 }
