@@ -11,7 +11,8 @@
 // Rows and work.  The query rows of one (sequence, kv head) are the pairs
 // (node, head of the group), the group padded to a power of two; they all read
 // the same K/V, so an item is up to 128 of them, and streams the context in
-// chunks of 128 keys (8 blocks).  One unit of work is one chunk of one item; the
+// chunks of 128 keys (8 blocks).  One unit of work is one chunk of one item (an item's start
+// and end count as kItem more); the
 // launch has one persistent CTA per SM, and CTA k takes units [k u, (k + 1) u)
 // of the batch in order, u = ceil(units / CTAs): every CTA streams the same
 // number of chunks whatever the lengths.  The lengths stay on the device: each
@@ -78,9 +79,10 @@ constexpr int kBlk = kKeys / 16;
 constexpr int kRows = 128;  // rows of an item
 constexpr float kMove = 8.f;  // log2 of how far an exponent may outgrow its reference
 constexpr uint32_t kTmemCols = 512;
-// tensor memory columns: S^T [tile] x 64, minus the references [tile] x 64,
-// O^T [piece parity][tile] x 64
-constexpr uint32_t kColS = 0, kColR = 128, kColO = 256;
+// tensor memory columns: S^T [tile] x 64, minus the references [tile] x 64, O^T
+// [piece parity][tile] x 64.  Pieces of more than 64 rows keep O^T in the first
+// of its two places and use the other as a second S^T, for odd chunks.
+constexpr uint32_t kColS = 0, kColR = 128, kColO = 256, kColS2 = 384;
 constexpr uint64_t kLimit = 2000000000ull;
 
 struct TreeArgs {
@@ -132,7 +134,9 @@ __device__ __forceinline__ Seq seq_of(const TreeArgs& a, int b, bool report) {
   s.nch = max(1, (s.L + kKeys - 1) / kKeys);  // a sequence without keys still owns its zero rows
   return s;
 }
-__device__ __forceinline__ int units_of(const TreeArgs& a, const Seq& s) { return s.tiles * a.Hkv * s.nch; }
+// An item's cost in units: its chunks, and kItem for its start and end.
+constexpr int kItem = 3;
+__device__ __forceinline__ int units_of(const TreeArgs& a, const Seq& s) { return s.tiles * a.Hkv * (s.nch + kItem); }
 __device__ __forceinline__ int warp_sum(int v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(FULL, v, off);
@@ -161,7 +165,7 @@ struct Lay {
   static constexpr int NS = D == 64 ? 8 : 4;
   static constexpr int SCALES = RING + NS * SLOT;    // 1-byte codes: [8 chunks][K 128, V 128] float
   static constexpr int BAR = SCALES + (Q8 ? 8 * 1024 : 0);
-  static constexpr int NBAR = 3 * NS + 26;
+  static constexpr int NBAR = 3 * NS + 28;
   static constexpr int MISC = (BAR + NBAR * 8 + 15) & ~15;  // tensor memory, items issued, force; at 64: bad keys
   static constexpr int PIECE = MISC + 128;           // Piece [4]
   static constexpr int PUB = PIECE + 4 * 48;         // float2 [2 tiles][64]
@@ -241,15 +245,6 @@ __device__ __forceinline__ void more_registers() {
 // Loads that have arrived when they return (load and wait in one statement, so
 // no use of the registers can be scheduled between them).
 #define PA_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : PA_R8(r, 0), PA_R8(r, 8), PA_R8(r, 16), PA_R8(r, 24)
-      : "r"(taddr)
-      : "memory");
-}
 // 16 columns at two places under one wait.
 __device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, uint32_t (&r)[16], uint32_t (&s)[16]) {
   asm volatile(
@@ -290,13 +285,17 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return d;
 }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
+// l += a pair of 16-bit weights, without unpacking it.
+template <typename T>
+__device__ __forceinline__ void add16x2(float2& l, uint32_t pair) {
+  if constexpr (std::is_same<T, __half>::value)
+    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tadd.rn.f32.f16 %0, x, %0;\n\tadd.rn.f32.f16 %1, y, %1;\n\t}"
+        : "+f"(l.x), "+f"(l.y)
+        : "r"(pair));
+  else
+    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tadd.rn.f32.bf16 %0, x, %0;\n\tadd.rn.f32.bf16 %1, y, %1;\n\t}"
+        : "+f"(l.x), "+f"(l.y)
+        : "r"(pair));
 }
 __device__ __forceinline__ float warp_max(float v) {
   float m;
@@ -341,17 +340,17 @@ struct Sync {
   __device__ __forceinline__ uint32_t empty(int s) const { return at(2 * L::NS + s); }   // its last product ended
   __device__ __forceinline__ uint32_t ready(int s) const { return L::Q8 ? conv(s) : full(s); }
   __device__ __forceinline__ uint32_t ext(int i) const { return at(3 * L::NS + i); }
-  __device__ __forceinline__ uint32_t sfull(int t) const { return ext(t); }        // S^T of tile t
-  __device__ __forceinline__ uint32_t sfree(int t) const { return ext(2 + t); }    // and read
-  __device__ __forceinline__ uint32_t pfull(int t) const { return ext(4 + t); }    // P^T in shared memory
-  __device__ __forceinline__ uint32_t pdone(int t) const { return ext(6 + t); }    // O^T += V^T P^T ended
-  __device__ __forceinline__ uint32_t qfull(int i) const { return ext(8 + i); }    // Q of a piece landed
-  __device__ __forceinline__ uint32_t qfree(int i) const { return ext(10 + i); }   // its last S^T ended
-  __device__ __forceinline__ uint32_t ofree(int i) const { return ext(12 + i); }   // piece parity i: both warpgroups are done
-  __device__ __forceinline__ uint32_t pub(int t) const { return ext(14 + t); }     // tile t's l and references of the piece
-  __device__ __forceinline__ uint32_t mfull(int i) const { return ext(16 + i); }   // mask words of a piece
-  __device__ __forceinline__ uint32_t pieces(int i) const { return ext(18 + i); }  // piece i % 4 published
-  __device__ __forceinline__ uint32_t mdone() const { return ext(22); }            // after a timeout: products have ended
+  __device__ __forceinline__ uint32_t sfull(int t, int b) const { return ext(2 * t + b); }      // S^T of tile t, buffer b
+  __device__ __forceinline__ uint32_t sfree(int t, int b) const { return ext(4 + 2 * t + b); }  // and read
+  __device__ __forceinline__ uint32_t pfull(int t) const { return ext(8 + t); }     // P^T in shared memory
+  __device__ __forceinline__ uint32_t pdone(int t) const { return ext(10 + t); }    // O^T += V^T P^T ended
+  __device__ __forceinline__ uint32_t qfull(int i) const { return ext(12 + i); }    // Q of a piece landed
+  __device__ __forceinline__ uint32_t qfree(int i) const { return ext(14 + i); }    // its last S^T ended
+  __device__ __forceinline__ uint32_t ofree(int i) const { return ext(16 + i); }    // piece parity i: both warpgroups are done
+  __device__ __forceinline__ uint32_t pub(int t) const { return ext(18 + t); }      // tile t's l and references of the piece
+  __device__ __forceinline__ uint32_t mfull(int i) const { return ext(20 + i); }    // mask words of a piece
+  __device__ __forceinline__ uint32_t pieces(int i) const { return ext(22 + i); }   // piece i % 4 published
+  __device__ __forceinline__ uint32_t mdone() const { return ext(26); }             // after a timeout: products have ended
   __device__ __forceinline__ uint32_t issued() const { return base + L::MISC + 16; }
   // piece i of the CTA; false after the last (or a timeout)
   __device__ __forceinline__ bool piece(const uint8_t* gb, int i, Piece& p, bool& ok) const {
@@ -409,15 +408,22 @@ __device__ __forceinline__ void plan(const TreeArgs& a, uint8_t* gb, Sync<L> sy)
     if (ok && i >= 4) ok = wait_warp(sy.ofree(i & 1), ((i - 4) >> 1) & 1);
     if (i <= pieces && pieces == INT32_MAX) {
       Piece p;
-      p.live = u < end;
-      if (u < end) {
+      p.live = 0;
+#pragma unroll 1
+      while (u < end && !p.live) {
         Seq s = seq_of(a, b, false);
 #pragma unroll 1
         while (u >= ub + units_of(a, s)) {
           ub += units_of(a, s);
           s = seq_of(a, ++b, false);
         }
-        const int at = u - ub, item = at / s.nch;
+        const int cost = s.nch + kItem, at = u - ub, item = at / cost, off = at - item * cost;
+        const int stop = min(cost, off + end - u);  // of the item, for this CTA
+        p.c0 = max(0, off - kItem);
+        p.c1 = stop - kItem;
+        u += stop - off;
+        if (p.c1 <= p.c0) continue;  // the range ends before the item's first chunk
+        p.live = 1;
         p.b = b;
         p.qs = s.qs;
         p.n = s.n;
@@ -425,18 +431,14 @@ __device__ __forceinline__ void plan(const TreeArgs& a, uint8_t* gb, Sync<L> sy)
         p.g = item / s.tiles;
         p.row0 = (item - p.g * s.tiles) * kRows;
         p.rows = min(kRows, (s.n << a.gl) - p.row0);
-        p.c0 = at - item * s.nch;
-        p.c1 = min(s.nch, p.c0 + end - u);
-        p.slot = p.c0 == 0 && p.c1 == s.nch ? -1 : 2 * static_cast<int>(blockIdx.x) + (u == start ? 0 : 1);
+        p.slot = p.c0 == 0 && p.c1 == s.nch ? -1 : 2 * static_cast<int>(blockIdx.x) + (i == 0 ? 0 : 1);
         if (p.c0 == 0 && p.c1 < s.nch) {  // the item goes on in the next CTAs: what tree_merge needs
-          sp0 = make_int4((u + s.nch - 1) / upc - static_cast<int>(blockIdx.x) + 1, p.slot, s.qs, p.row0);
+          sp0 = make_int4((ub + (item + 1) * cost - 1) / upc - static_cast<int>(blockIdx.x) + 1, p.slot, s.qs, p.row0);
           sp1 = make_int4(p.g, p.rows, 0, 0);
         }
-        u += p.c1 - p.c0;
-        p.last = u >= end;
-      } else {
-        pieces = i;
       }
+      p.last = u >= end;  // (or only an item's start is left)
+      if (!p.live) pieces = i;
       if (lane == 0) {
         ring[i & 3] = p;
         mbar_arrive(sy.pieces(i & 3));
@@ -516,7 +518,9 @@ __device__ __forceinline__ void produce(const TreeArgs& a, const CUtensorMap* tm
         ids = ids_next;
         ids_next = c + 4 < p.c1 ? fetch(p, (c + 4) * kBlk) : ids_n;
       }
-      const int id = __shfl_sync(FULL, ids, k4 * kBlk + (lane & 7));
+      int blk[kBlk];  // the chunk's block ids
+#pragma unroll
+      for (int k = 0; k < kBlk; ++k) blk[k] = __shfl_sync(FULL, ids, k4 * kBlk + k);
       const int live = max(0, min(kBlk, nblk - c * kBlk));  // blocks of this chunk that exist
 #pragma unroll 1
       for (int v = 0; v < 2; ++v) {
@@ -534,21 +538,21 @@ __device__ __forceinline__ void produce(const TreeArgs& a, const CUtensorMap* tm
         }
         __syncwarp();
         const CUtensorMap* m = v ? tmV : tmK;
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kBlk; ++k) {
-          const int blk = uniform(__shfl_sync(FULL, id, k));
-          if (k < live && elect_one()) {
+          for (int k = 0; k < kBlk; ++k) {
+            if (k >= live) break;
             if constexpr (L::Q8) {
-              dev::tma_load_3d(dst + L::SLOT / 2 + k * 2048, m, bar, 0, p.g * 16, blk);
+              dev::tma_load_3d(dst + L::SLOT / 2 + k * 2048, m, bar, 0, p.g * 16, blk[k]);
               if (v == 0) {
                 const uint32_t sc = sy.base + L::SCALES + (((it - 1) >> 1) & 7) * 1024 + k * 64;
-                dev::bulk_load(sc, a.k_scale + static_cast<size_t>(blk) * 16, 64, bar);
-                dev::bulk_load(sc + 512, a.v_scale + static_cast<size_t>(blk) * 16, 64, bar);
+                dev::bulk_load(sc, a.k_scale + static_cast<size_t>(blk[k]) * 16, 64, bar);
+                dev::bulk_load(sc + 512, a.v_scale + static_cast<size_t>(blk[k]) * 16, 64, bar);
               }
             } else if constexpr (D == 64) {  // [block][16][128 B]
-              dev::tma_load_3d(dst + k * 2048, m, bar, 0, p.g * 16, blk);
+              dev::tma_load_3d(dst + k * 2048, m, bar, 0, p.g * 16, blk[k]);
             } else {                         // [block][group of 8][span][8][128 B]
-              dev::tma_load_5d(dst + k * 4096, m, bar, 0, 0, 0, 2 * p.g, blk);
+              dev::tma_load_5d(dst + k * 4096, m, bar, 0, 0, 0, 2 * p.g, blk[k]);
             }
           }
         }
@@ -588,11 +592,12 @@ struct Cursor {
     if (!pair) ph ^= nc & 1;
     ++i;
   }
-  __device__ __forceinline__ void next(const Sync<L>& sy, const uint8_t* gb, bool& ok) {
-    if (++c == nc) {
-      close();
-      open(sy, gb, ok);
-    }
+  // true: the next chunk is another piece's
+  __device__ __forceinline__ bool next(const Sync<L>& sy, const uint8_t* gb, bool& ok) {
+    if (++c < nc) return false;
+    close();
+    open(sy, gb, ok);
+    return true;
   }
   __device__ __forceinline__ int tile() const { return pair ? 0 : (ph + c) & 1; }
 };
@@ -621,7 +626,8 @@ __device__ __forceinline__ void multiply(const TreeArgs& a, uint8_t* gb, Sync<L>
   same(s);
   same(o);
   int ahead = 0, spin = 0;                 // chunks whose S^T is issued and O^T not
-  int ns0 = 0, ns1 = 0, no0 = 0, no1 = 0;  // S^T, O^T issued per tile
+  int ns00 = 0, ns01 = 0, ns10 = 0, ns11 = 0;  // S^T issued per tile and buffer
+  int no0 = 0, no1 = 0, pieces_over = 0;       // O^T per tile; pieces that both warpgroups are done with
   uint64_t t0 = 0;
   auto test = [&](uint32_t bar, int parity) { return uniform(dev::mbar_test(bar, parity & 1)) != 0; };
   auto landed = [&](int i) { return test(sy.ready(i % NS), i / NS); };
@@ -636,7 +642,7 @@ __device__ __forceinline__ void multiply(const TreeArgs& a, uint8_t* gb, Sync<L>
         const uint32_t id = idesc<T>((o.p.rows + 15) & ~15, true) | (1u << 15);
         const uint64_t vd = sdesc(sy.base + L::RING + (i % NS) * L::SLOT, D == 128 ? 1024 : 0, L::GRP);
         const uint64_t pd = sdesc(sy.base + L::P0 + t * 16384, 16384, 1024);
-        const uint32_t od = tmem + kColO + 128 * (o.i & 1) + 64 * t;
+        const uint32_t od = tmem + kColO + (o.pair ? 0 : 128 * (o.i & 1) + 64 * t);
         const uint32_t forced = uniform(force[t]);
         const uint32_t acc = o.c >= (o.pair ? 1 : 2) || forced ? 1u : 0u;
         if (elect_one()) {
@@ -652,35 +658,41 @@ __device__ __forceinline__ void multiply(const TreeArgs& a, uint8_t* gb, Sync<L>
         no0 += o.pair || t == 0;
         no1 += o.pair || t == 1;
         --ahead;
-        o.next(sy, gb, ok);
-        same(o);
+        if (o.next(sy, gb, ok)) same(o);
         moved = true;
       }
     }
     if (s.live && ahead < 2) {
-      const int t = s.tile(), i = s.it0 + 2 * s.c, qb = s.i % L::QB, ns = t ? ns1 : ns0;
-      if ((s.c > 0 || test(sy.qfull(qb), s.i / L::QB)) && landed(i) && (ns == 0 || test(sy.sfree(t), ns - 1)) &&
-          (!s.pair || ns1 == 0 || test(sy.sfree(1), ns1 - 1))) {
+      const int t = s.tile(), i = s.it0 + 2 * s.c, qb = s.i % L::QB;
+      // The buffer's last scores are read.  A first chunk also waits for the
+      // piece before last to be over; a pair's second buffer may hold O^T of the
+      // piece before.
+      const int sb = s.pair ? s.c & 1 : 0, n0 = sb ? ns01 : ns00, n1 = sb ? ns11 : ns10;
+      const int over = sb && s.c == 1 ? s.i : s.c == 0 ? s.i - 1 : 0;
+      if (pieces_over < over && test(sy.ofree(pieces_over & 1), pieces_over >> 1)) ++pieces_over;
+      if (pieces_over >= over && (t == 1 || n0 == 0 || test(sy.sfree(0, sb), n0 - 1)) &&
+          ((t == 0 && !s.pair) || n1 == 0 || test(sy.sfree(1, sb), n1 - 1)) &&
+          (s.c > 0 || test(sy.qfull(qb), s.i / L::QB)) && landed(i)) {
         fence_after();
         const uint32_t id = idesc<T>((s.p.rows + 15) & ~15, false) | (a.negate << 14);
         const uint64_t kd = sdesc(sy.base + L::RING + (i % NS) * L::SLOT, 16, L::GRP);
         const uint64_t qd = sdesc(sy.base + qb * L::QTILE, 16, 1024);
+        const uint32_t sd = tmem + (sb ? kColS2 : kColS + 64 * t);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(tmem + kColS + 64 * t, kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
+            mma_ss(sd, kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
                    qd + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4), id, kk > 0 ? 1u : 0u);
-          commit(sy.sfull(t));
-          if (s.pair) commit(sy.sfull(1));
+          commit(sy.sfull(t, sb));
+          if (s.pair) commit(sy.sfull(1, sb));
           commit(sy.empty(i % NS));
           if (s.c + 1 == s.nc) commit(sy.qfree(qb));
         }
         __syncwarp();
-        ns0 += s.pair || t == 0;
-        ns1 += s.pair || t == 1;
+        if (s.pair || t == 0) ++(sb ? ns01 : ns00);
+        if (s.pair || t == 1) ++(sb ? ns11 : ns10);
         ++ahead;
-        s.next(sy, gb, ok);
-        same(s);
+        if (s.next(sy, gb, ok)) same(s);
         moved = true;
       }
     }
@@ -782,22 +794,28 @@ __device__ __forceinline__ uint2 visible(const TreeArgs& a, const uint8_t* gb, c
 // be multiplied by, in scratch[320 ..], if the result's bit 0 is set.  Bit 1:
 // some row still has no reference.
 template <typename L>
-__device__ __forceinline__ int settle(const Lane& x, float ks, uint2 vis, int words, uint32_t oc, bool exists, bool& seen,
+__device__ __forceinline__ int settle(const Lane& x, uint32_t sc, float ks, uint2 vis, int words, uint32_t oc, bool exists, bool& seen,
                                    float& ref) {
   const int bar = 2 + x.t;
+  float best0 = -INFINITY, best1 = -INFINITY;  // of rows lane, 32 + lane
 #pragma unroll 1
-  for (int w = 0; w < words; ++w) {
-    uint32_t u[32];
-    tmem_ld32(x.tl + kColS + 64 * x.t + 32 * w, u);
-    const uint32_t v = w ? vis.y : vis.x;
-    float mine = -INFINITY;
+  for (int j = 0; j < 32 * words; j += 8) {
+    uint32_t u[8];
+    tmem_ld8(sc + j, u);
+    const uint32_t v = (j & 32 ? vis.y : vis.x) >> (j & 31);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const float m = warp_max((v >> j) & 1u ? __uint_as_float(u[j]) * ks : -INFINITY);
-      if (x.lane == j) mine = m;
+    for (int e = 0; e < 8; ++e) {
+      const float m = warp_max((v >> e) & 1u ? __uint_as_float(u[e]) * ks : -INFINITY);
+      if (x.lane == (j & 31) + e) {
+        if (j & 32)
+          best1 = m;
+        else
+          best0 = m;
+      }
     }
-    x.scratch[64 * x.w4 + 32 * w + x.lane] = mine;
   }
+  x.scratch[64 * x.w4 + x.lane] = best0;
+  x.scratch[64 * x.w4 + 32 + x.lane] = best1;
   named_bar(bar, 128);
   bool rescale = false;
   if (x.r < 32 * words) {
@@ -815,15 +833,15 @@ __device__ __forceinline__ int settle(const Lane& x, float ks, uint2 vis, int wo
   rescale = bar_or(bar, 128, rescale);
 #pragma unroll 1
   for (int j = 0; j < 32 * words; j += 8) {
-    uint32_t u[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) u[e] = __float_as_uint(x.scratch[256 + j + e]);
+    const uint4* f = reinterpret_cast<const uint4*>(x.scratch + 256 + j);
+    const uint32_t u[8] = {f[0].x, f[0].y, f[0].z, f[0].w, f[1].x, f[1].y, f[1].z, f[1].w};
     tmem_st8(x.tl + kColR + 64 * x.t + j, u);
     if (rescale) {
-      tmem_ld8(oc + j, u);
+      uint32_t o[8];
+      tmem_ld8(oc + j, o);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * x.scratch[320 + j + e]);
-      tmem_st8(oc + j, u);
+      for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * x.scratch[320 + j + e]);
+      tmem_st8(oc + j, o);
     }
   }
   tcg::wait_st();
@@ -906,9 +924,11 @@ __device__ __forceinline__ void write_rows(const TreeArgs& a, const Lane& x, con
                                         bool both, int row0, int rows, bool exists) {
   constexpr int D = L::D;
   const bool direct = p.slot < 0, narrow = direct && !a.out_f32;
-  const int gm = (1 << a.gl) - 1, base = p.row0 + row0;
-  const size_t prow = direct ? 0 : static_cast<size_t>(p.slot) * kRows + row0;
+  const int base = p.row0 + row0;
   float* wts = x.scratch + 512;  // [2 accumulators][64]
+  int* place = reinterpret_cast<int*>(x.scratch + 640);
+  float* to32 = (direct ? static_cast<float*>(a.out) : a.part_o) + x.r;
+  T* to16 = static_cast<T*>(a.out) + x.r;
   if (x.r < 64) {
     const float2 c0 = pubs[(both ? 0 : 64 * x.t) + x.r], c1 = both ? pubs[64 + x.r] : make_float2(-INFINITY, 0.f);
     const float m = fmaxf(c0.x, c1.x), mz = m == -INFINITY ? 0.f : m;
@@ -917,9 +937,12 @@ __device__ __forceinline__ void write_rows(const TreeArgs& a, const Lane& x, con
     const float inv = direct && m != -INFINITY ? 1.f / sum : 1.f;
     wts[x.r] = w0 * inv;
     wts[64 + x.r] = w1 * inv;
+    // where the row goes, in rows of out or of the partials
+    const int row = base + x.r, h = row & ((1 << a.gl) - 1);
+    place[x.r] = !exists ? -1 : direct ? (p.qs + (row >> a.gl)) * a.Hq + p.g * a.G + h : p.slot * kRows + row0 + x.r;
     if (!direct && exists) {
-      a.part_m[prow + x.r] = m;
-      a.part_l[prow + x.r] = sum;
+      a.part_m[place[x.r]] = m;
+      a.part_l[place[x.r]] = sum;
     }
   }
   named_bar(2 + x.t, 128);
@@ -931,20 +954,15 @@ __device__ __forceinline__ void write_rows(const TreeArgs& a, const Lane& x, con
     if (both) tmem_ld8(oa + 64 + j0, v);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int row = j0 + e, h = (base + row) & gm;
-      const float w0 = wts[row], w1 = wts[64 + row];
+      const float w0 = wts[j0 + e], w1 = wts[64 + j0 + e];
       float o = w0 == 0.f ? 0.f : __uint_as_float(u[e]) * w0;
       if (both && w1 != 0.f) o = fmaf(__uint_as_float(v[e]), w1, o);
-      if (row >= rows || h >= a.G) continue;
-      if (!direct) {
-        a.part_o[(prow + row) * D + x.r] = o;
-      } else {
-        const size_t at = static_cast<size_t>((p.qs + ((base + row) >> a.gl)) * a.Hq + p.g * a.G + h) * D + x.r;
-        if (narrow)
-          static_cast<uint16_t*>(a.out)[at] = static_cast<uint16_t>(dev::pack2<T>(o, 0.f));
-        else
-          static_cast<float*>(a.out)[at] = o;
-      }
+      const int at = place[j0 + e];
+      if (at < 0) continue;
+      if (narrow)
+        to16[static_cast<size_t>(at) * D] = static_cast<T>(o);
+      else
+        to32[static_cast<size_t>(at) * D] = o;
     }
   }
   __syncwarp();
@@ -972,8 +990,10 @@ __global__ void __launch_bounds__(Lay<KT, D>::THREADS, 1)
       dev::mbar_init(sy.empty(s), 1);
     }
     for (int t = 0; t < 2; ++t) {
-      dev::mbar_init(sy.sfull(t), 1);
-      dev::mbar_init(sy.sfree(t), 4);
+      for (int b = 0; b < 2; ++b) {
+        dev::mbar_init(sy.sfull(t, b), 1);
+        dev::mbar_init(sy.sfree(t, b), 4);
+      }
       dev::mbar_init(sy.pfull(t), 4);
       dev::mbar_init(sy.pdone(t), 1);
       dev::mbar_init(sy.qfull(t), 1);
@@ -1031,7 +1051,7 @@ __global__ void __launch_bounds__(Lay<KT, D>::THREADS, 1)
     uint8_t* prow = pbuf + (r >> 3) * 1024 + (r & 7) * 128;  // the key's row of P^T, swizzled by r & 7
     const float sl2 = a.scale_log2;
     bool ok = true;
-    int n = 0;  // chunks of this tile so far
+    int n = 0, n_s0 = 0, n_s1 = 0;  // chunks of this tile so far; per score buffer
     Cursor<L> k;
     k.i = k.it0 = k.ph = 0;
 #pragma unroll 1
@@ -1042,7 +1062,7 @@ __global__ void __launch_bounds__(Lay<KT, D>::THREADS, 1)
       const Piece& p = k.p;
       const int half = k.pair ? 64 * t : 0, rows = k.pair ? min(64, p.rows - half) : p.rows;
       const int words = rows > 32 ? 2 : 1, pp = k.i & 1, shift = p.L - p.n;
-      const uint32_t oc = x.tl + kColO + 128 * pp + 64 * t;
+      const uint32_t oc = x.tl + kColO + (k.pair ? 0 : 128 * pp) + 64 * t;
       const bool exists = r < rows && ((p.row0 + half + r) & ((1 << a.gl) - 1)) < a.G;  // row r (r < 64)
       bool seen = !exists, unset = true;  // row r has a reference; some row may have none
       float ref = 0.f;
@@ -1055,14 +1075,16 @@ __global__ void __launch_bounds__(Lay<KT, D>::THREADS, 1)
       for (int c = c_first; c < k.nc; c += step, ++n) {
         const int key0 = (p.c0 + c) * kKeys, jn = key0 + r - shift;  // node that key r is
         const bool masked = key0 + kKeys > shift;
-        if (ok) ok = wait_warp(sy.sfull(t), n & 1);
+        const int sb = k.pair ? c & 1 : 0;
+        if (ok) ok = wait_warp(sy.sfull(t, sb), (sb ? n_s1 : n_s0) & 1);
+        ++(sb ? n_s1 : n_s0);
         fence_after();
         float ks = sl2, vsc = 1.f;
         if constexpr (Q8) {
-          const float* sc = reinterpret_cast<const float*>(gb + L::SCALES + (((k.it0 >> 1) + c) & 7) * 1024);
+          const float* scales = reinterpret_cast<const float*>(gb + L::SCALES + (((k.it0 >> 1) + c) & 7) * 1024);
           if (key0 + r < p.L) {  // (stale past the end)
-            ks = sl2 * sc[r];
-            vsc = sc[128 + r];
+            ks = sl2 * scales[r];
+            vsc = scales[128 + r];
           }
         }
         uint2 vis = make_uint2(FULL, FULL);  // the rows that see the key
@@ -1071,13 +1093,14 @@ __global__ void __launch_bounds__(Lay<KT, D>::THREADS, 1)
           vis = visible<L>(a, gb, p, k.i, p.row0 + half, jn);
           __syncwarp();
         }
+        const uint32_t sc = x.tl + (sb ? kColS2 : kColS) + 64 * t;
         uint32_t pk[32];  // weights, 16-bit pairs of rows
         bool moved = unset;
         for (;;) {
           if (moved) {
-            if (ok && n > 0) ok = wait_warp(sy.pdone(t), (n - 1) & 1);  // P^T's buffer is free, O^T at rest
+            if (ok && n > 0) ok = wait_warp(sy.pdone(t), (n - 1) & 1);  // (P^T free, O^T at rest)
             fence_after();
-            const int what = settle<L>(x, ks, vis, words, oc, exists, seen, ref);
+            const int what = settle<L>(x, sc, ks, vis, words, oc, exists, seen, ref);
             unset = what & 2;
             if (what & 1) {
 #pragma unroll
@@ -1089,10 +1112,13 @@ __global__ void __launch_bounds__(Lay<KT, D>::THREADS, 1)
             }
           }
           float top = -INFINITY;
-          auto part = [&](auto q_c) {  // 16 rows
-            constexpr int Q = decltype(q_c)::value;
+          // 16 rows.  16-bit caches: exponents, their maximum, weights in one pass;
+          // 1-byte caches: the maximum first (l sums the weights before V's scale
+          // and the one rounding of their product).
+          auto part = [&](auto q_c, auto pass_c) {
+            constexpr int Q = decltype(q_c)::value, PASS = decltype(pass_c)::value;
             uint32_t u[16], v[16];
-            tmem_ld16x2(x.tl + kColS + 64 * t + 16 * Q, x.tl + kColR + 64 * t + 16 * Q, u, v);
+            tmem_ld16x2(sc + 16 * Q, x.tl + kColR + 64 * t + 16 * Q, u, v);
             float2 e[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -1108,40 +1134,47 @@ __global__ void __launch_bounds__(Lay<KT, D>::THREADS, 1)
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              top = max3(top, e[j].x, e[j].y);
-              pk[8 * Q + j] = dev::pack2<T>(dev::ex2(e[j].x), dev::ex2(e[j].y));
+              if constexpr (!Q8 || PASS == 0) top = max3(top, e[j].x, e[j].y);
+              if constexpr (!Q8) {
+                pk[8 * Q + j] = dev::pack2<T>(dev::ex2(e[j].x), dev::ex2(e[j].y));
+              } else if constexpr (PASS == 1) {
+                const float2 w = make_float2(dev::ex2(e[j].x), dev::ex2(e[j].y));
+                l[8 * Q + j] = make_float2(l[8 * Q + j].x + w.x, l[8 * Q + j].y + w.y);
+                // a weight of 0 must not meet a stale or NaN scale
+                pk[8 * Q + j] = masked ? dev::pack2<T>(w.x == 0.f ? 0.f : w.x * vsc, w.y == 0.f ? 0.f : w.y * vsc)
+                                       : dev::pack2<T>(w.x * vsc, w.y * vsc);
+              }
             }
           };
-          part(std::integral_constant<int, 0>{});
-          part(std::integral_constant<int, 1>{});
-          if (words == 2) {
-            part(std::integral_constant<int, 2>{});
-            part(std::integral_constant<int, 3>{});
+          auto parts = [&](auto pass_c) {
+            part(std::integral_constant<int, 0>{}, pass_c);
+            part(std::integral_constant<int, 1>{}, pass_c);
+            if (words == 2) {
+              part(std::integral_constant<int, 2>{}, pass_c);
+              part(std::integral_constant<int, 3>{}, pass_c);
+            }
+          };
+          if (!Q8 || !moved) parts(std::integral_constant<int, 0>{});
+          const bool again = !moved && bar_or(bar, 128, top > kMove);
+          if (again) {
+            moved = true;
+            continue;
           }
-          if (moved) break;
-          if (!bar_or(bar, 128, top > kMove)) break;
-          moved = true;
+          if constexpr (Q8) parts(std::integral_constant<int, 1>{});
+          break;
         }
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(sy.sfree(t));  // the scores are read
-        // l sums the rounded weights
+        if (lane == 0) mbar_arrive(sy.sfree(t, sb));  // the scores are read
+        if constexpr (!Q8) {  // l sums the rounded weights
 #pragma unroll
-        for (int j = 0; j < 16; ++j) l[j] = add2(l[j], dev::unpack2<T>(pk[j]));
-        if (words == 2) {
+          for (int j = 0; j < 16; ++j) add16x2<T>(l[j], pk[j]);
+          if (words == 2) {
 #pragma unroll
-          for (int j = 16; j < 32; ++j) l[j] = add2(l[j], dev::unpack2<T>(pk[j]));
-        }
-        if (ok && n > 0) ok = wait_warp(sy.pdone(t), (n - 1) & 1);  // P^T's buffer is free
-        if constexpr (Q8) {
-          // V's scale rides on the weight, rounded once more; a weight of 0 must
-          // not meet a stale or NaN scale
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float2 f = dev::unpack2<T>(pk[j]);
-            pk[j] = dev::pack2<T>(f.x == 0.f ? 0.f : f.x * vsc, f.y == 0.f ? 0.f : f.y * vsc);
+            for (int j = 16; j < 32; ++j) add16x2<T>(l[j], pk[j]);
           }
         }
+        if (ok && n > 0) ok = wait_warp(sy.pdone(t), (n - 1) & 1);  // P^T's buffer is free
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           *reinterpret_cast<uint4*>(prow + ((j ^ (r & 7)) << 4)) =
@@ -1196,7 +1229,7 @@ __global__ void __launch_bounds__(Lay<KT, D>::THREADS, 1)
         if (!k.pair && ok) ok = wait_warp(sy.pub(t ^ 1), k.i & 1);  // (after that tile's last product)
         named_bar(bar, 128);
         fence_after();
-        write_rows<T, L>(a, x, p, pubs, x.tl + kColO + 128 * pp + (k.pair ? 64 * t : 0), !k.pair, half, rows, exists);
+        write_rows<T, L>(a, x, p, pubs, x.tl + kColO + (k.pair ? 64 * t : 128 * pp), !k.pair, half, rows, exists);
       }
       if (ok) ok = wait_warp(sy.mfull(pp), (k.i >> 1) & 1);  // (every phase is seen in order)
       fence_before();
@@ -1344,7 +1377,7 @@ pa_status launch_t(const TreeLaunch& l, CUtensorMapDataType dt, cudaStream_t str
   a.scale_log2 = mag * 1.4426950408889634f > 1e-30f ? mag * 1.4426950408889634f : 1e-30f;
   a.negate = l.scale < 0.f ? 1u : 0u;
   a.out_f32 = l.out_dtype == PA_DTYPE_F32;
-  a.min_units = 2;
+  a.min_units = kItem + 2;
   const size_t rows = static_cast<size_t>(2) * a.n_cta * kRows;
   a.part_o = static_cast<float*>(l.workspace);
   a.part_m = a.part_o + rows * D;
@@ -1376,7 +1409,7 @@ pa_status launch_t(const TreeLaunch& l, CUtensorMapDataType dt, cudaStream_t str
     return fail(PA_ERR_CUDA, "pa_tree_attention: %s", cudaGetErrorString(setup[dev]));
   cudaError_t e = launch_dependent(tree_main<KT, T, D>, dim3(static_cast<unsigned>(a.n_cta)), dim3(L::THREADS),
                                    L::BYTES, stream, tmK, tmV, tmQ, a);
-  if (e == cudaSuccess && l.max_context_len > a.min_units * kKeys)
+  if (e == cudaSuccess && l.max_context_len > kKeys)
     e = launch_dependent(tree_merge<T, D>, dim3(static_cast<unsigned>(a.n_cta), kRows / kMergeRows),
                          dim3(32 * kMergeRows), 0, stream, a);
   if (e == cudaSuccess) e = cudaGetLastError();
