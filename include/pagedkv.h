@@ -571,7 +571,7 @@ size_t pa_tree_attention_workspace_size(int32_t num_q_heads, int32_t max_q_len, 
  *
  * Work: one persistent CTA per SM streams an equal share of the batch's
  * 128-key chunks (planned on the device from context_lens) and multiplies on
- * tcgen05 tensor cores, 128 or 256 (node, head) rows at a time; items that
+ * tcgen05 tensor cores, up to 128 (node, head) rows at a time; items that
  * span CTAs are merged by a second kernel.
  */
 pa_status pa_tree_attention(const void* q, int32_t q_dtype, const int32_t* q_start, int32_t num_tokens,

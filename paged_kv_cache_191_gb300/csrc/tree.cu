@@ -156,13 +156,13 @@ struct Lay {
   static constexpr bool Q8 = sizeof(KT) == 1;
   static constexpr int D = D_;
   static constexpr int SPANS = D / 64;               // 128-byte spans of a 16-bit row
+  // Q of a piece [span][rows][128 B]: 128 rows, or in either half of the place 64
   static constexpr int QTILE = kRows * D * 2;
-  static constexpr int QB = Q8 ? 1 : 2;              // pieces whose Q fits
   static constexpr int SLOT = kKeys * D * 2;         // one K or V chunk, 16-bit
   static constexpr int GRP = 1024 * SPANS;           // 8 keys of a slot: [span][8][128 B]
-  static constexpr int P0 = QB * QTILE;              // P^T [tile][128 keys][128 B]
+  static constexpr int P0 = QTILE;                   // P^T [tile][128 keys][128 B]
   static constexpr int RING = P0 + 2 * 16384;
-  static constexpr int NS = D == 64 ? 8 : 4;
+  static constexpr int NS = D == 64 ? 10 : Q8 ? 4 : 5;
   static constexpr int SCALES = RING + NS * SLOT;    // 1-byte codes: [8 chunks][K 128, V 128] float
   static constexpr int BAR = SCALES + (Q8 ? 8 * 1024 : 0);
   static constexpr int NBAR = 3 * NS + 28;
@@ -224,19 +224,19 @@ __device__ __forceinline__ bool bar_or(int id, int threads, bool x) {
 
 // Registers move from the single-thread roles (and the converters) to the
 // softmax warpgroups: 384 x 168 = 256 x 200 + 128 x 104, and with converters
-// 512 x 128 = 256 x 168 + 256 x 88.  Every warp calls its one.  (A spilled
+// 512 x 128 = 256 x 176 + 256 x 80.  Every warp calls its one.  (A spilled
 // register goes to L2 here: shared memory leaves the L1 no room.)
 template <bool Q8>
 __device__ __forceinline__ void fewer_registers() {
   if constexpr (Q8)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
   else
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
 }
 template <bool Q8>
 __device__ __forceinline__ void more_registers() {
   if constexpr (Q8)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
   else
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
 }
@@ -283,6 +283,14 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\t"
+      "mul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b));
   return d;
 }
 // l += a pair of 16-bit weights, without unpacking it.
@@ -469,7 +477,8 @@ __device__ __forceinline__ void produce(const TreeArgs& a, const CUtensorMap* tm
   constexpr int NS = L::NS, D = L::D;
   const int lane = static_cast<int>(threadIdx.x & 31);
   bool ok = true;
-  int it = 0, q_issued = 0;  // ring items, Qs of pieces, so far
+  int it = 0, q_issued = 0, q_free = 0;  // ring items, Qs of pieces, pieces done with theirs
+  bool before_pair = false;
   // Loads that wait behind a full ring take microseconds, so the block ids of
   // the next 32 blocks, and the next piece's first, are fetched well ahead.
   auto fetch = [&](const Piece& x, int j0) {  // lane's block id, blocks j0 .. j0 + 31 of the piece
@@ -482,21 +491,24 @@ __device__ __forceinline__ void produce(const TreeArgs& a, const CUtensorMap* tm
     }
     return v;
   };
-  // Q: boxes of br rows (whole nodes), a lane per (box, span)
-  auto load_q = [&](const Piece& x) {
-    const int qb = q_issued % L::QB;
-    if (ok && q_issued >= L::QB) ok = wait_warp(sy.qfree(qb), (q_issued / L::QB - 1) & 1);
+  // Q of piece i: boxes of br rows (whole nodes), a lane per (box, span).  Its
+  // place is free once `need` pieces have ended their last S^T.
+  auto load_q = [&](const Piece& x, int i, int need) {
+#pragma unroll 1
+    for (; q_free < need; ++q_free)
+      if (ok) ok = wait_warp(sy.qfree(q_free & 1), (q_free >> 1) & 1);
     if (!ok) return;
     ++q_issued;
+    const bool pair = x.rows > 64;
     const int br = max(32, 1 << a.gl);
     const int sp = lane % L::SPANS, y = lane / L::SPANS * br;
     const bool mine = y < x.rows;
     const uint32_t n = static_cast<uint32_t>(__popc(__ballot_sync(FULL, mine)));
-    if (lane == 0) dev::mbar_arrive_expect_tx(sy.qfull(qb), n * br * 128);
+    if (lane == 0) dev::mbar_arrive_expect_tx(sy.qfull(i & 1), n * br * 128);
     __syncwarp();
     if (mine)
-      dev::tma_load_3d(sy.base + qb * L::QTILE + sp * 16384 + y * 128, tmQ, sy.qfull(qb), sp * 64, x.g * a.G,
-                       x.qs + ((x.row0 + y) >> a.gl));
+      dev::tma_load_3d(sy.base + (pair ? sp * 16384 : (i & 1) * (L::QTILE / 2) + sp * 8192) + y * 128, tmQ,
+                       sy.qfull(i & 1), sp * 64, x.g * a.G, x.qs + ((x.row0 + y) >> a.gl));
     __syncwarp();
   };
   Piece p, pn;
@@ -510,7 +522,11 @@ __device__ __forceinline__ void produce(const TreeArgs& a, const CUtensorMap* tm
     p.c1 = uniform(p.c1);
     const int nblk = uniform((p.L + 15) / 16), ids_n = more_n ? fetch(pn, pn.c0 * kBlk) : 0;
     int ids = 0;
-    if (L::QB == 2) load_q(p);
+    // 64 rows in alternate halves; 128 rows, and what follows them, want the
+    // whole place, which frees late: the first chunk then goes ahead
+    const bool late = p.rows > 64 || before_pair;
+    before_pair = p.rows > 64;
+    if (!late) load_q(p, i - 1, i - 2);
 #pragma unroll 1
     for (int c = p.c0; c < p.c1; ++c) {
       const int k4 = (c - p.c0) & 3;
@@ -558,14 +574,13 @@ __device__ __forceinline__ void produce(const TreeArgs& a, const CUtensorMap* tm
         }
         __syncwarp();
       }
-      if (L::QB == 1 && c == p.c0) load_q(p);  // its buffer frees late: the first chunk goes ahead of it
+      if (late && c == p.c0) load_q(p, i - 1, i - 1);
     }
     p = pn;
     more = more_n && ok;
   }
   // no copy may still be landing when the CTA exits
-  for (int i = max(0, q_issued - L::QB); i < q_issued; ++i)
-    wait_thread(sy.qfull(i % L::QB), (i / L::QB) & 1);
+  for (int i = max(0, q_issued - 2); i < q_issued; ++i) wait_thread(sy.qfull(i & 1), (i >> 1) & 1);
   for (int i = max(0, it - NS); i < it; ++i) wait_thread(sy.full(i % NS), (i / NS) & 1);
   if (!ok && lane == 0) flag(PA_DEVERR_TIMEOUT);
   __syncwarp();
@@ -663,7 +678,7 @@ __device__ __forceinline__ void multiply(const TreeArgs& a, uint8_t* gb, Sync<L>
       }
     }
     if (s.live && ahead < 2) {
-      const int t = s.tile(), i = s.it0 + 2 * s.c, qb = s.i % L::QB;
+      const int t = s.tile(), i = s.it0 + 2 * s.c, qb = s.i & 1;
       // The buffer's last scores are read.  A first chunk also waits for the
       // piece before last to be over; a pair's second buffer may hold O^T of the
       // piece before.
@@ -672,17 +687,18 @@ __device__ __forceinline__ void multiply(const TreeArgs& a, uint8_t* gb, Sync<L>
       if (pieces_over < over && test(sy.ofree(pieces_over & 1), pieces_over >> 1)) ++pieces_over;
       if (pieces_over >= over && (t == 1 || n0 == 0 || test(sy.sfree(0, sb), n0 - 1)) &&
           ((t == 0 && !s.pair) || n1 == 0 || test(sy.sfree(1, sb), n1 - 1)) &&
-          (s.c > 0 || test(sy.qfull(qb), s.i / L::QB)) && landed(i)) {
+          (s.c > 0 || test(sy.qfull(qb), s.i >> 1)) && landed(i)) {
         fence_after();
         const uint32_t id = idesc<T>((s.p.rows + 15) & ~15, false) | (a.negate << 14);
         const uint64_t kd = sdesc(sy.base + L::RING + (i % NS) * L::SLOT, 16, L::GRP);
-        const uint64_t qd = sdesc(sy.base + qb * L::QTILE, 16, 1024);
+        const uint64_t qd = sdesc(sy.base + (s.pair ? 0 : qb * (L::QTILE / 2)), 16, 1024);
+        const uint32_t span = (s.pair ? 16384 : 8192) >> 4;
         const uint32_t sd = tmem + (sb ? kColS2 : kColS + 64 * t);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
             mma_ss(sd, kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
-                   qd + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4), id, kk > 0 ? 1u : 0u);
+                   qd + (kk >> 2) * span + (((kk & 3) * 32) >> 4), id, kk > 0 ? 1u : 0u);
           commit(sy.sfull(t, sb));
           if (s.pair) commit(sy.sfull(1, sb));
           commit(sy.empty(i % NS));
@@ -976,6 +992,7 @@ __global__ void __launch_bounds__(Lay<KT, D>::THREADS, 1)
   using L = Lay<KT, D>;
   constexpr bool Q8 = L::Q8;
   constexpr int NS = L::NS;
+  using W = std::conditional_t<Q8, __half, T>;  // of the weights before V's scale: at most 2^kMove
   extern __shared__ __align__(1024) uint8_t gb[];
   const Sync<L> sy{dev::smem_addr(gb)};
   if (sy.base & 1023u) {  // the swizzled tiles need it; a launch without static shared memory has it
@@ -1112,11 +1129,9 @@ __global__ void __launch_bounds__(Lay<KT, D>::THREADS, 1)
             }
           }
           float top = -INFINITY;
-          // 16 rows.  16-bit caches: exponents, their maximum, weights in one pass;
-          // 1-byte caches: the maximum first (l sums the weights before V's scale
-          // and the one rounding of their product).
-          auto part = [&](auto q_c, auto pass_c) {
-            constexpr int Q = decltype(q_c)::value, PASS = decltype(pass_c)::value;
+          // 16 rows: exponents, their maximum, weights
+          auto part = [&](auto q_c) {
+            constexpr int Q = decltype(q_c)::value;
             uint32_t u[16], v[16];
             tmem_ld16x2(sc + 16 * Q, x.tl + kColR + 64 * t + 16 * Q, u, v);
             float2 e[8];
@@ -1134,44 +1149,34 @@ __global__ void __launch_bounds__(Lay<KT, D>::THREADS, 1)
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              if constexpr (!Q8 || PASS == 0) top = max3(top, e[j].x, e[j].y);
-              if constexpr (!Q8) {
-                pk[8 * Q + j] = dev::pack2<T>(dev::ex2(e[j].x), dev::ex2(e[j].y));
-              } else if constexpr (PASS == 1) {
-                const float2 w = make_float2(dev::ex2(e[j].x), dev::ex2(e[j].y));
-                l[8 * Q + j] = make_float2(l[8 * Q + j].x + w.x, l[8 * Q + j].y + w.y);
-                // a weight of 0 must not meet a stale or NaN scale
-                pk[8 * Q + j] = masked ? dev::pack2<T>(w.x == 0.f ? 0.f : w.x * vsc, w.y == 0.f ? 0.f : w.y * vsc)
-                                       : dev::pack2<T>(w.x * vsc, w.y * vsc);
-              }
+              top = max3(top, e[j].x, e[j].y);
+              pk[8 * Q + j] = dev::pack2<W>(dev::ex2(e[j].x), dev::ex2(e[j].y));
             }
           };
-          auto parts = [&](auto pass_c) {
-            part(std::integral_constant<int, 0>{}, pass_c);
-            part(std::integral_constant<int, 1>{}, pass_c);
-            if (words == 2) {
-              part(std::integral_constant<int, 2>{}, pass_c);
-              part(std::integral_constant<int, 3>{}, pass_c);
-            }
-          };
-          if (!Q8 || !moved) parts(std::integral_constant<int, 0>{});
-          const bool again = !moved && bar_or(bar, 128, top > kMove);
-          if (again) {
-            moved = true;
-            continue;
+          part(std::integral_constant<int, 0>{});
+          part(std::integral_constant<int, 1>{});
+          if (words == 2) {
+            part(std::integral_constant<int, 2>{});
+            part(std::integral_constant<int, 3>{});
           }
-          if constexpr (Q8) parts(std::integral_constant<int, 1>{});
-          break;
+          if (moved || !bar_or(bar, 128, top > kMove)) break;
+          moved = true;
         }
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(sy.sfree(t, sb));  // the scores are read
-        if constexpr (!Q8) {  // l sums the rounded weights
 #pragma unroll
-          for (int j = 0; j < 16; ++j) add16x2<T>(l[j], pk[j]);
-          if (words == 2) {
+        for (int j = 0; j < 16; ++j) add16x2<W>(l[j], pk[j]);  // l sums the rounded weights
+        if (words == 2) {
 #pragma unroll
-            for (int j = 16; j < 32; ++j) add16x2<T>(l[j], pk[j]);
+          for (int j = 16; j < 32; ++j) add16x2<W>(l[j], pk[j]);
+        }
+        if constexpr (Q8) {  // times V's scale, which is the key's: rounded once more
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float2 w = dev::unpack2<W>(pk[j]), y = mul2(w, vsc);
+            // (a weight of 0 must not meet a stale or NaN scale)
+            pk[j] = masked ? dev::pack2<T>(w.x == 0.f ? 0.f : y.x, w.y == 0.f ? 0.f : y.y) : dev::pack2<T>(y.x, y.y);
           }
         }
         if (ok && n > 0) ok = wait_warp(sy.pdone(t), (n - 1) & 1);  // P^T's buffer is free
