@@ -22,7 +22,8 @@ COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE
           "--expt-relaxed-constexpr"]
 SOURCES = ["decode.cu", "decode_static.cu", "prefill.cu", "cache_ops.cu", "api.cpp", "allocator.cpp", "scheduler.cpp",
            "serve.cpp", "segments.cpp", "tree.cu", "tree_step.cu", "tree.cpp"]
-HEADERS = ["device_common.cuh", "tcgen05.cuh", "cache_rows.cuh", "pa_internal.h", "kv_map.h"]
+HEADERS = ["device_common.cuh", "tcgen05.cuh", "cache_rows.cuh", "tree_common.cuh", "tree_keys.cuh",
+           "tree_rows.cuh", "pa_internal.h", "kv_map.h"]
 
 
 def nvcc():

@@ -175,6 +175,8 @@ struct TreeLaunch {
   int32_t out_dtype;
   void* workspace;
   int32_t n_cta;  // persistent CTAs: one per SM
+  int64_t rows;   // query rows of one (sequence, kv head) at most, the group padded to a power of two
+  int32_t slot_rows;  // rows of a set of partial rows in the workspace
 };
 pa_status launch_tree(const TreeLaunch& a, void* stream);
 

@@ -31,11 +31,17 @@ pa_status check_tree(int32_t T, int32_t num_q_heads, int32_t max_q_len, const pa
   return PA_OK;
 }
 
-// Per CTA two sets of 128 partial rows (o, m, l) and 32 bytes on the item it
-// leaves unfinished.
-size_t tree_workspace(const pa_cache_desc* d) {
+// Query rows of one (sequence, kv head) at most, and the rows of a set of
+// partial rows: an item's, at most 256.
+int64_t tree_rows(int32_t num_q_heads, int32_t max_q_len, const pa_cache_desc* d) {
+  return static_cast<int64_t>(max_q_len) * node_rows(num_q_heads, d);
+}
+int32_t slot_rows(int64_t rows) { return rows <= 64 ? 64 : rows <= 128 ? 128 : 256; }
+// Per CTA two sets of partial rows (o, m, l) and 32 bytes on the item it leaves
+// unfinished.
+size_t tree_workspace(int64_t rows, const pa_cache_desc* d) {
   const size_t ctas = static_cast<size_t>(pa::sm_count());
-  return (ctas * (2 * 128 * (d->head_dim + 2) * sizeof(float) + 32) + 255) & ~static_cast<size_t>(255);
+  return (ctas * (2 * slot_rows(rows) * (d->head_dim + 2) * sizeof(float) + 32) + 255) & ~static_cast<size_t>(255);
 }
 
 }  // namespace
@@ -118,7 +124,7 @@ pa_status pa_rope_cache_write(const void* q, const void* k, const void* v, int32
 
 size_t pa_tree_attention_workspace_size(int32_t num_q_heads, int32_t max_q_len, const pa_cache_desc* desc) {
   if (check_tree(0, num_q_heads, max_q_len, desc) != PA_OK) return 0;
-  return tree_workspace(desc);
+  return tree_workspace(tree_rows(num_q_heads, max_q_len, desc), desc);
 }
 
 pa_status pa_tree_attention(const void* q, int32_t q_dtype, const int32_t* q_start, int32_t num_tokens,
@@ -152,12 +158,13 @@ pa_status pa_tree_attention(const void* q, int32_t q_dtype, const int32_t* q_sta
     return fail(PA_ERR_INVALID, "%s: misaligned pointer", fn);
   // units of work (128-key chunks of every item, and 3 for its start and end) are counted in 32 bits
   const int64_t G = node_rows(num_q_heads, desc), chunks = static_cast<int64_t>(max_context_len) / 128 + 4;
-  const int64_t items = static_cast<int64_t>(num_tokens) * G / 128 + B;
+  const int64_t items = static_cast<int64_t>(num_tokens) * G / 64 + B;
   if (items * desc->num_kv_heads > INT32_MAX / 2 / chunks)
     return fail(PA_ERR_UNSUPPORTED, "%s: more than 2^30 units of work", fn);
   if (static_cast<int64_t>(num_tokens) * num_q_heads > INT32_MAX)
     return fail(PA_ERR_UNSUPPORTED, "%s: too many query rows for one grid", fn);
-  const size_t need = tree_workspace(desc);
+  const int64_t rows = tree_rows(num_q_heads, max_q_len, desc);
+  const size_t need = tree_workspace(rows, desc);
   if (!workspace || !pa::aligned16(workspace) || workspace_bytes < need)
     return fail(PA_ERR_INVALID, "%s: workspace NULL, misaligned or %zu of %zu bytes", fn, workspace_bytes, need);
   pa::TreeLaunch a;
@@ -187,6 +194,8 @@ pa_status pa_tree_attention(const void* q, int32_t q_dtype, const int32_t* q_sta
   a.out_dtype = out_dtype;
   a.workspace = workspace;
   a.n_cta = pa::sm_count();
+  a.rows = rows;
+  a.slot_rows = slot_rows(rows);
   return pa::launch_tree(a, stream);
 }
 

@@ -1,0 +1,475 @@
+// The tree-attention kernel with a thread per row: items of up to 256 rows.
+//
+// S = Q K^T (M = 128 rows, N = the chunk's keys) and O += P V, P in tensor memory
+// in the place of the scores it came from.  Two tiles of 128 rows take turns,
+// one in its products while the other is in its softmax: an item of up to 128
+// rows gives each tile every other chunk (own accumulator, own references,
+// joined at the item's end), a larger one gives each tile half of its rows and
+// every chunk.  A thread holds its row's 128 scores in registers: its maximum,
+// reference and sum need no other lane, and O moves with the reference inside
+// the warp.
+#pragma once
+
+#include "tree_common.cuh"
+
+namespace pa {
+namespace {
+
+// tensor memory columns: scores [tile] x 128, O [tile] x 128
+constexpr uint32_t kRowS = 0, kRowO = 256;
+
+// A walk over the units of all pieces, in order: the chunks, or two (one per
+// tile) of each chunk.  Units alternate between the tiles.
+template <typename L>
+struct Units {
+  Cursor<L> k;
+  int j, tile;  // unit of the chunk
+  __device__ __forceinline__ void settle() {
+    k.live = uniform(k.live);
+    k.nc = uniform(k.nc);
+    k.p.rows = uniform(k.p.rows);
+    k.both = k.p.rows > L::HQ;
+  }
+  __device__ __forceinline__ void start(const Sync<L>& sy, const uint8_t* gb, bool& ok) {
+    k.start(sy, gb, ok);
+    j = tile = 0;
+    settle();
+  }
+  __device__ __forceinline__ bool ends_chunk() const { return !k.both || j == 1; }
+  __device__ __forceinline__ bool ends_piece() const { return ends_chunk() && k.c + 1 == k.nc; }
+  __device__ __forceinline__ void next(const Sync<L>& sy, const uint8_t* gb, bool& ok) {
+    tile ^= 1;
+    if (!ends_chunk()) {
+      j = 1;
+      return;
+    }
+    j = 0;
+    if (k.next(sy, gb, ok)) settle();
+  }
+};
+
+// The MMA warp: a unit's scores once K has landed and its tile's last product is
+// issued (products complete in order), O += P V once P is written and V has
+// landed.  The same arrangement as with a thread per key: one warp that waits on
+// all barriers in order, converged, on uniform values, one elected lane issuing.
+template <typename T, typename L>
+__device__ __forceinline__ void multiply_rows(const TreeArgs& a, uint8_t* gb, Sync<L> sy, uint32_t tmem) {
+  using namespace tcg;
+  constexpr int NS = L::NS, D = L::D;
+  volatile uint32_t* force = reinterpret_cast<volatile uint32_t*>(gb + L::MISC + 32);
+  bool ok = true;
+  Units<L> s, o;
+  s.start(sy, gb, ok);
+  o.start(sy, gb, ok);
+  int ahead = 0, spin = 0;     // units whose scores are issued and O not
+  int no0 = 0, no1 = 0;        // O issued per tile
+  int pieces_over = 0;         // pieces that both warpgroups are done with
+  uint64_t t0 = 0;
+  auto test = [&](uint32_t bar, int parity) { return uniform(dev::mbar_test(bar, parity & 1)) != 0; };
+  auto landed = [&](int i) { return test(sy.ready(i % NS), i / NS); };
+  const uint32_t id_s = idesc<T>(kKeys, false) | (a.negate << 13), id_o = idesc<T>(D, true);
+#pragma unroll 1
+  while (o.k.live) {
+    bool moved = false;
+    if (ahead > 0) {
+      const int t = o.tile, i = o.k.it0 + 2 * o.k.c + 1;
+      // a tile's first product of a piece overwrites the O of the piece before
+      if (o.k.c < 2 && pieces_over < o.k.i && test(sy.ofree(pieces_over & 1), pieces_over >> 1)) ++pieces_over;
+      if ((o.k.c >= 2 || pieces_over >= o.k.i) && test(sy.pfull(t), t ? no1 : no0) && landed(i)) {
+        fence_after();
+        const uint64_t vd = sdesc(sy.base + L::RING + (i % NS) * L::SLOT, D == 128 ? 1024 : 0, L::GRP);
+        const uint32_t od = tmem + kRowO + 128 * t, pd = tmem + kRowS + 128 * t;
+        const uint32_t forced = uniform(force[t]);
+        const uint32_t acc = o.k.c >= (o.k.both ? 1 : 2) || forced ? 1u : 0u;
+        const bool last = o.ends_chunk();
+        if (elect_one()) {
+          if (forced) force[t] = 0;
+#pragma unroll
+          for (int kk = 0; kk < kBlk; ++kk)
+            mma_ts(od, pd + 8 * kk, vd + ((kk * 2 * L::GRP) >> 4), id_o, kk > 0 ? 1u : acc);
+          commit(sy.pdone(t));
+          if (last) commit(sy.empty(i % NS));
+        }
+        __syncwarp();
+        ++(t ? no1 : no0);
+        --ahead;
+        o.next(sy, gb, ok);
+        moved = true;
+      }
+    }
+    if (s.k.live && ahead < 2) {
+      const int t = s.tile, i = s.k.it0 + 2 * s.k.c, qb = s.k.i & 1;
+      if ((s.k.c > 0 || s.j > 0 || test(sy.qfull(qb), s.k.i >> 1)) && (s.j > 0 || landed(i))) {
+        fence_after();
+        const uint64_t kd = sdesc(sy.base + L::RING + (i % NS) * L::SLOT, 16, L::GRP);
+        const uint64_t qd = sdesc(sy.base + (s.k.both ? t : qb) * L::QTILE, 16, 1024);
+        const uint32_t sd = tmem + kRowS + 128 * t;
+        const bool last = s.ends_chunk(), over = s.ends_piece();
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(sd, qd + (((kk >> 2) * (L::HQ * 128) + (kk & 3) * 32) >> 4),
+                   kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id_s, kk > 0 ? 1u : 0u);
+          commit(sy.sfull(t));
+          if (last) commit(sy.empty(i % NS));
+          if (over) commit(sy.qfree(qb));
+        }
+        __syncwarp();
+        ++ahead;
+        s.next(sy, gb, ok);
+        moved = true;
+      }
+    }
+    if (moved) {
+      spin = 0;
+    } else if ((++spin & 63) == 0) {
+      const uint64_t t1 = dev::global_timer_ns();
+      if (spin == 64) t0 = t1;
+      if (uniform(t1 - t0 > kLimit)) {
+        ok = false;
+        break;
+      }
+    }
+  }
+  ok = __all_sync(FULL, ok);
+  if (!ok && elect_one()) {
+    flag(PA_DEVERR_TIMEOUT);
+    commit(sy.mdone());  // products in flight complete before their tensor memory is released
+    wait_thread(sy.mdone(), 0);
+  }
+  __syncwarp();
+}
+
+// A thread's row of a piece.
+struct Row {
+  int t, w4, lane, r;  // tile, warp of the tile, lane, tensor memory lane
+  uint32_t s, o;       // tensor memory: its scores, its O
+  bool live, exists;   // the warp has a row; the thread has one
+  int node;            // of the sequence
+  const uint64_t* mask;  // its mask row
+  uint64_t m0, m1;     // the row's words 0 and 1
+};
+// Visibility of the 32 keys from node j0 on (the context's before 0, none from n on).
+__device__ __forceinline__ uint32_t sees(const TreeArgs& a, const Row& x, int j0, int n) {
+  if (j0 <= -32) return FULL;
+  if (j0 >= n) return 0u;
+  auto word = [&](int w) -> uint64_t { return w == 0 ? x.m0 : w == 1 ? x.m1 : w < a.words ? x.mask[w] : 0ull; };
+  if (j0 < 0) {
+    uint32_t m = static_cast<uint32_t>(x.m0 << -j0);
+    if (n - j0 < 32) m &= (1u << (n - j0)) - 1u;
+    return m | ((1u << -j0) - 1u);
+  }
+  const int w = j0 >> 6, sh = j0 & 63;
+  uint64_t m = word(w) >> sh;
+  if (sh > 32) m |= word(w + 1) << (64 - sh);
+  return static_cast<uint32_t>(m) & (n - j0 < 32 ? (1u << (n - j0)) - 1u : FULL);
+}
+
+// V rows that must not reach the product: past the context's end, or a node's
+// with an infinity or NaN.  Thread r checks key r (jn: its node).  Such a node is
+// added to O by hand, where its weight, in tensor memory, is not 0.
+template <typename T, typename L>
+__device__ __forceinline__ void guard_rows(const Row& x, uint8_t* gb, uint8_t* vslot, int parity, bool both, int jn,
+                                           int n, bool fresh) {
+  volatile uint32_t* force = reinterpret_cast<volatile uint32_t*>(gb + L::MISC + 32);
+  volatile uint32_t* bw =
+      reinterpret_cast<volatile uint32_t*>(gb + L::MISC + 64) + parity * 8 + (both ? 0 : 4 * x.t);
+  const bool scan = !both || x.t == 0;
+  const int bar = both ? 1 : 2 + x.t, bar_n = both ? 256 : 128;
+  uint8_t* vrow = vslot + (x.r >> 3) * L::GRP + (x.r & 7) * 128;
+  auto clear = [&]() {
+#pragma unroll 4
+    for (int ch = 0; ch < 8 * L::SPANS; ++ch)
+      *reinterpret_cast<uint4*>(vrow + (ch >> 3) * 1024 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+  };
+  if (scan) {
+    bool bad = false;
+    if (jn >= n) {
+      clear();
+    } else if (jn >= 0) {
+#pragma unroll 4
+      for (int ch = 0; ch < 8 * L::SPANS; ++ch) {
+        const uint4 v = *reinterpret_cast<const uint4*>(vrow + (ch >> 3) * 1024 + (ch & 7) * 16);
+        bad |= bad16<T>(v.x) | bad16<T>(v.y) | bad16<T>(v.z) | bad16<T>(v.w);
+      }
+    }
+    const uint32_t word = __ballot_sync(FULL, bad);
+    if (x.lane == 0) bw[x.w4] = word;
+    dev::fence_proxy_async_smem();
+  }
+  named_bar(bar, bar_n);
+  if (!(bw[0] | bw[1] | bw[2] | bw[3])) return;
+  const bool first = fresh;
+#pragma unroll 1
+  for (int key = 0; key < kKeys; ++key) {
+    if (!((bw[key >> 5] >> (key & 31)) & 1u)) continue;
+    uint32_t p;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(p)
+                 : "r"(x.s + (key >> 1))
+                 : "memory");
+    const float2 pp = dev::unpack2<T>(p);
+    const float w = key & 1 ? pp.y : pp.x;
+    const uint8_t* vk = vslot + (key >> 3) * L::GRP + (key & 7) * 128;
+#pragma unroll 1
+    for (int d = 0; d < L::D; d += 8) {
+      uint32_t u[8];
+      tmem_ld8(x.o + d, u);
+      const uint4 q = *reinterpret_cast<const uint4*>(vk + (d >> 6) * 1024 + ((((d & 63) >> 3) ^ (key & 7)) << 4));
+      const uint32_t v2[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float v = e & 1 ? dev::unpack2<T>(v2[e >> 1]).y : dev::unpack2<T>(v2[e >> 1]).x;
+        const float o0 = fresh ? 0.f : __uint_as_float(u[e]);
+        u[e] = __float_as_uint(w == 0.f ? o0 : o0 + w * v);
+      }
+      tmem_st8(x.o + d, u);
+    }
+    tcg::wait_st();
+    fresh = false;
+  }
+  if (first && x.r == 0) force[x.t] = 1;  // the product adds to O
+  named_bar(bar, bar_n);                  // every reader is done with the rows
+  if (scan && ((bw[x.w4] >> x.lane) & 1u)) clear();
+  dev::fence_proxy_async_smem();
+  named_bar(bar, bar_n);
+}
+
+// Dims [d0, d1) of the thread's row out: O of one tile, or of both, times their
+// weights.
+template <typename T, typename L>
+__device__ __forceinline__ void write_row(const TreeArgs& a, const Row& x, const Piece& p, int row, float w, float w_other,
+                                          uint32_t o_other, bool other, int d0, int d1) {
+  const bool direct = p.slot < 0, narrow = direct && !a.out_f32;
+  const int h = (p.row0 + row) & ((1 << a.gl) - 1);
+  const size_t at = direct ? static_cast<size_t>(p.qs + x.node) * a.Hq + p.g * a.G + h
+                           : static_cast<size_t>(p.slot) * a.slot_rows + row;
+  float* to32 = (direct ? static_cast<float*>(a.out) : a.part_o) + at * L::D;
+  T* to16 = static_cast<T*>(a.out) + at * L::D;
+#pragma unroll 1
+  for (int d = d0; d < d1; d += 8) {
+    uint32_t u[8], v[8];
+    tmem_ld8(x.o + d, u);
+    if (other) tmem_ld8(o_other + d, v);
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      f[e] = w == 0.f ? 0.f : __uint_as_float(u[e]) * w;
+      if (other && w_other != 0.f) f[e] = fmaf(__uint_as_float(v[e]), w_other, f[e]);
+    }
+    if (!x.exists) continue;
+    if (narrow) {
+      *reinterpret_cast<uint4*>(to16 + d) = make_uint4(dev::pack2<T>(f[0], f[1]), dev::pack2<T>(f[2], f[3]),
+                                                       dev::pack2<T>(f[4], f[5]), dev::pack2<T>(f[6], f[7]));
+    } else {
+      *reinterpret_cast<float4*>(to32 + d) = make_float4(f[0], f[1], f[2], f[3]);
+      *reinterpret_cast<float4*>(to32 + d + 4) = make_float4(f[4], f[5], f[6], f[7]);
+    }
+  }
+  __syncwarp();
+}
+
+template <typename KT, typename T, int D>
+__global__ void __launch_bounds__(Lay<KT, D, true>::THREADS, 1)
+    tree_rows(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+              const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ TreeArgs a) {
+  using namespace tcg;
+  using L = Lay<KT, D, true>;
+  constexpr bool Q8 = L::Q8;
+  constexpr int NS = L::NS;
+  extern __shared__ __align__(1024) uint8_t gb[];
+  const Sync<L> sy{dev::smem_addr(gb)};
+  if (sy.base & 1023u) {  // the swizzled tiles need it; a launch without static shared memory has it
+    if (threadIdx.x == 0) flag(PA_DEVERR_TIMEOUT);
+    return;
+  }
+  const int wid = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  const uint32_t tmem = setup<L>(gb, sy, wid, &tmK, &tmV, &tmQ);
+
+  if (wid == 0) {
+    fewer_registers<Q8>();
+    produce<KT, L>(a, &tmK, &tmV, &tmQ, gb, sy);
+  } else if (wid == 1) {
+    fewer_registers<Q8>();
+    multiply_rows<T, L>(a, gb, sy, static_cast<uint32_t>(uniform(static_cast<int>(tmem))));
+  } else if (wid == 2) {
+    fewer_registers<Q8>();
+  } else if (wid == 3) {
+    fewer_registers<Q8>();
+    plan<L>(a, gb, sy);
+  } else if (wid < 12) {
+    // ---- softmax warpgroups: thread r owns row r of its tile -----------------------------
+    more_registers<Q8>();
+    Row x;
+    x.t = (wid - 4) >> 2;
+    x.w4 = wid & 3;
+    x.lane = lane;
+    x.r = 32 * x.w4 + lane;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(32 * x.w4) << 16);
+    x.s = tl + kRowS + 128 * x.t;
+    x.o = tl + kRowO + 128 * x.t;
+    const int t = x.t, r = x.r;
+    float2* pubs = reinterpret_cast<float2*>(gb + L::PUB);
+    const float sl2 = a.scale_log2;
+    bool ok = true;
+    int n = 0;  // units of this tile so far
+    Cursor<L> k;
+    k.i = k.it0 = k.ph = 0;
+#pragma unroll 1
+    for (;; k.close()) {
+      k.open(sy, gb, ok);
+      ok = __all_sync(FULL, ok);
+      if (!__all_sync(FULL, k.live)) break;
+      const Piece& p = k.p;
+      const int row = (k.both ? 128 * t : 0) + r, pp = k.i & 1, shift = p.L - p.n;
+      x.live = row - lane < p.rows;
+      x.exists = row < p.rows && ((p.row0 + row) & ((1 << a.gl) - 1)) < a.G;
+      x.node = (p.row0 + row) >> a.gl;
+      x.mask = a.mask + static_cast<size_t>(p.qs + x.node) * a.words;
+      const bool tree = x.exists && p.c1 * kKeys > shift;  // (else every key of the piece is the context's)
+      x.m0 = tree ? x.mask[0] : 0ull;
+      x.m1 = tree && a.words > 1 ? x.mask[1] : 0ull;
+      float ref = 0.f, l = 0.f;
+      bool seen = false;  // the row has a reference
+      const int c_first = k.both ? 0 : (t ^ k.ph) & 1, step = k.both ? 1 : 2;
+      const bool any = c_first < k.nc;
+#pragma unroll 1
+      for (int c = c_first; c < k.nc; c += step, ++n) {
+        const int key0 = (p.c0 + c) * kKeys;
+        const bool masked = key0 + kKeys > shift;
+        if (ok) ok = wait_warp(sy.sfull(t), n & 1);  // (the tile's products before it have ended too)
+        fence_after();
+        if (x.live) {
+          float f[kKeys];
+          load_scores(x.s, f);
+          const float* ks = reinterpret_cast<const float*>(gb + L::SCALES + (((k.it0 >> 1) + c) & 7) * 1024);
+          if constexpr (Q8) {
+#pragma unroll
+            for (int j = 0; j < kKeys; j += 4) {
+              const float4 s4 = *reinterpret_cast<const float4*>(ks + j);
+              f[j] *= s4.x;
+              f[j + 1] *= s4.y;
+              f[j + 2] *= s4.z;
+              f[j + 3] *= s4.w;
+            }
+          }
+          if (masked) {  // whatever the key's score and scale are
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t m = x.exists ? sees(a, x, key0 + 32 * w - shift, p.n) : 0u;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) f[32 * w + j] = (m >> j) & 1u ? f[32 * w + j] : -INFINITY;
+            }
+          }
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int j = 0; j < kKeys; j += 8)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) m4[q] = max3(m4[q], f[j + q], f[j + 4 + q]);
+          const float top = max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * sl2;
+          const bool move = x.exists && (seen ? top > ref + kMove : top > -INFINITY);
+          if (__any_sync(FULL, move && seen)) {  // O and l follow the reference
+            const float alpha = move && seen ? dev::ex2(ref - top) : 1.f;
+            l *= alpha;
+#pragma unroll 1
+            for (int d = 0; d < D; d += 8) {
+              uint32_t u[8];
+              tmem_ld8(x.o + d, u);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
+              tmem_st8(x.o + d, u);
+            }
+          }
+          if (move) {
+            ref = top;
+            seen = true;
+          }
+          float2 ls = make_float2(0.f, 0.f), ls1 = ls;
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const int i = 32 * h + 2 * j;
+              const float2 e = fma2(make_float2(f[i], f[i + 1]), make_float2(sl2, sl2), make_float2(-ref, -ref));
+              float2 w = make_float2(dev::ex2(e.x), dev::ex2(e.y));
+              if constexpr (Q8) {
+                // the key's V scale rides on the weight; l sums the weights before it
+                ls = add2(ls, w);
+                const float2 vs = *reinterpret_cast<const float2*>(ks + 128 + i);
+                float2 y = make_float2(w.x * vs.x, w.y * vs.y);
+                if (masked) {  // (a weight of 0 must not meet a stale or NaN scale)
+                  y.x = w.x == 0.f ? 0.f : y.x;
+                  y.y = w.y == 0.f ? 0.f : y.y;
+                }
+                pk[j] = dev::pack2<T>(y.x, y.y);
+              } else {
+                pk[j] = dev::pack2<T>(w.x, w.y);
+                add16x2<T>(j & 1 ? ls1 : ls, pk[j]);  // l sums the rounded weights
+              }
+            }
+            tmem_st16(x.s + 16 * h, pk);
+          }
+          l += (ls.x + ls.y) + (ls1.x + ls1.y);
+          wait_st();
+        }
+        if (masked) {
+          const int vi = k.it0 + 2 * c + 1, vs = vi % NS;
+          if (ok) ok = __all_sync(FULL, wait_issued(sy.issued(), vi)) && wait_warp(sy.ready(vs), (vi / NS) & 1);
+          guard_rows<T, L>(x, gb, gb + L::RING + vs * L::SLOT, (p.c0 + c) & 1, k.both, key0 + r - shift, p.n,
+                           c == c_first);
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sy.pfull(t));
+      }
+      // ---- the piece's end --------------------------------------------------------------
+      if (p.last) dev::grid_launch_dependents();
+      if (ok && any) ok = wait_warp(sy.pdone(t), (n - 1) & 1);  // O final
+      fence_after();
+      // a row that saw only NaN scores has no reference and a sum of NaN
+      const float m = any && seen ? ref : l != l ? 0.f : -INFINITY;
+      float M = m, w = m == -INFINITY ? 0.f : 1.f, w_other = 0.f, sum = l;
+      if (!k.both) {
+        // both warpgroups are done with what the piece before published
+        if (ok && k.i >= 1) ok = wait_warp(sy.ofree(pp ^ 1), ((k.i - 1) >> 1) & 1);
+        pubs[128 * t + r] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sy.pub(t));
+        if (ok) ok = wait_warp(sy.pub(t ^ 1), k.i & 1);  // (after that tile's last product)
+        fence_after();
+        const float2 other = pubs[128 * (t ^ 1) + r];
+        M = fmaxf(m, other.x);
+        const float mz = M == -INFINITY ? 0.f : M;
+        w = dev::ex2(m - mz);
+        w_other = dev::ex2(other.x - mz);
+        sum = w * l + w_other * other.y;
+      } else {
+        __syncwarp();
+        if (ok && k.i >= 1) ok = wait_warp(sy.ofree(pp ^ 1), ((k.i - 1) >> 1) & 1);
+        if (lane == 0) mbar_arrive(sy.pub(t));
+        if (ok) ok = wait_warp(sy.pub(t ^ 1), k.i & 1);
+      }
+      if (x.live) {
+        const float inv = p.slot < 0 && M != -INFINITY ? 1.f / sum : 1.f;
+        if (p.slot >= 0 && x.exists && (k.both || t == 0)) {
+          a.part_m[p.slot * a.slot_rows + row] = M;
+          a.part_l[p.slot * a.slot_rows + row] = sum;
+        }
+        write_row<T, L>(a, x, p, row, w * inv, w_other * inv, tl + kRowO + 128 * (t ^ 1), !k.both,
+                        k.both ? 0 : (D / 2) * t, k.both ? D : (D / 2) * (t + 1));
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sy.ofree(pp));
+    }
+    if (!ok && lane == 0) flag(PA_DEVERR_TIMEOUT);
+  } else if (Q8) {
+    fewer_registers<Q8>();
+    convert<KT, T, L>(gb, sy);
+  }
+  teardown(wid, tmem);
+}
+
+}  // namespace
+}  // namespace pa
