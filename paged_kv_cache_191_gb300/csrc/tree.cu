@@ -206,7 +206,7 @@ pa_status launch_t(const TreeLaunch& l, CUtensorMapDataType dt, cudaStream_t str
   a.negate = l.scale < 0.f ? 1u : 0u;
   a.out_f32 = l.out_dtype == PA_DTYPE_F32;
   a.min_units = kItem + 2;
-  a.item_rows = ROWS ? 256 : 64;
+  a.item_rows = L::ITEM;
   a.slot_rows = l.slot_rows;
   const size_t rows = static_cast<size_t>(2) * a.n_cta * a.slot_rows;
   a.part_o = static_cast<float*>(l.workspace);

@@ -93,18 +93,24 @@ struct Lay {
   static constexpr bool Q8 = sizeof(KT) == 1, ROWS = ROWS_;
   static constexpr int D = D_;
   static constexpr int SPANS = D / 64;               // 128-byte spans of a 16-bit row
-  // Q of pieces, two places of HQ rows [span][HQ][128 B]: a piece of up to HQ
-  // rows takes one, in turns, a larger one both
+  // Q of pieces, places of HQ rows [span][HQ][128 B].  Two: a piece of up to HQ
+  // rows takes one, in turns, a larger one both.  1-byte caches have one.
   static constexpr int HQ = ROWS ? 128 : 64;
+  static constexpr int QP = Q8 ? 1 : 2;
+  static constexpr int ITEM = ROWS ? QP * HQ : HQ;   // rows of an item
   static constexpr int QTILE = HQ * D * 2;
   static constexpr int SLOT = kKeys * D * 2;         // one K or V chunk, 16-bit
   static constexpr int GRP = 1024 * SPANS;           // 8 keys of a slot: [span][8][128 B]
-  static constexpr int P0 = 2 * QTILE;               // P^T [tile][128 keys][128 B] (a thread per key)
+  static constexpr int P0 = QP * QTILE;              // P^T [tile][128 keys][128 B] (a thread per key)
   static constexpr int RING = P0 + (ROWS ? 0 : 2 * 16384);
   static constexpr int NS = D == 64 ? 10 : Q8 ? 4 : 5;
-  static constexpr int SCALES = RING + NS * SLOT;    // 1-byte codes: [8 chunks][K 128, V 128] float
+  // 1-byte caches: codes land in stages of their own, and are converted into the ring
+  static constexpr int NL = Q8 ? (ROWS ? 3 : 2) : NS;  // places that chunks land in
+  static constexpr int PRODUCERS = Q8 ? 2 : 1;
+  static constexpr int STAGE = RING + NS * SLOT;
+  static constexpr int SCALES = STAGE + (Q8 ? NL * kKeys * D : 0);  // [8 chunks][K 128, V 128] float
   static constexpr int BAR = SCALES + (Q8 ? 8 * 1024 : 0);
-  static constexpr int NBAR = 3 * NS + 23;
+  static constexpr int NBAR = 2 * NL + 2 * NS + 23;
   static constexpr int MISC = (BAR + NBAR * 8 + 15) & ~15;  // tensor memory, items issued, force; at 64: bad keys
   static constexpr int PIECE = MISC + 128;           // Piece [4]
   static constexpr int PUB = PIECE + 4 * 48;         // float2 [2 tiles][HQ]
@@ -130,9 +136,9 @@ __device__ __forceinline__ bool wait_thread(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
   return __all_sync(FULL, wait_thread(bar, parity));
 }
-// Wait until the producer has issued ring item i.  A slot's full barrier tells
-// one phase from the next by parity only; with the item issued, the slot's
-// phase before it is over.
+// Wait until ring item i is on its way into its slot (issued by the producer, or
+// begun by the converters).  A slot's barrier tells one phase from the next by
+// parity only; with the item under way, the slot's phase before it is over.
 __device__ __forceinline__ bool wait_issued(uint32_t count, int item) {
 #pragma unroll 1
   for (int i = 0; i < kTries; ++i) {
@@ -142,6 +148,9 @@ __device__ __forceinline__ bool wait_issued(uint32_t count, int item) {
     __nanosleep(200);
   }
   return false;
+}
+__device__ __forceinline__ void publish(uint32_t count, int items) {
+  asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(count), "r"(items) : "memory");
 }
 __device__ __forceinline__ void flag(uint32_t bits) { atomicOr(&g_tree_err, bits); }
 
@@ -203,7 +212,7 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
       : "memory");
 }
 #undef PA_R8
-#define PA_RW8(r, i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])
+#define PA_RW8(r, i) "+f"(r[i]), "+f"(r[i + 1]), "+f"(r[i + 2]), "+f"(r[i + 3]), "+f"(r[i + 4]), "+f"(r[i + 5]), "+f"(r[i + 6]), "+f"(r[i + 7])
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
@@ -217,20 +226,34 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// 128 columns under one wait.
-__device__ __forceinline__ void load_scores(uint32_t taddr, float (&f)[128]) {
-  uint32_t u[4][32];
+// 32 scores on their way; after arrived() (of every load before it) they are here.
+__device__ __forceinline__ void issue_scores(uint32_t taddr, float (&f)[32]) {
+  uint32_t u[32];
+  tcg::ld32(taddr, u);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) tcg::ld32(taddr + 32 * i, u[i]);
+  for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(u[j]);
+}
+__device__ __forceinline__ void pin(float* f) {  // no use of these registers moves above this
+#pragma unroll
+  for (int j = 0; j < 32; j += 8) asm volatile("" : PA_RW8(f, j));
+}
+__device__ __forceinline__ void arrived(float (&f)[32]) {
+  tcg::wait_ld();
+  pin(f);
+}
+__device__ __forceinline__ void store_scores(uint32_t taddr, const float (&f)[32]) {
+  uint32_t u[32];
+#pragma unroll
+  for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(f[j]);
+  tcg::st32(taddr, u);
+}
+// 128 of them under one wait.
+__device__ __forceinline__ void load_scores(uint32_t taddr, float (&f)[128]) {
+#pragma unroll
+  for (int i = 0; i < 128; i += 32) issue_scores(taddr + i, *reinterpret_cast<float(*)[32]>(f + i));
   tcg::wait_ld();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-#pragma unroll
-    for (int j = 0; j < 32; j += 8)  // no use of a register moves above the wait
-      asm volatile("" : PA_RW8(u[i], j));
-#pragma unroll
-    for (int j = 0; j < 32; ++j) f[32 * i + j] = __uint_as_float(u[i][j]);
-  }
+  for (int i = 0; i < 128; i += 32) pin(f + i);
 }
 #undef PA_RW8
 
@@ -257,12 +280,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
-__device__ __forceinline__ float2 mul2(float2 a, float b) {
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 d;
-  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\t"
+  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
       "mul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
       : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b));
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
 // l += a pair of 16-bit weights, without unpacking it.
@@ -315,11 +338,12 @@ template <typename L>
 struct Sync {
   uint32_t base;
   __device__ __forceinline__ uint32_t at(int i) const { return base + L::BAR + 8 * i; }
-  __device__ __forceinline__ uint32_t full(int s) const { return at(s); }                // slot s landed
-  __device__ __forceinline__ uint32_t conv(int s) const { return at(L::NS + s); }        // its codes converted
-  __device__ __forceinline__ uint32_t empty(int s) const { return at(2 * L::NS + s); }   // its last product ended
+  __device__ __forceinline__ uint32_t full(int s) const { return at(s); }                // landing place s: landed
+  __device__ __forceinline__ uint32_t taken(int s) const { return at(L::NL + s); }       // 1-byte caches: its codes are read
+  __device__ __forceinline__ uint32_t conv(int s) const { return at(2 * L::NL + s); }    // and converted into slot s
+  __device__ __forceinline__ uint32_t empty(int s) const { return at(2 * L::NL + L::NS + s); }  // its last product ended
   __device__ __forceinline__ uint32_t ready(int s) const { return L::Q8 ? conv(s) : full(s); }
-  __device__ __forceinline__ uint32_t ext(int i) const { return at(3 * L::NS + i); }
+  __device__ __forceinline__ uint32_t ext(int i) const { return at(2 * L::NL + 2 * L::NS + i); }
   __device__ __forceinline__ uint32_t sfull(int t) const { return ext(t); }         // scores of tile t
   __device__ __forceinline__ uint32_t sfree(int t) const { return ext(2 + t); }     // and read
   __device__ __forceinline__ uint32_t pfull(int t) const { return ext(4 + t); }     // weights of tile t written
@@ -441,12 +465,13 @@ __device__ __forceinline__ void plan(const TreeArgs& a, uint8_t* gb, Sync<L> sy)
   }
 }
 
-// The producer warp: each piece's Q rows, and its K and V chunks into the ring
-// (lane i < 8 issues block i).
+// The producer warps: each piece's Q rows, and its K and V chunks into the ring,
+// one box per block.  1-byte caches have two of them, with half of each chunk's
+// blocks (a single thread's issue rate would bound their 32 copies per chunk).
 template <typename KT, typename L>
 __device__ __forceinline__ void produce(const TreeArgs& a, const CUtensorMap* tmK, const CUtensorMap* tmV,
-                                     const CUtensorMap* tmQ, uint8_t* gb, Sync<L> sy) {
-  constexpr int NS = L::NS, D = L::D;
+                                     const CUtensorMap* tmQ, uint8_t* gb, Sync<L> sy, int part) {
+  constexpr int NL = L::NL, D = L::D, kPart = kBlk / L::PRODUCERS;
   const int lane = static_cast<int>(threadIdx.x & 31);
   bool ok = true;
   int it = 0, q_issued = 0, q_free = 0;  // ring items, Qs of pieces, pieces done with theirs
@@ -466,6 +491,7 @@ __device__ __forceinline__ void produce(const TreeArgs& a, const CUtensorMap* tm
   // Q of piece i: boxes of br rows (whole nodes), a lane per (box, span).  Its
   // place is free once `need` pieces have ended their last scores.
   auto load_q = [&](const Piece& x, int i, int need) {
+    if (part > 0) return;
 #pragma unroll 1
     for (; q_free < need; ++q_free)
       if (ok) ok = wait_warp(sy.qfree(q_free & 1), (q_free >> 1) & 1);
@@ -479,7 +505,7 @@ __device__ __forceinline__ void produce(const TreeArgs& a, const CUtensorMap* tm
     if (lane == 0) dev::mbar_arrive_expect_tx(sy.qfull(i & 1), n * br * 128);
     __syncwarp();
     if (mine)
-      dev::tma_load_3d(sy.base + (both ? y / L::HQ : i & 1) * L::QTILE + (sp * L::HQ + y % L::HQ) * 128, tmQ, sy.qfull(i & 1),
+      dev::tma_load_3d(sy.base + (both ? y / L::HQ : i % L::QP) * L::QTILE + (sp * L::HQ + y % L::HQ) * 128, tmQ, sy.qfull(i & 1),
                        sp * 64, x.g * a.G, x.qs + ((x.row0 + y) >> a.gl));
     __syncwarp();
   };
@@ -496,7 +522,7 @@ __device__ __forceinline__ void produce(const TreeArgs& a, const CUtensorMap* tm
     int ids = 0;
     // a piece in both places, and the one after it, wait for the piece before to
     // end: the first chunk then goes ahead
-    const bool late = p.rows > L::HQ || before_both;
+    const bool late = L::QP == 1 || p.rows > L::HQ || before_both;
     before_both = p.rows > L::HQ;
     if (!late) load_q(p, i - 1, i - 2);
 #pragma unroll 1
@@ -506,34 +532,35 @@ __device__ __forceinline__ void produce(const TreeArgs& a, const CUtensorMap* tm
         ids = ids_next;
         ids_next = c + 4 < p.c1 ? fetch(p, (c + 4) * kBlk) : ids_n;
       }
-      int blk[kBlk];  // the chunk's block ids
+      int blk[kPart];  // the chunk's block ids
 #pragma unroll
-      for (int k = 0; k < kBlk; ++k) blk[k] = __shfl_sync(FULL, ids, k4 * kBlk + k);
-      const int live = max(0, min(kBlk, nblk - c * kBlk));  // blocks of this chunk that exist
+      for (int k = 0; k < kPart; ++k) blk[k] = __shfl_sync(FULL, ids, k4 * kBlk + kPart * part + k);
+      const int live = max(0, min(kPart, nblk - c * kBlk - kPart * part));  // those that exist
 #pragma unroll 1
       for (int v = 0; v < 2; ++v) {
-        const int s = it % NS;
-        if (ok && it >= NS) ok = wait_warp(sy.empty(s), (it / NS - 1) & 1);
+        const int s = it % NL;
+        if (ok && it >= NL) ok = wait_warp(L::Q8 ? sy.taken(s) : sy.empty(s), (it / NL - 1) & 1);
         if (!ok) break;
         dev::fence_proxy_async_smem();  // the softmax's and converters' accesses precede the refill
-        const uint32_t dst = sy.base + L::RING + s * L::SLOT, bar = sy.full(s);
+        const uint32_t bar = sy.full(s);
+        const uint32_t dst = sy.base + (L::Q8 ? L::STAGE + s * (L::SLOT / 2) + part * kPart * 2048
+                                              : L::RING + s * L::SLOT + part * kPart * 32 * D);
         ++it;
         if (lane == 0) {
-          // codes land in the upper half of the slot; K's with both scale rows
-          const int bytes = L::Q8 ? 16 * D + (v ? 0 : 128) : 32 * D;
+          const int bytes = L::Q8 ? 16 * D + (v ? 0 : 128) : 32 * D;  // (K's codes come with both scale rows)
           dev::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(live * bytes));
-          asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(sy.issued()), "r"(it) : "memory");
+          if (!L::Q8 && part == 0) publish(sy.issued(), it);
         }
         __syncwarp();
         const CUtensorMap* m = v ? tmV : tmK;
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kBlk; ++k) {
+          for (int k = 0; k < kPart; ++k) {
             if (k >= live) break;
             if constexpr (L::Q8) {
-              dev::tma_load_3d(dst + L::SLOT / 2 + k * 2048, m, bar, 0, p.g * 16, blk[k]);
+              dev::tma_load_3d(dst + k * 2048, m, bar, 0, p.g * 16, blk[k]);
               if (v == 0) {
-                const uint32_t sc = sy.base + L::SCALES + (((it - 1) >> 1) & 7) * 1024 + k * 64;
+                const uint32_t sc = sy.base + L::SCALES + (((it - 1) >> 1) & 7) * 1024 + (part * kPart + k) * 64;
                 dev::bulk_load(sc, a.k_scale + static_cast<size_t>(blk[k]) * 16, 64, bar);
                 dev::bulk_load(sc + 512, a.v_scale + static_cast<size_t>(blk[k]) * 16, 64, bar);
               }
@@ -553,7 +580,7 @@ __device__ __forceinline__ void produce(const TreeArgs& a, const CUtensorMap* tm
   }
   // no copy may still be landing when the CTA exits
   for (int i = max(0, q_issued - 2); i < q_issued; ++i) wait_thread(sy.qfull(i & 1), (i >> 1) & 1);
-  for (int i = max(0, it - NS); i < it; ++i) wait_thread(sy.full(i % NS), (i / NS) & 1);
+  for (int i = max(0, it - NL); i < it; ++i) wait_thread(sy.full(i % NL), (i / NL) & 1);
   if (!ok && lane == 0) flag(PA_DEVERR_TIMEOUT);
   __syncwarp();
 }
@@ -589,11 +616,11 @@ struct Cursor {
   __device__ __forceinline__ int tile() const { return (ph + c) & 1; }
 };
 
-// The converter warpgroup (1-byte caches): codes of a landed slot -> 16-bit
-// values, in place, in the layout the MMAs read.
+// The converter warpgroup (1-byte caches): codes of a landed chunk -> 16-bit
+// values in its slot of the ring, in the layout the MMAs read.
 template <typename KT, typename T, typename L>
 __device__ __forceinline__ void convert(uint8_t* gb, Sync<L> sy) {
-  constexpr int NS = L::NS;
+  constexpr int NS = L::NS, NL = L::NL;
   const int lane = static_cast<int>(threadIdx.x & 31), i0 = static_cast<int>(threadIdx.x) - 384;
   bool ok = true;
   int it = 0;
@@ -603,16 +630,19 @@ __device__ __forceinline__ void convert(uint8_t* gb, Sync<L> sy) {
     const int n = 2 * (p.c1 - p.c0);
 #pragma unroll 1
     for (int k = 0; k < n; ++k, ++it) {
-      const int s = it % NS;
-      if (ok) ok = wait_warp(sy.full(s), (it / NS) & 1);
-      uint8_t* st = gb + L::RING + s * L::SLOT;
+      const int s = it % NL, to = it % NS;
+      if (ok) ok = wait_warp(sy.full(s), (it / NL) & 1);
+      const uint8_t* st = gb + L::STAGE + s * (L::SLOT / 2);
       uint4 w[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {  // 16 codes: chunk c16 of row `key`
         const int x = i0 + 128 * j, key = x >> 3, c16 = x & 7;
-        w[j] = *reinterpret_cast<const uint4*>(st + L::SLOT / 2 + key * 128 + ((c16 ^ (key & 7)) << 4));
+        w[j] = *reinterpret_cast<const uint4*>(st + key * 128 + ((c16 ^ (key & 7)) << 4));
       }
-      named_bar(4, 128);  // every code is in registers before the slot is rewritten
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sy.taken(s));
+      if (ok && it >= NS) ok = wait_warp(sy.empty(to), (it / NS - 1) & 1);
+      if (i0 == 0) publish(sy.issued(), it + 1);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int x = i0 + 128 * j, key = x >> 3, c16 = x & 7, cc = 2 * (c16 & 3);
@@ -621,13 +651,17 @@ __device__ __forceinline__ void convert(uint8_t* gb, Sync<L> sy) {
         dev::code8x4_to<KT, T>(w[j].y, f[2], f[3]);
         dev::code8x4_to<KT, T>(w[j].z, f[4], f[5]);
         dev::code8x4_to<KT, T>(w[j].w, f[6], f[7]);
-        uint8_t* row = st + (key >> 3) * L::GRP + (c16 >> 2) * 1024 + (key & 7) * 128;
-        *reinterpret_cast<uint4*>(row + ((cc ^ (key & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
-        *reinterpret_cast<uint4*>(row + (((cc + 1) ^ (key & 7)) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
+        uint8_t* row = gb + L::RING + to * L::SLOT + (key >> 3) * L::GRP + (c16 >> 2) * 1024 + (key & 7) * 128;
+        // (the two spans' threads store their halves in opposite order: no bank conflict)
+        const bool up = c16 & 4;
+        *reinterpret_cast<uint4*>(row + (((cc + up) ^ (key & 7)) << 4)) =
+            make_uint4(up ? f[4] : f[0], up ? f[5] : f[1], up ? f[6] : f[2], up ? f[7] : f[3]);
+        *reinterpret_cast<uint4*>(row + (((cc + !up) ^ (key & 7)) << 4)) =
+            make_uint4(up ? f[0] : f[4], up ? f[1] : f[5], up ? f[2] : f[6], up ? f[3] : f[7]);
       }
       dev::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(sy.conv(s));
+      if (lane == 0) mbar_arrive(sy.conv(to));
     }
   }
   if (!ok && lane == 0) flag(PA_DEVERR_TIMEOUT);
@@ -638,8 +672,11 @@ template <typename L>
 __device__ __forceinline__ uint32_t setup(uint8_t* gb, Sync<L> sy, int wid, const CUtensorMap* tmK,
                                           const CUtensorMap* tmV, const CUtensorMap* tmQ) {
   if (threadIdx.x == 0) {
+    for (int s = 0; s < L::NL; ++s) {
+      dev::mbar_init(sy.full(s), L::PRODUCERS);
+      dev::mbar_init(sy.taken(s), 4);
+    }
     for (int s = 0; s < L::NS; ++s) {
-      dev::mbar_init(sy.full(s), 1);
       dev::mbar_init(sy.conv(s), 4);
       dev::mbar_init(sy.empty(s), 1);
     }

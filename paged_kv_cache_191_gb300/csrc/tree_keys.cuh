@@ -77,7 +77,7 @@ __device__ __forceinline__ void multiply(const TreeArgs& a, uint8_t* gb, Sync<L>
         fence_after();
         const uint32_t id = idesc<T>((s.p.rows + 15) & ~15, false) | (a.negate << 14);
         const uint64_t kd = sdesc(sy.base + L::RING + (i % NS) * L::SLOT, 16, L::GRP);
-        const uint64_t qd = sdesc(sy.base + qb * L::QTILE, 16, 1024);
+        const uint64_t qd = sdesc(sy.base + s.i % L::QP * L::QTILE, 16, 1024);
         const uint32_t sd = tmem + kColS + 64 * t;
         if (elect_one()) {
 #pragma unroll
@@ -338,12 +338,13 @@ __global__ void __launch_bounds__(Lay<KT, D, false>::THREADS, 1)
 
   if (wid == 0) {
     fewer_registers<Q8>();
-    produce<KT, L>(a, &tmK, &tmV, &tmQ, gb, sy);
+    produce<KT, L>(a, &tmK, &tmV, &tmQ, gb, sy, 0);
   } else if (wid == 1) {
     fewer_registers<Q8>();
     multiply<T, L>(a, gb, sy, static_cast<uint32_t>(uniform(static_cast<int>(tmem))));
   } else if (wid == 2) {
     fewer_registers<Q8>();
+    if constexpr (L::PRODUCERS == 2) produce<KT, L>(a, &tmK, &tmV, &tmQ, gb, sy, 1);
   } else if (wid == 3) {
     fewer_registers<Q8>();
     plan<L>(a, gb, sy);
@@ -463,12 +464,12 @@ __global__ void __launch_bounds__(Lay<KT, D, false>::THREADS, 1)
 #pragma unroll
           for (int j = 16; j < 32; ++j) add16x2<W>(l[j], pk[j]);
         }
+        const bool finite = fabsf(vsc) < INFINITY;  // (else a weight of 0 must not meet it)
         if constexpr (Q8) {  // times V's scale, which is the key's: rounded once more
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            const float2 w = dev::unpack2<W>(pk[j]), y = mul2(w, vsc);
-            // (a weight of 0 must not meet a stale or NaN scale)
-            pk[j] = masked ? dev::pack2<T>(w.x == 0.f ? 0.f : y.x, w.y == 0.f ? 0.f : y.y) : dev::pack2<T>(y.x, y.y);
+            const float2 w = dev::unpack2<W>(pk[j]), y = mul2(w, make_float2(vsc, vsc));
+            pk[j] = finite ? dev::pack2<T>(y.x, y.y) : dev::pack2<T>(w.x == 0.f ? 0.f : y.x, w.y == 0.f ? 0.f : y.y);
           }
         }
         if (ok && n > 0) ok = wait_warp(sy.pdone(t), (n - 1) & 1);  // P^T's buffer is free

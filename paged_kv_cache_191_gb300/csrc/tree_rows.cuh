@@ -102,7 +102,7 @@ __device__ __forceinline__ void multiply_rows(const TreeArgs& a, uint8_t* gb, Sy
       if ((s.k.c > 0 || s.j > 0 || test(sy.qfull(qb), s.k.i >> 1)) && (s.j > 0 || landed(i))) {
         fence_after();
         const uint64_t kd = sdesc(sy.base + L::RING + (i % NS) * L::SLOT, 16, L::GRP);
-        const uint64_t qd = sdesc(sy.base + (s.k.both ? t : qb) * L::QTILE, 16, 1024);
+        const uint64_t qd = sdesc(sy.base + (s.k.both ? t : s.k.i % L::QP) * L::QTILE, 16, 1024);
         const uint32_t sd = tmem + kRowS + 128 * t;
         const bool last = s.ends_chunk(), over = s.ends_piece();
         if (elect_one()) {
@@ -288,12 +288,13 @@ __global__ void __launch_bounds__(Lay<KT, D, true>::THREADS, 1)
 
   if (wid == 0) {
     fewer_registers<Q8>();
-    produce<KT, L>(a, &tmK, &tmV, &tmQ, gb, sy);
+    produce<KT, L>(a, &tmK, &tmV, &tmQ, gb, sy, 0);
   } else if (wid == 1) {
     fewer_registers<Q8>();
     multiply_rows<T, L>(a, gb, sy, static_cast<uint32_t>(uniform(static_cast<int>(tmem))));
   } else if (wid == 2) {
     fewer_registers<Q8>();
+    if constexpr (L::PRODUCERS == 2) produce<KT, L>(a, &tmK, &tmV, &tmQ, gb, sy, 1);
   } else if (wid == 3) {
     fewer_registers<Q8>();
     plan<L>(a, gb, sy);
@@ -340,32 +341,50 @@ __global__ void __launch_bounds__(Lay<KT, D, true>::THREADS, 1)
         if (ok) ok = wait_warp(sy.sfull(t), n & 1);  // (the tile's products before it have ended too)
         fence_after();
         if (x.live) {
-          float f[kKeys];
-          load_scores(x.s, f);
+          // (1-byte caches: K's scales, one per column, go on the scores in tensor
+          // memory, so a thread never holds 128 scores next to its scales)
+          float f[Q8 ? 1 : kKeys];
           const float* ks = reinterpret_cast<const float*>(gb + L::SCALES + (((k.it0 >> 1) + c) & 7) * 1024);
-          if constexpr (Q8) {
-#pragma unroll
-            for (int j = 0; j < kKeys; j += 4) {
-              const float4 s4 = *reinterpret_cast<const float4*>(ks + j);
-              f[j] *= s4.x;
-              f[j + 1] *= s4.y;
-              f[j + 2] *= s4.z;
-              f[j + 3] *= s4.w;
-            }
-          }
-          if (masked) {  // whatever the key's score and scale are
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          // the scores of word w of the chunk: masked ones replaced, whatever they are; maximum
+          auto scan = [&](int w, float* g) {
+            if (masked) {
               const uint32_t m = x.exists ? sees(a, x, key0 + 32 * w - shift, p.n) : 0u;
 #pragma unroll
-              for (int j = 0; j < 32; ++j) f[32 * w + j] = (m >> j) & 1u ? f[32 * w + j] : -INFINITY;
+              for (int j = 0; j < 32; ++j) g[j] = (m >> j) & 1u ? g[j] : -INFINITY;
             }
+#pragma unroll
+            for (int j = 0; j < 32; j += 8)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) m4[q] = max3(m4[q], g[j + q], g[j + 4 + q]);
+          };
+          if constexpr (Q8) {
+            float g[2][32];
+            issue_scores(x.s, g[0]);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              float* b = g[w & 1];
+              arrived(g[w & 1]);
+              if (w < 3) issue_scores(x.s + 32 * (w + 1), g[(w + 1) & 1]);
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                const float4 s4 = *reinterpret_cast<const float4*>(ks + 32 * w + j);
+                const float2 a0 = mul2(make_float2(b[j], b[j + 1]), make_float2(s4.x, s4.y));
+                const float2 a1 = mul2(make_float2(b[j + 2], b[j + 3]), make_float2(s4.z, s4.w));
+                b[j] = a0.x;
+                b[j + 1] = a0.y;
+                b[j + 2] = a1.x;
+                b[j + 3] = a1.y;
+              }
+              scan(w, b);
+              store_scores(x.s + 32 * w, g[w & 1]);
+            }
+            wait_st();
+          } else {
+            load_scores(x.s, f);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) scan(w, f + 32 * w);
           }
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int j = 0; j < kKeys; j += 8)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) m4[q] = max3(m4[q], f[j + q], f[j + 4 + q]);
           const float top = max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * sl2;
           const bool move = x.exists && (seen ? top > ref + kMove : top > -INFINITY);
           if (__any_sync(FULL, move && seen)) {  // O and l follow the reference
@@ -384,31 +403,57 @@ __global__ void __launch_bounds__(Lay<KT, D, true>::THREADS, 1)
             ref = top;
             seen = true;
           }
+          // weights of word w: 16-bit pairs in the place of scores already read
           float2 ls = make_float2(0.f, 0.f), ls1 = ls;
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
+          auto weights = [&](int w, const float* g, auto hidden) {
             uint32_t pk[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int i = 32 * h + 2 * j;
-              const float2 e = fma2(make_float2(f[i], f[i + 1]), make_float2(sl2, sl2), make_float2(-ref, -ref));
-              float2 w = make_float2(dev::ex2(e.x), dev::ex2(e.y));
+            for (int j = 0; j < 16; j += 2) {
+              const float2 e0 = fma2(make_float2(g[2 * j], g[2 * j + 1]), make_float2(sl2, sl2), make_float2(-ref, -ref));
+              const float2 e1 = fma2(make_float2(g[2 * j + 2], g[2 * j + 3]), make_float2(sl2, sl2), make_float2(-ref, -ref));
+              float2 w0 = make_float2(dev::ex2(e0.x), dev::ex2(e0.y)), w1 = make_float2(dev::ex2(e1.x), dev::ex2(e1.y));
               if constexpr (Q8) {
                 // the key's V scale rides on the weight; l sums the weights before it
-                ls = add2(ls, w);
-                const float2 vs = *reinterpret_cast<const float2*>(ks + 128 + i);
-                float2 y = make_float2(w.x * vs.x, w.y * vs.y);
-                if (masked) {  // (a weight of 0 must not meet a stale or NaN scale)
-                  y.x = w.x == 0.f ? 0.f : y.x;
-                  y.y = w.y == 0.f ? 0.f : y.y;
+                ls = add2(ls, w0);
+                ls1 = add2(ls1, w1);
+                const float4 vs = *reinterpret_cast<const float4*>(ks + 128 + 32 * w + 2 * j);
+                const float2 y0 = mul2(w0, make_float2(vs.x, vs.y)), y1 = mul2(w1, make_float2(vs.z, vs.w));
+                if constexpr (!decltype(hidden)::value) {
+                  pk[j] = dev::pack2<T>(y0.x, y0.y);
+                  pk[j + 1] = dev::pack2<T>(y1.x, y1.y);
+                } else {  // a weight of 0 must not meet a stale or NaN scale
+                  pk[j] = dev::pack2<T>(w0.x == 0.f ? 0.f : y0.x, w0.y == 0.f ? 0.f : y0.y);
+                  pk[j + 1] = dev::pack2<T>(w1.x == 0.f ? 0.f : y1.x, w1.y == 0.f ? 0.f : y1.y);
                 }
-                pk[j] = dev::pack2<T>(y.x, y.y);
-              } else {
-                pk[j] = dev::pack2<T>(w.x, w.y);
-                add16x2<T>(j & 1 ? ls1 : ls, pk[j]);  // l sums the rounded weights
+              } else {  // l sums the rounded weights
+                pk[j] = dev::pack2<T>(w0.x, w0.y);
+                pk[j + 1] = dev::pack2<T>(w1.x, w1.y);
+                add16x2<T>(ls, pk[j]);
+                add16x2<T>(ls1, pk[j + 1]);
               }
             }
-            tmem_st16(x.s + 16 * h, pk);
+            tmem_st16(x.s + 16 * w, pk);
+          };
+          if (Q8 && masked) {
+#pragma unroll 1
+            for (int w = 0; w < 4; ++w) {
+              float g[32];
+              issue_scores(x.s + 32 * w, g);
+              arrived(g);
+              weights(w, g, std::true_type{});
+            }
+          } else if constexpr (Q8) {
+            float g[2][32];
+            issue_scores(x.s, g[0]);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              arrived(g[w & 1]);
+              if (w < 3) issue_scores(x.s + 32 * (w + 1), g[(w + 1) & 1]);
+              weights(w, g[w & 1], std::false_type{});
+            }
+          } else {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) weights(w, f + 32 * w, std::false_type{});
           }
           l += (ls.x + ls.y) + (ls1.x + ls1.y);
           wait_st();
