@@ -36,7 +36,7 @@ __device__ __forceinline__ void multiply(const TreeArgs& a, uint8_t* gb, Sync<L>
   int ns0 = 0, ns1 = 0, no0 = 0, no1 = 0;  // S^T and O^T issued per tile
   int pieces_over = 0;                     // pieces that both warpgroups are done with
   uint64_t t0 = 0;
-  auto test = [&](uint32_t bar, int parity) { return uniform(dev::mbar_test(bar, parity & 1)) != 0; };
+  auto test = [&](uint32_t bar, int parity) { return __all_sync(FULL, dev::mbar_test(bar, parity & 1)) != 0; };
   auto landed = [&](int i) { return test(sy.ready(i % NS), i / NS); };
 #pragma unroll 1
   while (o.live) {

@@ -65,7 +65,7 @@ __device__ __forceinline__ void multiply_rows(const TreeArgs& a, uint8_t* gb, Sy
   int no0 = 0, no1 = 0;        // O issued per tile
   int pieces_over = 0;         // pieces that both warpgroups are done with
   uint64_t t0 = 0;
-  auto test = [&](uint32_t bar, int parity) { return uniform(dev::mbar_test(bar, parity & 1)) != 0; };
+  auto test = [&](uint32_t bar, int parity) { return __all_sync(FULL, dev::mbar_test(bar, parity & 1)) != 0; };
   auto landed = [&](int i) { return test(sy.ready(i % NS), i / NS); };
   const uint32_t id_s = idesc<T>(kKeys, false) | (a.negate << 13), id_o = idesc<T>(D, true);
 #pragma unroll 1

@@ -8,6 +8,7 @@ streams only.  There is no fallback: if the library is missing, every call
 raises.
 """
 import ctypes as C
+import functools
 import os
 
 import torch
@@ -224,29 +225,46 @@ def cache_write(k, v, slot_mapping, k_cache, v_cache, k_scale=None, v_scale=None
                                 C.byref(desc), _stream(stream)), "pa_cache_write")
 
 
-def _same_device(*named):
-    """All the tensors (None allowed) are CUDA tensors of one device, whose
-    index is returned."""
+def _operands(names, *tensors, strided=0):
+    """The tensors (None allowed; `names` names them) are CUDA tensors of the
+    current device, and all but the first `strided` contiguous."""
     dev = None
-    for t, n in named:
+    for i, t in enumerate(tensors):
         if t is None:
             continue
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise ValueError(f"{n} must be a CUDA tensor")
-        d = t.get_device()
+            raise ValueError(f"{names.split()[i]} must be a CUDA tensor")
         if dev is None:
-            dev = d
-        elif d != dev:
-            raise ValueError(f"{n} is on another device")
-    if dev != torch.cuda.current_device():
-        raise ValueError("the tensors are not on the current device")
-    return dev
+            dev = torch.cuda.current_device()
+        if t.get_device() != dev:
+            raise ValueError(f"{names.split()[i]} is not on the current device")
+        if i >= strided and not t.is_contiguous():
+            raise ValueError(f"{names.split()[i]} must be contiguous")
 
 
-def _dense(*named):
-    for t, n in named:
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{n} must be contiguous")
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    # (the address torch.cuda.current_stream().cuda_stream holds, without building the object)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
+@functools.lru_cache(maxsize=64)
+def _desc_of(shape, dtype):
+    return cache_desc(torch.empty(shape, dtype=dtype, device="meta"))
+
+
+def _caches(k_cache, v_cache, k_scale, v_scale):
+    """The caches' descriptor (read only: it is shared between calls)."""
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache differ")
+    if k_scale is not None or v_scale is not None:
+        _scales(k_scale, v_scale, k_cache)
+    return _desc_of(k_cache.shape, k_cache.dtype)
 
 
 def _scales(k_scale, v_scale, k_cache):
@@ -305,16 +323,10 @@ def rope_cache_write(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cach
     inv_freq: float64 [rot_dim / 2] on the device, factor: rope_frequencies.
     q, k and v may be views of one packed projection (only their heads and
     dims have to be dense).  q_out may be q itself."""
-    _same_device((q, "q"), (k, "k"), (v, "v"), (positions, "positions"), (inv_freq, "inv_freq"),
-                 (slot_mapping, "slot_mapping"), (k_cache, "k_cache"), (v_cache, "v_cache"), (q_out, "q_out"),
-                 (k_scale, "k_scale"), (v_scale, "v_scale"))
-    _dense((positions, "positions"), (inv_freq, "inv_freq"), (slot_mapping, "slot_mapping"), (k_cache, "k_cache"),
-           (v_cache, "v_cache"), (k_scale, "k_scale"), (v_scale, "v_scale"))
-    desc = cache_desc(k_cache)
+    _operands("q k v q_out positions inv_freq slot_mapping k_cache v_cache k_scale v_scale", q, k, v, q_out, positions,
+              inv_freq, slot_mapping, k_cache, v_cache, k_scale, v_scale, strided=4)
+    desc = _caches(k_cache, v_cache, k_scale, v_scale)
     D = desc.head_dim
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
-        raise ValueError("k_cache and v_cache differ")
-    _scales(k_scale, v_scale, k_cache)
     ks, vs = _rows(k, "k", D), _rows(v, "v", D)
     T = k.shape[0]
     if k.shape != (T, desc.num_kv_heads, D) or v.shape != k.shape:
@@ -334,14 +346,14 @@ def rope_cache_write(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cach
         if q.shape[0] != T or q.shape[2] != D or q.dtype != k.dtype:
             raise ValueError("q must be [T, num_q_heads, head_dim] in k's dtype")
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=out_dtype or q.dtype, device=q.device)
+            q_out = q.new_empty((T, Hq, D), dtype=out_dtype)
         elif q_out.shape != q.shape or q_out.dtype not in (torch.float16, torch.bfloat16, torch.float32):
             raise ValueError("q_out must be [T, num_q_heads, head_dim] in f16 / bf16 / f32")
         os_, odt = _rows(q_out, "q_out", D), q_out.dtype
-    _check(lib().pa_rope_cache_write(_ptr(q), _ptr(k), _ptr(v), _TORCH_DT[k.dtype], qs, ks, vs, _ptr(positions),
-                                     _ptr(inv_freq), 2 * inv_freq.shape[0], 1 if interleaved else 0, float(factor),
-                                     _ptr(slot_mapping), T, Hq, _ptr(q_out), _TORCH_DT[odt], os_, _ptr(k_cache),
-                                     _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), C.byref(desc), _stream(stream)),
+    _check(lib().pa_rope_cache_write(_addr(q), _addr(k), _addr(v), _TORCH_DT[k.dtype], qs, ks, vs, _addr(positions),
+                                     _addr(inv_freq), 2 * inv_freq.shape[0], 1 if interleaved else 0, float(factor),
+                                     _addr(slot_mapping), T, Hq, _addr(q_out), _TORCH_DT[odt], os_, _addr(k_cache),
+                                     _addr(v_cache), _addr(k_scale), _addr(v_scale), C.byref(desc), _raw_stream(stream)),
            "pa_rope_cache_write")
     return q_out if q is not None else None
 
@@ -378,18 +390,11 @@ def tree_attention(q, q_start, tree_mask, k_cache, v_cache, block_tables, contex
     before the tree and the nodes whose bits its row of tree_mask (int64
     [T, words], ops.tree_mask) sets.  q: [T, Hq, D] packed; returns out
     [T, Hq, D] (q dtype, or out_dtype)."""
-    _same_device((q, "q"), (q_start, "q_start"), (tree_mask, "tree_mask"), (k_cache, "k_cache"),
-                 (v_cache, "v_cache"), (block_tables, "block_tables"), (context_lens, "context_lens"), (out, "out"),
-                 (workspace, "workspace"), (k_scale, "k_scale"), (v_scale, "v_scale"))
-    _dense((q, "q"), (q_start, "q_start"), (tree_mask, "tree_mask"), (k_cache, "k_cache"), (v_cache, "v_cache"),
-           (block_tables, "block_tables"), (context_lens, "context_lens"), (out, "out"), (workspace, "workspace"),
-           (k_scale, "k_scale"), (v_scale, "v_scale"))
-    desc = cache_desc(k_cache)
+    _operands("q q_start tree_mask k_cache v_cache block_tables context_lens out workspace k_scale v_scale", q, q_start,
+              tree_mask, k_cache, v_cache, block_tables, context_lens, out, workspace, k_scale, v_scale)
+    desc = _caches(k_cache, v_cache, k_scale, v_scale)
     T, Hq, D = q.shape
     B = context_lens.numel()
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
-        raise ValueError("k_cache and v_cache differ")
-    _scales(k_scale, v_scale, k_cache)
     if D != desc.head_dim:
         raise ValueError("q head_dim differs from the cache")
     if q_start.dtype != torch.int32 or q_start.numel() != B + 1:
@@ -401,18 +406,18 @@ def tree_attention(q, q_start, tree_mask, k_cache, v_cache, block_tables, contex
     if context_lens.dtype != torch.int32:
         raise ValueError("context_lens must be int32 [B]")
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=out_dtype or q.dtype, device=q.device)
+        out = q.new_empty((T, Hq, D), dtype=out_dtype)
     elif out.shape != (T, Hq, D):
         raise ValueError("out must be [T, Hq, D]")
     L = lib()
     if workspace is None:
         workspace = torch.empty(int(L.pa_tree_attention_workspace_size(Hq, int(max_q_len), C.byref(desc))),
                                 dtype=torch.uint8, device=q.device)
-    _check(L.pa_tree_attention(_ptr(q), _dtype(q, "q"), _ptr(q_start), T, int(max_q_len), _ptr(tree_mask),
-                               tree_mask.shape[1], _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-                               _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), int(max_context_len),
-                               B, Hq, float(scale), _ptr(out), _dtype(out, "out"), C.byref(desc), _ptr(workspace),
-                               workspace.numel() * workspace.element_size(), _stream(stream)), "pa_tree_attention")
+    _check(L.pa_tree_attention(_addr(q), _dtype(q, "q"), _addr(q_start), T, int(max_q_len), _addr(tree_mask),
+                               tree_mask.shape[1], _addr(k_cache), _addr(v_cache), _addr(k_scale), _addr(v_scale),
+                               _addr(block_tables), block_tables.shape[1], _addr(context_lens), int(max_context_len),
+                               B, Hq, float(scale), _addr(out), _dtype(out, "out"), C.byref(desc), _addr(workspace),
+                               workspace.numel() * workspace.element_size(), _raw_stream(stream)), "pa_tree_attention")
     return out
 
 
@@ -428,10 +433,7 @@ def tree_accept(draft_tokens, target_tokens, parents, q_start, max_path, stream=
     path_len int32 [B], next_token int64 [B]).  draft_tokens, target_tokens
     int64 [T]: the nodes' tokens and the model's pick after each; parents
     int32 [T]; q_start int32 [B + 1]."""
-    _same_device((draft_tokens, "draft_tokens"), (target_tokens, "target_tokens"), (parents, "parents"),
-                 (q_start, "q_start"))
-    _dense((draft_tokens, "draft_tokens"), (target_tokens, "target_tokens"), (parents, "parents"),
-           (q_start, "q_start"))
+    _operands("draft_tokens target_tokens parents q_start", draft_tokens, target_tokens, parents, q_start)
     T, B = draft_tokens.numel(), q_start.numel() - 1
     if draft_tokens.dtype != torch.int64 or target_tokens.dtype != torch.int64 or target_tokens.numel() != T:
         raise ValueError("draft_tokens and target_tokens must be int64 [T]")
@@ -439,12 +441,11 @@ def tree_accept(draft_tokens, target_tokens, parents, q_start, max_path, stream=
         raise ValueError("parents must be int32 [T]")
     if q_start.dtype != torch.int32 or B < 0:
         raise ValueError("q_start must be int32 [B + 1]")
-    dev = q_start.device
-    path = torch.empty((B, max_path), dtype=torch.int32, device=dev)
-    path_len = torch.empty((B,), dtype=torch.int32, device=dev)
-    token = torch.empty((B,), dtype=torch.int64, device=dev)
-    _check(lib().pa_tree_accept(_ptr(draft_tokens), _ptr(target_tokens), _ptr(parents), _ptr(q_start), T, B,
-                                int(max_path), _ptr(path), _ptr(path_len), _ptr(token), _stream(stream)),
+    path = q_start.new_empty((B, max_path))
+    path_len = q_start.new_empty((B,))
+    token = draft_tokens.new_empty((B,))
+    _check(lib().pa_tree_accept(_addr(draft_tokens), _addr(target_tokens), _addr(parents), _addr(q_start), T, B,
+                                int(max_path), _addr(path), _addr(path_len), _addr(token), _raw_stream(stream)),
            "pa_tree_accept")
     return path, path_len, token
 
@@ -454,17 +455,10 @@ def tree_commit(k_cache, v_cache, block_tables, context_lens, q_start, path, pat
     """Move the accepted nodes' cache rows together, in place: path element i
     of sequence b goes to the i-th position of its tree.  Returns the new
     context lengths (int32 [B])."""
-    _same_device((k_cache, "k_cache"), (v_cache, "v_cache"), (block_tables, "block_tables"),
-                 (context_lens, "context_lens"), (q_start, "q_start"), (path, "path"), (path_len, "path_len"),
-                 (k_scale, "k_scale"), (v_scale, "v_scale"), (new_lens, "new_lens"))
-    _dense((k_cache, "k_cache"), (v_cache, "v_cache"), (block_tables, "block_tables"),
-           (context_lens, "context_lens"), (q_start, "q_start"), (path, "path"), (path_len, "path_len"),
-           (k_scale, "k_scale"), (v_scale, "v_scale"), (new_lens, "new_lens"))
-    desc = cache_desc(k_cache)
+    _operands("k_cache v_cache block_tables context_lens q_start path path_len k_scale v_scale new_lens", k_cache,
+              v_cache, block_tables, context_lens, q_start, path, path_len, k_scale, v_scale, new_lens)
+    desc = _caches(k_cache, v_cache, k_scale, v_scale)
     B = context_lens.numel()
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
-        raise ValueError("k_cache and v_cache differ")
-    _scales(k_scale, v_scale, k_cache)
     if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or block_tables.shape[0] != B:
         raise ValueError("block_tables must be int32 [B, max_blocks]")
     if context_lens.dtype != torch.int32 or path_len.dtype != torch.int32 or path_len.numel() != B:
@@ -474,12 +468,12 @@ def tree_commit(k_cache, v_cache, block_tables, context_lens, q_start, path, pat
     if path.dtype != torch.int32 or path.dim() != 2 or path.shape[0] != B:
         raise ValueError("path must be int32 [B, max_path]")
     if new_lens is None:
-        new_lens = torch.empty((B,), dtype=torch.int32, device=context_lens.device)
+        new_lens = context_lens.new_empty((B,))
     elif new_lens.dtype != torch.int32 or new_lens.numel() != B:
         raise ValueError("new_lens must be int32 [B]")
-    _check(lib().pa_tree_commit(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_tables),
-                                block_tables.shape[1], _ptr(context_lens), _ptr(q_start), _ptr(path), path.shape[1],
-                                _ptr(path_len), B, _ptr(new_lens), C.byref(desc), _stream(stream)),
+    _check(lib().pa_tree_commit(_addr(k_cache), _addr(v_cache), _addr(k_scale), _addr(v_scale), _addr(block_tables),
+                                block_tables.shape[1], _addr(context_lens), _addr(q_start), _addr(path), path.shape[1],
+                                _addr(path_len), B, _addr(new_lens), C.byref(desc), _raw_stream(stream)),
            "pa_tree_commit")
     return new_lens
 
