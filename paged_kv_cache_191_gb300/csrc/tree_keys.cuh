@@ -326,7 +326,6 @@ __global__ void __launch_bounds__(Lay<KT, D, false>::THREADS, 1)
   using L = Lay<KT, D, false>;
   constexpr bool Q8 = L::Q8;
   constexpr int NS = L::NS;
-  using W = std::conditional_t<Q8, __half, T>;  // of the weights before V's scale: at most 2^kMove
   extern __shared__ __align__(1024) uint8_t gb[];
   const Sync<L> sy{dev::smem_addr(gb)};
   if (sy.base & 1023u) {  // the swizzled tiles need it; a launch without static shared memory has it
@@ -422,9 +421,11 @@ __global__ void __launch_bounds__(Lay<KT, D, false>::THREADS, 1)
             }
           }
           float top = -INFINITY;
-          // 16 rows: exponents, their maximum, weights
-          auto part = [&](auto q_c) {
-            constexpr int Q = decltype(q_c)::value;
+          // 16 rows.  16-bit caches: exponents, their maximum, weights in one pass.
+          // 1-byte caches: the maximum first, so that l can sum the weights as they
+          // are and only their product with V's scale, the key's, is rounded.
+          auto part = [&](auto q_c, auto pass_c) {
+            constexpr int Q = decltype(q_c)::value, PASS = decltype(pass_c)::value;
             uint32_t u[16], v[16];
             tmem_ld16x2(sc + 16 * Q, x.tl + kColR + 64 * t + 16 * Q, u, v);
             float2 e[8];
@@ -442,34 +443,43 @@ __global__ void __launch_bounds__(Lay<KT, D, false>::THREADS, 1)
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              top = max3(top, e[j].x, e[j].y);
-              pk[8 * Q + j] = dev::pack2<W>(dev::ex2(e[j].x), dev::ex2(e[j].y));
+              if constexpr (!Q8 || PASS == 0) top = max3(top, e[j].x, e[j].y);
+              if constexpr (!Q8) {
+                pk[8 * Q + j] = dev::pack2<T>(dev::ex2(e[j].x), dev::ex2(e[j].y));
+              } else if constexpr (PASS == 1) {
+                const float2 w = make_float2(dev::ex2(e[j].x), dev::ex2(e[j].y));
+                l[8 * Q + j] = add2(l[8 * Q + j], w);
+                const float2 y = mul2(w, make_float2(vsc, vsc));
+                // (a weight of 0 must not meet a NaN scale)
+                pk[8 * Q + j] = dev::pack2<T>(w.x == 0.f ? 0.f : y.x, w.y == 0.f ? 0.f : y.y);
+              }
             }
           };
-          part(std::integral_constant<int, 0>{});
-          part(std::integral_constant<int, 1>{});
-          if (words == 2) {
-            part(std::integral_constant<int, 2>{});
-            part(std::integral_constant<int, 3>{});
+          auto parts = [&](auto pass_c) {
+            part(std::integral_constant<int, 0>{}, pass_c);
+            part(std::integral_constant<int, 1>{}, pass_c);
+            if (words == 2) {
+              part(std::integral_constant<int, 2>{}, pass_c);
+              part(std::integral_constant<int, 3>{}, pass_c);
+            }
+          };
+          if (!Q8 || !moved) parts(std::integral_constant<int, 0>{});
+          if (!moved && bar_or(bar, 128, top > kMove)) {
+            moved = true;
+            continue;
           }
-          if (moved || !bar_or(bar, 128, top > kMove)) break;
-          moved = true;
+          if constexpr (Q8) parts(std::integral_constant<int, 1>{});
+          break;
         }
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(sy.sfree(t));  // the scores are read
+        if constexpr (!Q8) {  // l sums the rounded weights
 #pragma unroll
-        for (int j = 0; j < 16; ++j) add16x2<W>(l[j], pk[j]);  // l sums the rounded weights
-        if (words == 2) {
+          for (int j = 0; j < 16; ++j) add16x2<T>(l[j], pk[j]);
+          if (words == 2) {
 #pragma unroll
-          for (int j = 16; j < 32; ++j) add16x2<W>(l[j], pk[j]);
-        }
-        const bool finite = fabsf(vsc) < INFINITY;  // (else a weight of 0 must not meet it)
-        if constexpr (Q8) {  // times V's scale, which is the key's: rounded once more
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float2 w = dev::unpack2<W>(pk[j]), y = mul2(w, make_float2(vsc, vsc));
-            pk[j] = finite ? dev::pack2<T>(y.x, y.y) : dev::pack2<T>(w.x == 0.f ? 0.f : y.x, w.y == 0.f ? 0.f : y.y);
+            for (int j = 16; j < 32; ++j) add16x2<T>(l[j], pk[j]);
           }
         }
         if (ok && n > 0) ok = wait_warp(sy.pdone(t), (n - 1) & 1);  // P^T's buffer is free
