@@ -227,19 +227,22 @@ def cache_write(k, v, slot_mapping, k_cache, v_cache, k_scale=None, v_scale=None
 
 def _operands(names, *tensors, strided=0):
     """The tensors (None allowed; `names` names them) are CUDA tensors of the
-    current device, and all but the first `strided` contiguous."""
+    current device, whose index is returned, and all but the first `strided`
+    are contiguous."""
     dev = None
     for i, t in enumerate(tensors):
         if t is None:
             continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise ValueError(f"{names.split()[i]} must be a CUDA tensor")
-        if dev is None:
-            dev = torch.cuda.current_device()
-        if t.get_device() != dev:
-            raise ValueError(f"{names.split()[i]} is not on the current device")
+        at = t.get_device() if isinstance(t, torch.Tensor) else -1  # (-1 on the CPU)
+        if at != dev:
+            if at < 0:
+                raise ValueError(f"{names.split()[i]} must be a CUDA tensor")
+            if dev is not None or at != torch.cuda.current_device():
+                raise ValueError(f"{names.split()[i]} is not on the current device")
+            dev = at
         if i >= strided and not t.is_contiguous():
             raise ValueError(f"{names.split()[i]} must be contiguous")
+    return dev
 
 
 def _addr(t):
@@ -346,7 +349,7 @@ def rope_cache_write(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cach
         if q.shape[0] != T or q.shape[2] != D or q.dtype != k.dtype:
             raise ValueError("q must be [T, num_q_heads, head_dim] in k's dtype")
         if q_out is None:
-            q_out = q.new_empty((T, Hq, D), dtype=out_dtype)
+            q_out = torch.empty((T, Hq, D), dtype=out_dtype or q.dtype, device=q.device)
         elif q_out.shape != q.shape or q_out.dtype not in (torch.float16, torch.bfloat16, torch.float32):
             raise ValueError("q_out must be [T, num_q_heads, head_dim] in f16 / bf16 / f32")
         os_, odt = _rows(q_out, "q_out", D), q_out.dtype
@@ -383,6 +386,12 @@ def tree_attention_workspace_size(num_q_heads, max_q_len, k_cache):
     return int(lib().pa_tree_attention_workspace_size(num_q_heads, int(max_q_len), C.byref(cache_desc(k_cache))))
 
 
+@functools.lru_cache(maxsize=256)
+def _tree_workspace(dev, num_q_heads, max_q_len, shape, dtype):
+    """Bytes on the current device, `dev` (their number goes by its SMs)."""
+    return int(lib().pa_tree_attention_workspace_size(num_q_heads, max_q_len, C.byref(_desc_of(shape, dtype))))
+
+
 def tree_attention(q, q_start, tree_mask, k_cache, v_cache, block_tables, context_lens, max_context_len, max_q_len,
                    scale, out=None, out_dtype=None, workspace=None, stream=None, k_scale=None, v_scale=None):
     """Paged attention of drafted trees: the last q_start[b+1] - q_start[b]
@@ -390,8 +399,8 @@ def tree_attention(q, q_start, tree_mask, k_cache, v_cache, block_tables, contex
     before the tree and the nodes whose bits its row of tree_mask (int64
     [T, words], ops.tree_mask) sets.  q: [T, Hq, D] packed; returns out
     [T, Hq, D] (q dtype, or out_dtype)."""
-    _operands("q q_start tree_mask k_cache v_cache block_tables context_lens out workspace k_scale v_scale", q, q_start,
-              tree_mask, k_cache, v_cache, block_tables, context_lens, out, workspace, k_scale, v_scale)
+    dev = _operands("q q_start tree_mask k_cache v_cache block_tables context_lens out workspace k_scale v_scale", q, q_start,
+                    tree_mask, k_cache, v_cache, block_tables, context_lens, out, workspace, k_scale, v_scale)
     desc = _caches(k_cache, v_cache, k_scale, v_scale)
     T, Hq, D = q.shape
     B = context_lens.numel()
@@ -406,12 +415,12 @@ def tree_attention(q, q_start, tree_mask, k_cache, v_cache, block_tables, contex
     if context_lens.dtype != torch.int32:
         raise ValueError("context_lens must be int32 [B]")
     if out is None:
-        out = q.new_empty((T, Hq, D), dtype=out_dtype)
+        out = torch.empty((T, Hq, D), dtype=out_dtype or q.dtype, device=q.device)
     elif out.shape != (T, Hq, D):
         raise ValueError("out must be [T, Hq, D]")
     L = lib()
     if workspace is None:
-        workspace = torch.empty(int(L.pa_tree_attention_workspace_size(Hq, int(max_q_len), C.byref(desc))),
+        workspace = torch.empty(_tree_workspace(dev, Hq, int(max_q_len), k_cache.shape, k_cache.dtype),
                                 dtype=torch.uint8, device=q.device)
     _check(L.pa_tree_attention(_addr(q), _dtype(q, "q"), _addr(q_start), T, int(max_q_len), _addr(tree_mask),
                                tree_mask.shape[1], _addr(k_cache), _addr(v_cache), _addr(k_scale), _addr(v_scale),
@@ -441,9 +450,10 @@ def tree_accept(draft_tokens, target_tokens, parents, q_start, max_path, stream=
         raise ValueError("parents must be int32 [T]")
     if q_start.dtype != torch.int32 or B < 0:
         raise ValueError("q_start must be int32 [B + 1]")
-    path = q_start.new_empty((B, max_path))
-    path_len = q_start.new_empty((B,))
-    token = draft_tokens.new_empty((B,))
+    dev = q_start.device
+    path = torch.empty((B, max_path), dtype=torch.int32, device=dev)
+    path_len = torch.empty((B,), dtype=torch.int32, device=dev)
+    token = torch.empty((B,), dtype=torch.int64, device=dev)
     _check(lib().pa_tree_accept(_addr(draft_tokens), _addr(target_tokens), _addr(parents), _addr(q_start), T, B,
                                 int(max_path), _addr(path), _addr(path_len), _addr(token), _raw_stream(stream)),
            "pa_tree_accept")
@@ -468,7 +478,7 @@ def tree_commit(k_cache, v_cache, block_tables, context_lens, q_start, path, pat
     if path.dtype != torch.int32 or path.dim() != 2 or path.shape[0] != B:
         raise ValueError("path must be int32 [B, max_path]")
     if new_lens is None:
-        new_lens = context_lens.new_empty((B,))
+        new_lens = torch.empty((B,), dtype=torch.int32, device=context_lens.device)
     elif new_lens.dtype != torch.int32 or new_lens.numel() != B:
         raise ValueError("new_lens must be int32 [B]")
     _check(lib().pa_tree_commit(_addr(k_cache), _addr(v_cache), _addr(k_scale), _addr(v_scale), _addr(block_tables),
