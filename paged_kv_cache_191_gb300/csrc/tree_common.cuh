@@ -114,8 +114,9 @@ struct Lay {
   static constexpr int MISC = (BAR + NBAR * 8 + 15) & ~15;  // tensor memory, items issued, force; at 64: bad keys
   static constexpr int PIECE = MISC + 128;           // Piece [4]
   static constexpr int PUB = PIECE + 4 * 48;         // float2 [2 tiles][HQ]
-  static constexpr int MASK = PUB + 16 * HQ;         // uint64 [2 pieces][64 nodes] (a thread per key)
-  static constexpr int BYTES = MASK + (ROWS ? 0 : 1024);
+  static constexpr bool WORDS = !ROWS || Q8;         // the planner fetches mask words
+  static constexpr int MASK = PUB + 16 * HQ;         // uint64 [2 pieces][64 nodes]
+  static constexpr int BYTES = MASK + (WORDS ? 1024 : 0);
   static constexpr int THREADS = Q8 ? 512 : 384;
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
@@ -211,7 +212,34 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
       : "r"(taddr)
       : "memory");
 }
+// 16 rows (lanes 16 h .. of the warp's 32) of 128 columns: thread 4 a + b has
+// columns 8 i + 2 b and + 1 of row a in r[4 i], r[4 i + 1], of row a + 8 in the
+// next two.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : PA_R8(r, 0), PA_R8(r, 8), PA_R8(r, 16), PA_R8(r, 24), PA_R8(r, 32), PA_R8(r, 40), PA_R8(r, 48), PA_R8(r, 56)
+      : "r"(taddr)
+      : "memory");
+}
 #undef PA_R8
+#define PA_I8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
+// The same rows of 64 columns: thread 4 a + b gives column 4 i + b of rows a, a + 8
+// in r[2 i], r[2 i + 1].
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], {"
+      "%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      PA_I8(r, 0), PA_I8(r, 8), PA_I8(r, 16), PA_I8(r, 24)
+      : "memory");
+}
+#undef PA_I8
 #define PA_RW8(r, i) "+f"(r[i]), "+f"(r[i + 1]), "+f"(r[i + 2]), "+f"(r[i + 3]), "+f"(r[i + 4]), "+f"(r[i + 5]), "+f"(r[i + 6]), "+f"(r[i + 7])
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
@@ -226,34 +254,18 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// 32 scores on their way; after arrived() (of every load before it) they are here.
-__device__ __forceinline__ void issue_scores(uint32_t taddr, float (&f)[32]) {
-  uint32_t u[32];
-  tcg::ld32(taddr, u);
-#pragma unroll
-  for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(u[j]);
-}
-__device__ __forceinline__ void pin(float* f) {  // no use of these registers moves above this
-#pragma unroll
-  for (int j = 0; j < 32; j += 8) asm volatile("" : PA_RW8(f, j));
-}
-__device__ __forceinline__ void arrived(float (&f)[32]) {
-  tcg::wait_ld();
-  pin(f);
-}
-__device__ __forceinline__ void store_scores(uint32_t taddr, const float (&f)[32]) {
-  uint32_t u[32];
-#pragma unroll
-  for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(f[j]);
-  tcg::st32(taddr, u);
-}
-// 128 of them under one wait.
+// 128 columns under one wait.
 __device__ __forceinline__ void load_scores(uint32_t taddr, float (&f)[128]) {
 #pragma unroll
-  for (int i = 0; i < 128; i += 32) issue_scores(taddr + i, *reinterpret_cast<float(*)[32]>(f + i));
+  for (int i = 0; i < 128; i += 32) {
+    uint32_t u[32];
+    tcg::ld32(taddr + i, u);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) f[i + j] = __uint_as_float(u[j]);
+  }
   tcg::wait_ld();
 #pragma unroll
-  for (int i = 0; i < 128; i += 32) pin(f + i);
+  for (int j = 0; j < 128; j += 8) asm volatile("" : PA_RW8(f, j));  // no use of a register moves above the wait
 }
 #undef PA_RW8
 
@@ -452,7 +464,7 @@ __device__ __forceinline__ void plan(const TreeArgs& a, uint8_t* gb, Sync<L> sy)
     const int m = i - 2;
     if (m >= 0 && m < pieces) {
       const Piece& x = ring[m & 3];
-      if (!L::ROWS && x.n <= 64 && x.c1 * kKeys > x.L - x.n)
+      if (L::WORDS && x.n <= 64 && x.c1 * kKeys > x.L - x.n)
         for (int k = lane; k < x.n; k += 32) words[(m & 1) * 64 + k] = a.mask[static_cast<size_t>(x.qs + k) * a.words];
       __syncwarp();
       if (lane == 0) mbar_arrive(sy.mfull(m & 1));

@@ -235,6 +235,42 @@ __device__ __forceinline__ void guard_rows(const Row& x, uint8_t* gb, uint8_t* v
   named_bar(bar, bar_n);
 }
 
+// O of the warp's rows times alpha, a row per lane.
+template <typename L>
+__device__ __forceinline__ void rescale(const Row& x, float alpha) {
+#pragma unroll 1
+  for (int d = 0; d < L::D; d += 8) {
+    uint32_t u[8];
+    tmem_ld8(x.o + d, u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
+    tmem_st8(x.o + d, u);
+  }
+}
+// Two rows of a quad of lanes (1-byte caches: thread 4 a + b has columns 8 i + 2 b
+// and + 1 of rows a and a + 8, so that a key's scales are read once for many rows).
+struct Pair {
+  float ref0, ref1;   // references
+  float l0, l1;       // sums over the thread's columns
+  bool seen0, seen1;  // the row has a reference
+  bool has0, has1;    // the row exists
+};
+__device__ __forceinline__ float quad_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(FULL, v, 1));
+  return fmaxf(v, __shfl_xor_sync(FULL, v, 2));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+  v += __shfl_xor_sync(FULL, v, 1);
+  return v + __shfl_xor_sync(FULL, v, 2);
+}
+// Of four rows a quad (a, a + 8, a + 16, a + 24), the value of row `lane`.
+__device__ __forceinline__ float to_lane(int lane, float v0, float v1, float v2, float v3) {
+  const int from = 4 * (lane & 7);
+  const float a = __shfl_sync(FULL, v0, from), b = __shfl_sync(FULL, v1, from);
+  const float c = __shfl_sync(FULL, v2, from), d = __shfl_sync(FULL, v3, from);
+  return lane < 16 ? (lane < 8 ? a : b) : (lane < 24 ? c : d);
+}
+
 // Dims [d0, d1) of the thread's row out: O of one tile, or of both, times their
 // weights.
 template <typename T, typename L>
@@ -267,6 +303,110 @@ __device__ __forceinline__ void write_row(const TreeArgs& a, const Row& x, const
     }
   }
   __syncwarp();
+}
+
+// The weights of a chunk over a 1-byte cache: 16 rows at a time, as fragments.
+// K's scales go on the scores and V's, once l has summed the weights, on them;
+// only that product is rounded.
+template <typename T, typename L>
+__device__ __forceinline__ void soften(const TreeArgs& a, const Row& x, const uint8_t* gb, const Piece& p, int piece,
+                                       Pair& ra, Pair& rb, const uint8_t* scales, bool masked, int j0, int tile_row,
+                                       float sl2) {
+  const int b2 = 2 * (x.lane & 3);
+  const float2* ks = reinterpret_cast<const float2*>(scales + b2 * 4);
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    uint32_t u[64];
+    tmem_ld_frag(x.s + (static_cast<uint32_t>(16 * h) << 16), u);
+    float2 f[32];  // [i][row]
+#pragma unroll
+    for (int i = 0; i < 32; ++i) f[i] = mul2(make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])), ks[4 * (i >> 1)]);
+    // apply(y, w, m): bits 8 i and 8 i + 1 of m say whether row a + 8 y sees the
+    // thread's two columns of word w's group i
+    auto by_mask = [&](auto apply) {
+#pragma unroll 1
+      for (int y = 0; y < 2; ++y) {
+        const int r = tile_row + 32 * x.w4 + 16 * h + 8 * y + (x.lane >> 2);
+        const bool has = y ? ra.has1 : ra.has0;
+        Row z;
+        z.node = (p.row0 + r) >> a.gl;
+        z.mask = a.mask + static_cast<size_t>(p.qs + z.node) * a.words;
+        z.m0 = !has ? 0ull : p.n <= 64 ? reinterpret_cast<const uint64_t*>(gb + L::MASK)[(piece & 1) * 64 + z.node] : z.mask[0];
+        z.m1 = !has || p.n <= 64 ? 0ull : z.mask[1];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) apply(y, w, (has ? sees(a, z, j0 + 32 * w, p.n) : 0u) >> b2);
+      }
+    };
+    if (masked) {  // whatever the key's score is
+      by_mask([&](int y, int w, uint32_t m) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool s0 = (m >> (8 * i)) & 1u, s1 = (m >> (8 * i + 1)) & 1u;
+          float2 &g0 = f[2 * (4 * w + i)], &g1 = f[2 * (4 * w + i) + 1];
+          if (y == 0) g0 = make_float2(s0 ? g0.x : -INFINITY, s1 ? g0.y : -INFINITY);
+          if (y == 1) g1 = make_float2(s0 ? g1.x : -INFINITY, s1 ? g1.y : -INFINITY);
+        }
+      });
+    }
+    float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      t0 = max3(t0, f[i].x, f[i].y);
+      t1 = max3(t1, f[i + 1].x, f[i + 1].y);
+    }
+    t0 *= sl2;
+    t1 *= sl2;
+    // the rows' maxima are wanted only where a reference is missing or outgrown
+    if (__any_sync(FULL, (ra.has0 && (ra.seen0 ? t0 > ra.ref0 + kMove : t0 > -INFINITY)) ||
+                             (ra.has1 && (ra.seen1 ? t1 > ra.ref1 + kMove : t1 > -INFINITY)))) {
+      t0 = quad_max(t0);
+      t1 = quad_max(t1);
+      const bool move0 = ra.has0 && (ra.seen0 ? t0 > ra.ref0 + kMove : t0 > -INFINITY);
+      const bool move1 = ra.has1 && (ra.seen1 ? t1 > ra.ref1 + kMove : t1 > -INFINITY);
+      if (__any_sync(FULL, (move0 && ra.seen0) || (move1 && ra.seen1))) {  // O and l follow the reference
+        const float a0 = move0 && ra.seen0 ? dev::ex2(ra.ref0 - t0) : 1.f;
+        const float a1 = move1 && ra.seen1 ? dev::ex2(ra.ref1 - t1) : 1.f;
+        ra.l0 *= a0;
+        ra.l1 *= a1;
+        rescale<L>(x, h ? to_lane(x.lane, 1.f, 1.f, a0, a1) : to_lane(x.lane, a0, a1, 1.f, 1.f));
+      }
+      ra.ref0 = move0 ? t0 : ra.ref0;
+      ra.ref1 = move1 ? t1 : ra.ref1;
+      ra.seen0 |= move0;
+      ra.seen1 |= move1;
+    }
+    const float2 n0 = make_float2(-ra.ref0, -ra.ref0), n1 = make_float2(-ra.ref1, -ra.ref1);
+    float2 ls0 = make_float2(0.f, 0.f), ls1 = ls0;
+    uint32_t pk[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float2 e = fma2(f[i], make_float2(sl2, sl2), i & 1 ? n1 : n0);
+      const float2 w = make_float2(dev::ex2(e.x), dev::ex2(e.y));
+      if (i & 1)
+        ls1 = add2(ls1, w);
+      else
+        ls0 = add2(ls0, w);
+      const float2 y = mul2(w, ks[64 + 4 * (i >> 1)]);
+      pk[i] = dev::pack2<T>(y.x, y.y);
+    }
+    if (masked) {  // nor its V scale, which may be stale or NaN
+      by_mask([&](int y, int w, uint32_t m) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t keep = ((m >> (8 * i)) & 1u ? 0xFFFFu : 0u) | ((m >> (8 * i + 1)) & 1u ? 0xFFFF0000u : 0u);
+          if (y == 0) pk[2 * (4 * w + i)] &= keep;
+          if (y == 1) pk[2 * (4 * w + i) + 1] &= keep;
+        }
+      });
+    }
+    ra.l0 += ls0.x + ls0.y;
+    ra.l1 += ls1.x + ls1.y;
+    tmem_st_frag(x.s + (static_cast<uint32_t>(16 * h) << 16), pk);
+    const Pair other = rb;  // the other 16 rows' turn (and back)
+    rb = ra;
+    ra = other;
+  }
+  tcg::wait_st();
 }
 
 template <typename KT, typename T, int D>
@@ -327,11 +467,21 @@ __global__ void __launch_bounds__(Lay<KT, D, true>::THREADS, 1)
       x.exists = row < p.rows && ((p.row0 + row) & ((1 << a.gl) - 1)) < a.G;
       x.node = (p.row0 + row) >> a.gl;
       x.mask = a.mask + static_cast<size_t>(p.qs + x.node) * a.words;
-      const bool tree = x.exists && p.c1 * kKeys > shift;  // (else every key of the piece is the context's)
+      const bool tree = !Q8 && x.exists && p.c1 * kKeys > shift;  // (else every key of the piece is the context's)
       x.m0 = tree ? x.mask[0] : 0ull;
       x.m1 = tree && a.words > 1 ? x.mask[1] : 0ull;
       float ref = 0.f, l = 0.f;
       bool seen = false;  // the row has a reference
+      Pair ra, rb;        // 1-byte caches: of rows a, a + 8 of the warp and a + 16, a + 24
+      if constexpr (Q8) {
+        ra = Pair{0.f, 0.f, 0.f, 0.f, false, false, false, false};
+        rb = ra;
+        const unsigned has = __ballot_sync(FULL, x.exists);
+        ra.has0 = (has >> (lane >> 2)) & 1u;
+        ra.has1 = (has >> ((lane >> 2) + 8)) & 1u;
+        rb.has0 = (has >> ((lane >> 2) + 16)) & 1u;
+        rb.has1 = (has >> ((lane >> 2) + 24)) & 1u;
+      }
       const int c_first = k.both ? 0 : (t ^ k.ph) & 1, step = k.both ? 1 : 2;
       const bool any = c_first < k.nc;
 #pragma unroll 1
@@ -340,120 +490,52 @@ __global__ void __launch_bounds__(Lay<KT, D, true>::THREADS, 1)
         const bool masked = key0 + kKeys > shift;
         if (ok) ok = wait_warp(sy.sfull(t), n & 1);  // (the tile's products before it have ended too)
         fence_after();
-        if (x.live) {
-          // (1-byte caches: K's scales, one per column, go on the scores in tensor
-          // memory, so a thread never holds 128 scores next to its scales)
-          float f[Q8 ? 1 : kKeys];
-          const float* ks = reinterpret_cast<const float*>(gb + L::SCALES + (((k.it0 >> 1) + c) & 7) * 1024);
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          // the scores of word w of the chunk: masked ones replaced, whatever they are; maximum
-          auto scan = [&](int w, float* g) {
-            if (masked) {
-              const uint32_t m = x.exists ? sees(a, x, key0 + 32 * w - shift, p.n) : 0u;
-#pragma unroll
-              for (int j = 0; j < 32; ++j) g[j] = (m >> j) & 1u ? g[j] : -INFINITY;
-            }
-#pragma unroll
-            for (int j = 0; j < 32; j += 8)
-#pragma unroll
-              for (int q = 0; q < 4; ++q) m4[q] = max3(m4[q], g[j + q], g[j + 4 + q]);
-          };
-          if constexpr (Q8) {
-            float g[2][32];
-            issue_scores(x.s, g[0]);
+        if constexpr (Q8) {
+          if (masked && p.n <= 64 && ok) ok = wait_warp(sy.mfull(pp), (k.i >> 1) & 1);
+          if (x.live)
+            soften<T, L>(a, x, gb, p, k.i, ra, rb, gb + L::SCALES + (((k.it0 >> 1) + c) & 7) * 1024, masked, key0 - shift, row - x.r, sl2);
+        } else if (x.live) {
+          float f[kKeys];
+          load_scores(x.s, f);
+          if (masked) {  // whatever the key's score is
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              float* b = g[w & 1];
-              arrived(g[w & 1]);
-              if (w < 3) issue_scores(x.s + 32 * (w + 1), g[(w + 1) & 1]);
+              const uint32_t m = x.exists ? sees(a, x, key0 + 32 * w - shift, p.n) : 0u;
 #pragma unroll
-              for (int j = 0; j < 32; j += 4) {
-                const float4 s4 = *reinterpret_cast<const float4*>(ks + 32 * w + j);
-                const float2 a0 = mul2(make_float2(b[j], b[j + 1]), make_float2(s4.x, s4.y));
-                const float2 a1 = mul2(make_float2(b[j + 2], b[j + 3]), make_float2(s4.z, s4.w));
-                b[j] = a0.x;
-                b[j + 1] = a0.y;
-                b[j + 2] = a1.x;
-                b[j + 3] = a1.y;
-              }
-              scan(w, b);
-              store_scores(x.s + 32 * w, g[w & 1]);
+              for (int j = 0; j < 32; ++j) f[32 * w + j] = (m >> j) & 1u ? f[32 * w + j] : -INFINITY;
             }
-            wait_st();
-          } else {
-            load_scores(x.s, f);
-#pragma unroll
-            for (int w = 0; w < 4; ++w) scan(w, f + 32 * w);
           }
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int j = 0; j < kKeys; j += 8)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) m4[q] = max3(m4[q], f[j + q], f[j + 4 + q]);
           const float top = max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * sl2;
           const bool move = x.exists && (seen ? top > ref + kMove : top > -INFINITY);
           if (__any_sync(FULL, move && seen)) {  // O and l follow the reference
             const float alpha = move && seen ? dev::ex2(ref - top) : 1.f;
             l *= alpha;
-#pragma unroll 1
-            for (int d = 0; d < D; d += 8) {
-              uint32_t u[8];
-              tmem_ld8(x.o + d, u);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
-              tmem_st8(x.o + d, u);
-            }
+            rescale<L>(x, alpha);
           }
           if (move) {
             ref = top;
             seen = true;
           }
-          // weights of word w: 16-bit pairs in the place of scores already read
           float2 ls = make_float2(0.f, 0.f), ls1 = ls;
-          auto weights = [&](int w, const float* g, auto hidden) {
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
             uint32_t pk[16];
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
-              const float2 e0 = fma2(make_float2(g[2 * j], g[2 * j + 1]), make_float2(sl2, sl2), make_float2(-ref, -ref));
-              const float2 e1 = fma2(make_float2(g[2 * j + 2], g[2 * j + 3]), make_float2(sl2, sl2), make_float2(-ref, -ref));
-              float2 w0 = make_float2(dev::ex2(e0.x), dev::ex2(e0.y)), w1 = make_float2(dev::ex2(e1.x), dev::ex2(e1.y));
-              if constexpr (Q8) {
-                // the key's V scale rides on the weight; l sums the weights before it
-                ls = add2(ls, w0);
-                ls1 = add2(ls1, w1);
-                const float4 vs = *reinterpret_cast<const float4*>(ks + 128 + 32 * w + 2 * j);
-                const float2 y0 = mul2(w0, make_float2(vs.x, vs.y)), y1 = mul2(w1, make_float2(vs.z, vs.w));
-                if constexpr (!decltype(hidden)::value) {
-                  pk[j] = dev::pack2<T>(y0.x, y0.y);
-                  pk[j + 1] = dev::pack2<T>(y1.x, y1.y);
-                } else {  // a weight of 0 must not meet a stale or NaN scale
-                  pk[j] = dev::pack2<T>(w0.x == 0.f ? 0.f : y0.x, w0.y == 0.f ? 0.f : y0.y);
-                  pk[j + 1] = dev::pack2<T>(w1.x == 0.f ? 0.f : y1.x, w1.y == 0.f ? 0.f : y1.y);
-                }
-              } else {  // l sums the rounded weights
-                pk[j] = dev::pack2<T>(w0.x, w0.y);
-                pk[j + 1] = dev::pack2<T>(w1.x, w1.y);
-                add16x2<T>(ls, pk[j]);
-                add16x2<T>(ls1, pk[j + 1]);
-              }
+              const int i = 32 * h + 2 * j;
+              const float2 e0 = fma2(make_float2(f[i], f[i + 1]), make_float2(sl2, sl2), make_float2(-ref, -ref));
+              const float2 e1 = fma2(make_float2(f[i + 2], f[i + 3]), make_float2(sl2, sl2), make_float2(-ref, -ref));
+              pk[j] = dev::pack2<T>(dev::ex2(e0.x), dev::ex2(e0.y));
+              pk[j + 1] = dev::pack2<T>(dev::ex2(e1.x), dev::ex2(e1.y));
+              add16x2<T>(ls, pk[j]);  // l sums the rounded weights
+              add16x2<T>(ls1, pk[j + 1]);
             }
-            tmem_st16(x.s + 16 * w, pk);
-          };
-          if (Q8 && masked) {
-#pragma unroll 1
-            for (int w = 0; w < 4; ++w) {
-              float g[32];
-              issue_scores(x.s + 32 * w, g);
-              arrived(g);
-              weights(w, g, std::true_type{});
-            }
-          } else if constexpr (Q8) {
-            float g[2][32];
-            issue_scores(x.s, g[0]);
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              arrived(g[w & 1]);
-              if (w < 3) issue_scores(x.s + 32 * (w + 1), g[(w + 1) & 1]);
-              weights(w, g[w & 1], std::false_type{});
-            }
-          } else {
-#pragma unroll
-            for (int w = 0; w < 4; ++w) weights(w, f + 32 * w, std::false_type{});
+            tmem_st16(x.s + 16 * h, pk);
           }
           l += (ls.x + ls.y) + (ls1.x + ls1.y);
           wait_st();
@@ -472,6 +554,11 @@ __global__ void __launch_bounds__(Lay<KT, D, true>::THREADS, 1)
       if (p.last) dev::grid_launch_dependents();
       if (ok && any) ok = wait_warp(sy.pdone(t), (n - 1) & 1);  // O final
       fence_after();
+      if constexpr (Q8) {
+        l = to_lane(lane, quad_sum(ra.l0), quad_sum(ra.l1), quad_sum(rb.l0), quad_sum(rb.l1));
+        ref = to_lane(lane, ra.ref0, ra.ref1, rb.ref0, rb.ref1);
+        seen = to_lane(lane, ra.seen0, ra.seen1, rb.seen0, rb.seen1) != 0.f;
+      }
       // a row that saw only NaN scores has no reference and a sum of NaN
       const float m = any && seen ? ref : l != l ? 0.f : -INFINITY;
       float M = m, w = m == -INFINITY ? 0.f : 1.f, w_other = 0.f, sum = l;
@@ -504,6 +591,7 @@ __global__ void __launch_bounds__(Lay<KT, D, true>::THREADS, 1)
         write_row<T, L>(a, x, p, row, w * inv, w_other * inv, tl + kRowO + 128 * (t ^ 1), !k.both,
                         k.both ? 0 : (D / 2) * t, k.both ? D : (D / 2) * (t + 1));
       }
+      if (Q8 && ok) ok = wait_warp(sy.mfull(pp), (k.i >> 1) & 1);  // (every phase is seen in order)
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(sy.ofree(pp));
