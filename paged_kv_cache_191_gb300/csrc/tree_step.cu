@@ -170,14 +170,18 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write(const RopeArgs a) {
   const int upr = a.D >> 4, nq = a.Hq * upr, nk = a.Hkv * upr;
   const int64_t slot = a.slots[t];
   const int64_t pos = a.positions[t];
-  if (threadIdx.x < (a.rot >> 1)) cs[threadIdx.x] = rotation(pos, a.inv_freq[threadIdx.x], a.factor);
+  const double freq = threadIdx.x < (a.rot >> 1) ? a.inv_freq[threadIdx.x] : 0.;
+  auto angles = [&]() {
+    if (threadIdx.x < (a.rot >> 1)) cs[threadIdx.x] = rotation(pos, freq, a.factor);
+    __syncthreads();
+  };
   const bool keep = slot >= 0 && slot < static_cast<int64_t>(a.num_blocks) * PA_BLOCK_SIZE;
   if (blockIdx.y == 0 && threadIdx.x == 0 && slot >= static_cast<int64_t>(a.num_blocks) * PA_BLOCK_SIZE)
     atomicOr(&g_step_err, PA_DEVERR_SLOT_RANGE);
   const int64_t blk = keep ? slot / PA_BLOCK_SIZE : 0, off = keep ? slot % PA_BLOCK_SIZE : 0;
   if constexpr (Q8) {
     if (blockIdx.y == 0) {
-      __syncthreads();
+      angles();
       if (!keep) return;
 #pragma unroll 1
       for (int which = 0; which < 2; ++which) {
@@ -220,7 +224,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write(const RopeArgs a) {
       return;
     }
   }
-  // every unit's loads are in flight before the angles are waited for
+  // Every unit's loads are in flight before the angles are formed, and before
+  // the slot is known (rows without one are read too, and dropped).
   constexpr int NV = IN == PA_DTYPE_F32 ? 2 : 1;  // 16-byte vectors per 8 values
   const int first = (static_cast<int>(blockIdx.y) - (Q8 ? 1 : 0)) * (U * kRopeThreads) + static_cast<int>(threadIdx.x);
   const int total = nq + (Q8 ? 0 : 2 * nk);
@@ -228,7 +233,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write(const RopeArgs a) {
 #pragma unroll
   for (int w = 0; w < U; ++w) {
     const int i = first + w * kRopeThreads;
-    if (i >= total || (i >= nq && !keep)) continue;
+    if (i >= total) continue;
     const int kind = i < nq ? 0 : i < nq + nk ? 1 : 2;  // q, k, v
     const int j = i - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk), h = j / upr;
     int d0, d1;
@@ -242,7 +247,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write(const RopeArgs a) {
       raw[w][1][x] = reinterpret_cast<const uint4*>(src + (row + d1) * (2 * NV))[x];
     }
   }
-  __syncthreads();
+  angles();
 #pragma unroll
   for (int w = 0; w < U; ++w) {
     const int i = first + w * kRopeThreads;
