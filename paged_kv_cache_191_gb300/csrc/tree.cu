@@ -10,54 +10,52 @@
 //
 // Rows and work.  The query rows of one (sequence, kv head) are the pairs
 // (node, head of the group), the group padded to a power of two; they all read
-// the same K/V, so an item is up to 128 of them, and streams the context in
-// chunks of 128 keys (8 blocks).  One unit of work is one chunk of one item (an item's start
-// and end count as kItem more); the
-// launch has one persistent CTA per SM, and CTA k takes units [k u, (k + 1) u)
-// of the batch in order, u = ceil(units / CTAs): every CTA streams the same
-// number of chunks whatever the lengths.  The lengths stay on the device: each
-// CTA counts the units itself from context_lens and q_start.  An item that
-// spans CTAs leaves partial rows (o, m, l), at most two sets per CTA, merged by
-// tree_merge with log-sum-exp weights.
+// the same K/V, so an item is up to 64, 128 or 256 of them (Lay::ITEM), and
+// streams the context in chunks of 128 keys (8 blocks).  One unit of work is one
+// chunk of one item (an item's start and end count as kItem more); the launch
+// has one persistent CTA per SM, and CTA k takes units [k u, (k + 1) u) of the
+// batch in order, u = ceil(units / CTAs): every CTA streams the same number of
+// chunks whatever the lengths.  The lengths stay on the device: each CTA counts
+// the units itself from context_lens and q_start.  An item that spans CTAs
+// leaves partial rows (o, m, l), at most two sets per CTA, merged by tree_merge
+// with log-sum-exp weights.
 //
-// The products are transposed: S^T = K Q^T (M = the chunk's 128 keys, N = rows)
-// and O^T += V^T P^T (M = dims, N = rows), so the tensor cores and the
-// exponentials do work in proportion to the rows, 16 at a time, and a whole
-// warpgroup is busy however few they are.  Thread r of a warpgroup owns key r
-// of the chunk: a key's scales are its own registers, P^T leaves through shared
-// memory (one 128-byte row per key), and an output column needs no exchange
-// between lanes.  Inside a CTA:
+// Inside a CTA (tree_common.cuh):
 //   warp 0       producer: Q rows and the K and V chunks into a ring of slots
-//                by TMA (128-byte swizzle, one box per block);
-//   warp 1       issues the MMAs from one thread, S^T ahead of O^T;
+//                by TMA (128-byte swizzle, one box per block); with 1-byte
+//                caches warp 2 issues half of each chunk's boxes;
+//   warp 1       issues the MMAs from one thread;
 //   warp 3       planner: the CTA's pieces of items, published a few ahead, and
 //                their mask words;
-//   warps 4-7,   two softmax warpgroups.  Up to 64 rows: they take alternate
-//   8-11         chunks, each with its own accumulator and references, and the
-//                one that had the last chunk joins the two while the other
-//                starts on the next piece.  65 .. 128 rows: each takes half of
-//                the rows and every chunk, and one MMA serves both;
-//   warps 12-15  1-byte caches only: convert a landed slot's codes in place to
-//                the 16-bit layouts the MMAs read.
-// A row's reference is the maximum of the first chunk in which it sees a key,
-// kept in tensor memory beside the scores (read as cheaply as they are, where
-// shared memory, which feeds the MMAs, has no bandwidth to spare); it moves,
-// O^T and l with it, only when an exponent outgrows it by 2^8.  P is rounded to
-// the 16 bits of V's type, which the product shares, and normalised by the sum
-// of the rounded weights, so a row that rests on one key returns that key's
-// value; the rounding (half a step, independent over keys) adds as much as the
-// rounding of a 16-bit output.  References, l and O are float32.
+//   warps 4-7,   two softmax warpgroups, each with a tile: a score buffer and an
+//   8-11         O accumulator in tensor memory;
+//   warps 12-15  1-byte caches only: convert landed codes to the 16-bit layouts
+//                the MMAs read.
+// Two kernels differ in what a softmax thread owns.  Up to 64 rows of a kv head
+// (tree_keys.cuh): a key, with transposed products, so that work is in
+// proportion to the rows.  More (tree_rows.cuh): a row, with products of 128 rows.
+// At 64 rows (16 sequences of 32 kv heads, contexts of 2048 .. 4096 tokens) the
+// first takes 145 us, 85 % of the copy rate, and the second would compute on twice
+// the rows; at 128 rows (64 sequences of 8 kv heads, mean context 2064) the first,
+// with two tiles of 64 rows, took 163 us where the second takes 111.
+//
+// P is rounded to the 16 bits of V's type, which the product shares, and
+// normalised by the sum of the rounded weights (1-byte caches: weight x V scale is
+// rounded, and the sum is of the weights before it), so a row that rests on one
+// key returns that key's value; the rounding (half a step, independent over keys)
+// adds as much as the rounding of a 16-bit output.  References, l and O are
+// float32.
 //
 // What bounds it: HBM while the rows per kv head stay below ~290 (4 D flops
 // per key and row against 4 D bytes per key at 16 bits), the exponentials and
-// the MMAs above that.  The hot loops are kept short and the rest out of their
-// way: the instruction cache, not the issue rate, limits a kernel of this many
-// roles.
+// the MMAs above that, shared memory with 1-byte caches.  The hot loops are kept
+// short and the rest out of their way: the instruction cache, not the issue rate,
+// limits a kernel of this many roles.
 //
 // Values in masked places: a masked exponent is replaced; V rows past the
 // context's end are zeroed in shared memory, and a node's V row that holds an
 // infinity or NaN (a slot nothing was ever written to) is zeroed too and added
-// to O^T by hand for the rows that do see it, so it reaches no other row.
+// to O by hand for the rows that do see it, so it reaches no other row.
 #include <cudaTypedefs.h>
 
 #include <mutex>

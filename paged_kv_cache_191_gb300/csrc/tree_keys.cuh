@@ -1,4 +1,25 @@
 // The tree-attention kernel with a thread per key: items of up to 64 rows.
+//
+// The products are transposed: S^T = K Q^T (M = the chunk's 128 keys, N = rows)
+// and O^T += V^T P^T (M = dims, N = rows), so the tensor cores and the
+// exponentials do work in proportion to the rows, 16 at a time, and a whole
+// warpgroup is busy however few they are.  Thread r of a warpgroup owns key r
+// of the chunk: a key's scales are its own registers, P^T leaves through shared
+// memory (one 128-byte row per key), and an output column needs no exchange
+// between lanes.  The two warpgroups take alternate chunks, each with its own
+// accumulator and references, and the one that had the last chunk joins the two
+// while the other starts on the next piece.
+//
+// A row's reference is the maximum of the first chunk in which it sees a key,
+// kept in tensor memory beside the scores (read as cheaply as they are, where
+// shared memory, which feeds the MMAs, has no bandwidth to spare); it moves,
+// O^T and l with it, only when an exponent outgrows it by 2^8.
+//
+// Bound by HBM.  32 sequences of 32 kv heads, 9 .. 26 nodes, f16, mean context
+// 1044: 113 us, 4.93 TB/s, 74 % of the copy rate; what is missing is the launch,
+// the merge (8 us together) and the ~5000 cycles around the first and the last
+// chunk of an item, of which a CTA has 7 here.  With contexts of 2048 .. 4096 it
+// reaches 85 %.
 #pragma once
 
 #include "tree_common.cuh"
