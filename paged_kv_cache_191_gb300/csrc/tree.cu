@@ -232,6 +232,11 @@ pa_status launch_t(const TreeLaunch& l, CUtensorMapDataType dt, cudaStream_t str
   static cudaError_t setup[kMaxDevices];
   std::call_once(once[dev], [dev, kernel] {
     setup[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+    // the registers that the roles ask for have to be the launch's, or they would wait for them forever
+    constexpr int WANT = 256 * L::HIGH + (L::THREADS - 256) * L::LOW;
+    cudaFuncAttributes fa;
+    if (setup[dev] == cudaSuccess) setup[dev] = cudaFuncGetAttributes(&fa, kernel);
+    if (setup[dev] == cudaSuccess && fa.numRegs * L::THREADS < WANT) setup[dev] = cudaErrorInvalidConfiguration;
   });
   if (setup[dev] != cudaSuccess)
     return fail(PA_ERR_CUDA, "pa_tree_attention: %s", cudaGetErrorString(setup[dev]));

@@ -118,6 +118,7 @@ struct Lay {
   static constexpr int MASK = PUB + 16 * HQ;         // uint64 [2 pieces][64 nodes]
   static constexpr int BYTES = MASK + (WORDS ? 1024 : 0);
   static constexpr int THREADS = Q8 ? 512 : 384;
+  static constexpr int HIGH = Q8 ? 176 : 200, LOW = Q8 ? 80 : 104;  // registers: softmax threads', the others'
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
 
@@ -175,19 +176,13 @@ __device__ __forceinline__ bool bar_or(int id, int threads, bool x) {
 // softmax warpgroups: 384 x 168 = 256 x 200 + 128 x 104, and with converters
 // 512 x 128 = 256 x 176 + 256 x 80.  Every warp calls its one.  (A spilled
 // register goes to L2 here: shared memory leaves the L1 no room.)
-template <bool Q8>
+template <typename L>
 __device__ __forceinline__ void fewer_registers() {
-  if constexpr (Q8)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-  else
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::LOW));
 }
-template <bool Q8>
+template <typename L>
 __device__ __forceinline__ void more_registers() {
-  if constexpr (Q8)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
-  else
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::HIGH));
 }
 
 // ---- tensor memory -----------------------------------------------------------

@@ -357,20 +357,20 @@ __global__ void __launch_bounds__(Lay<KT, D, false>::THREADS, 1)
   const uint32_t tmem = setup<L>(gb, sy, wid, &tmK, &tmV, &tmQ);
 
   if (wid == 0) {
-    fewer_registers<Q8>();
+    fewer_registers<L>();
     produce<KT, L>(a, &tmK, &tmV, &tmQ, gb, sy, 0);
   } else if (wid == 1) {
-    fewer_registers<Q8>();
+    fewer_registers<L>();
     multiply<T, L>(a, gb, sy, static_cast<uint32_t>(uniform(static_cast<int>(tmem))));
   } else if (wid == 2) {
-    fewer_registers<Q8>();
+    fewer_registers<L>();
     if constexpr (L::PRODUCERS == 2) produce<KT, L>(a, &tmK, &tmV, &tmQ, gb, sy, 1);
   } else if (wid == 3) {
-    fewer_registers<Q8>();
+    fewer_registers<L>();
     plan<L>(a, gb, sy);
   } else if (wid < 12) {
     // ---- softmax warpgroups: thread r owns key r of a chunk -----------------------------
-    more_registers<Q8>();
+    more_registers<L>();
     Lane x;
     x.t = (wid - 4) >> 2;
     x.w4 = wid & 3;
@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(Lay<KT, D, false>::THREADS, 1)
     }
     if (!ok && lane == 0) flag(PA_DEVERR_TIMEOUT);
   } else if (Q8) {
-    fewer_registers<Q8>();
+    fewer_registers<L>();
     convert<KT, T, L>(gb, sy);
   }
   teardown(wid, tmem);

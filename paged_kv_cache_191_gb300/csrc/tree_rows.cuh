@@ -14,7 +14,8 @@
 // A tile's cycle is softmax (~1500 clocks a chunk), P V and the next scores (~600
 // each) and the waits between them (~1000); two tiles in turns keep the MMA warp
 // busy two thirds of it.  P V in two halves, the first issued before the second
-// half's weights exist, was slower (357 us for 335 below).
+// half's weights exist, was slower (357 us for 335 below), and so were two softmax
+// warpgroups per tile (345 us, and 130 for 111): 104 registers a thread spill.
 //   64 sequences of 8 kv heads, 128 rows, bf16, mean context 2064: 111 us, 5.2
 //   TB/s, 78 % of the copy rate: HBM, and the launch and merge (10 us).
 //   8 sequences of 8 kv heads, 512 rows, f16, contexts to 32768: 335 us, 1.23
@@ -442,20 +443,20 @@ __global__ void __launch_bounds__(Lay<KT, D, true>::THREADS, 1)
   const uint32_t tmem = setup<L>(gb, sy, wid, &tmK, &tmV, &tmQ);
 
   if (wid == 0) {
-    fewer_registers<Q8>();
+    fewer_registers<L>();
     produce<KT, L>(a, &tmK, &tmV, &tmQ, gb, sy, 0);
   } else if (wid == 1) {
-    fewer_registers<Q8>();
+    fewer_registers<L>();
     multiply_rows<T, L>(a, gb, sy, static_cast<uint32_t>(uniform(static_cast<int>(tmem))));
   } else if (wid == 2) {
-    fewer_registers<Q8>();
+    fewer_registers<L>();
     if constexpr (L::PRODUCERS == 2) produce<KT, L>(a, &tmK, &tmV, &tmQ, gb, sy, 1);
   } else if (wid == 3) {
-    fewer_registers<Q8>();
+    fewer_registers<L>();
     plan<L>(a, gb, sy);
   } else if (wid < 12) {
     // ---- softmax warpgroups: thread r owns row r of its tile -----------------------------
-    more_registers<Q8>();
+    more_registers<L>();
     Row x;
     x.t = (wid - 4) >> 2;
     x.w4 = wid & 3;
@@ -613,7 +614,7 @@ __global__ void __launch_bounds__(Lay<KT, D, true>::THREADS, 1)
     }
     if (!ok && lane == 0) flag(PA_DEVERR_TIMEOUT);
   } else if (Q8) {
-    fewer_registers<Q8>();
+    fewer_registers<L>();
     convert<KT, T, L>(gb, sy);
   }
   teardown(wid, tmem);
