@@ -156,8 +156,8 @@ pa_status pa_tree_attention(const void* q, int32_t q_dtype, const int32_t* q_sta
   if (mis(q, 16) || mis(k_cache, 16) || mis(v_cache, 16) || mis(out, 16) || mis(tree_mask, 8) || mis(q_start, 4) ||
       mis(block_tables, 4) || mis(context_lens, 4))
     return fail(PA_ERR_INVALID, "%s: misaligned pointer", fn);
-  // units of work (128-key chunks of every item, and 3 for its start and end) are counted in 32 bits
-  const int64_t G = node_rows(num_q_heads, desc), chunks = static_cast<int64_t>(max_context_len) / 128 + 4;
+  // units of work (128-key chunks of every item, and 4 for its start and end) are counted in 32 bits
+  const int64_t G = node_rows(num_q_heads, desc), chunks = static_cast<int64_t>(max_context_len) / 128 + 5;
   const int64_t items = static_cast<int64_t>(num_tokens) * G / 64 + B;
   if (items * desc->num_kv_heads > INT32_MAX / 2 / chunks)
     return fail(PA_ERR_UNSUPPORTED, "%s: more than 2^30 units of work", fn);

@@ -37,7 +37,7 @@
 // At 64 rows (16 sequences of 32 kv heads, contexts of 2048 .. 4096 tokens) the
 // first takes 145 us, 85 % of the copy rate, and the second would compute on twice
 // the rows; at 128 rows (64 sequences of 8 kv heads, mean context 2064) the first,
-// with two tiles of 64 rows, took 163 us where the second takes 111.
+// with two tiles of 64 rows, took 163 us where the second takes 110.
 //
 // P is rounded to the 16 bits of V's type, which the product shares, and
 // normalised by the sum of the rounded weights (1-byte caches: weight x V scale is
@@ -203,7 +203,9 @@ pa_status launch_t(const TreeLaunch& l, CUtensorMapDataType dt, cudaStream_t str
   a.scale_log2 = mag * 1.4426950408889634f > 1e-30f ? mag * 1.4426950408889634f : 1e-30f;
   a.negate = l.scale < 0.f ? 1u : 0u;
   a.out_f32 = l.out_dtype == PA_DTYPE_F32;
-  a.min_units = kItem + 2;
+  // few units: many CTAs and a longer merge against long runs (one sequence of 600
+  // tokens, 8 kv heads: 13.3 us at 2, 15.9 at 5)
+  a.min_units = 2;
   a.item_rows = L::ITEM;
   a.slot_rows = l.slot_rows;
   const size_t rows = static_cast<size_t>(2) * a.n_cta * a.slot_rows;

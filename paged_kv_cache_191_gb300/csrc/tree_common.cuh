@@ -69,8 +69,9 @@ __device__ __forceinline__ Seq seq_of(const TreeArgs& a, int b, bool report) {
   s.nch = max(1, (s.L + kKeys - 1) / kKeys);  // a sequence without keys still owns its zero rows
   return s;
 }
-// An item's cost in units: its chunks, and kItem for its start and end.
-constexpr int kItem = 3;
+// An item's cost in units: its chunks, and kItem for its start and end (32
+// sequences of 32 kv heads, mean context 1044: 124, 112, 105, 106 us at 2 .. 5).
+constexpr int kItem = 4;
 __device__ __forceinline__ int units_of(const TreeArgs& a, const Seq& s) { return s.tiles * a.Hkv * (s.nch + kItem); }
 __device__ __forceinline__ int warp_sum(int v) {
 #pragma unroll

@@ -14,11 +14,11 @@
 // A tile's cycle is softmax (~1500 clocks a chunk), P V and the next scores (~600
 // each) and the waits between them (~1000); two tiles in turns keep the MMA warp
 // busy two thirds of it.  P V in two halves, the first issued before the second
-// half's weights exist, was slower (357 us for 335 below), and so were two softmax
-// warpgroups per tile (345 us, and 130 for 111): 104 registers a thread spill.
-//   64 sequences of 8 kv heads, 128 rows, bf16, mean context 2064: 111 us, 5.2
+// half's weights exist, was slower (357 us for 333 below), and so were two softmax
+// warpgroups per tile (345 us, and 130 for 110): 104 registers a thread spill.
+//   64 sequences of 8 kv heads, 128 rows, bf16, mean context 2064: 110 us, 5.2
 //   TB/s, 78 % of the copy rate: HBM, and the launch and merge (10 us).
-//   8 sequences of 8 kv heads, 512 rows, f16, contexts to 32768: 335 us, 1.23
+//   8 sequences of 8 kv heads, 512 rows, f16, contexts to 32768: 333 us, 1.23
 //   PFLOP/s, 63 % of cuBLAS: the cycle above.
 //   8 sequences of 8 kv heads, 96 .. 128 rows, E4M3, contexts to 32768: 137 us,
 //   3.0 TB/s, 45 % of the copy rate: shared memory, ~83 % of whose cycles are taken
