@@ -188,6 +188,43 @@ def test_any_scale(scale):
     check(run(w), w)
 
 
+@pytest.mark.parametrize("kind", ["f16", "bf16", "fp8", "int8"])
+@pytest.mark.parametrize("G,sizes", [(2, [9, 20]), (8, [12, 16]), (16, [12, 20])])
+def test_references_that_move(kind, G, sizes):
+    """Scores that spread over tens of octaves, and grow along the context: 64
+    rows of a kv head, 128, more."""
+    w = TreeBatch(29, 2 * G, 2, 128, kind, sizes, [1500, 700])
+    w.scale = 0.8
+    if kind in ("f16", "bf16"):
+        for b, L in enumerate(w.lens):
+            for j, blk in enumerate(w.tables[b][:-(-L // 16)]):
+                w.k[blk] = (w.k[blk].float() * (0.3 + 0.02 * j)).to(w.k.dtype)
+    check(run(w), w)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16", "fp8", "int8"])
+@pytest.mark.parametrize("G", [2, 16, 48])
+def test_a_nan_score_is_a_nan_row(kind, G):
+    """Also where it is the only score; the rows that do not see it stay exact."""
+    w = TreeBatch(30, 2 * G, 2, 128, kind, [6], [6])  # no context before the tree
+    w.mask[:] = np.array([2, 4, 6, 0, 4, 2])[:, None]  # rows see nodes {1}, {2}, {1, 2}, {}, {2}, {1}
+    blk = w.tables[0][0]
+    if w.k_scale is None:
+        v2 = np_exact(w.v)[blk, :, 2]
+        w.k[blk, :, 1, 3] = float("nan")
+    else:
+        w.k_scale[blk, 1] = float("nan")
+        dec = e4m3_decode if kind == "fp8" else (lambda c: c.view(np.int8).astype(np.float64))
+        v2 = dec(w.v[blk, :, 2].numpy().view(np.uint8)) * float(w.v_scale[blk, 2])
+    out = run(w).numpy()
+    assert np.isnan(out[[0, 2, 5]]).all()
+    assert (out[3] == 0).all()
+    want = np.repeat(np.asarray(v2, dtype=np.float64), G, axis=0)  # a single key: its value
+    tol = np.abs(want) * ((0 if w.k_scale is None else U[w.q.dtype]) + 2.0 ** -22)
+    for i in (1, 4):
+        assert (np.abs(out[i] - want) <= tol).all()
+
+
 def test_a_chain_is_chunked_prefill():
     w = TreeBatch(26, 16, 4, 128, "bf16", [40, 3, 17], [900, 3, 64])
     for b, n in enumerate(w.sizes):
