@@ -72,12 +72,8 @@ __device__ __forceinline__ Seq seq_of(const TreeArgs& a, int b, bool report) {
 // An item's cost in units: its chunks, and kItem for its start and end (32
 // sequences of 32 kv heads, mean context 1044: 124, 112, 105, 106 us at 2 .. 5).
 constexpr int kItem = 4;
+constexpr int kMaxUnits = INT32_MAX / 2;
 __device__ __forceinline__ int units_of(const TreeArgs& a, const Seq& s) { return s.tiles * a.Hkv * (s.nch + kItem); }
-__device__ __forceinline__ int warp_sum(int v) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(FULL, v, off);
-  return v;
-}
 
 // One item's run of chunks [c0, c1) for a CTA.
 struct __align__(16) Piece {
@@ -383,10 +379,14 @@ __device__ __forceinline__ void plan(const TreeArgs& a, uint8_t* gb, Sync<L> sy)
   const int lane = static_cast<int>(threadIdx.x & 31);
   const bool report = blockIdx.x == 0;
   // units of the batch, 32 sequences at a time; then the first of this CTA's
-  int total = 0;
+  int64_t sum = 0;
 #pragma unroll 1
-  for (int b0 = 0; b0 < a.B; b0 += 32) total += b0 + lane < a.B ? units_of(a, seq_of(a, b0 + lane, report)) : 0;
-  total = warp_sum(total);
+  for (int b0 = 0; b0 < a.B; b0 += 32) sum += b0 + lane < a.B ? units_of(a, seq_of(a, b0 + lane, report)) : 0;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(FULL, sum, off);
+  // more than the launch was checked for: q_start has ranges that overlap
+  if (sum > kMaxUnits && report && lane == 0) flag(PA_DEVERR_QUERY_RANGE);
+  const int total = sum > kMaxUnits ? 0 : static_cast<int>(sum);
   const int upc = max((total + a.n_cta - 1) / a.n_cta, a.min_units);
   const int start = min(static_cast<int>(blockIdx.x) * upc, total), end = min(start + upc, total);
   int b = 0, ub = 0;  // the sequence of unit `u`, and the units before it
