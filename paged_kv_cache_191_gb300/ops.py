@@ -312,9 +312,10 @@ def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_c
 
 def _rows(t, name, heads_dim):
     """Token stride of [T, H, D] rows whose last two dims are dense."""
-    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != heads_dim):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or stride[2] != 1 or (shape[1] > 1 and stride[1] != heads_dim):
         raise ValueError(f"{name} must be [T, heads, head_dim] with dense heads")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return stride[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
 def rope_cache_write(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, interleaved=False, factor=1.0,
