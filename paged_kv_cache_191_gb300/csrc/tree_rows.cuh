@@ -80,6 +80,7 @@ __device__ __forceinline__ void multiply_rows(const TreeArgs& a, uint8_t* gb, Sy
   int ahead = 0, spin = 0;     // units whose scores are issued and O not
   int no0 = 0, no1 = 0;        // O issued per tile
   int pieces_over = 0;         // pieces that both warpgroups are done with
+  bool k_ok = false, v_ok = false;  // all but its turn is there for the next scores, O
   uint64_t t0 = 0;
   auto test = [&](uint32_t bar, int parity) { return __all_sync(FULL, dev::mbar_test(bar, parity & 1)) != 0; };
   auto landed = [&](int i) { return test(sy.ready(i % NS), i / NS); };
@@ -87,19 +88,52 @@ __device__ __forceinline__ void multiply_rows(const TreeArgs& a, uint8_t* gb, Sy
 #pragma unroll 1
   while (o.k.live) {
     bool moved = false;
+    // Scores first: a tile's follow its product without a look at the other tile.
+    // What a step needs besides its turn is tested ahead of it, while idle.
+    if (s.k.live && !k_ok) {
+      const int i = s.k.it0 + 2 * s.k.c;
+      k_ok = s.j > 0 || ((s.k.c > 0 || test(sy.qfull(s.k.i & 1), s.k.i >> 1)) && landed(i));
+    }
+    if (k_ok && ahead < 2) {
+      const int t = s.tile, i = s.k.it0 + 2 * s.k.c;
+      fence_after();
+      const uint64_t kd = sdesc(sy.base + L::RING + (i % NS) * L::SLOT, 16, L::GRP);
+      const uint64_t qd = sdesc(sy.base + (s.k.both ? t : s.k.i % L::QP) * L::QTILE, 16, 1024);
+      const uint32_t sd = tmem + kRowS + 128 * t;
+      const bool last = s.ends_chunk(), over = s.ends_piece();
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss(sd, qd + (((kk >> 2) * (L::HQ * 128) + (kk & 3) * 32) >> 4),
+                 kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id_s, kk > 0 ? 1u : 0u);
+        commit(sy.sfull(t));
+        if (last) commit(sy.empty(i % NS));
+        if (over) commit(sy.qfree(s.k.i & 1));
+      }
+      __syncwarp();
+      ++ahead;
+      s.next(sy, gb, ok);
+      k_ok = false;
+      moved = true;
+    }
     if (ahead > 0) {
       const int t = o.tile, i = o.k.it0 + 2 * o.k.c + 1;
-      // a tile's first product of a piece overwrites the O of the piece before
-      if (o.k.c < 2 && pieces_over < o.k.i && test(sy.ofree(pieces_over & 1), pieces_over >> 1)) ++pieces_over;
-      if ((o.k.c >= 2 || pieces_over >= o.k.i) && test(sy.pfull(t), t ? no1 : no0) && landed(i)) {
+      if (!v_ok) {
+        // a tile's first product of a piece overwrites the O of the piece before
+        if (o.k.c < 2 && pieces_over < o.k.i && test(sy.ofree(pieces_over & 1), pieces_over >> 1)) ++pieces_over;
+        v_ok = (o.k.c >= 2 || pieces_over >= o.k.i) && (o.j > 0 || landed(i));
+      }
+      if (v_ok && test(sy.pfull(t), t ? no1 : no0)) {
         fence_after();
         const uint64_t vd = sdesc(sy.base + L::RING + (i % NS) * L::SLOT, D == 128 ? 1024 : 0, L::GRP);
         const uint32_t od = tmem + kRowO + 128 * t, pd = tmem + kRowS + 128 * t;
-        const uint32_t forced = uniform(force[t]);
-        const uint32_t acc = o.k.c >= (o.k.both ? 1 : 2) || forced ? 1u : 0u;
+        uint32_t acc = 1;
+        if (o.k.c < (o.k.both ? 1 : 2)) {  // the tile's first chunk: O starts, unless rows were added by hand
+          acc = uniform(force[t]);
+          if (acc && elect_one()) force[t] = 0;
+        }
         const bool last = o.ends_chunk();
         if (elect_one()) {
-          if (forced) force[t] = 0;
 #pragma unroll
           for (int kk = 0; kk < kBlk; ++kk)
             mma_ts(od, pd + 8 * kk, vd + ((kk * 2 * L::GRP) >> 4), id_o, kk > 0 ? 1u : acc);
@@ -110,29 +144,7 @@ __device__ __forceinline__ void multiply_rows(const TreeArgs& a, uint8_t* gb, Sy
         ++(t ? no1 : no0);
         --ahead;
         o.next(sy, gb, ok);
-        moved = true;
-      }
-    }
-    if (s.k.live && ahead < 2) {
-      const int t = s.tile, i = s.k.it0 + 2 * s.k.c, qb = s.k.i & 1;
-      if ((s.k.c > 0 || s.j > 0 || test(sy.qfull(qb), s.k.i >> 1)) && (s.j > 0 || landed(i))) {
-        fence_after();
-        const uint64_t kd = sdesc(sy.base + L::RING + (i % NS) * L::SLOT, 16, L::GRP);
-        const uint64_t qd = sdesc(sy.base + (s.k.both ? t : s.k.i % L::QP) * L::QTILE, 16, 1024);
-        const uint32_t sd = tmem + kRowS + 128 * t;
-        const bool last = s.ends_chunk(), over = s.ends_piece();
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(sd, qd + (((kk >> 2) * (L::HQ * 128) + (kk & 3) * 32) >> 4),
-                   kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id_s, kk > 0 ? 1u : 0u);
-          commit(sy.sfull(t));
-          if (last) commit(sy.empty(i % NS));
-          if (over) commit(sy.qfree(qb));
-        }
-        __syncwarp();
-        ++ahead;
-        s.next(sy, gb, ok);
+        v_ok = false;
         moved = true;
       }
     }
