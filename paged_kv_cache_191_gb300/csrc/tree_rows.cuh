@@ -18,10 +18,10 @@
 // warpgroups per tile (345 us, and 130 for 110): 104 registers a thread spill.
 //   64 sequences of 8 kv heads, 128 rows, bf16, mean context 2064: 110 us, 5.2
 //   TB/s, 78 % of the copy rate: HBM, and the launch and merge (10 us).
-//   8 sequences of 8 kv heads, 512 rows, f16, contexts to 32768: 333 us, 1.23
-//   PFLOP/s, 63 % of cuBLAS: the cycle above.
-//   8 sequences of 8 kv heads, 96 .. 128 rows, E4M3, contexts to 32768: 137 us,
-//   3.0 TB/s, 45 % of the copy rate: shared memory, ~83 % of whose cycles are taken
+//   8 sequences of 8 kv heads, 512 rows, f16, contexts to 32768: 328 us, 1.25
+//   PFLOP/s, 65 % of the library product's burst rate: the cycle above, at the board's power limit.
+//   8 sequences of 8 kv heads, 96 .. 128 rows, E4M3, contexts to 32768: 132 us,
+//   3.1 TB/s, 46 % of the copy rate: shared memory, ~83 % of whose cycles are taken
 //   by codes in (32 KB a chunk, read again), their conversion out (64 KB), the
 //   MMAs' operands (96 KB) and the scales (64 KB).
 #pragma once
@@ -80,69 +80,117 @@ __device__ __forceinline__ void multiply_rows(const TreeArgs& a, uint8_t* gb, Sy
   int ahead = 0, spin = 0;     // units whose scores are issued and O not
   int no0 = 0, no1 = 0;        // O issued per tile
   int pieces_over = 0;         // pieces that both warpgroups are done with
-  bool k_ok = false, v_ok = false;  // all but its turn is there for the next scores, O
   uint64_t t0 = 0;
   auto test = [&](uint32_t bar, int parity) { return __all_sync(FULL, dev::mbar_test(bar, parity & 1)) != 0; };
-  auto landed = [&](int i) { return test(sy.ready(i % NS), i / NS); };
   const uint32_t id_s = idesc<T>(kKeys, false) | (a.negate << 13), id_o = idesc<T>(D, true);
+  // The ring items of the next scores and the next O: slot, and parity of its fill.
+  int ks = 0, kf = 0, vs = 1, vf = 0;
+  auto advance = [](int& slot, int& fill) {
+    slot += 2;
+    if (slot >= NS) {
+      slot -= NS;
+      fill ^= 1;
+    }
+  };
+  auto scores = [&](int slot, int tile, int place, bool last) {  // by one thread
+    const uint64_t kd = sdesc(sy.base + L::RING + slot * L::SLOT, 16, L::GRP);
+    const uint64_t qd = sdesc(sy.base + place * L::QTILE, 16, 1024);
+    const uint32_t sd = tmem + kRowS + 128 * tile;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+      mma_ss(sd, qd + (((kk >> 2) * (L::HQ * 128) + (kk & 3) * 32) >> 4),
+             kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id_s, kk > 0 ? 1u : 0u);
+    commit(sy.sfull(tile));
+    if (last) commit(sy.empty(slot));
+  };
+  auto product = [&](int slot, int tile, uint32_t acc, bool last) {
+    const uint64_t vd = sdesc(sy.base + L::RING + slot * L::SLOT, D == 128 ? 1024 : 0, L::GRP);
+    const uint32_t od = tmem + kRowO + 128 * tile, pd = tmem + kRowS + 128 * tile;
+#pragma unroll
+    for (int kk = 0; kk < kBlk; ++kk)
+      mma_ts(od, pd + 8 * kk, vd + ((kk * 2 * L::GRP) >> 4), id_o, kk > 0 ? 1u : acc);
+    commit(sy.pdone(tile));
+    if (last) commit(sy.empty(slot));
+  };
+  bool k_ok = false, v_ok = false;  // all but its turn is there for the next scores, O
 #pragma unroll 1
   while (o.k.live) {
     bool moved = false;
+    // 1-byte caches: the middle of a piece in a fixed order and in little code, a
+    // tile's product, then its next scores.  (What the general steps below do
+    // between two groups of MMAs takes 300 to 400 clocks.  8 sequences of 8 kv heads,
+    // 128 rows, E4M3: 132 us for 138.  16-bit caches, closer to the copy rate, lose by
+    // waiting for K before the other tile's product: 335 us for 328 at 512 rows.)
+    // (Their pieces have one unit per chunk.)
+    if (L::Q8 && ahead == 2 && s.k.i == o.k.i && o.k.c >= 2 && s.k.c + 1 < s.k.nc) {
+      const int count = s.k.nc - 1 - s.k.c;
+      int t = uniform(o.tile), n = uniform(t ? no1 : no0), n_other = uniform(t ? no0 : no1);
+#pragma unroll 1
+      for (int u = 0; u < count; ++u) {
+        ok = wait_warp(sy.pfull(t), n & 1) && wait_warp(sy.ready(vs), vf);
+        if (!ok) break;
+        fence_after();
+        if (elect_one()) product(vs, t, 1u, true);
+        __syncwarp();
+        advance(vs, vf);
+        ok = wait_warp(sy.ready(ks), kf);
+        if (!ok) break;
+        fence_after();
+        if (elect_one()) scores(ks, t, s.k.i % L::QP, true);
+        __syncwarp();
+        advance(ks, kf);
+        t ^= 1;
+        const int x = n + 1;
+        n = n_other;
+        n_other = x;
+      }
+      if (!ok) break;
+      no0 = t ? n_other : n;
+      no1 = t ? n : n_other;
+      o.tile = s.tile = t;
+      o.k.c += count;
+      s.k.c += count;
+      k_ok = v_ok = false;
+      continue;
+    }
     // Scores first: a tile's follow its product without a look at the other tile.
     // What a step needs besides its turn is tested ahead of it, while idle.
-    if (s.k.live && !k_ok) {
-      const int i = s.k.it0 + 2 * s.k.c;
-      k_ok = s.j > 0 || ((s.k.c > 0 || test(sy.qfull(s.k.i & 1), s.k.i >> 1)) && landed(i));
-    }
+    if (s.k.live && !k_ok)
+      k_ok = s.j > 0 || ((s.k.c > 0 || test(sy.qfull(s.k.i & 1), s.k.i >> 1)) && test(sy.ready(ks), kf));
     if (k_ok && ahead < 2) {
-      const int t = s.tile, i = s.k.it0 + 2 * s.k.c;
       fence_after();
-      const uint64_t kd = sdesc(sy.base + L::RING + (i % NS) * L::SLOT, 16, L::GRP);
-      const uint64_t qd = sdesc(sy.base + (s.k.both ? t : s.k.i % L::QP) * L::QTILE, 16, 1024);
-      const uint32_t sd = tmem + kRowS + 128 * t;
       const bool last = s.ends_chunk(), over = s.ends_piece();
       if (elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss(sd, qd + (((kk >> 2) * (L::HQ * 128) + (kk & 3) * 32) >> 4),
-                 kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id_s, kk > 0 ? 1u : 0u);
-        commit(sy.sfull(t));
-        if (last) commit(sy.empty(i % NS));
+        scores(ks, s.tile, s.k.both ? s.tile : s.k.i % L::QP, last);
         if (over) commit(sy.qfree(s.k.i & 1));
       }
       __syncwarp();
       ++ahead;
+      if (last) advance(ks, kf);
       s.next(sy, gb, ok);
       k_ok = false;
       moved = true;
     }
     if (ahead > 0) {
-      const int t = o.tile, i = o.k.it0 + 2 * o.k.c + 1;
+      const int t = o.tile;
       if (!v_ok) {
         // a tile's first product of a piece overwrites the O of the piece before
         if (o.k.c < 2 && pieces_over < o.k.i && test(sy.ofree(pieces_over & 1), pieces_over >> 1)) ++pieces_over;
-        v_ok = (o.k.c >= 2 || pieces_over >= o.k.i) && (o.j > 0 || landed(i));
+        v_ok = (o.k.c >= 2 || pieces_over >= o.k.i) && (o.j > 0 || test(sy.ready(vs), vf));
       }
       if (v_ok && test(sy.pfull(t), t ? no1 : no0)) {
         fence_after();
-        const uint64_t vd = sdesc(sy.base + L::RING + (i % NS) * L::SLOT, D == 128 ? 1024 : 0, L::GRP);
-        const uint32_t od = tmem + kRowO + 128 * t, pd = tmem + kRowS + 128 * t;
         uint32_t acc = 1;
         if (o.k.c < (o.k.both ? 1 : 2)) {  // the tile's first chunk: O starts, unless rows were added by hand
           acc = uniform(force[t]);
           if (acc && elect_one()) force[t] = 0;
         }
         const bool last = o.ends_chunk();
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < kBlk; ++kk)
-            mma_ts(od, pd + 8 * kk, vd + ((kk * 2 * L::GRP) >> 4), id_o, kk > 0 ? 1u : acc);
-          commit(sy.pdone(t));
-          if (last) commit(sy.empty(i % NS));
-        }
+        if (elect_one()) product(vs, t, acc, last);
         __syncwarp();
         ++(t ? no1 : no0);
         --ahead;
+        if (last) advance(vs, vf);
         o.next(sy, gb, ok);
         v_ok = false;
         moved = true;
