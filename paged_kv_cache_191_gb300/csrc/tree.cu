@@ -37,7 +37,7 @@
 // At 64 rows (16 sequences of 32 kv heads, contexts of 2048 .. 4096 tokens) the
 // first takes 145 us, 85 % of the copy rate, and the second would compute on twice
 // the rows; at 128 rows (64 sequences of 8 kv heads, mean context 2064) the first,
-// with two tiles of 64 rows, took 163 us where the second takes 110.
+// with two tiles of 64 rows, took 163 us where the second takes 109.
 //
 // P is rounded to the 16 bits of V's type, which the product shares, and
 // normalised by the sum of the rounded weights (1-byte caches: weight x V scale is
@@ -81,7 +81,8 @@ __global__ void __launch_bounds__(32 * kMergeRows) tree_merge(const __grid_const
   const int lane = static_cast<int>(threadIdx.x & 31), k0 = static_cast<int>(blockIdx.x);
   const int row = static_cast<int>(blockIdx.y) * kMergeRows + static_cast<int>(threadIdx.x >> 5);
   dev::grid_dependency_wait();
-  const int4 s0 = a.split[2 * k0], s1 = a.split[2 * k0 + 1];  // parts, first slot, first query row, item row | kv head, rows
+  // parts, first slot, first query row, row of the tree | kv head, rows
+  const int4 s0 = a.split[2 * k0], s1 = a.split[2 * k0 + 1];
   const int h = (s0.w + row) & ((1 << a.gl) - 1);
   if (s0.x == 0 || row >= s1.y || h >= a.G) return;
   auto slot_row = [&](int i) { return static_cast<size_t>(i == 0 ? s0.y : 2 * (k0 + i)) * a.slot_rows + row; };

@@ -185,7 +185,8 @@ __device__ __forceinline__ void more_registers() {
 // ---- tensor memory -----------------------------------------------------------
 // Loads that have arrived when they return (load and wait in one statement, so
 // no use of the registers can be scheduled between them).
-#define PA_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+#define PA_8(c, r, i) c(r[i]), c(r[i + 1]), c(r[i + 2]), c(r[i + 3]), c(r[i + 4]), c(r[i + 5]), c(r[i + 6]), c(r[i + 7])
+#define PA_R8(r, i) PA_8("=r", r, i)
 // 16 columns at two places under one wait.
 __device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, uint32_t (&r)[16], uint32_t (&s)[16]) {
   asm volatile(
@@ -220,7 +221,7 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[64]) 
       : "memory");
 }
 #undef PA_R8
-#define PA_I8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
+#define PA_I8(r, i) PA_8("r", r, i)
 // The same rows of 64 columns: thread 4 a + b gives column 4 i + b of rows a, a + 8
 // in r[2 i], r[2 i + 1].
 __device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -232,7 +233,7 @@ __device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)
       : "memory");
 }
 #undef PA_I8
-#define PA_RW8(r, i) "+f"(r[i]), "+f"(r[i + 1]), "+f"(r[i + 2]), "+f"(r[i + 3]), "+f"(r[i + 4]), "+f"(r[i + 5]), "+f"(r[i + 6]), "+f"(r[i + 7])
+#define PA_RW8(r, i) PA_8("+f", r, i)
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
@@ -260,6 +261,7 @@ __device__ __forceinline__ void load_scores(uint32_t taddr, float (&f)[128]) {
   for (int j = 0; j < 128; j += 8) asm volatile("" : PA_RW8(f, j));  // no use of a register moves above the wait
 }
 #undef PA_RW8
+#undef PA_8
 
 // ---- arithmetic --------------------------------------------------------------
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -343,9 +345,9 @@ struct Sync {
   uint32_t base;
   __device__ __forceinline__ uint32_t at(int i) const { return base + L::BAR + 8 * i; }
   __device__ __forceinline__ uint32_t full(int s) const { return at(s); }                // landing place s: landed
-  __device__ __forceinline__ uint32_t taken(int s) const { return at(L::NL + s); }       // 1-byte caches: its codes are read
+  __device__ __forceinline__ uint32_t taken(int s) const { return at(L::NL + s); }       // 1-byte: its codes are read
   __device__ __forceinline__ uint32_t conv(int s) const { return at(2 * L::NL + s); }    // and converted into slot s
-  __device__ __forceinline__ uint32_t empty(int s) const { return at(2 * L::NL + L::NS + s); }  // its last product ended
+  __device__ __forceinline__ uint32_t empty(int s) const { return at(2 * L::NL + L::NS + s); }  // slot used
   __device__ __forceinline__ uint32_t ready(int s) const { return L::Q8 ? conv(s) : full(s); }
   __device__ __forceinline__ uint32_t ext(int i) const { return at(2 * L::NL + 2 * L::NS + i); }
   __device__ __forceinline__ uint32_t sfull(int t) const { return ext(t); }         // scores of tile t
@@ -354,11 +356,11 @@ struct Sync {
   __device__ __forceinline__ uint32_t pdone(int t) const { return ext(6 + t); }     // their product with V ended
   __device__ __forceinline__ uint32_t qfull(int i) const { return ext(8 + i) ; }    // Q of a piece landed
   __device__ __forceinline__ uint32_t qfree(int i) const { return ext(10 + i); }    // its last scores are computed
-  __device__ __forceinline__ uint32_t ofree(int i) const { return ext(12 + i); }    // piece parity i: both warpgroups are done
-  __device__ __forceinline__ uint32_t pub(int t) const { return ext(14 + t); }      // tile t's l and references of the piece
+  __device__ __forceinline__ uint32_t ofree(int i) const { return ext(12 + i); }    // piece parity i: all are done
+  __device__ __forceinline__ uint32_t pub(int t) const { return ext(14 + t); }      // tile t's l and references
   __device__ __forceinline__ uint32_t mfull(int i) const { return ext(16 + i); }    // mask words of a piece
   __device__ __forceinline__ uint32_t pieces(int i) const { return ext(18 + i); }   // piece i % 4 published
-  __device__ __forceinline__ uint32_t mdone() const { return ext(22); }             // after a timeout: products have ended
+  __device__ __forceinline__ uint32_t mdone() const { return ext(22); }             // after a timeout: no products
   __device__ __forceinline__ uint32_t issued() const { return base + L::MISC + 16; }
   // piece i of the CTA; false after the last (or a timeout)
   __device__ __forceinline__ bool piece(const uint8_t* gb, int i, Piece& p, bool& ok) const {
@@ -513,8 +515,8 @@ __device__ __forceinline__ void produce(const TreeArgs& a, const CUtensorMap* tm
     if (lane == 0) dev::mbar_arrive_expect_tx(sy.qfull(i & 1), n * br * 128);
     __syncwarp();
     if (mine)
-      dev::tma_load_3d(sy.base + (both ? y / L::HQ : i % L::QP) * L::QTILE + (sp * L::HQ + y % L::HQ) * 128, tmQ, sy.qfull(i & 1),
-                       sp * 64, x.g * a.G, x.qs + ((x.row0 + y) >> a.gl));
+      dev::tma_load_3d(sy.base + (both ? y / L::HQ : i % L::QP) * L::QTILE + (sp * L::HQ + y % L::HQ) * 128, tmQ,
+                       sy.qfull(i & 1), sp * 64, x.g * a.G, x.qs + ((x.row0 + y) >> a.gl));
     __syncwarp();
   };
   Piece p, pn;

@@ -94,7 +94,8 @@ __device__ __forceinline__ void multiply(const TreeArgs& a, uint8_t* gb, Sync<L>
       // before last to be over, whose O^T its piece will overwrite.
       const int n = t ? ns1 : ns0, over = s.c == 0 ? s.i - 1 : 0;
       if (pieces_over < over && test(sy.ofree(pieces_over & 1), pieces_over >> 1)) ++pieces_over;
-      if (pieces_over >= over && (n == 0 || test(sy.sfree(t), n - 1)) && (s.c > 0 || test(sy.qfull(qb), s.i >> 1)) && landed(i)) {
+      if (pieces_over >= over && (n == 0 || test(sy.sfree(t), n - 1)) &&
+          (s.c > 0 || test(sy.qfull(qb), s.i >> 1)) && landed(i)) {
         fence_after();
         const uint32_t id = idesc<T>((s.p.rows + 15) & ~15, false) | (a.negate << 14);
         const uint64_t kd = sdesc(sy.base + L::RING + (i % NS) * L::SLOT, 16, L::GRP);
@@ -170,8 +171,8 @@ __device__ __forceinline__ uint2 visible(const TreeArgs& a, const uint8_t* gb, c
 // be multiplied by, in scratch[320 ..], if the result's bit 0 is set.  Bit 1:
 // some row still has no reference.
 template <typename L>
-__device__ __forceinline__ int settle(const Lane& x, uint32_t sc, float ks, uint2 vis, int words, uint32_t oc, bool exists, bool& seen,
-                                   float& ref) {
+__device__ __forceinline__ int settle(const Lane& x, uint32_t sc, float ks, uint2 vis, int words, uint32_t oc,
+                                      bool exists, bool& seen, float& ref) {
   const int bar = 2 + x.t;
   float best0 = -INFINITY, best1 = -INFINITY;  // of rows lane, 32 + lane
 #pragma unroll 1
@@ -195,7 +196,8 @@ __device__ __forceinline__ int settle(const Lane& x, uint32_t sc, float ks, uint
   named_bar(bar, 128);
   bool rescale = false;
   if (x.r < 32 * words) {
-    const float cm = fmaxf(fmaxf(x.scratch[x.r], x.scratch[64 + x.r]), fmaxf(x.scratch[128 + x.r], x.scratch[192 + x.r]));
+    const float cm =
+        fmaxf(fmaxf(x.scratch[x.r], x.scratch[64 + x.r]), fmaxf(x.scratch[128 + x.r], x.scratch[192 + x.r]));
     float alpha = 1.f;
     if (exists && (seen ? cm > ref + kMove : cm > -INFINITY)) {
       rescale = seen;
@@ -293,7 +295,8 @@ __device__ __forceinline__ void guard(const Lane& x, uint8_t* gb, uint8_t* vslot
 // The rows of a piece out, by the warpgroup that joins: O^T of both tiles times
 // the rows' weights, a warp 32 dims of a row at a time.
 template <typename T, typename L>
-__device__ __forceinline__ void write_rows(const TreeArgs& a, const Lane& x, const Piece& p, const float2* pubs, uint32_t oa, bool exists) {
+__device__ __forceinline__ void write_rows(const TreeArgs& a, const Lane& x, const Piece& p, const float2* pubs,
+                                           uint32_t oa, bool exists) {
   constexpr int D = L::D;
   const bool direct = p.slot < 0, narrow = direct && !a.out_f32;
   float* wts = x.scratch + 512;  // [2 accumulators][64]

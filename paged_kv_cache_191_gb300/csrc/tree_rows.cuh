@@ -14,12 +14,13 @@
 // A tile's cycle is softmax (~1500 clocks a chunk), P V and the next scores (~600
 // each) and the waits between them (~1000); two tiles in turns keep the MMA warp
 // busy two thirds of it.  P V in two halves, the first issued before the second
-// half's weights exist, was slower (357 us for 333 below), and so were two softmax
-// warpgroups per tile (345 us, and 130 for 110): 104 registers a thread spill.
-//   64 sequences of 8 kv heads, 128 rows, bf16, mean context 2064: 110 us, 5.2
-//   TB/s, 78 % of the copy rate: HBM, and the launch and merge (10 us).
+// half's weights exist, was slower (357 us for 328 below), and so were two softmax
+// warpgroups per tile (345 us, and 130 for 109): 104 registers a thread spill.
+//   64 sequences of 8 kv heads, 128 rows, bf16, mean context 2064: 109 us, 5.3
+//   TB/s, 79 % of the copy rate: HBM, and the launch and merge (10 us).
 //   8 sequences of 8 kv heads, 512 rows, f16, contexts to 32768: 328 us, 1.25
-//   PFLOP/s, 65 % of the library product's burst rate: the cycle above, at the board's power limit.
+//   PFLOP/s, 65 % of the library product's burst rate: the cycle above, and the board's
+//   power limit (1360 W).
 //   8 sequences of 8 kv heads, 96 .. 128 rows, E4M3, contexts to 32768: 132 us,
 //   3.1 TB/s, 46 % of the copy rate: shared memory, ~83 % of whose cycles are taken
 //   by codes in (32 KB a chunk, read again), their conversion out (64 KB), the
@@ -350,8 +351,8 @@ __device__ __forceinline__ float to_lane(int lane, float v0, float v1, float v2,
 // Dims [d0, d1) of the thread's row out: O of one tile, or of both, times their
 // weights.
 template <typename T, typename L>
-__device__ __forceinline__ void write_row(const TreeArgs& a, const Row& x, const Piece& p, int row, float w, float w_other,
-                                          uint32_t o_other, bool other, int d0, int d1) {
+__device__ __forceinline__ void write_row(const TreeArgs& a, const Row& x, const Piece& p, int row, float w,
+                                          float w_other, uint32_t o_other, bool other, int d0, int d1) {
   const bool direct = p.slot < 0, narrow = direct && !a.out_f32;
   const int h = (p.row0 + row) & ((1 << a.gl) - 1);
   const size_t at = direct ? static_cast<size_t>(p.qs + x.node) * a.Hq + p.g * a.G + h
@@ -396,7 +397,8 @@ __device__ __forceinline__ void soften(const TreeArgs& a, const Row& x, const ui
     tmem_ld_frag(x.s + (static_cast<uint32_t>(16 * h) << 16), u);
     float2 f[32];  // [i][row]
 #pragma unroll
-    for (int i = 0; i < 32; ++i) f[i] = mul2(make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])), ks[4 * (i >> 1)]);
+    for (int i = 0; i < 32; ++i)
+      f[i] = mul2(make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])), ks[4 * (i >> 1)]);
     // apply(y, w, m): bits 8 i and 8 i + 1 of m say whether row a + 8 y sees the
     // thread's two columns of word w's group i
     auto by_mask = [&](auto apply) {
@@ -407,7 +409,8 @@ __device__ __forceinline__ void soften(const TreeArgs& a, const Row& x, const ui
         Row z;
         z.node = (p.row0 + r) >> a.gl;
         z.mask = a.mask + static_cast<size_t>(p.qs + z.node) * a.words;
-        z.m0 = !has ? 0ull : p.n <= 64 ? reinterpret_cast<const uint64_t*>(gb + L::MASK)[(piece & 1) * 64 + z.node] : z.mask[0];
+        const uint64_t* words = reinterpret_cast<const uint64_t*>(gb + L::MASK) + (piece & 1) * 64;
+        z.m0 = !has ? 0ull : p.n <= 64 ? words[z.node] : z.mask[0];
         z.m1 = !has || p.n <= 64 ? 0ull : z.mask[1];
 #pragma unroll
         for (int w = 0; w < 4; ++w) apply(y, w, (has ? sees(a, z, j0 + 32 * w, p.n) : 0u) >> b2);
@@ -569,7 +572,8 @@ __global__ void __launch_bounds__(Lay<KT, D, true>::THREADS, 1)
         if constexpr (Q8) {
           if (masked && p.n <= 64 && ok) ok = wait_warp(sy.mfull(pp), (k.i >> 1) & 1);
           if (x.live)
-            soften<T, L>(a, x, gb, p, k.i, ra, rb, gb + L::SCALES + (((k.it0 >> 1) + c) & 7) * 1024, masked, key0 - shift, row - x.r, sl2);
+            soften<T, L>(a, x, gb, p, k.i, ra, rb, gb + L::SCALES + (((k.it0 >> 1) + c) & 7) * 1024, masked,
+                         key0 - shift, row - x.r, sl2);
         } else if (x.live) {
           float f[kKeys];
           load_scores(x.s, f);

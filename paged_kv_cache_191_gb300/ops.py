@@ -225,35 +225,46 @@ def cache_write(k, v, slot_mapping, k_cache, v_cache, k_scale=None, v_scale=None
                                 C.byref(desc), _stream(stream)), "pa_cache_write")
 
 
-def _operands(names, *tensors, strided=0):
-    """The tensors (None allowed; `names` names them) are CUDA tensors of the
-    current device, whose index is returned, and all but the first `strided`
-    are contiguous."""
-    dev = None
-    for i, t in enumerate(tensors):
-        if t is None:
+def _operands(names, dense, strided=()):
+    """The tensors (None allowed but for the first; `names` names them) are CUDA
+    tensors of the current device, whose index is returned, and the dense ones
+    contiguous."""
+    try:
+        dev = dense[0].get_device()  # (-1 on the CPU)
+        if dev >= 0 and dev == torch.cuda.current_device():
+            for t in dense:
+                if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+                    break
+            else:
+                for t in strided:
+                    if t is not None and t.get_device() != dev:
+                        break
+                else:
+                    return dev
+    except AttributeError:
+        pass
+    names = names.split()
+    for i, t in enumerate(dense + strided):
+        if t is None and i > 0:
             continue
-        at = t.get_device() if isinstance(t, torch.Tensor) else -1  # (-1 on the CPU)
-        if at != dev:
-            if at < 0:
-                raise ValueError(f"{names.split()[i]} must be a CUDA tensor")
-            if dev is not None or at != torch.cuda.current_device():
-                raise ValueError(f"{names.split()[i]} is not on the current device")
-            dev = at
-        if i >= strided and not t.is_contiguous():
-            raise ValueError(f"{names.split()[i]} must be contiguous")
-    return dev
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError(f"{names[i]} must be a CUDA tensor")
+        if t.get_device() != torch.cuda.current_device():
+            raise ValueError(f"{names[i]} is not on the current device")
+        if i < len(dense) and not t.is_contiguous():
+            raise ValueError(f"{names[i]} must be contiguous")
+    raise ValueError("tensors expected")
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream(stream):
+def _raw_stream(stream, dev):
     if stream is not None:
         return stream.cuda_stream
     # (the address torch.cuda.current_stream().cuda_stream holds, without building the object)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 @functools.lru_cache(maxsize=64)
@@ -327,8 +338,8 @@ def rope_cache_write(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cach
     inv_freq: float64 [rot_dim / 2] on the device, factor: rope_frequencies.
     q, k and v may be views of one packed projection (only their heads and
     dims have to be dense).  q_out may be q itself."""
-    _operands("q k v q_out positions inv_freq slot_mapping k_cache v_cache k_scale v_scale", q, k, v, q_out, positions,
-              inv_freq, slot_mapping, k_cache, v_cache, k_scale, v_scale, strided=4)
+    dev = _operands("positions inv_freq slot_mapping k_cache v_cache k_scale v_scale k v q q_out",
+                    (positions, inv_freq, slot_mapping, k_cache, v_cache, k_scale, v_scale), (k, v, q, q_out))
     desc = _caches(k_cache, v_cache, k_scale, v_scale)
     D = desc.head_dim
     ks, vs = _rows(k, "k", D), _rows(v, "v", D)
@@ -354,10 +365,11 @@ def rope_cache_write(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cach
         elif q_out.shape != q.shape or q_out.dtype not in (torch.float16, torch.bfloat16, torch.float32):
             raise ValueError("q_out must be [T, num_q_heads, head_dim] in f16 / bf16 / f32")
         os_, odt = _rows(q_out, "q_out", D), q_out.dtype
-    _check(lib().pa_rope_cache_write(_addr(q), _addr(k), _addr(v), _TORCH_DT[k.dtype], qs, ks, vs, _addr(positions),
-                                     _addr(inv_freq), 2 * inv_freq.shape[0], 1 if interleaved else 0, float(factor),
-                                     _addr(slot_mapping), T, Hq, _addr(q_out), _TORCH_DT[odt], os_, _addr(k_cache),
-                                     _addr(v_cache), _addr(k_scale), _addr(v_scale), C.byref(desc), _raw_stream(stream)),
+    _check(lib().pa_rope_cache_write(_addr(q), k.data_ptr(), v.data_ptr(), _TORCH_DT[k.dtype], qs, ks, vs,
+                                     positions.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.shape[0],
+                                     1 if interleaved else 0, float(factor), slot_mapping.data_ptr(), T, Hq,
+                                     _addr(q_out), _TORCH_DT[odt], os_, k_cache.data_ptr(), v_cache.data_ptr(),
+                                     _addr(k_scale), _addr(v_scale), C.byref(desc), _raw_stream(stream, dev)),
            "pa_rope_cache_write")
     return q_out if q is not None else None
 
@@ -400,8 +412,9 @@ def tree_attention(q, q_start, tree_mask, k_cache, v_cache, block_tables, contex
     before the tree and the nodes whose bits its row of tree_mask (int64
     [T, words], ops.tree_mask) sets.  q: [T, Hq, D] packed; returns out
     [T, Hq, D] (q dtype, or out_dtype)."""
-    dev = _operands("q q_start tree_mask k_cache v_cache block_tables context_lens out workspace k_scale v_scale", q, q_start,
-                    tree_mask, k_cache, v_cache, block_tables, context_lens, out, workspace, k_scale, v_scale)
+    dev = _operands("q q_start tree_mask k_cache v_cache block_tables context_lens out workspace k_scale v_scale",
+                    (q, q_start, tree_mask, k_cache, v_cache, block_tables, context_lens, out, workspace, k_scale,
+                     v_scale))
     desc = _caches(k_cache, v_cache, k_scale, v_scale)
     T, Hq, D = q.shape
     B = context_lens.numel()
@@ -423,11 +436,13 @@ def tree_attention(q, q_start, tree_mask, k_cache, v_cache, block_tables, contex
     if workspace is None:
         workspace = torch.empty(_tree_workspace(dev, Hq, int(max_q_len), k_cache.shape, k_cache.dtype),
                                 dtype=torch.uint8, device=q.device)
-    _check(L.pa_tree_attention(_addr(q), _dtype(q, "q"), _addr(q_start), T, int(max_q_len), _addr(tree_mask),
-                               tree_mask.shape[1], _addr(k_cache), _addr(v_cache), _addr(k_scale), _addr(v_scale),
-                               _addr(block_tables), block_tables.shape[1], _addr(context_lens), int(max_context_len),
-                               B, Hq, float(scale), _addr(out), _dtype(out, "out"), C.byref(desc), _addr(workspace),
-                               workspace.numel() * workspace.element_size(), _raw_stream(stream)), "pa_tree_attention")
+    _check(L.pa_tree_attention(_addr(q), _dtype(q, "q"), q_start.data_ptr(), T, int(max_q_len), tree_mask.data_ptr(),
+                               tree_mask.shape[1], k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale),
+                               _addr(v_scale), block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
+                               int(max_context_len), B, Hq, float(scale), out.data_ptr(), _dtype(out, "out"),
+                               C.byref(desc), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                               _raw_stream(stream, dev)),
+           "pa_tree_attention")
     return out
 
 
@@ -443,7 +458,7 @@ def tree_accept(draft_tokens, target_tokens, parents, q_start, max_path, stream=
     path_len int32 [B], next_token int64 [B]).  draft_tokens, target_tokens
     int64 [T]: the nodes' tokens and the model's pick after each; parents
     int32 [T]; q_start int32 [B + 1]."""
-    _operands("draft_tokens target_tokens parents q_start", draft_tokens, target_tokens, parents, q_start)
+    dev = _operands("draft_tokens target_tokens parents q_start", (draft_tokens, target_tokens, parents, q_start))
     T, B = draft_tokens.numel(), q_start.numel() - 1
     if draft_tokens.dtype != torch.int64 or target_tokens.dtype != torch.int64 or target_tokens.numel() != T:
         raise ValueError("draft_tokens and target_tokens must be int64 [T]")
@@ -451,12 +466,13 @@ def tree_accept(draft_tokens, target_tokens, parents, q_start, max_path, stream=
         raise ValueError("parents must be int32 [T]")
     if q_start.dtype != torch.int32 or B < 0:
         raise ValueError("q_start must be int32 [B + 1]")
-    dev = q_start.device
-    path = torch.empty((B, max_path), dtype=torch.int32, device=dev)
-    path_len = torch.empty((B,), dtype=torch.int32, device=dev)
-    token = torch.empty((B,), dtype=torch.int64, device=dev)
-    _check(lib().pa_tree_accept(_addr(draft_tokens), _addr(target_tokens), _addr(parents), _addr(q_start), T, B,
-                                int(max_path), _addr(path), _addr(path_len), _addr(token), _raw_stream(stream)),
+    on = q_start.device
+    path = torch.empty((B, max_path), dtype=torch.int32, device=on)
+    path_len = torch.empty((B,), dtype=torch.int32, device=on)
+    token = torch.empty((B,), dtype=torch.int64, device=on)
+    _check(lib().pa_tree_accept(draft_tokens.data_ptr(), target_tokens.data_ptr(), parents.data_ptr(),
+                                q_start.data_ptr(), T, B, int(max_path), path.data_ptr(), path_len.data_ptr(),
+                                token.data_ptr(), _raw_stream(stream, dev)),
            "pa_tree_accept")
     return path, path_len, token
 
@@ -466,8 +482,9 @@ def tree_commit(k_cache, v_cache, block_tables, context_lens, q_start, path, pat
     """Move the accepted nodes' cache rows together, in place: path element i
     of sequence b goes to the i-th position of its tree.  Returns the new
     context lengths (int32 [B])."""
-    _operands("k_cache v_cache block_tables context_lens q_start path path_len k_scale v_scale new_lens", k_cache,
-              v_cache, block_tables, context_lens, q_start, path, path_len, k_scale, v_scale, new_lens)
+    dev = _operands("k_cache v_cache block_tables context_lens q_start path path_len k_scale v_scale new_lens",
+                    (k_cache, v_cache, block_tables, context_lens, q_start, path, path_len, k_scale, v_scale,
+                     new_lens))
     desc = _caches(k_cache, v_cache, k_scale, v_scale)
     B = context_lens.numel()
     if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or block_tables.shape[0] != B:
@@ -482,9 +499,10 @@ def tree_commit(k_cache, v_cache, block_tables, context_lens, q_start, path, pat
         new_lens = torch.empty((B,), dtype=torch.int32, device=context_lens.device)
     elif new_lens.dtype != torch.int32 or new_lens.numel() != B:
         raise ValueError("new_lens must be int32 [B]")
-    _check(lib().pa_tree_commit(_addr(k_cache), _addr(v_cache), _addr(k_scale), _addr(v_scale), _addr(block_tables),
-                                block_tables.shape[1], _addr(context_lens), _addr(q_start), _addr(path), path.shape[1],
-                                _addr(path_len), B, _addr(new_lens), C.byref(desc), _raw_stream(stream)),
+    _check(lib().pa_tree_commit(k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale),
+                                block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
+                                q_start.data_ptr(), path.data_ptr(), path.shape[1], path_len.data_ptr(), B,
+                                new_lens.data_ptr(), C.byref(desc), _raw_stream(stream, dev)),
            "pa_tree_commit")
     return new_lens
 
