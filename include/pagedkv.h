@@ -558,7 +558,9 @@ size_t pa_tree_attention_workspace_size(int32_t num_q_heads, int32_t max_q_len, 
  *              n_b > L_b is flagged PA_DEVERR_CONTEXT_LEN; the nodes before
  *              the cached ones have no key then.
  * max_q_len    host upper bound on n_b (<= 65535); longer sequences are
- *              skipped and flagged PA_DEVERR_QUERY_RANGE.
+ *              skipped and flagged PA_DEVERR_QUERY_RANGE.  (So is the whole
+ *              call when a q_start out of order has ranges that overlap to
+ *              more than 2^30 units of work.)
  * tree_mask    device int64 [num_tokens][mask_words], the rows packed as q's
  *              tokens are (pa_tree_mask builds them); any bits are allowed,
  *              those from n_b on are not read as keys.

@@ -144,7 +144,8 @@ struct Lane {
   float* scratch;       // the tile's P^T buffer, between a product's end and the next P^T
 };
 
-// The rows (bits) that see the lane's key, node jn of its sequence.
+// The rows (bits) that see the lane's key, node jn of its sequence.  (64 rows: at
+// most 64 nodes, a mask word each.)
 template <typename L>
 __device__ __forceinline__ uint2 visible(const TreeArgs& a, const uint8_t* gb, const Piece& p, int piece, int jn) {
   uint32_t vis[2] = {0u, 0u};
@@ -158,9 +159,7 @@ __device__ __forceinline__ uint2 visible(const TreeArgs& a, const uint8_t* gb, c
     const int n0 = (32 * w) >> a.gl, cnt = min(per, p.n - n0);
 #pragma unroll 2
     for (int i = 0; i < cnt; ++i) {
-      const uint64_t m =
-          p.n <= 64 ? words[n0 + i] : a.mask[static_cast<size_t>(p.qs + n0 + i) * a.words + (jn >> 6)];
-      if ((m >> (jn & 63)) & 1) vis[w] |= each << (i << a.gl);
+      if ((words[n0 + i] >> jn) & 1) vis[w] |= each << (i << a.gl);
     }
   }
   return make_uint2(vis[0], vis[1]);
@@ -422,7 +421,7 @@ __global__ void __launch_bounds__(Lay<KT, D, false>::THREADS, 1)
         }
         uint2 vis = make_uint2(FULL, FULL);  // the rows that see the key
         if (masked) {
-          if (p.n <= 64 && ok) ok = wait_warp(sy.mfull(pp), (k.i >> 1) & 1);
+          if (ok) ok = wait_warp(sy.mfull(pp), (k.i >> 1) & 1);
           vis = visible<L>(a, gb, p, k.i, jn);
           __syncwarp();
         }
