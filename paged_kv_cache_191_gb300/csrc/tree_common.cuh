@@ -120,10 +120,10 @@ struct Lay {
 };
 
 // ---- waits -------------------------------------------------------------------
-// Bounded: each try sleeps up to a microsecond.  (Inlined and without a clock,
-// to keep the code small; a function call would tie every role to one register
-// count.)
-constexpr int kTries = 2000000;
+// Bounded, at about 2 s: a try that comes to nothing takes 3.8 us, whatever its
+// hint.  (Inlined and without a clock, to keep the code small; a function call
+// would tie every role to one register count.)
+constexpr int kTries = 500000;
 __device__ __forceinline__ bool wait_thread(uint32_t bar, uint32_t parity) {
 #pragma unroll 1
   for (int i = 0; i < kTries; ++i)
@@ -140,7 +140,7 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
 // parity only; with the item under way, the slot's phase before it is over.
 __device__ __forceinline__ bool wait_issued(uint32_t count, int item) {
 #pragma unroll 1
-  for (int i = 0; i < kTries; ++i) {
+  for (int i = 0; i < 16 * kTries; ++i) {  // (200 ns each)
     int v;
     asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(v) : "r"(count) : "memory");
     if (v > item) return true;
