@@ -381,9 +381,27 @@ __device__ __forceinline__ void plan(const TreeArgs& a, uint8_t* gb, Sync<L> sy)
   const int lane = static_cast<int>(threadIdx.x & 31);
   const bool report = blockIdx.x == 0;
   // units of the batch, 32 sequences at a time; then the first of this CTA's
+  // Sequences are read 32 at a time, a lane each, and once where that is the batch:
+  // every read of them is a round trip to L2 at the start of the CTA.
+  Seq mine;
+  int group = -1;
+  auto read = [&](int g, bool rep) {
+    if (g == group) return;
+    group = g;
+    const int b = 32 * g + lane;
+    mine = b < a.B ? seq_of(a, b, rep) : Seq{0, 0, 0, 0, 0};
+  };
+  auto seq = [&](int b) {
+    read(b >> 5, false);
+    return Seq{__shfl_sync(FULL, mine.qs, b & 31), __shfl_sync(FULL, mine.n, b & 31), __shfl_sync(FULL, mine.L, b & 31),
+               __shfl_sync(FULL, mine.tiles, b & 31), __shfl_sync(FULL, mine.nch, b & 31)};
+  };
   int64_t sum = 0;
 #pragma unroll 1
-  for (int b0 = 0; b0 < a.B; b0 += 32) sum += b0 + lane < a.B ? units_of(a, seq_of(a, b0 + lane, report)) : 0;
+  for (int g = 0; 32 * g < a.B; ++g) {
+    read(g, report);
+    sum += units_of(a, mine);
+  }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(FULL, sum, off);
   // more than the launch was checked for: q_start has ranges that overlap
@@ -394,7 +412,8 @@ __device__ __forceinline__ void plan(const TreeArgs& a, uint8_t* gb, Sync<L> sy)
   int b = 0, ub = 0;  // the sequence of unit `u`, and the units before it
 #pragma unroll 1
   for (int b0 = 0; start < end; b0 += 32) {
-    const int w = b0 + lane < a.B ? units_of(a, seq_of(a, b0 + lane, false)) : 0;
+    read(b0 >> 5, false);
+    const int w = units_of(a, mine);
     int inc = w;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -425,11 +444,11 @@ __device__ __forceinline__ void plan(const TreeArgs& a, uint8_t* gb, Sync<L> sy)
       p.live = 0;
 #pragma unroll 1
       while (u < end && !p.live) {
-        Seq s = seq_of(a, b, false);
+        Seq s = seq(b);
 #pragma unroll 1
         while (u >= ub + units_of(a, s)) {
           ub += units_of(a, s);
-          s = seq_of(a, ++b, false);
+          s = seq(++b);
         }
         const int cost = s.nch + kItem, at = u - ub, item = at / cost, off = at - item * cost;
         const int stop = min(cost, off + end - u);  // of the item, for this CTA

@@ -237,10 +237,10 @@ __device__ __forceinline__ void guard(const Lane& x, uint8_t* gb, uint8_t* vslot
       reinterpret_cast<volatile uint32_t*>(gb + L::MISC + 64) + parity * 8 + 4 * x.t;
   const int bar = 2 + x.t;
   uint8_t* vrow = vslot + (x.r >> 3) * L::GRP + (x.r & 7) * 128;
-  auto clear = [&]() {
+  auto clear = [&]() {  // (in the order that the lanes' banks differ)
 #pragma unroll 4
     for (int ch = 0; ch < 8 * L::SPANS; ++ch)
-      *reinterpret_cast<uint4*>(vrow + (ch >> 3) * 1024 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(vrow + (ch >> 3) * 1024 + ((ch ^ x.r) & 7) * 16) = make_uint4(0, 0, 0, 0);
   };
   bool bad = false;
   if (jn >= n) {
@@ -248,7 +248,7 @@ __device__ __forceinline__ void guard(const Lane& x, uint8_t* gb, uint8_t* vslot
   } else if (jn >= 0) {
 #pragma unroll 4
     for (int ch = 0; ch < 8 * L::SPANS; ++ch) {
-      const uint4 v = *reinterpret_cast<const uint4*>(vrow + (ch >> 3) * 1024 + (ch & 7) * 16);
+      const uint4 v = *reinterpret_cast<const uint4*>(vrow + (ch >> 3) * 1024 + ((ch ^ x.r) & 7) * 16);
       bad |= bad16<T>(v.x) | bad16<T>(v.y) | bad16<T>(v.z) | bad16<T>(v.w);
     }
   }

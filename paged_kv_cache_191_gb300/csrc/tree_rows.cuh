@@ -254,10 +254,10 @@ __device__ __forceinline__ void guard_rows(const Row& x, uint8_t* gb, uint8_t* v
   const bool scan = !both || x.t == 0;
   const int bar = both ? 1 : 2 + x.t, bar_n = both ? 256 : 128;
   uint8_t* vrow = vslot + (x.r >> 3) * L::GRP + (x.r & 7) * 128;
-  auto clear = [&]() {
+  auto clear = [&]() {  // (in the order that the lanes' banks differ)
 #pragma unroll 4
     for (int ch = 0; ch < 8 * L::SPANS; ++ch)
-      *reinterpret_cast<uint4*>(vrow + (ch >> 3) * 1024 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(vrow + (ch >> 3) * 1024 + ((ch ^ x.r) & 7) * 16) = make_uint4(0, 0, 0, 0);
   };
   if (scan) {
     bool bad = false;
@@ -266,7 +266,7 @@ __device__ __forceinline__ void guard_rows(const Row& x, uint8_t* gb, uint8_t* v
     } else if (jn >= 0) {
 #pragma unroll 4
       for (int ch = 0; ch < 8 * L::SPANS; ++ch) {
-        const uint4 v = *reinterpret_cast<const uint4*>(vrow + (ch >> 3) * 1024 + (ch & 7) * 16);
+        const uint4 v = *reinterpret_cast<const uint4*>(vrow + (ch >> 3) * 1024 + ((ch ^ x.r) & 7) * 16);
         bad |= bad16<T>(v.x) | bad16<T>(v.y) | bad16<T>(v.z) | bad16<T>(v.w);
       }
     }
