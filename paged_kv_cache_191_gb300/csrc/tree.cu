@@ -35,7 +35,7 @@
 // (tree_keys.cuh): a key, with transposed products, so that work is in
 // proportion to the rows.  More (tree_rows.cuh): a row, with products of 128 rows.
 // At 64 rows (16 sequences of 32 kv heads, contexts of 2048 .. 4096 tokens) the
-// first takes 145 us, 85 % of the copy rate, and the second would compute on twice
+// first takes 143 us, 86 % of the copy rate, and the second would compute on twice
 // the rows; at 128 rows (64 sequences of 8 kv heads, mean context 2064) the first,
 // with two tiles of 64 rows, took 163 us where the second takes 109.
 //

@@ -478,8 +478,9 @@ __device__ __forceinline__ void plan(const TreeArgs& a, uint8_t* gb, Sync<L> sy)
       }
       __syncwarp();
     }
-    const int m = i - 2;
-    if (m >= 0 && m < pieces) {
+    // (the first two pieces' words find their places free)
+#pragma unroll 1
+    for (int m = i == 1 ? 0 : max(i - 2, 2); m <= (i == 1 ? 1 : i - 2) && m < pieces; ++m) {
       const Piece& x = ring[m & 3];
       if (L::WORDS && x.n <= 64 && x.c1 * kKeys > x.L - x.n)
         for (int k = lane; k < x.n; k += 32) words[(m & 1) * 64 + k] = a.mask[static_cast<size_t>(x.qs + k) * a.words];

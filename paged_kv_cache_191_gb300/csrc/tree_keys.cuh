@@ -16,10 +16,10 @@
 // O^T and l with it, only when an exponent outgrows it by 2^8.
 //
 // Bound by HBM.  32 sequences of 32 kv heads, 9 .. 26 nodes, f16, mean context
-// 1044: 104 us, 5.36 TB/s, 80 % of the copy rate; what is missing is the launch,
+// 1044: 102 us, 5.44 TB/s, 81 % of the copy rate; what is missing is the launch,
 // the merge (8 us together) and the ~5000 cycles around the first and the last
 // chunk of an item, of which a CTA has 7 here.  With contexts of 2048 .. 4096 it
-// reaches 85 %.
+// reaches 86 %.
 #pragma once
 
 #include "tree_common.cuh"

@@ -21,8 +21,8 @@
 //   8 sequences of 8 kv heads, 512 rows, f16, contexts to 32768: 328 us, 1.25
 //   PFLOP/s, 65 % of the library product's burst rate: the cycle above, and the board's
 //   power limit (1360 W).
-//   8 sequences of 8 kv heads, 96 .. 128 rows, E4M3, contexts to 32768: 132 us,
-//   3.1 TB/s, 46 % of the copy rate: shared memory, ~83 % of whose cycles are taken
+//   8 sequences of 8 kv heads, 96 .. 128 rows, E4M3, contexts to 32768: 131 us,
+//   3.1 TB/s, 47 % of the copy rate: shared memory, ~83 % of whose cycles are taken
 //   by codes in (32 KB a chunk, read again), their conversion out (64 KB), the
 //   MMAs' operands (96 KB) and the scales (64 KB).
 #pragma once
