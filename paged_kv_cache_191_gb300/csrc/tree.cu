@@ -92,6 +92,22 @@ __global__ void __launch_bounds__(32 * kMergeRows) tree_merge(const __grid_const
 #pragma unroll 1
   for (int i0 = 0; i0 < s0.x; i0 += 32) {
     const int n = min(32, s0.x - i0);
+    auto row_of = [&](int i, float2 (&f)[V / 2]) {
+      const float* src = a.part_o + slot_row(i0 + i) * D + lane * V;
+#pragma unroll
+      for (int v = 0; v < V / 2; ++v) f[v] = *reinterpret_cast<const float2*>(src + 2 * v);
+    };
+    auto add = [&](float wi, const float2 (&f)[V / 2]) {
+#pragma unroll
+      for (int v = 0; v < V / 2; ++v) {
+        acc[2 * v] = fmaf(wi, f[v].x, acc[2 * v]);
+        acc[2 * v + 1] = fmaf(wi, f[v].y, acc[2 * v + 1]);
+      }
+    };
+    float2 early[4][V / 2];  // the first rows are on their way with the weights
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) row_of(i, early[i]);
     const float mv = lane < n ? a.part_m[slot_row(i0 + lane)] : -INFINITY;
     const float lv = lane < n ? a.part_l[slot_row(i0 + lane)] : 0.f;
     const float nm = fmaxf(M, warp_max(mv));
@@ -104,16 +120,14 @@ __global__ void __launch_bounds__(32 * kMergeRows) tree_merge(const __grid_const
     ls = ls * again + wl;
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] *= again;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float wi = __shfl_sync(FULL, w, i);
-      const float* src = a.part_o + slot_row(i0 + i) * D + lane * V;
 #pragma unroll
-      for (int v = 0; v < V; v += 2) {
-        const float2 f = *reinterpret_cast<const float2*>(src + v);
-        acc[v] = fmaf(wi, f.x, acc[v]);
-        acc[v + 1] = fmaf(wi, f.y, acc[v + 1]);
-      }
+    for (int i = 0; i < 4; ++i)
+      if (i < n) add(__shfl_sync(FULL, w, i), early[i]);
+#pragma unroll 4
+    for (int i = 4; i < n; ++i) {
+      float2 f[V / 2];
+      row_of(i, f);
+      add(__shfl_sync(FULL, w, i), f);
     }
   }
   const float inv = M == -INFINITY ? 0.f : 1.f / ls;
