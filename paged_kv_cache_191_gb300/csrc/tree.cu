@@ -219,7 +219,7 @@ pa_status launch_t(const TreeLaunch& l, CUtensorMapDataType dt, cudaStream_t str
   a.negate = l.scale < 0.f ? 1u : 0u;
   a.out_f32 = l.out_dtype == PA_DTYPE_F32;
   // few units: many CTAs and a longer merge against long runs (one sequence of 600
-  // tokens, 8 kv heads: 13.3 us at 2, 15.9 at 5)
+  // tokens, 8 kv heads: 13.3 us for 15.9 at 5)
   a.min_units = 2;
   a.item_rows = L::ITEM;
   a.slot_rows = l.slot_rows;

@@ -14,7 +14,6 @@ __device__ uint32_t g_tree_err;
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int kKeys = 128;  // keys per chunk
 constexpr int kBlk = kKeys / 16;
-constexpr float kMove = 8.f;  // log2 of how far an exponent may outgrow its reference
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kLimit = 2000000000ull;
 
@@ -115,6 +114,12 @@ struct Lay {
   static constexpr int MASK = PUB + 16 * HQ;         // uint64 [2 pieces][64 nodes]
   static constexpr int BYTES = MASK + (WORDS ? 1024 : 0);
   static constexpr int THREADS = Q8 ? 512 : 384;
+  // log2 of how far an exponent may outgrow its reference.  1-byte caches: a
+  // reference is 4 octaves below the maximum, so weight x V scale, which V's small
+  // scales would push below what 16 bits hold to full precision, starts that much
+  // higher; in f16 it is finite for scales below 2^6, values of 8128 at least.  (At 8
+  // octaves references move often enough to cost 7 % of a long context.)
+  static constexpr float LIFT = Q8 ? 4.f : 0.f, MOVE = Q8 ? 10.f : 8.f;
   static constexpr int HIGH = Q8 ? 176 : 200, LOW = Q8 ? 80 : 104;  // registers: softmax threads', the others'
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };

@@ -16,7 +16,7 @@
 // O^T and l with it, only when an exponent outgrows it by 2^8.
 //
 // Bound by HBM.  32 sequences of 32 kv heads, 9 .. 26 nodes, f16, mean context
-// 1044: 102 us, 5.44 TB/s, 81 % of the copy rate; what is missing is the launch,
+// 1044: 101 us, 5.5 TB/s, 82 % of the copy rate; what is missing is the launch,
 // the merge (8 us together) and the ~5000 cycles around the first and the last
 // chunk of an item, of which a CTA has 7 here.  With contexts of 2048 .. 4096 it
 // reaches 86 %.
@@ -198,10 +198,10 @@ __device__ __forceinline__ int settle(const Lane& x, uint32_t sc, float ks, uint
     const float cm =
         fmaxf(fmaxf(x.scratch[x.r], x.scratch[64 + x.r]), fmaxf(x.scratch[128 + x.r], x.scratch[192 + x.r]));
     float alpha = 1.f;
-    if (exists && (seen ? cm > ref + kMove : cm > -INFINITY)) {
+    if (exists && (seen ? cm > ref + L::MOVE : cm > -INFINITY)) {
       rescale = seen;
-      if (seen) alpha = dev::ex2(ref - cm);
-      ref = cm;
+      if (seen) alpha = dev::ex2(ref - (cm - L::LIFT));
+      ref = cm - L::LIFT;
       seen = true;
     }
     x.scratch[256 + x.r] = exists ? -ref : -INFINITY;  // rows that do not exist get weight 0
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(Lay<KT, D, false>::THREADS, 1)
             }
           };
           if (!Q8 || !moved) parts(std::integral_constant<int, 0>{});
-          if (!moved && bar_or(bar, 128, top > kMove)) {
+          if (!moved && bar_or(bar, 128, top > L::MOVE)) {
             moved = true;
             continue;
           }

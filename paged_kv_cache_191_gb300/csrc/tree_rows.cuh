@@ -21,8 +21,8 @@
 //   8 sequences of 8 kv heads, 512 rows, f16, contexts to 32768: 328 us, 1.25
 //   PFLOP/s, 65 % of the library product's burst rate: the cycle above, and the board's
 //   power limit (1360 W).
-//   8 sequences of 8 kv heads, 96 .. 128 rows, E4M3, contexts to 32768: 131 us,
-//   3.1 TB/s, 47 % of the copy rate: shared memory, ~83 % of whose cycles are taken
+//   8 sequences of 8 kv heads, 96 .. 128 rows, E4M3, contexts to 32768: 132 us,
+//   3.1 TB/s, 46 % of the copy rate: shared memory, ~83 % of whose cycles are taken
 //   by codes in (32 KB a chunk, read again), their conversion out (64 KB), the
 //   MMAs' operands (96 KB) and the scales (64 KB).
 #pragma once
@@ -436,21 +436,21 @@ __device__ __forceinline__ void soften(const TreeArgs& a, const Row& x, const ui
     t0 *= sl2;
     t1 *= sl2;
     // the rows' maxima are wanted only where a reference is missing or outgrown
-    if (__any_sync(FULL, (ra.has0 && (ra.seen0 ? t0 > ra.ref0 + kMove : t0 > -INFINITY)) ||
-                             (ra.has1 && (ra.seen1 ? t1 > ra.ref1 + kMove : t1 > -INFINITY)))) {
+    if (__any_sync(FULL, (ra.has0 && (ra.seen0 ? t0 > ra.ref0 + L::MOVE : t0 > -INFINITY)) ||
+                             (ra.has1 && (ra.seen1 ? t1 > ra.ref1 + L::MOVE : t1 > -INFINITY)))) {
       t0 = quad_max(t0);
       t1 = quad_max(t1);
-      const bool move0 = ra.has0 && (ra.seen0 ? t0 > ra.ref0 + kMove : t0 > -INFINITY);
-      const bool move1 = ra.has1 && (ra.seen1 ? t1 > ra.ref1 + kMove : t1 > -INFINITY);
+      const bool move0 = ra.has0 && (ra.seen0 ? t0 > ra.ref0 + L::MOVE : t0 > -INFINITY);
+      const bool move1 = ra.has1 && (ra.seen1 ? t1 > ra.ref1 + L::MOVE : t1 > -INFINITY);
       if (__any_sync(FULL, (move0 && ra.seen0) || (move1 && ra.seen1))) {  // O and l follow the reference
-        const float a0 = move0 && ra.seen0 ? dev::ex2(ra.ref0 - t0) : 1.f;
-        const float a1 = move1 && ra.seen1 ? dev::ex2(ra.ref1 - t1) : 1.f;
+        const float a0 = move0 && ra.seen0 ? dev::ex2(ra.ref0 - (t0 - L::LIFT)) : 1.f;
+        const float a1 = move1 && ra.seen1 ? dev::ex2(ra.ref1 - (t1 - L::LIFT)) : 1.f;
         ra.l0 *= a0;
         ra.l1 *= a1;
         rescale<L>(x, h ? to_lane(x.lane, 1.f, 1.f, a0, a1) : to_lane(x.lane, a0, a1, 1.f, 1.f));
       }
-      ra.ref0 = move0 ? t0 : ra.ref0;
-      ra.ref1 = move1 ? t1 : ra.ref1;
+      ra.ref0 = move0 ? t0 - L::LIFT : ra.ref0;
+      ra.ref1 = move1 ? t1 - L::LIFT : ra.ref1;
       ra.seen0 |= move0;
       ra.seen1 |= move1;
     }
@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(Lay<KT, D, true>::THREADS, 1)
 #pragma unroll
             for (int q = 0; q < 4; ++q) m4[q] = max3(m4[q], f[j + q], f[j + 4 + q]);
           const float top = max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * sl2;
-          const bool move = x.exists && (seen ? top > ref + kMove : top > -INFINITY);
+          const bool move = x.exists && (seen ? top > ref + L::MOVE : top > -INFINITY);
           if (__any_sync(FULL, move && seen)) {  // O and l follow the reference
             const float alpha = move && seen ? dev::ex2(ref - top) : 1.f;
             l *= alpha;

@@ -9,7 +9,10 @@ rounded to (2^-11 f16, 2^-8 bf16), w the exact weights.
   weights below 2^-14 are off by 2^-25 of the largest instead, up to L of them.
 * Scores: a float32 sum of D products is off by at most D 2^-23 sum |q K|
   scale, which moves a weight and the sum of weights by that much relative.
-* 1-byte caches round weight x V scale instead of the weight: u once more.
+* 1-byte caches round weight x V scale instead of the weight: u once more.  In
+  f16 a product below 2^-14 is off by 2^-25; weights are 2^4 at the reference,
+  and so is their sum at least, and a product meets a code of at most 448:
+  2^-29 x 448 for every key.
 * 16-bit outputs: half a step.
 Rotation: three float32 roundings and an angle within 2^-22: 2^-21 of |x1| +
 |x2|, then half a step of the destination.
@@ -73,6 +76,8 @@ def check(out, w, ref=None, what=""):
     tol = spread * ((2 if w.k_scale is None else 3) * u + 2 * w.D * 2.0 ** -23 * score[..., None] + 2.0 ** -18)
     if w.q.dtype == torch.float16:
         tol = tol + seen * 2.0 ** -25 * np.maximum(spread.max(-1, keepdims=True), 4.0)
+        if w.k_scale is not None:
+            tol = tol + seen * 2.0 ** -29 * 448
     if out.dtype != torch.float32:
         tol = tol + half_ulp(np.abs(want) + tol, out.dtype)
     got = out.double().numpy()
@@ -223,6 +228,18 @@ def test_a_nan_score_is_a_nan_row(kind, G):
     tol = np.abs(want) * ((0 if w.k_scale is None else U[w.q.dtype]) + 2.0 ** -22)
     for i in (1, 4):
         assert (np.abs(out[i] - want) <= tol).all()
+
+
+@pytest.mark.parametrize("kind", ["fp8", "int8"])
+@pytest.mark.parametrize("G,sizes", [(2, [9, 20]), (8, [12, 16])])
+def test_small_value_scales(kind, G, sizes):
+    """Values of 2^-9 and of 2^6 of the usual size, next to one another."""
+    w = TreeBatch(31, 2 * G, 2, 128, kind, sizes, [700, 90])
+    w.v_scale *= 2.0 ** -9
+    w.v_scale[::3] *= 2.0 ** 15
+    check(run(w), w)
+    w.v_scale[::3] *= 2.0 ** -15
+    check(run(w), w)
 
 
 def test_a_chain_is_chunked_prefill():
