@@ -15,7 +15,8 @@
 // chunk of one item (an item's start and end count as kItem more); the launch
 // has one persistent CTA per SM, and CTA k takes units [k u, (k + 1) u) of the
 // batch in order, u = ceil(units / CTAs): every CTA streams the same number of
-// chunks whatever the lengths.  The lengths stay on the device: each CTA counts
+// chunks whatever the lengths.  (Items of the same kv head side by side where the
+// planner finds that they line up.)  The lengths stay on the device: each CTA counts
 // the units itself from context_lens and q_start.  An item that spans CTAs
 // leaves partial rows (o, m, l), at most two sets per CTA, merged by tree_merge
 // with log-sum-exp weights.
@@ -81,11 +82,11 @@ __global__ void __launch_bounds__(32 * kMergeRows) tree_merge(const __grid_const
   const int lane = static_cast<int>(threadIdx.x & 31), k0 = static_cast<int>(blockIdx.x);
   const int row = static_cast<int>(blockIdx.y) * kMergeRows + static_cast<int>(threadIdx.x >> 5);
   dev::grid_dependency_wait();
-  // parts, first slot, first query row, row of the tree | kv head, rows
+  // parts, first slot, first query row, row of the tree | kv head, rows, CTAs from part to part
   const int4 s0 = a.split[2 * k0], s1 = a.split[2 * k0 + 1];
   const int h = (s0.w + row) & ((1 << a.gl) - 1);
   if (s0.x == 0 || row >= s1.y || h >= a.G) return;
-  auto slot_row = [&](int i) { return static_cast<size_t>(i == 0 ? s0.y : 2 * (k0 + i)) * a.slot_rows + row; };
+  auto slot_row = [&](int i) { return static_cast<size_t>(i == 0 ? s0.y : 2 * (k0 + i * s1.z)) * a.slot_rows + row; };
   float M = -INFINITY, ls = 0.f, acc[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = 0.f;

@@ -14,12 +14,12 @@
 // A tile's cycle is softmax (~1500 clocks a chunk), P V and the next scores (~600
 // each) and the waits between them (~1000); two tiles in turns keep the MMA warp
 // busy two thirds of it.  P V in two halves, the first issued before the second
-// half's weights exist, was slower (357 us for 328 below), and so were two softmax
-// warpgroups per tile (345 us, and 130 for 109): 104 registers a thread spill.
+// half's weights exist, was slower (357 us for 334 then), and so were two softmax
+// warpgroups per tile (345 us for 334, and 130 for 110): 104 registers a thread spill.
 //   64 sequences of 8 kv heads, 128 rows, bf16, mean context 2064: 109 us, 5.3
 //   TB/s, 79 % of the copy rate: HBM, and the launch and merge (10 us).
-//   8 sequences of 8 kv heads, 512 rows, f16, contexts to 32768: 328 us, 1.25
-//   PFLOP/s, 65 % of the library product's burst rate: the cycle above, and the board's
+//   8 sequences of 8 kv heads, 512 rows, f16, contexts to 32768: 323 us, 1.27
+//   PFLOP/s, 66 % of the library product's burst rate: the cycle above, and the board's
 //   power limit (1360 W).
 //   8 sequences of 8 kv heads, 96 .. 128 rows, E4M3, contexts to 32768: 132 us,
 //   3.1 TB/s, 46 % of the copy rate: shared memory, ~83 % of whose cycles are taken

@@ -113,6 +113,14 @@ def test_items_that_span_many_ctas(shape):
     check(run(w, out_dtype=w.q.dtype), w)
 
 
+@pytest.mark.parametrize("kind,sizes", [("f16", [40, 33, 0, 48]), ("int8", [40, 33, 48]), ("bf16", [100, 99])])
+def test_items_side_by_side(kind, sizes):
+    """Every sequence has the same number of items per kv head: 2 of 256 rows, 3
+    of 128, 4; their CTAs go through the same chunks together."""
+    w = TreeBatch(6, 16, 2, 128, kind, sizes, [3000, 1500, 700, 200][:len(sizes)])
+    check(run(w), w)
+
+
 @pytest.mark.parametrize("sizes", [[8, 8], [70, 70]])
 def test_rows_that_see_nothing_are_zero(sizes):
     w = TreeBatch(21, 8, 2, 128, "f16", sizes, sizes)  # no context before the trees
