@@ -113,6 +113,21 @@ def test_items_that_span_many_ctas(shape):
     check(run(w, out_dtype=w.q.dtype), w)
 
 
+@pytest.mark.parametrize("kind,D,odd", [("f16", 128, 0), ("f16", 128, 1), ("bf16", 64, 1), ("int8", 128, 0)])
+def test_many_short_pieces_in_a_cta(kind, D, odd):
+    """Items of one and two chunks, a dozen of them and more in every CTA, so that
+    either warpgroup ends one while the other's next has begun: the same bits ten
+    times over, and every row right."""
+    B = 160
+    rng = W.rng_for(40 + odd)
+    lens = [int(x) for x in rng.integers(1, 129 if odd else 257, B)]
+    w = TreeBatch(41, 16, 16, D, kind, [min(n, 1 + b % 9) for b, n in enumerate(lens)], lens)
+    first = run(w)
+    check(first, w)
+    for _ in range(9):
+        assert torch.equal(run(w), first)
+
+
 @pytest.mark.parametrize("kind,sizes", [("f16", [40, 33, 0, 48]), ("int8", [40, 33, 48]), ("bf16", [100, 99])])
 def test_items_side_by_side(kind, sizes):
     """Every sequence has the same number of items per kv head: 2 of 256 rows, 3
