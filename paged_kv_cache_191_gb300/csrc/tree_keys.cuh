@@ -392,10 +392,11 @@ __global__ void __launch_bounds__(Lay<KT, D, false>::THREADS, 1)
 #pragma unroll 1
     for (;; k.close()) {
       k.open(sy, gb, ok);
-      ok = __all_sync(FULL, ok);
-      if (!__all_sync(FULL, k.live)) break;
-      // every warp has read the sums of l that the piece before left in the scratch
-      named_bar(bar, 128);
+      // The barriers inside a piece have no limit, so where one warp has given up a
+      // wait the whole warpgroup leaves, here.  (And every warp has read the sums of l
+      // that the piece before left in the scratch.)
+      ok = !bar_or(bar, 128, !ok);
+      if (!ok || !__all_sync(FULL, k.live)) break;
       const Piece& p = k.p;
       const int words = p.rows > 32 ? 2 : 1, pp = k.i & 1, shift = p.L - p.n;
       const uint32_t oc = x.tl + kColO + 128 * pp + 64 * t;

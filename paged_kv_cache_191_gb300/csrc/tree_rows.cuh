@@ -538,8 +538,10 @@ __global__ void __launch_bounds__(Lay<KT, D, true>::THREADS, 1)
 #pragma unroll 1
     for (;; k.close()) {
       k.open(sy, gb, ok);
-      ok = __all_sync(FULL, ok);
-      if (!__all_sync(FULL, k.live)) break;
+      // The barriers inside a piece, of one or both warpgroups, have no limit: where a
+      // warp has given up a wait, both warpgroups leave, here.
+      ok = !bar_or(1, 256, !ok);
+      if (!ok || !__all_sync(FULL, k.live)) break;
       const Piece& p = k.p;
       const int row = (k.both ? 128 * t : 0) + r, pp = k.i & 1, shift = p.L - p.n;
       x.live = row - lane < p.rows;
