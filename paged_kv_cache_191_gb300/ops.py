@@ -181,6 +181,20 @@ def _stream(stream):
     return C.c_void_p(s.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream, result=True):
+    """Memory of a call on `stream` (None: the current one), a result or scratch.
+    It comes from that stream's pool: what is freed while the call still runs is
+    not handed to another stream, and nothing that was queued elsewhere still uses
+    it.  A result is also kept for the current stream, on which it is read."""
+    if stream is None or stream.cuda_stream == torch.cuda.current_stream(device).cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if result:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _dev(t, name):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -361,7 +375,7 @@ def rope_cache_write(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cach
         if q.shape[0] != T or q.shape[2] != D or q.dtype != k.dtype:
             raise ValueError("q must be [T, num_q_heads, head_dim] in k's dtype")
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=out_dtype or q.dtype, device=q.device)
+            q_out = _empty((T, Hq, D), out_dtype or q.dtype, q.device, stream)
         elif q_out.shape != q.shape or q_out.dtype not in (torch.float16, torch.bfloat16, torch.float32):
             raise ValueError("q_out must be [T, num_q_heads, head_dim] in f16 / bf16 / f32")
         os_, odt = _rows(q_out, "q_out", D), q_out.dtype
@@ -429,13 +443,13 @@ def tree_attention(q, q_start, tree_mask, k_cache, v_cache, block_tables, contex
     if context_lens.dtype != torch.int32:
         raise ValueError("context_lens must be int32 [B]")
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=out_dtype or q.dtype, device=q.device)
+        out = _empty((T, Hq, D), out_dtype or q.dtype, q.device, stream)
     elif out.shape != (T, Hq, D):
         raise ValueError("out must be [T, Hq, D]")
     L = lib()
     if workspace is None:
-        workspace = torch.empty(_tree_workspace(dev, Hq, int(max_q_len), k_cache.shape, k_cache.dtype),
-                                dtype=torch.uint8, device=q.device)
+        workspace = _empty(_tree_workspace(dev, Hq, int(max_q_len), k_cache.shape, k_cache.dtype), torch.uint8,
+                           q.device, stream, result=False)
     _check(L.pa_tree_attention(_addr(q), _dtype(q, "q"), q_start.data_ptr(), T, int(max_q_len), tree_mask.data_ptr(),
                                tree_mask.shape[1], k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale),
                                _addr(v_scale), block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
@@ -467,9 +481,9 @@ def tree_accept(draft_tokens, target_tokens, parents, q_start, max_path, stream=
     if q_start.dtype != torch.int32 or B < 0:
         raise ValueError("q_start must be int32 [B + 1]")
     on = q_start.device
-    path = torch.empty((B, max_path), dtype=torch.int32, device=on)
-    path_len = torch.empty((B,), dtype=torch.int32, device=on)
-    token = torch.empty((B,), dtype=torch.int64, device=on)
+    path = _empty((B, max_path), torch.int32, on, stream)
+    path_len = _empty((B,), torch.int32, on, stream)
+    token = _empty((B,), torch.int64, on, stream)
     _check(lib().pa_tree_accept(draft_tokens.data_ptr(), target_tokens.data_ptr(), parents.data_ptr(),
                                 q_start.data_ptr(), T, B, int(max_path), path.data_ptr(), path_len.data_ptr(),
                                 token.data_ptr(), _raw_stream(stream, dev)),
@@ -496,7 +510,7 @@ def tree_commit(k_cache, v_cache, block_tables, context_lens, q_start, path, pat
     if path.dtype != torch.int32 or path.dim() != 2 or path.shape[0] != B:
         raise ValueError("path must be int32 [B, max_path]")
     if new_lens is None:
-        new_lens = torch.empty((B,), dtype=torch.int32, device=context_lens.device)
+        new_lens = _empty((B,), torch.int32, context_lens.device, stream)
     elif new_lens.dtype != torch.int32 or new_lens.numel() != B:
         raise ValueError("new_lens must be int32 [B]")
     _check(lib().pa_tree_commit(k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale),

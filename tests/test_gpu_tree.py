@@ -25,7 +25,7 @@ from oracle import tree as O
 from oracle.attention import paged_decode
 from oracle.fp8_e4m3 import e4m3_decode
 from paged_kv_cache_191_gb300 import ops, workloads as W
-from tests.gpu_util import half_ulp, np_exact, requires_cuda
+from tests.gpu_util import half_ulp, held_by_a_call_on_another_stream, np_exact, requires_cuda
 from tests.tree_inputs import KV, TreeBatch, parents_of
 
 pytestmark = [pytest.mark.gpu, requires_cuda]
@@ -349,6 +349,24 @@ def test_graph_replays_follow_the_inputs():
         torch.cuda.synchronize()
         for (_, _, out, _), w in zip(calls, batch):
             check(out.cpu(), w)
+
+
+@pytest.mark.parametrize("what", ["rope", "attention", "accept", "commit"])
+def test_a_call_keeps_its_memory_on_another_stream(monkeypatch, what):
+    w = TreeBatch(35, 8, 2, 128, "f16", [12, 5], [1500, 400])
+    a, _ = args_of(w)
+    f, _ = ops.rope_frequencies(64, device=DEV)
+    k = torch.randn(17, 2, 128, device=DEV).half()
+    no_slot, pos = torch.full((17,), -1, device=DEV), torch.arange(17, device=DEV)
+    par = dev(np.concatenate(w.parents))
+    tok = torch.zeros(17, dtype=torch.int64, device=DEV)
+    path, n = dev(np.zeros((2, 1), np.int32)), dev(np.ones(2, np.int32))
+    call = {"rope": lambda s: [ops.rope_cache_write(a[0], k, k, pos, f, no_slot, a[3], a[4], stream=s)],
+            "attention": lambda s: [ops.tree_attention(*a, stream=s)],
+            "accept": lambda s: list(ops.tree_accept(tok, tok, par, a[1], 12, stream=s)),
+            "commit": lambda s: [ops.tree_commit(*a[3:7], a[1], path, n, stream=s)]}[what]
+    plain, other = held_by_a_call_on_another_stream(monkeypatch, ops, call)
+    assert all(torch.equal(x, y) for x, y in zip(plain, other))
 
 
 # ---- rotary cache write --------------------------------------------------------
