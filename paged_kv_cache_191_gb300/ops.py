@@ -562,7 +562,7 @@ def decode(q, k_cache, v_cache, block_tables, context_lens, max_context_len, sca
         raise ValueError("context_lens must be int32 [B]")
     odt = out_dtype or q.dtype
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=odt, device=q.device)
+        out = _empty((B, Hq, D), odt, q.device, stream)
     else:
         _dev(out, "out")
         if out.shape != (B, Hq, D):
@@ -570,7 +570,7 @@ def decode(q, k_cache, v_cache, block_tables, context_lens, max_context_len, sca
         odt = out.dtype
     need = int(lib().pa_decode_workspace_size(B, Hq, max_context_len, C.byref(desc), split_tokens))
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(need, torch.uint8, q.device, stream, result=False)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib().pa_decode(_ptr(q), _TORCH_DT[q.dtype], _ptr(k_cache), _ptr(v_cache),
                            _ptr(k_scale), _ptr(v_scale), _ptr(block_tables), block_tables.shape[1],
@@ -605,7 +605,7 @@ def chunked_prefill(q, q_start, k_cache, v_cache, block_tables, context_lens, ma
         raise ValueError("context_lens must be int32 [B]")
     odt = out_dtype or q.dtype
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=odt, device=q.device)
+        out = _empty((T, Hq, D), odt, q.device, stream)
     else:
         _dev(out, "out")
         if out.shape != (T, Hq, D):
@@ -614,7 +614,7 @@ def chunked_prefill(q, q_start, k_cache, v_cache, block_tables, context_lens, ma
     need = int(lib().pa_chunked_prefill_workspace_size(T, B, Hq, int(max_q_len), int(max_context_len),
                                                        C.byref(desc), int(split_tokens)))
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(need, torch.uint8, q.device, stream, result=False)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib().pa_chunked_prefill(_ptr(q), _TORCH_DT[q.dtype], _ptr(q_start), T, int(max_q_len),
                                     _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
@@ -645,13 +645,13 @@ def decode_append(k_new, v_new, slot_mapping, q, k_cache, v_cache, block_tables,
         raise ValueError("context_lens must be int32 [B]")
     odt = out_dtype or q.dtype
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=odt, device=q.device)
+        out = _empty((B, Hq, D), odt, q.device, stream)
     else:
         _dev(out, "out")
         odt = out.dtype
     need = int(lib().pa_decode_workspace_size(B, Hq, max_context_len, C.byref(desc), split_tokens))
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(need, torch.uint8, q.device, stream, result=False)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib().pa_decode_append(_ptr(k_new), _ptr(v_new), _TORCH_DT[k_new.dtype], _ptr(slot_mapping),
                                   _ptr(q), _TORCH_DT[q.dtype], _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
@@ -689,14 +689,14 @@ def decode_append_grouped(k_new, v_new, slot_mapping, q, k_cache, v_cache, block
         raise ValueError("context_lens must be int32 [B]")
     odt = out_dtype or q.dtype
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=odt, device=q.device)
+        out = _empty((B, Hq, D), odt, q.device, stream)
     else:
         _dev(out, "out")
         odt = out.dtype
     need = int(lib().pa_decode_grouped_workspace_size(B, Hq, int(max_context_len), n_groups, int(max_group_size),
                                                       int(max_prefix_blocks), C.byref(desc), int(split_tokens)))
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(need, torch.uint8, q.device, stream, result=False)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib().pa_decode_append_grouped(
         _ptr(k_new), _ptr(v_new), _TORCH_DT[k_new.dtype], _ptr(slot_mapping), _ptr(q), _TORCH_DT[q.dtype],
@@ -736,14 +736,14 @@ def decode_append_segments(k_new, v_new, slot_mapping, q, k_cache, v_cache, bloc
         raise ValueError("context_lens must be int32 [B]")
     odt = out_dtype or q.dtype
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=odt, device=q.device)
+        out = _empty((B, Hq, D), odt, q.device, stream)
     else:
         _dev(out, "out")
         odt = out.dtype
     need = int(lib().pa_decode_segments_workspace_size(B, Hq, n_groups, int(max_group_size), int(max_group_items),
                                                        C.byref(desc)))
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(need, torch.uint8, q.device, stream, result=False)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib().pa_decode_append_segments(
         _ptr(k_new), _ptr(v_new), _TORCH_DT[k_new.dtype], _ptr(slot_mapping), _ptr(q), _TORCH_DT[q.dtype],
