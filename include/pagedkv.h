@@ -556,8 +556,9 @@ size_t pa_tree_attention_workspace_size(int32_t num_q_heads, int32_t max_q_len, 
  * q, q_start, k_scale, v_scale, block_tables, context_lens, max_context_len,
  * out          as pa_chunked_prefill; up to 128 query heads per kv head.
  *              n_b > L_b is flagged PA_DEVERR_CONTEXT_LEN; the nodes before
- *              the cached ones have no key then.  With F16 queries over a
- *              1-byte cache, V scales below 2^6 (weight x V scale is f16).
+ *              the cached ones have no key then.  Scales of 1-byte caches may
+ *              have any size and sign (references follow weight x V scale, so
+ *              its 16 bits hold the row's largest whatever the scales).
  * max_q_len    host upper bound on n_b (<= 65535); longer sequences are
  *              skipped and flagged PA_DEVERR_QUERY_RANGE.  (So is the whole
  *              call when a q_start out of order has ranges that overlap to

@@ -76,6 +76,29 @@ def tree_attention(q, q_start, mask, k_cache, v_cache, tables, lens, scale, k_sc
     return out, spread, score
 
 
+def tree_largest(q, q_start, mask, k_cache, tables, lens, scale, k_scale=None, v_scale=None):
+    """float64 [T, Hq]: the largest softmax weight of a row, times its key's V scale."""
+    q = np.asarray(q).astype(np.float64)
+    T, Hq, _ = q.shape
+    G = Hq // k_cache.shape[1]
+    most = np.zeros((T, Hq))
+    for b, L in enumerate(int(x) for x in lens):
+        lo, n = int(q_start[b]), int(q_start[b + 1]) - int(q_start[b])
+        t = np.arange(L)
+        vs = np.ones(L) if v_scale is None else np.abs(v_scale[tables[b][t // BLOCK_SIZE], t % BLOCK_SIZE]).astype(np.float64)
+        for g in range(Hq // G):
+            K = gather_kv(k_cache, tables[b], L, g, k_scale)
+            for i in range(n):
+                sees = np.ones(L, dtype=bool)
+                nodes = np.arange(max(0, L - n), L)
+                sees[nodes] = visible(mask[lo + i], n)[nodes - (L - n)]
+                for h in range(g * G, (g + 1) * G):
+                    s = scale * (K[sees] @ q[lo + i, h])
+                    w = np.exp(s - s.max(initial=-np.inf))
+                    most[lo + i, h] = (w * vs[sees]).max(initial=0.0) / max(w.sum(), 1e-300)
+    return most
+
+
 def tree_accept(draft, target, parents, q_start, max_path):
     """(paths, next tokens): lists per sequence."""
     paths, tokens = [], []

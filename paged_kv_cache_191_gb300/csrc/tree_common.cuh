@@ -114,12 +114,12 @@ struct Lay {
   static constexpr int MASK = PUB + 16 * HQ;         // uint64 [2 pieces][64 nodes]
   static constexpr int BYTES = MASK + (WORDS ? 1024 : 0);
   static constexpr int THREADS = Q8 ? 512 : 384;
-  // log2 of how far an exponent may outgrow its reference.  1-byte caches: a
-  // reference is 4 octaves below the maximum, so weight x V scale, which V's small
-  // scales would push below what 16 bits hold to full precision, starts that much
-  // higher; in f16 it is finite for scales below 2^6, values of 8128 at least.  (At 8
-  // octaves references move often enough to cost 7 % of a long context.)
-  static constexpr float LIFT = Q8 ? 4.f : 0.f, MOVE = Q8 ? 10.f : 8.f;
+  // log2 of how far below its row's maximum a reference is set, and of how far that
+  // maximum may outgrow it.  1-byte caches: the maximum is of weight x V scale, which
+  // is what the product takes in 16 bits, so whatever the scales are a row's largest is
+  // 2^7 .. 2^15: finite in f16, and as far above what f16 drops as it goes.  (The
+  // weight itself is float32: 2^95 with scales of 2^-80, which smaller ones count as here.)
+  static constexpr float LIFT = Q8 ? 7.f : 0.f, MOVE = Q8 ? 15.f : 8.f;
   static constexpr int HIGH = Q8 ? 176 : 200, LOW = Q8 ? 80 : 104;  // registers: softmax threads', the others'
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
@@ -329,6 +329,8 @@ __device__ __forceinline__ float warp_sums(float (&v)[32], int lane) {
   }
   return v[0];
 }
+// log2 of a V scale's size, for references.
+__device__ __forceinline__ float log2_scale(float v) { return __log2f(fmaxf(fabsf(v), 0x1p-80f)); }
 template <typename T>
 __device__ __forceinline__ bool bad16(uint32_t w) {  // a pair holds an infinity or NaN
   constexpr uint32_t E = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;

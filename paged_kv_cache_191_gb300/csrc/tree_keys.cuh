@@ -170,7 +170,7 @@ __device__ __forceinline__ uint2 visible(const TreeArgs& a, const uint8_t* gb, c
 // be multiplied by, in scratch[320 ..], if the result's bit 0 is set.  Bit 1:
 // some row still has no reference.
 template <typename L>
-__device__ __forceinline__ int settle(const Lane& x, uint32_t sc, float ks, uint2 vis, int words, uint32_t oc,
+__device__ __forceinline__ int settle(const Lane& x, uint32_t sc, float ks, float lv, uint2 vis, int words, uint32_t oc,
                                       bool exists, bool& seen, float& ref) {
   const int bar = 2 + x.t;
   float best0 = -INFINITY, best1 = -INFINITY;  // of rows lane, 32 + lane
@@ -181,7 +181,7 @@ __device__ __forceinline__ int settle(const Lane& x, uint32_t sc, float ks, uint
     const uint32_t v = (j & 32 ? vis.y : vis.x) >> (j & 31);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float m = warp_max((v >> e) & 1u ? __uint_as_float(u[e]) * ks : -INFINITY);
+      const float m = warp_max((v >> e) & 1u ? fmaf(__uint_as_float(u[e]), ks, lv) : -INFINITY);
       if (x.lane == (j & 31) + e) {
         if (j & 32)
           best1 = m;
@@ -414,12 +414,13 @@ __global__ void __launch_bounds__(Lay<KT, D, false>::THREADS, 1)
         const bool masked = key0 + kKeys > shift;
         if (ok) ok = wait_warp(sy.sfull(t), n & 1);
         fence_after();
-        float ks = sl2, vsc = 1.f;
+        float ks = sl2, vsc = 1.f, lv = 0.f;  // the key's scales, log2 of V's
         if constexpr (Q8) {
           const float* scales = reinterpret_cast<const float*>(gb + L::SCALES + (((k.it0 >> 1) + c) & 7) * 1024);
           if (key0 + r < p.L) {  // (stale past the end)
             ks = sl2 * scales[r];
             vsc = scales[128 + r];
+            lv = log2_scale(vsc);
           }
         }
         uint2 vis = make_uint2(FULL, FULL);  // the rows that see the key
@@ -435,7 +436,7 @@ __global__ void __launch_bounds__(Lay<KT, D, false>::THREADS, 1)
           if (moved) {
             if (ok && n > 0) ok = wait_warp(sy.pdone(t), (n - 1) & 1);  // (P^T free, O^T at rest)
             fence_after();
-            const int what = settle<L>(x, sc, ks, vis, words, oc, exists, seen, ref);
+            const int what = settle<L>(x, sc, ks, lv, vis, words, oc, exists, seen, ref);
             unset = what & 2;
             if (what & 1) {
 #pragma unroll
@@ -490,7 +491,7 @@ __global__ void __launch_bounds__(Lay<KT, D, false>::THREADS, 1)
             }
           };
           if (!Q8 || !moved) parts(std::integral_constant<int, 0>{});
-          if (!moved && bar_or(bar, 128, top > L::MOVE)) {
+          if (!moved && bar_or(bar, 128, top > L::MOVE - lv)) {
             moved = true;
             continue;
           }

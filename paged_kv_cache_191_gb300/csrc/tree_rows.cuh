@@ -384,103 +384,101 @@ __device__ __forceinline__ void write_row(const TreeArgs& a, const Row& x, const
 
 // The weights of a chunk over a 1-byte cache: 16 rows at a time, as fragments.
 // K's scales go on the scores and V's, once l has summed the weights, on them;
-// only that product is rounded.
+// only that product is rounded.  References go by its maximum: it is taken against
+// them as they are, and again where it turns out to have outgrown one.
 template <typename T, typename L>
 __device__ __forceinline__ void soften(const TreeArgs& a, const Row& x, const uint8_t* gb, const Piece& p, int piece,
                                        Pair& ra, Pair& rb, const uint8_t* scales, bool masked, int j0, int tile_row,
                                        float sl2) {
+  constexpr float kMost = static_cast<float>(1 << static_cast<int>(L::MOVE));
   const int b2 = 2 * (x.lane & 3);
   const float2* ks = reinterpret_cast<const float2*>(scales + b2 * 4);
 #pragma unroll 1
   for (int h = 0; h < 2; ++h) {
-    uint32_t u[64];
-    tmem_ld_frag(x.s + (static_cast<uint32_t>(16 * h) << 16), u);
-    float2 f[32];  // [i][row]
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      f[i] = mul2(make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])), ks[4 * (i >> 1)]);
-    // apply(y, w, m): bits 8 i and 8 i + 1 of m say whether row a + 8 y sees the
-    // thread's two columns of word w's group i
-    auto by_mask = [&](auto apply) {
-#pragma unroll 1
-      for (int y = 0; y < 2; ++y) {
-        const int r = tile_row + 32 * x.w4 + 16 * h + 8 * y + (x.lane >> 2);
-        const bool has = y ? ra.has1 : ra.has0;
-        Row z;
-        z.node = (p.row0 + r) >> a.gl;
-        z.mask = a.mask + static_cast<size_t>(p.qs + z.node) * a.words;
-        const uint64_t* words = reinterpret_cast<const uint64_t*>(gb + L::MASK) + (piece & 1) * 64;
-        z.m0 = !has ? 0ull : p.n <= 64 ? words[z.node] : z.mask[0];
-        z.m1 = !has || p.n <= 64 ? 0ull : z.mask[1];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) apply(y, w, (has ? sees(a, z, j0 + 32 * w, p.n) : 0u) >> b2);
-      }
-    };
-    if (masked) {  // whatever the key's score is
-      by_mask([&](int y, int w, uint32_t m) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool s0 = (m >> (8 * i)) & 1u, s1 = (m >> (8 * i + 1)) & 1u;
-          float2 &g0 = f[2 * (4 * w + i)], &g1 = f[2 * (4 * w + i) + 1];
-          if (y == 0) g0 = make_float2(s0 ? g0.x : -INFINITY, s1 ? g0.y : -INFINITY);
-          if (y == 1) g1 = make_float2(s0 ? g1.x : -INFINITY, s1 ? g1.y : -INFINITY);
-        }
-      });
-    }
-    float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      t0 = max3(t0, f[i].x, f[i].y);
-      t1 = max3(t1, f[i + 1].x, f[i + 1].y);
-    }
-    t0 *= sl2;
-    t1 *= sl2;
-    // the rows' maxima are wanted only where a reference is missing or outgrown
-    if (__any_sync(FULL, (ra.has0 && (ra.seen0 ? t0 > ra.ref0 + L::MOVE : t0 > -INFINITY)) ||
-                             (ra.has1 && (ra.seen1 ? t1 > ra.ref1 + L::MOVE : t1 > -INFINITY)))) {
-      t0 = quad_max(t0);
-      t1 = quad_max(t1);
-      const bool move0 = ra.has0 && (ra.seen0 ? t0 > ra.ref0 + L::MOVE : t0 > -INFINITY);
-      const bool move1 = ra.has1 && (ra.seen1 ? t1 > ra.ref1 + L::MOVE : t1 > -INFINITY);
-      if (__any_sync(FULL, (move0 && ra.seen0) || (move1 && ra.seen1))) {  // O and l follow the reference
-        const float a0 = move0 && ra.seen0 ? dev::ex2(ra.ref0 - (t0 - L::LIFT)) : 1.f;
-        const float a1 = move1 && ra.seen1 ? dev::ex2(ra.ref1 - (t1 - L::LIFT)) : 1.f;
-        ra.l0 *= a0;
-        ra.l1 *= a1;
-        rescale<L>(x, h ? to_lane(x.lane, 1.f, 1.f, a0, a1) : to_lane(x.lane, a0, a1, 1.f, 1.f));
-      }
-      ra.ref0 = move0 ? t0 - L::LIFT : ra.ref0;
-      ra.ref1 = move1 ? t1 - L::LIFT : ra.ref1;
-      ra.seen0 |= move0;
-      ra.seen1 |= move1;
-    }
-    const float2 n0 = make_float2(-ra.ref0, -ra.ref0), n1 = make_float2(-ra.ref1, -ra.ref1);
-    float2 ls0 = make_float2(0.f, 0.f), ls1 = ls0;
+    const uint32_t sc = x.s + (static_cast<uint32_t>(16 * h) << 16);
+    float2 ls0, ls1;
     uint32_t pk[32];
+    bool settle = __any_sync(FULL, (ra.has0 && !ra.seen0) || (ra.has1 && !ra.seen1));
+#pragma unroll 1
+    for (;; settle = true) {
+      uint32_t u[64];
+      tmem_ld_frag(sc, u);
+      float2 f[32];  // [i][row]
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float2 e = fma2(f[i], make_float2(sl2, sl2), i & 1 ? n1 : n0);
-      const float2 w = make_float2(dev::ex2(e.x), dev::ex2(e.y));
-      if (i & 1)
-        ls1 = add2(ls1, w);
-      else
-        ls0 = add2(ls0, w);
-      const float2 y = mul2(w, ks[64 + 4 * (i >> 1)]);
-      pk[i] = dev::pack2<T>(y.x, y.y);
-    }
-    if (masked) {  // nor its V scale, which may be stale or NaN
-      by_mask([&](int y, int w, uint32_t m) {
+      for (int i = 0; i < 32; ++i)
+        f[i] = mul2(make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])), ks[4 * (i >> 1)]);
+      if (masked) {  // whatever the key's score is
+#pragma unroll 1
+        for (int y = 0; y < 2; ++y) {
+          const int r = tile_row + 32 * x.w4 + 16 * h + 8 * y + (x.lane >> 2);
+          const bool has = y ? ra.has1 : ra.has0;
+          Row z;
+          z.node = (p.row0 + r) >> a.gl;
+          z.mask = a.mask + static_cast<size_t>(p.qs + z.node) * a.words;
+          const uint64_t* words = reinterpret_cast<const uint64_t*>(gb + L::MASK) + (piece & 1) * 64;
+          z.m0 = !has ? 0ull : p.n <= 64 ? words[z.node] : z.mask[0];
+          z.m1 = !has || p.n <= 64 ? 0ull : z.mask[1];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t keep = ((m >> (8 * i)) & 1u ? 0xFFFFu : 0u) | ((m >> (8 * i + 1)) & 1u ? 0xFFFF0000u : 0u);
-          if (y == 0) pk[2 * (4 * w + i)] &= keep;
-          if (y == 1) pk[2 * (4 * w + i) + 1] &= keep;
+          for (int w = 0; w < 4; ++w) {
+            // bits 8 i and 8 i + 1: the row sees the thread's two keys of group i
+            const uint32_t m = (has ? sees(a, z, j0 + 32 * w, p.n) : 0u) >> b2;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const bool s0 = (m >> (8 * i)) & 1u, s1 = (m >> (8 * i + 1)) & 1u;
+              float2 &g0 = f[2 * (4 * w + i)], &g1 = f[2 * (4 * w + i) + 1];
+              if (y == 0) g0 = make_float2(s0 ? g0.x : -INFINITY, s1 ? g0.y : -INFINITY);
+              if (y == 1) g1 = make_float2(s0 ? g1.x : -INFINITY, s1 ? g1.y : -INFINITY);
+            }
+          }
         }
-      });
+      }
+      if (settle) {  // references from the maxima of score + log2 V scale; O and l follow
+        float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const float2 v = ks[64 + 2 * i], lg = make_float2(log2_scale(v.x), log2_scale(v.y));
+          const float2 z0 = fma2(f[i], make_float2(sl2, sl2), lg), z1 = fma2(f[i + 1], make_float2(sl2, sl2), lg);
+          t0 = max3(t0, z0.x, z0.y);
+          t1 = max3(t1, z1.x, z1.y);
+        }
+        t0 = quad_max(t0);
+        t1 = quad_max(t1);
+        const bool move0 = ra.has0 && (ra.seen0 ? t0 > ra.ref0 + L::MOVE : t0 > -INFINITY);
+        const bool move1 = ra.has1 && (ra.seen1 ? t1 > ra.ref1 + L::MOVE : t1 > -INFINITY);
+        if (__any_sync(FULL, (move0 && ra.seen0) || (move1 && ra.seen1))) {
+          const float a0 = move0 && ra.seen0 ? dev::ex2(ra.ref0 - (t0 - L::LIFT)) : 1.f;
+          const float a1 = move1 && ra.seen1 ? dev::ex2(ra.ref1 - (t1 - L::LIFT)) : 1.f;
+          ra.l0 *= a0;
+          ra.l1 *= a1;
+          rescale<L>(x, h ? to_lane(x.lane, 1.f, 1.f, a0, a1) : to_lane(x.lane, a0, a1, 1.f, 1.f));
+        }
+        ra.ref0 = move0 ? t0 - L::LIFT : ra.ref0;
+        ra.ref1 = move1 ? t1 - L::LIFT : ra.ref1;
+        ra.seen0 |= move0;
+        ra.seen1 |= move1;
+      }
+      const float2 n0 = make_float2(-ra.ref0, -ra.ref0), n1 = make_float2(-ra.ref1, -ra.ref1);
+      float t0 = 0.f, t1 = 0.f;
+      ls0 = ls1 = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float2 e = fma2(f[i], make_float2(sl2, sl2), i & 1 ? n1 : n0);
+        const float2 w = make_float2(dev::ex2(e.x), dev::ex2(e.y));
+        const float2 y = mul2(w, ks[64 + 4 * (i >> 1)]);
+        if (i & 1) {
+          ls1 = add2(ls1, w);
+          t1 = max3(t1, fabsf(y.x), fabsf(y.y));
+        } else {
+          ls0 = add2(ls0, w);
+          t0 = max3(t0, fabsf(y.x), fabsf(y.y));
+        }
+        pk[i] = dev::pack2<T>(y.x, y.y);
+      }
+      if (settle || !__any_sync(FULL, (ra.has0 && t0 > kMost) || (ra.has1 && t1 > kMost))) break;
     }
     ra.l0 += ls0.x + ls0.y;
     ra.l1 += ls1.x + ls1.y;
-    tmem_st_frag(x.s + (static_cast<uint32_t>(16 * h) << 16), pk);
+    tmem_st_frag(sc, pk);
     const Pair other = rb;  // the other 16 rows' turn (and back)
     rb = ra;
     ra = other;
@@ -572,7 +570,17 @@ __global__ void __launch_bounds__(Lay<KT, D, true>::THREADS, 1)
         if (ok) ok = wait_warp(sy.sfull(t), n & 1);  // (the tile's products before it have ended too)
         fence_after();
         if constexpr (Q8) {
-          if (masked && p.n <= 64 && ok) ok = wait_warp(sy.mfull(pp), (k.i >> 1) & 1);
+          if (masked) {
+            if (p.n <= 64 && ok) ok = wait_warp(sy.mfull(pp), (k.i >> 1) & 1);
+            // A V scale that is no number (stale past the end, or a node's) is to meet no
+            // weight but of the rows that see its key: theirs become NaN by K's.
+            float* ksc = reinterpret_cast<float*>(gb + L::SCALES + (((k.it0 >> 1) + c) & 7) * 1024) + r;
+            if (!(fabsf(ksc[128]) < INFINITY)) {
+              ksc[0] = nanf("");
+              ksc[128] = 0.f;
+            }
+            named_bar(2 + t, 128);
+          }
           if (x.live)
             soften<T, L>(a, x, gb, p, k.i, ra, rb, gb + L::SCALES + (((k.it0 >> 1) + c) & 7) * 1024, masked,
                          key0 - shift, row - x.r, sl2);

@@ -265,6 +265,57 @@ def test_small_value_scales(kind, G, sizes):
     check(run(w), w)
 
 
+def tight(w, small, what=""):
+    """Relative to the row's own sums, with nothing for the size of the context but
+    what 16-bit weights drop: float32 outputs within
+    * spread u: one rounding of each weight (x V scale), whose sum, with 16-bit
+      caches, is of the rounded weights: 2 u;
+    * the scores' float32 sums (as above), 2^-18 for exponentials and references;
+    * in f16, a weight below 2^-14 is off by 2^-25.  A row's largest weight (x V
+      scale) is at least 2^small, so relative to it a key is off by 2^-25 - small, times
+      the largest value (code) that can meet it, and all keys by `L` times that."""
+    want, spread, score = oracle(w)
+    most = O.tree_largest(np_exact(w.q), w.q_start, w.mask, np_exact(w.k), w.tables, w.lens, w.scale,
+                          None if w.k_scale is None else w.k_scale.numpy(),
+                          None if w.v_scale is None else w.v_scale.numpy())[..., None]
+    u = U[w.q.dtype]
+    tol = spread * ((2 if w.k_scale is None else 1) * u + 2 * w.D * 2.0 ** -23 * score[..., None] + 2.0 ** -18)
+    top = {"fp8": 448.0, "int8": 127.0}.get(w.kind) or float(w.v.float().abs().max())
+    if w.q.dtype == torch.float16:
+        tol = tol + np.repeat(w.lens, w.sizes)[:, None, None] * 2.0 ** -(25 + small) * top * most
+    # what the check is for: an output of zeros, or of half the size, does not pass
+    assert (tol < 0.5 * np.abs(want)).mean() > 0.9, f"{what}: tolerance too wide to tell"
+    got = run(w).double().numpy()
+    assert np.isfinite(got).all(), what
+    worst = (np.abs(got - want) / tol).max()
+    assert worst <= 1.0, f"{what}: {worst:.3f} of the tolerance"
+
+
+@pytest.mark.parametrize("kind,qdt", [("fp8", torch.float16), ("int8", torch.float16), ("fp8", torch.bfloat16)])
+@pytest.mark.parametrize("G,sizes", [(2, [9, 20]), (8, [12, 16])])
+@pytest.mark.parametrize("octaves", [-40, -20, -9, 0, 12, 40])
+def test_value_scales_of_any_size(kind, qdt, G, sizes, octaves):
+    """V scales far below and above what f16 holds, all alike and next to usual ones."""
+    w = TreeBatch(36, 2 * G, 2, 128, kind, sizes, [3000, 90], q_dtype=qdt)
+    w.v_scale *= 2.0 ** octaves
+    tight(w, 7, "alike")
+    w.v_scale[::3] *= 2.0 ** -octaves
+    tight(w, 7, "mixed")
+
+
+@pytest.mark.parametrize("G", [2, 16])
+def test_value_scales_of_zero_and_below(G):
+    w = TreeBatch(37, 2 * G, 2, 128, "int8", [9, 12], [300, 40])
+    w.v_scale[::3] *= -1
+    w.v_scale[1::3] = 0
+    want, spread, score = oracle(w)
+    tol = spread * (U[torch.float16] + 2 * w.D * 2.0 ** -23 * score[..., None] + 2.0 ** -18)
+    most = O.tree_largest(np_exact(w.q), w.q_start, w.mask, np_exact(w.k), w.tables, w.lens, w.scale, w.k_scale.numpy(),
+                          w.v_scale.numpy())[..., None]
+    tol = tol + 300 * 2.0 ** -32 * 127 * most
+    assert (np.abs(run(w).double().numpy() - want) <= tol).all()
+
+
 def test_a_chain_is_chunked_prefill():
     w = TreeBatch(26, 16, 4, 128, "bf16", [40, 3, 17], [900, 3, 64])
     for b, n in enumerate(w.sizes):
