@@ -42,7 +42,7 @@
 //
 // P is rounded to the 16 bits of V's type, which the product shares, and
 // normalised by the sum of the rounded weights (1-byte caches: weight x V scale is
-// rounded, and the sum is of the weights before it), so a row that rests on one
+// rounded to f16, and the sum is of the weights before it), so a row that rests on one
 // key returns that key's value; the rounding (half a step, independent over keys)
 // adds as much as the rounding of a 16-bit output.  References, l and O are
 // float32.

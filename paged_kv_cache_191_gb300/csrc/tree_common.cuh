@@ -87,6 +87,9 @@ struct __align__(16) Piece {
 template <typename KT, int D_, bool ROWS_>
 struct Lay {
   static constexpr bool Q8 = sizeof(KT) == 1, ROWS = ROWS_;
+  // V and its weights.  1-byte caches: f16 whatever the queries are, whose 11 bits
+  // bf16 queries would otherwise cut to 8.
+  using VT = std::conditional_t<Q8, __half, KT>;
   static constexpr int D = D_;
   static constexpr int SPANS = D / 64;               // 128-byte spans of a 16-bit row
   // Q of pieces, places of HQ rows [span][HQ][128 B].  Two: a piece of up to HQ
@@ -669,7 +672,8 @@ struct Cursor {
 };
 
 // The converter warpgroup (1-byte caches): codes of a landed chunk -> 16-bit
-// values in its slot of the ring, in the layout the MMAs read.
+// values in its slot of the ring, in the layout the MMAs read: K's of the queries'
+// type, V's f16, the type of their weights.  (Both hold every code exactly.)
 template <typename KT, typename T, typename L>
 __device__ __forceinline__ void convert(uint8_t* gb, Sync<L> sy) {
   constexpr int NS = L::NS, NL = L::NL;
@@ -699,10 +703,17 @@ __device__ __forceinline__ void convert(uint8_t* gb, Sync<L> sy) {
       for (int j = 0; j < 8; ++j) {
         const int x = i0 + 128 * j, key = x >> 3, c16 = x & 7, cc = 2 * (c16 & 3);
         uint32_t f[8];
-        dev::code8x4_to<KT, T>(w[j].x, f[0], f[1]);
-        dev::code8x4_to<KT, T>(w[j].y, f[2], f[3]);
-        dev::code8x4_to<KT, T>(w[j].z, f[4], f[5]);
-        dev::code8x4_to<KT, T>(w[j].w, f[6], f[7]);
+        if (std::is_same<T, __half>::value || (k & 1)) {
+          dev::code8x4_to<KT, __half>(w[j].x, f[0], f[1]);
+          dev::code8x4_to<KT, __half>(w[j].y, f[2], f[3]);
+          dev::code8x4_to<KT, __half>(w[j].z, f[4], f[5]);
+          dev::code8x4_to<KT, __half>(w[j].w, f[6], f[7]);
+        } else {
+          dev::code8x4_to<KT, T>(w[j].x, f[0], f[1]);
+          dev::code8x4_to<KT, T>(w[j].y, f[2], f[3]);
+          dev::code8x4_to<KT, T>(w[j].z, f[4], f[5]);
+          dev::code8x4_to<KT, T>(w[j].w, f[6], f[7]);
+        }
         uint8_t* row = gb + L::RING + to * L::SLOT + (key >> 3) * L::GRP + (c16 >> 2) * 1024 + (key & 7) * 128;
         // (the two spans' threads store their halves in opposite order: no bank conflict)
         const bool up = c16 & 4;

@@ -67,7 +67,7 @@ __device__ __forceinline__ void multiply(const TreeArgs& a, uint8_t* gb, Sync<L>
       if (test(sy.pfull(t), t ? no1 : no0) && landed(i)) {
         fence_after();
         // A = V^T (M-major), B = P^T (N-major)
-        const uint32_t id = idesc<T>((o.p.rows + 15) & ~15, true) | (1u << 15);
+        const uint32_t id = idesc<typename L::VT>((o.p.rows + 15) & ~15, true) | (1u << 15);
         const uint64_t vd = sdesc(sy.base + L::RING + (i % NS) * L::SLOT, D == 128 ? 1024 : 0, L::GRP);
         const uint64_t pd = sdesc(sy.base + L::P0 + t * 16384, 16384, 1024);
         const uint32_t od = tmem + kColO + 128 * (o.i & 1) + 64 * t;
@@ -347,6 +347,7 @@ __global__ void __launch_bounds__(Lay<KT, D, false>::THREADS, 1)
               const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ TreeArgs a) {
   using namespace tcg;
   using L = Lay<KT, D, false>;
+  using VT = typename L::VT;
   constexpr bool Q8 = L::Q8;
   constexpr int NS = L::NS;
   extern __shared__ __align__(1024) uint8_t gb[];
@@ -472,13 +473,13 @@ __global__ void __launch_bounds__(Lay<KT, D, false>::THREADS, 1)
             for (int j = 0; j < 8; ++j) {
               if constexpr (!Q8 || PASS == 0) top = max3(top, e[j].x, e[j].y);
               if constexpr (!Q8) {
-                pk[8 * Q + j] = dev::pack2<T>(dev::ex2(e[j].x), dev::ex2(e[j].y));
+                pk[8 * Q + j] = dev::pack2<VT>(dev::ex2(e[j].x), dev::ex2(e[j].y));
               } else if constexpr (PASS == 1) {
                 const float2 w = make_float2(dev::ex2(e[j].x), dev::ex2(e[j].y));
                 l[8 * Q + j] = add2(l[8 * Q + j], w);
                 const float2 y = mul2(w, make_float2(vsc, vsc));
                 // (a weight of 0 must not meet a NaN scale)
-                pk[8 * Q + j] = dev::pack2<T>(w.x == 0.f ? 0.f : y.x, w.y == 0.f ? 0.f : y.y);
+                pk[8 * Q + j] = dev::pack2<VT>(w.x == 0.f ? 0.f : y.x, w.y == 0.f ? 0.f : y.y);
               }
             }
           };
@@ -503,10 +504,10 @@ __global__ void __launch_bounds__(Lay<KT, D, false>::THREADS, 1)
         if (lane == 0) mbar_arrive(sy.sfree(t));  // the scores are read
         if constexpr (!Q8) {  // l sums the rounded weights
 #pragma unroll
-          for (int j = 0; j < 16; ++j) add16x2<T>(l[j], pk[j]);
+          for (int j = 0; j < 16; ++j) add16x2<VT>(l[j], pk[j]);
           if (words == 2) {
 #pragma unroll
-            for (int j = 16; j < 32; ++j) add16x2<T>(l[j], pk[j]);
+            for (int j = 16; j < 32; ++j) add16x2<VT>(l[j], pk[j]);
           }
         }
         if (ok && n > 0) ok = wait_warp(sy.pdone(t), (n - 1) & 1);  // P^T's buffer is free
@@ -524,7 +525,7 @@ __global__ void __launch_bounds__(Lay<KT, D, false>::THREADS, 1)
           const int vi = k.it0 + 2 * c + 1, vs = vi % NS;
           if (ok) ok = __all_sync(FULL, wait_issued(sy.issued(), vi)) && wait_warp(sy.ready(vs), (vi / NS) & 1);
           fence_after();
-          guard<T, L>(x, gb, gb + L::RING + vs * L::SLOT, pbuf, (p.c0 + c) & 1, jn, p.n, words, oc,
+          guard<VT, L>(x, gb, gb + L::RING + vs * L::SLOT, pbuf, (p.c0 + c) & 1, jn, p.n, words, oc,
                       c == c_first);
         }
         dev::fence_proxy_async_smem();

@@ -83,7 +83,7 @@ __device__ __forceinline__ void multiply_rows(const TreeArgs& a, uint8_t* gb, Sy
   int pieces_over = 0;         // pieces that both warpgroups are done with
   uint64_t t0 = 0;
   auto test = [&](uint32_t bar, int parity) { return __all_sync(FULL, dev::mbar_test(bar, parity & 1)) != 0; };
-  const uint32_t id_s = idesc<T>(kKeys, false) | (a.negate << 13), id_o = idesc<T>(D, true);
+  const uint32_t id_s = idesc<T>(kKeys, false) | (a.negate << 13), id_o = idesc<typename L::VT>(D, true);
   // The ring items of the next scores and the next O: slot, and parity of its fill.
   int ks = 0, kf = 0, vs = 1, vf = 0;
   auto advance = [](int& slot, int& fill) {
@@ -386,7 +386,7 @@ __device__ __forceinline__ void write_row(const TreeArgs& a, const Row& x, const
 // K's scales go on the scores and V's, once l has summed the weights, on them;
 // only that product is rounded.  References go by its maximum: it is taken against
 // them as they are, and again where it turns out to have outgrown one.
-template <typename T, typename L>
+template <typename L>
 __device__ __forceinline__ void soften(const TreeArgs& a, const Row& x, const uint8_t* gb, const Piece& p, int piece,
                                        Pair& ra, Pair& rb, const uint8_t* scales, bool masked, int j0, int tile_row,
                                        float sl2) {
@@ -472,7 +472,7 @@ __device__ __forceinline__ void soften(const TreeArgs& a, const Row& x, const ui
           ls0 = add2(ls0, w);
           t0 = max3(t0, fabsf(y.x), fabsf(y.y));
         }
-        pk[i] = dev::pack2<T>(y.x, y.y);
+        pk[i] = dev::pack2<typename L::VT>(y.x, y.y);
       }
       if (settle || !__any_sync(FULL, (ra.has0 && t0 > kMost) || (ra.has1 && t1 > kMost))) break;
     }
@@ -492,6 +492,7 @@ __global__ void __launch_bounds__(Lay<KT, D, true>::THREADS, 1)
               const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ TreeArgs a) {
   using namespace tcg;
   using L = Lay<KT, D, true>;
+  using VT = typename L::VT;
   constexpr bool Q8 = L::Q8;
   constexpr int NS = L::NS;
   extern __shared__ __align__(1024) uint8_t gb[];
@@ -582,7 +583,7 @@ __global__ void __launch_bounds__(Lay<KT, D, true>::THREADS, 1)
             named_bar(2 + t, 128);
           }
           if (x.live)
-            soften<T, L>(a, x, gb, p, k.i, ra, rb, gb + L::SCALES + (((k.it0 >> 1) + c) & 7) * 1024, masked,
+            soften<L>(a, x, gb, p, k.i, ra, rb, gb + L::SCALES + (((k.it0 >> 1) + c) & 7) * 1024, masked,
                          key0 - shift, row - x.r, sl2);
         } else if (x.live) {
           float f[kKeys];
@@ -620,10 +621,10 @@ __global__ void __launch_bounds__(Lay<KT, D, true>::THREADS, 1)
               const int i = 32 * h + 2 * j;
               const float2 e0 = fma2(make_float2(f[i], f[i + 1]), make_float2(sl2, sl2), make_float2(-ref, -ref));
               const float2 e1 = fma2(make_float2(f[i + 2], f[i + 3]), make_float2(sl2, sl2), make_float2(-ref, -ref));
-              pk[j] = dev::pack2<T>(dev::ex2(e0.x), dev::ex2(e0.y));
-              pk[j + 1] = dev::pack2<T>(dev::ex2(e1.x), dev::ex2(e1.y));
-              add16x2<T>(ls, pk[j]);  // l sums the rounded weights
-              add16x2<T>(ls1, pk[j + 1]);
+              pk[j] = dev::pack2<VT>(dev::ex2(e0.x), dev::ex2(e0.y));
+              pk[j + 1] = dev::pack2<VT>(dev::ex2(e1.x), dev::ex2(e1.y));
+              add16x2<VT>(ls, pk[j]);  // l sums the rounded weights
+              add16x2<VT>(ls1, pk[j + 1]);
             }
             tmem_st16(x.s + 16 * h, pk);
           }
@@ -633,7 +634,7 @@ __global__ void __launch_bounds__(Lay<KT, D, true>::THREADS, 1)
         if (masked) {
           const int vi = k.it0 + 2 * c + 1, vs = vi % NS;
           if (ok) ok = __all_sync(FULL, wait_issued(sy.issued(), vi)) && wait_warp(sy.ready(vs), (vi / NS) & 1);
-          guard_rows<T, L>(x, gb, gb + L::RING + vs * L::SLOT, (p.c0 + c) & 1, k.both, key0 + r - shift, p.n,
+          guard_rows<VT, L>(x, gb, gb + L::RING + vs * L::SLOT, (p.c0 + c) & 1, k.both, key0 + r - shift, p.n,
                            c == c_first);
         }
         fence_before();

@@ -316,6 +316,46 @@ def test_value_scales_of_zero_and_below(G):
     assert (np.abs(run(w).double().numpy() - want) <= tol).all()
 
 
+def exact_scores(w):
+    """Queries and keys of -1, 0 and 1: products that float32 sums exactly, so that
+    nothing but exponentials and the rounding of weights is off."""
+    rng = W.rng_for(7)
+    w.q = torch.from_numpy(rng.integers(-1, 2, w.q.shape)).to(w.q.dtype)
+    k = torch.from_numpy(rng.integers(-1, 2, w.k.shape))
+    if w.kind == "fp8":
+        w.k = torch.where(k == 0, 0, torch.where(k > 0, 0x38, 0xB8)).to(torch.uint8)
+    else:
+        w.k = k.to(w.k.dtype)
+    if w.k_scale is not None:
+        w.k_scale[:] = 1
+    w.scale = 0.25
+
+
+def check_weights(w, u):
+    """Float32 outputs, weights of half a step u: the scores in octaves are below 64,
+    off by 2^-24 of that (a weight by 2^-18), exponentials by 2^-22; a part's reference
+    and the merge as much again: 2^-17.  f16 products are at least 2^7 at a row's
+    largest (as above)."""
+    want, spread, _ = oracle(w)
+    tol = spread * (u + 2.0 ** -17)
+    if w.k_scale is not None:
+        most = O.tree_largest(np_exact(w.q), w.q_start, w.mask, np_exact(w.k), w.tables, w.lens, w.scale,
+                              w.k_scale.numpy(), w.v_scale.numpy())[..., None]
+        tol = tol + np.repeat(w.lens, w.sizes)[:, None, None] * 2.0 ** -32 * {"fp8": 448, "int8": 127}[w.kind] * most
+    worst = (np.abs(run(w).double().numpy() - want) / tol).max()
+    assert worst <= 1.0, f"{worst:.2f} of the tolerance"
+
+
+@pytest.mark.parametrize("kind", ["fp8", "int8"])
+@pytest.mark.parametrize("G,sizes", [(2, [9, 20, 3]), (8, [12, 16, 3])])
+def test_weights_over_one_byte_caches_have_11_bits(kind, G, sizes):
+    """With bf16 queries as with f16 ones."""
+    for qdt in (torch.float16, torch.bfloat16):
+        w = TreeBatch(38, 2 * G, 2, 128, kind, sizes, [700, 40, 3], q_dtype=qdt)
+        exact_scores(w)
+        check_weights(w, 2.0 ** -11)
+
+
 def test_a_chain_is_chunked_prefill():
     w = TreeBatch(26, 16, 4, 128, "bf16", [40, 3, 17], [900, 3, 64])
     for b, n in enumerate(w.sizes):
