@@ -83,20 +83,23 @@ struct __align__(16) Piece {
 
 // ---- shared memory -----------------------------------------------------------
 // ROWS: the kernel with a thread per row (items of up to 256 rows), else the one
-// with a thread per key (up to 64).
+// with a thread per key (up to 64; over bf16 caches 32, whose low halves take the
+// other 32 columns).
 template <typename KT, int D_, bool ROWS_>
 struct Lay {
   static constexpr bool Q8 = sizeof(KT) == 1, ROWS = ROWS_;
   // V and its weights.  1-byte caches: f16 whatever the queries are, whose 11 bits
   // bf16 queries would otherwise cut to 8.
   using VT = std::conditional_t<Q8, __half, KT>;
+  // bf16 caches: a weight is the sum of two bf16, which hold 16 of its bits.
+  static constexpr bool SPLIT = std::is_same<VT, __nv_bfloat16>::value;
   static constexpr int D = D_;
   static constexpr int SPANS = D / 64;               // 128-byte spans of a 16-bit row
   // Q of pieces, places of HQ rows [span][HQ][128 B].  Two: a piece of up to HQ
   // rows takes one, in turns, a larger one both.  1-byte caches have one.
   static constexpr int HQ = ROWS ? 128 : 64;
   static constexpr int QP = Q8 ? 1 : 2;
-  static constexpr int ITEM = ROWS ? QP * HQ : HQ;   // rows of an item
+  static constexpr int ITEM = ROWS ? QP * HQ : SPLIT ? HQ / 2 : HQ;  // rows of an item
   static constexpr int QTILE = HQ * D * 2;
   static constexpr int SLOT = kKeys * D * 2;         // one K or V chunk, 16-bit
   static constexpr int GRP = 1024 * SPANS;           // 8 keys of a slot: [span][8][128 B]
@@ -313,6 +316,11 @@ __device__ __forceinline__ void add16x2(float2& l, uint32_t pair) {
     asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tadd.rn.f32.bf16 %0, x, %0;\n\tadd.rn.f32.bf16 %1, y, %1;\n\t}"
         : "+f"(l.x), "+f"(l.y)
         : "r"(pair));
+}
+// What a pair of weights has beyond its bf16 halves, rounded to bf16 in turn.
+__device__ __forceinline__ uint32_t low_half(float2 w, uint32_t pair) {
+  const float2 h = dev::unpack2<__nv_bfloat16>(pair);
+  return dev::pack2<__nv_bfloat16>(w.x - h.x, w.y - h.y);
 }
 __device__ __forceinline__ float warp_max(float v) {
   float m;

@@ -1,4 +1,6 @@
-// The tree-attention kernel with a thread per key: items of up to 64 rows.
+// The tree-attention kernel with a thread per key: items of up to 64 rows (32 over
+// bf16 caches: the weights' low halves are columns 32 .. of P^T, and O^T's columns 32
+// .. their product, added at the end).
 //
 // The products are transposed: S^T = K Q^T (M = the chunk's 128 keys, N = rows)
 // and O^T += V^T P^T (M = dims, N = rows), so the tensor cores and the
@@ -67,7 +69,8 @@ __device__ __forceinline__ void multiply(const TreeArgs& a, uint8_t* gb, Sync<L>
       if (test(sy.pfull(t), t ? no1 : no0) && landed(i)) {
         fence_after();
         // A = V^T (M-major), B = P^T (N-major)
-        const uint32_t id = idesc<typename L::VT>((o.p.rows + 15) & ~15, true) | (1u << 15);
+        const int n = ((o.p.rows + 15) & ~15) + (L::SPLIT ? 32 : 0);
+        const uint32_t id = idesc<typename L::VT>(n, true) | (1u << 15);
         const uint64_t vd = sdesc(sy.base + L::RING + (i % NS) * L::SLOT, D == 128 ? 1024 : 0, L::GRP);
         const uint64_t pd = sdesc(sy.base + L::P0 + t * 16384, 16384, 1024);
         const uint32_t od = tmem + kColO + 128 * (o.i & 1) + 64 * t;
@@ -214,11 +217,14 @@ __device__ __forceinline__ int settle(const Lane& x, uint32_t sc, float ks, floa
     const uint32_t u[8] = {f[0].x, f[0].y, f[0].z, f[0].w, f[1].x, f[1].y, f[1].z, f[1].w};
     tmem_st8(x.tl + kColR + 64 * x.t + j, u);
     if (rescale) {
-      uint32_t o[8];
-      tmem_ld8(oc + j, o);
+#pragma unroll 1
+      for (int at = j; at < (L::SPLIT ? 64 : 32 * words); at += L::SPLIT ? 32 : 64) {
+        uint32_t o[8];
+        tmem_ld8(oc + at, o);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * x.scratch[320 + j + e]);
-      tmem_st8(oc + j, o);
+        for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * x.scratch[320 + j + e]);
+        tmem_st8(oc + at, o);
+      }
     }
   }
   tcg::wait_st();
@@ -270,16 +276,24 @@ __device__ __forceinline__ void guard(const Lane& x, uint8_t* gb, uint8_t* vslot
     for (int j = 0; j < 32 * words; j += 8) {
       uint32_t u[8];
       tmem_ld8(oc + j, u);
-      const uint4 q = *reinterpret_cast<const uint4*>(pbuf + (key >> 3) * 1024 + (key & 7) * 128 +
-                                                      (((j >> 3) ^ (key & 7)) << 4));
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      auto weights = [&](int chunk) {
+        return *reinterpret_cast<const uint4*>(pbuf + (key >> 3) * 1024 + (key & 7) * 128 +
+                                               ((chunk ^ (key & 7)) << 4));
+      };
+      const uint4 q = weights(j >> 3), q2 = L::SPLIT ? weights(4 + (j >> 3)) : make_uint4(0, 0, 0, 0);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w}, w2[4] = {q2.x, q2.y, q2.z, q2.w};
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float pj = e & 1 ? dev::unpack2<T>(w[e >> 1]).y : dev::unpack2<T>(w[e >> 1]).x;
+        const float2 a = dev::unpack2<T>(w[e >> 1]), b = dev::unpack2<T>(w2[e >> 1]);
+        const float pj = e & 1 ? a.y + b.y : a.x + b.x;
         const float o0 = fresh ? 0.f : __uint_as_float(u[e]);
         u[e] = __float_as_uint(pj == 0.f ? o0 : o0 + pj * v);
       }
       tmem_st8(oc + j, u);
+      if (L::SPLIT && fresh) {
+        const uint32_t none[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+        tmem_st8(oc + 32 + j, none);
+      }
     }
     tcg::wait_st();
     fresh = false;
@@ -325,9 +339,18 @@ __device__ __forceinline__ void write_rows(const TreeArgs& a, const Lane& x, con
     uint32_t u[8], v[8];
     tmem_ld8(oa + j0, u);
     tmem_ld8(oa + 64 + j0, v);
+    uint32_t u2[8], v2[8];
+    if constexpr (L::SPLIT) {
+      tmem_ld8(oa + 32 + j0, u2);
+      tmem_ld8(oa + 96 + j0, v2);
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float w0 = wts[j0 + e], w1 = wts[64 + j0 + e];
+      if constexpr (L::SPLIT) {
+        u[e] = __float_as_uint(__uint_as_float(u[e]) + __uint_as_float(u2[e]));
+        v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(v2[e]));
+      }
       float o = w0 == 0.f ? 0.f : __uint_as_float(u[e]) * w0;
       if (w1 != 0.f) o = fmaf(__uint_as_float(v[e]), w1, o);
       const int at = place[j0 + e];
@@ -399,7 +422,7 @@ __global__ void __launch_bounds__(Lay<KT, D, false>::THREADS, 1)
       ok = !bar_or(bar, 128, !ok);
       if (!ok || !__all_sync(FULL, k.live)) break;
       const Piece& p = k.p;
-      const int words = p.rows > 32 ? 2 : 1, pp = k.i & 1, shift = p.L - p.n;
+      const int words = !L::SPLIT && p.rows > 32 ? 2 : 1, pp = k.i & 1, shift = p.L - p.n;
       const uint32_t oc = x.tl + kColO + 128 * pp + 64 * t;
       const bool exists = r < p.rows && (r & ((1 << a.gl) - 1)) < a.G;  // row r (r < 64)
       bool seen = !exists, unset = true;  // row r has a reference; some row may have none
@@ -473,7 +496,9 @@ __global__ void __launch_bounds__(Lay<KT, D, false>::THREADS, 1)
             for (int j = 0; j < 8; ++j) {
               if constexpr (!Q8 || PASS == 0) top = max3(top, e[j].x, e[j].y);
               if constexpr (!Q8) {
-                pk[8 * Q + j] = dev::pack2<VT>(dev::ex2(e[j].x), dev::ex2(e[j].y));
+                const float2 w = make_float2(dev::ex2(e[j].x), dev::ex2(e[j].y));
+                pk[8 * Q + j] = dev::pack2<VT>(w.x, w.y);
+                if constexpr (L::SPLIT) pk[(8 * Q + j + 16) & 31] = low_half(w, pk[8 * Q + j]);
               } else if constexpr (PASS == 1) {
                 const float2 w = make_float2(dev::ex2(e[j].x), dev::ex2(e[j].y));
                 l[8 * Q + j] = add2(l[8 * Q + j], w);
@@ -504,7 +529,10 @@ __global__ void __launch_bounds__(Lay<KT, D, false>::THREADS, 1)
         if (lane == 0) mbar_arrive(sy.sfree(t));  // the scores are read
         if constexpr (!Q8) {  // l sums the rounded weights
 #pragma unroll
-          for (int j = 0; j < 16; ++j) add16x2<VT>(l[j], pk[j]);
+          for (int j = 0; j < 16; ++j) {
+            add16x2<VT>(l[j], pk[j]);
+            if constexpr (L::SPLIT) add16x2<VT>(l[j], pk[16 + j]);
+          }
           if (words == 2) {
 #pragma unroll
             for (int j = 16; j < 32; ++j) add16x2<VT>(l[j], pk[j]);
@@ -515,7 +543,7 @@ __global__ void __launch_bounds__(Lay<KT, D, false>::THREADS, 1)
         for (int j = 0; j < 4; ++j)
           *reinterpret_cast<uint4*>(prow + ((j ^ (r & 7)) << 4)) =
               make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
-        if (words == 2) {
+        if (L::SPLIT || words == 2) {
 #pragma unroll
           for (int j = 4; j < 8; ++j)
             *reinterpret_cast<uint4*>(prow + ((j ^ (r & 7)) << 4)) =

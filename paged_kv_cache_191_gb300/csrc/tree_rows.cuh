@@ -1,7 +1,8 @@
 // The tree-attention kernel with a thread per row: items of up to 256 rows.
 //
 // S = Q K^T (M = 128 rows, N = the chunk's keys) and O += P V, P in tensor memory
-// in the place of the scores it came from.  Two tiles of 128 rows take turns,
+// in the place of the scores it came from (over bf16 caches the weights' low halves
+// in columns 64 .., and another product with V).  Two tiles of 128 rows take turns,
 // one in its products while the other is in its softmax: an item of up to 128
 // rows gives each tile every other chunk (own accumulator, own references,
 // joined at the item's end), a larger one gives each tile half of its rows and
@@ -110,6 +111,10 @@ __device__ __forceinline__ void multiply_rows(const TreeArgs& a, uint8_t* gb, Sy
 #pragma unroll
     for (int kk = 0; kk < kBlk; ++kk)
       mma_ts(od, pd + 8 * kk, vd + ((kk * 2 * L::GRP) >> 4), id_o, kk > 0 ? 1u : acc);
+    if constexpr (L::SPLIT) {
+#pragma unroll
+      for (int kk = 0; kk < kBlk; ++kk) mma_ts(od, pd + 64 + 8 * kk, vd + ((kk * 2 * L::GRP) >> 4), id_o, 1u);
+    }
     commit(sy.pdone(tile));
     if (last) commit(sy.empty(slot));
   };
@@ -280,13 +285,17 @@ __device__ __forceinline__ void guard_rows(const Row& x, uint8_t* gb, uint8_t* v
 #pragma unroll 1
   for (int key = 0; key < kKeys; ++key) {
     if (!((bw[key >> 5] >> (key & 31)) & 1u)) continue;
-    uint32_t p;
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
-                 : "=r"(p)
-                 : "r"(x.s + (key >> 1))
-                 : "memory");
-    const float2 pp = dev::unpack2<T>(p);
-    const float w = key & 1 ? pp.y : pp.x;
+    auto weight = [&](uint32_t column) {
+      uint32_t p;
+      asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
+                   : "=r"(p)
+                   : "r"(x.s + column)
+                   : "memory");
+      const float2 pp = dev::unpack2<T>(p);
+      return key & 1 ? pp.y : pp.x;
+    };
+    float w = weight(key >> 1);
+    if constexpr (L::SPLIT) w += weight(64 + (key >> 1));
     const uint8_t* vk = vslot + (key >> 3) * L::GRP + (key & 7) * 128;
 #pragma unroll 1
     for (int d = 0; d < L::D; d += 8) {
@@ -615,18 +624,28 @@ __global__ void __launch_bounds__(Lay<KT, D, true>::THREADS, 1)
           float2 ls = make_float2(0.f, 0.f), ls1 = ls;
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
-            uint32_t pk[16];
+            uint32_t pk[16], low[L::SPLIT ? 16 : 1];  // (16 pairs at a time: 8 took 126 us for 120, 32 took 130)
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
               const int i = 32 * h + 2 * j;
               const float2 e0 = fma2(make_float2(f[i], f[i + 1]), make_float2(sl2, sl2), make_float2(-ref, -ref));
               const float2 e1 = fma2(make_float2(f[i + 2], f[i + 3]), make_float2(sl2, sl2), make_float2(-ref, -ref));
-              pk[j] = dev::pack2<VT>(dev::ex2(e0.x), dev::ex2(e0.y));
-              pk[j + 1] = dev::pack2<VT>(dev::ex2(e1.x), dev::ex2(e1.y));
-              add16x2<VT>(ls, pk[j]);  // l sums the rounded weights
-              add16x2<VT>(ls1, pk[j + 1]);
+              const float2 w0 = make_float2(dev::ex2(e0.x), dev::ex2(e0.y));
+              const float2 w1 = make_float2(dev::ex2(e1.x), dev::ex2(e1.y));
+              pk[j] = dev::pack2<VT>(w0.x, w0.y);
+              pk[j + 1] = dev::pack2<VT>(w1.x, w1.y);
+              if constexpr (L::SPLIT) {
+                low[j] = low_half(w0, pk[j]);
+                low[j + 1] = low_half(w1, pk[j + 1]);
+                ls = add2(ls, w0);
+                ls1 = add2(ls1, w1);
+              } else {
+                add16x2<VT>(ls, pk[j]);  // l sums the rounded weights
+                add16x2<VT>(ls1, pk[j + 1]);
+              }
             }
             tmem_st16(x.s + 16 * h, pk);
+            if constexpr (L::SPLIT) tmem_st16(x.s + 64 + 16 * h, low);
           }
           l += (ls.x + ls.y) + (ls1.x + ls1.y);
           wait_st();

@@ -335,14 +335,15 @@ def check_weights(w, u):
     """Float32 outputs, weights of half a step u: the scores in octaves are below 64,
     off by 2^-24 of that (a weight by 2^-18), exponentials by 2^-22; a part's reference
     and the merge as much again: 2^-17.  f16 products are at least 2^7 at a row's
-    largest (as above)."""
+    largest (as above).  The product's float32 sum goes on 16 keys at a time, 2^-23 each."""
     want, spread, _ = oracle(w)
-    tol = spread * (u + 2.0 ** -17)
+    steps = np.repeat(-(-w.lens // 16), w.sizes)[:, None, None]
+    tol = spread * (u + 2.0 ** -17 + steps * 2.0 ** -23)
     if w.k_scale is not None:
         most = O.tree_largest(np_exact(w.q), w.q_start, w.mask, np_exact(w.k), w.tables, w.lens, w.scale,
                               w.k_scale.numpy(), w.v_scale.numpy())[..., None]
         tol = tol + np.repeat(w.lens, w.sizes)[:, None, None] * 2.0 ** -32 * {"fp8": 448, "int8": 127}[w.kind] * most
-    worst = (np.abs(run(w).double().numpy() - want) / tol).max()
+    worst = (np.abs(run(w).double().numpy() - want) / (tol + 1e-30)).max()  # (rows that see nothing are 0)
     assert worst <= 1.0, f"{worst:.2f} of the tolerance"
 
 
@@ -354,6 +355,32 @@ def test_weights_over_one_byte_caches_have_11_bits(kind, G, sizes):
         w = TreeBatch(38, 2 * G, 2, 128, kind, sizes, [700, 40, 3], q_dtype=qdt)
         exact_scores(w)
         check_weights(w, 2.0 ** -11)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,sizes", [(1, [9, 0, 3]), (2, [9, 16, 3]), (3, [12, 4, 1]), (8, [12, 16, 3]), (16, [30, 16, 3])])
+@pytest.mark.parametrize("masks", ["tree", "any"])
+def test_weights_over_bf16_caches_have_16_bits(D, G, sizes, masks):
+    """Their sum of two bf16 is off by a half step of a half step, 2^-16; so is the
+    sum that divides, where it is of the rounded weights."""
+    w = TreeBatch(39, 2 * G, 2, D, "bf16", sizes, [700, 40, 3], masks=masks)
+    exact_scores(w)
+    check_weights(w, 2.0 ** -15)
+
+
+@pytest.mark.parametrize("G", [1, 2, 8])
+def test_a_bf16_chain_is_as_exact_as_chunked_prefill(G):
+    """The same causal rows through both calls, float32 outputs."""
+    w = TreeBatch(40, 2 * G, 2, 128, "bf16", [16, 9], [900, 70])
+    exact_scores(w)
+    for b, n in enumerate(w.sizes):
+        for i in range(n):
+            w.mask[w.q_start[b] + i] = (1 << (i + 1)) - 1
+    a, _ = args_of(w)
+    want, spread, _ = oracle(w)
+    chunks = ops.chunked_prefill(a[0], a[1], a[3], a[4], a[5], a[6], a[7], a[8], a[9], out_dtype=torch.float32)
+    for out in (chunks.cpu(), run(w)):
+        assert (np.abs(out.double().numpy() - want) <= spread * 2.0 ** -14).all()
 
 
 def test_a_chain_is_chunked_prefill():
