@@ -576,12 +576,12 @@ size_t pa_tree_attention_workspace_size(int32_t num_q_heads, int32_t max_q_len, 
  * Work: one persistent CTA per SM streams an equal share of the batch's
  * 128-key chunks (planned on the device from context_lens) and multiplies on
  * tcgen05 tensor cores.  While max_q_len * G (G up to a power of two) is at
- * most 64 (32 over a BF16 cache) a thread owns a key of a chunk, above that a
+ * most 64 (32 with BF16 queries) a thread owns a key of a chunk, above that a
  * (node, head) row; an item, the rows that share a stream of K/V, is that many,
  * then up to 256 rows (128 over 1-byte caches).  Items that span CTAs are merged
  * by a second kernel.
- * Softmax weights have 11 bits over F16 and 1-byte caches, 16 over BF16 ones
- * (two BF16 halves); everything else is float32.
+ * Softmax weights have 11 bits with F16 queries, 16 with BF16 ones (two BF16
+ * halves); everything else is float32.
  */
 pa_status pa_tree_attention(const void* q, int32_t q_dtype, const int32_t* q_start, int32_t num_tokens,
                             int32_t max_q_len, const int64_t* tree_mask, int32_t mask_words,

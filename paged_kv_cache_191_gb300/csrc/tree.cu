@@ -33,19 +33,19 @@
 //   warps 12-15  1-byte caches only: convert landed codes to the 16-bit layouts
 //                the MMAs read.
 // Two kernels differ in what a softmax thread owns.  Up to 64 rows of a kv head, 32
-// over bf16 caches (tree_keys.cuh): a key, with transposed products, so that work is
+// with bf16 queries (tree_keys.cuh): a key, with transposed products, so that work is
 // in proportion to the rows.  More (tree_rows.cuh): a row, with products of 128 rows.
 // At 64 rows (16 sequences of 32 kv heads, contexts of 2048 .. 4096 tokens) the
 // first takes 143 us, 86 % of the copy rate, and the second would compute on twice
 // the rows; at 128 rows (64 sequences of 8 kv heads, mean context 2064) the first,
 // with two tiles of 64 rows, took 163 us where the second takes 109.
 //
-// P is rounded to f16 where V is f16, which the product shares, and normalised by
-// the sum of the rounded weights (1-byte caches: V is converted to f16, weight x V
-// scale is rounded, and the sum is of the weights before it), so a row that rests on
-// one key returns that key's value.  Over bf16 caches, whose type has 8 bits, a weight
-// is carried as two bf16 halves (off by 2^-17, as in the other attention calls) and V
-// multiplied by both.  With one, 64 sequences of 8 kv heads, 128 rows, took 110 us
+// P is rounded to V's 16-bit type (the queries', which 1-byte codes are converted
+// to), which the product shares, and normalised by the sum of the rounded weights
+// (1-byte caches: weight x V scale is rounded, and the sum is of the weights before
+// it), so a row that rests on one key returns that key's value.  A bf16 weight would
+// have 8 bits: it is carried as two bf16 halves (off by 2^-17, as in the other
+// attention calls) and V multiplied by both.  With one, 64 sequences of 8 kv heads, 128 rows, took 110 us
 // where this takes 120, 512 rows 321 for 428; its errors were 2^8 times the half's, 1.3
 // times those of an exact softmax in bf16 outputs.  References, l and O are float32.
 //
@@ -186,7 +186,7 @@ pa_status make_q_map(CUtensorMap* m, const void* q, int D, int Hq, int T, int gp
 
 template <typename KT, typename T, int D, bool ROWS>
 pa_status launch_t(const TreeLaunch& l, CUtensorMapDataType dt, cudaStream_t stream) {
-  using L = Lay<KT, D, ROWS>;
+  using L = Lay<KT, T, D, ROWS>;
   const auto kernel = [] {
     if constexpr (ROWS)
       return tree_rows<KT, T, D>;
@@ -270,11 +270,11 @@ pa_status launch_t(const TreeLaunch& l, CUtensorMapDataType dt, cudaStream_t str
   return PA_OK;
 }
 
-// A thread per key while one kv head's rows fit its items (64, over bf16 caches
+// A thread per key while one kv head's rows fit its items (64, with bf16 weights
 // 32), else a thread per row (products and exponentials are then in 128s of rows).
 template <typename KT, typename T, int D>
 pa_status launch_d(const TreeLaunch& l, CUtensorMapDataType dt, cudaStream_t stream) {
-  return l.rows > Lay<KT, D, false>::ITEM ? launch_t<KT, T, D, true>(l, dt, stream) : launch_t<KT, T, D, false>(l, dt, stream);
+  return l.rows > Lay<KT, T, D, false>::ITEM ? launch_t<KT, T, D, true>(l, dt, stream) : launch_t<KT, T, D, false>(l, dt, stream);
 }
 
 }  // namespace

@@ -83,16 +83,13 @@ struct __align__(16) Piece {
 
 // ---- shared memory -----------------------------------------------------------
 // ROWS: the kernel with a thread per row (items of up to 256 rows), else the one
-// with a thread per key (up to 64; over bf16 caches 32, whose low halves take the
+// with a thread per key (up to 64; with bf16 weights 32, whose low halves take the
 // other 32 columns).
-template <typename KT, int D_, bool ROWS_>
+template <typename KT, typename T, int D_, bool ROWS_>
 struct Lay {
   static constexpr bool Q8 = sizeof(KT) == 1, ROWS = ROWS_;
-  // V and its weights.  1-byte caches: f16 whatever the queries are, whose 11 bits
-  // bf16 queries would otherwise cut to 8.
-  using VT = std::conditional_t<Q8, __half, KT>;
-  // bf16 caches: a weight is the sum of two bf16, which hold 16 of its bits.
-  static constexpr bool SPLIT = std::is_same<VT, __nv_bfloat16>::value;
+  // bf16 weights are the sum of two, which hold 16 bits.
+  static constexpr bool SPLIT = std::is_same<T, __nv_bfloat16>::value;
   static constexpr int D = D_;
   static constexpr int SPANS = D / 64;               // 128-byte spans of a 16-bit row
   // Q of pieces, places of HQ rows [span][HQ][128 B].  Two: a piece of up to HQ
@@ -123,9 +120,9 @@ struct Lay {
   // log2 of how far below its row's maximum a reference is set, and of how far that
   // maximum may outgrow it.  1-byte caches: the maximum is of weight x V scale, which
   // is what the product takes in 16 bits, so whatever the scales are a row's largest is
-  // 2^7 .. 2^15: finite in f16, and as far above what f16 drops as it goes.  (The
+  // 2^7 .. 2^15 in f16: finite, and as far above what f16 drops as it goes.  (The
   // weight itself is float32: 2^95 with scales of 2^-80, which smaller ones count as here.)
-  static constexpr float LIFT = Q8 ? 7.f : 0.f, MOVE = Q8 ? 15.f : 8.f;
+  static constexpr float LIFT = Q8 && !SPLIT ? 7.f : 0.f, MOVE = Q8 && !SPLIT ? 15.f : 8.f;
   static constexpr int HIGH = Q8 ? 176 : 200, LOW = Q8 ? 80 : 104;  // registers: softmax threads', the others'
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
@@ -680,8 +677,7 @@ struct Cursor {
 };
 
 // The converter warpgroup (1-byte caches): codes of a landed chunk -> 16-bit
-// values in its slot of the ring, in the layout the MMAs read: K's of the queries'
-// type, V's f16, the type of their weights.  (Both hold every code exactly.)
+// values in its slot of the ring, in the layout the MMAs read.
 template <typename KT, typename T, typename L>
 __device__ __forceinline__ void convert(uint8_t* gb, Sync<L> sy) {
   constexpr int NS = L::NS, NL = L::NL;
@@ -711,17 +707,10 @@ __device__ __forceinline__ void convert(uint8_t* gb, Sync<L> sy) {
       for (int j = 0; j < 8; ++j) {
         const int x = i0 + 128 * j, key = x >> 3, c16 = x & 7, cc = 2 * (c16 & 3);
         uint32_t f[8];
-        if (std::is_same<T, __half>::value || (k & 1)) {
-          dev::code8x4_to<KT, __half>(w[j].x, f[0], f[1]);
-          dev::code8x4_to<KT, __half>(w[j].y, f[2], f[3]);
-          dev::code8x4_to<KT, __half>(w[j].z, f[4], f[5]);
-          dev::code8x4_to<KT, __half>(w[j].w, f[6], f[7]);
-        } else {
-          dev::code8x4_to<KT, T>(w[j].x, f[0], f[1]);
-          dev::code8x4_to<KT, T>(w[j].y, f[2], f[3]);
-          dev::code8x4_to<KT, T>(w[j].z, f[4], f[5]);
-          dev::code8x4_to<KT, T>(w[j].w, f[6], f[7]);
-        }
+        dev::code8x4_to<KT, T>(w[j].x, f[0], f[1]);
+        dev::code8x4_to<KT, T>(w[j].y, f[2], f[3]);
+        dev::code8x4_to<KT, T>(w[j].z, f[4], f[5]);
+        dev::code8x4_to<KT, T>(w[j].w, f[6], f[7]);
         uint8_t* row = gb + L::RING + to * L::SLOT + (key >> 3) * L::GRP + (c16 >> 2) * 1024 + (key & 7) * 128;
         // (the two spans' threads store their halves in opposite order: no bank conflict)
         const bool up = c16 & 4;

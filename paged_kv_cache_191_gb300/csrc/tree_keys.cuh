@@ -1,5 +1,5 @@
-// The tree-attention kernel with a thread per key: items of up to 64 rows (32 over
-// bf16 caches: the weights' low halves are columns 32 .. of P^T, and O^T's columns 32
+// The tree-attention kernel with a thread per key: items of up to 64 rows (32 with
+// bf16 weights: their low halves are columns 32 .. of P^T, and O^T's columns 32
 // .. their product, added at the end).
 //
 // The products are transposed: S^T = K Q^T (M = the chunk's 128 keys, N = rows)
@@ -70,7 +70,7 @@ __device__ __forceinline__ void multiply(const TreeArgs& a, uint8_t* gb, Sync<L>
         fence_after();
         // A = V^T (M-major), B = P^T (N-major)
         const int n = ((o.p.rows + 15) & ~15) + (L::SPLIT ? 32 : 0);
-        const uint32_t id = idesc<typename L::VT>(n, true) | (1u << 15);
+        const uint32_t id = idesc<T>(n, true) | (1u << 15);
         const uint64_t vd = sdesc(sy.base + L::RING + (i % NS) * L::SLOT, D == 128 ? 1024 : 0, L::GRP);
         const uint64_t pd = sdesc(sy.base + L::P0 + t * 16384, 16384, 1024);
         const uint32_t od = tmem + kColO + 128 * (o.i & 1) + 64 * t;
@@ -365,12 +365,11 @@ __device__ __forceinline__ void write_rows(const TreeArgs& a, const Lane& x, con
 }
 
 template <typename KT, typename T, int D>
-__global__ void __launch_bounds__(Lay<KT, D, false>::THREADS, 1)
+__global__ void __launch_bounds__(Lay<KT, T, D, false>::THREADS, 1)
     tree_keys(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
               const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ TreeArgs a) {
   using namespace tcg;
-  using L = Lay<KT, D, false>;
-  using VT = typename L::VT;
+  using L = Lay<KT, T, D, false>;
   constexpr bool Q8 = L::Q8;
   constexpr int NS = L::NS;
   extern __shared__ __align__(1024) uint8_t gb[];
@@ -472,6 +471,10 @@ __global__ void __launch_bounds__(Lay<KT, D, false>::THREADS, 1)
             }
           }
           float top = -INFINITY;
+          auto put = [&](int i, float2 w) {
+            pk[i] = dev::pack2<T>(w.x, w.y);
+            if constexpr (L::SPLIT) pk[(i + 16) & 31] = low_half(w, pk[i]);
+          };
           // 16 rows.  16-bit caches: exponents, their maximum, weights in one pass.
           // 1-byte caches: the maximum first, so that l can sum the weights as they
           // are and only their product with V's scale, the key's, is rounded.
@@ -496,15 +499,13 @@ __global__ void __launch_bounds__(Lay<KT, D, false>::THREADS, 1)
             for (int j = 0; j < 8; ++j) {
               if constexpr (!Q8 || PASS == 0) top = max3(top, e[j].x, e[j].y);
               if constexpr (!Q8) {
-                const float2 w = make_float2(dev::ex2(e[j].x), dev::ex2(e[j].y));
-                pk[8 * Q + j] = dev::pack2<VT>(w.x, w.y);
-                if constexpr (L::SPLIT) pk[(8 * Q + j + 16) & 31] = low_half(w, pk[8 * Q + j]);
+                put(8 * Q + j, make_float2(dev::ex2(e[j].x), dev::ex2(e[j].y)));
               } else if constexpr (PASS == 1) {
                 const float2 w = make_float2(dev::ex2(e[j].x), dev::ex2(e[j].y));
                 l[8 * Q + j] = add2(l[8 * Q + j], w);
                 const float2 y = mul2(w, make_float2(vsc, vsc));
                 // (a weight of 0 must not meet a NaN scale)
-                pk[8 * Q + j] = dev::pack2<VT>(w.x == 0.f ? 0.f : y.x, w.y == 0.f ? 0.f : y.y);
+                put(8 * Q + j, make_float2(w.x == 0.f ? 0.f : y.x, w.y == 0.f ? 0.f : y.y));
               }
             }
           };
@@ -530,12 +531,12 @@ __global__ void __launch_bounds__(Lay<KT, D, false>::THREADS, 1)
         if constexpr (!Q8) {  // l sums the rounded weights
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            add16x2<VT>(l[j], pk[j]);
-            if constexpr (L::SPLIT) add16x2<VT>(l[j], pk[16 + j]);
+            add16x2<T>(l[j], pk[j]);
+            if constexpr (L::SPLIT) add16x2<T>(l[j], pk[16 + j]);
           }
           if (words == 2) {
 #pragma unroll
-            for (int j = 16; j < 32; ++j) add16x2<VT>(l[j], pk[j]);
+            for (int j = 16; j < 32; ++j) add16x2<T>(l[j], pk[j]);
           }
         }
         if (ok && n > 0) ok = wait_warp(sy.pdone(t), (n - 1) & 1);  // P^T's buffer is free
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__(Lay<KT, D, false>::THREADS, 1)
           const int vi = k.it0 + 2 * c + 1, vs = vi % NS;
           if (ok) ok = __all_sync(FULL, wait_issued(sy.issued(), vi)) && wait_warp(sy.ready(vs), (vi / NS) & 1);
           fence_after();
-          guard<VT, L>(x, gb, gb + L::RING + vs * L::SLOT, pbuf, (p.c0 + c) & 1, jn, p.n, words, oc,
+          guard<T, L>(x, gb, gb + L::RING + vs * L::SLOT, pbuf, (p.c0 + c) & 1, jn, p.n, words, oc,
                       c == c_first);
         }
         dev::fence_proxy_async_smem();

@@ -1,8 +1,8 @@
 // The tree-attention kernel with a thread per row: items of up to 256 rows.
 //
 // S = Q K^T (M = 128 rows, N = the chunk's keys) and O += P V, P in tensor memory
-// in the place of the scores it came from (over bf16 caches the weights' low halves
-// in columns 64 .., and another product with V).  Two tiles of 128 rows take turns,
+// in the place of the scores it came from (bf16 weights' low halves in columns 64 ..,
+// and another product with V).  Two tiles of 128 rows take turns,
 // one in its products while the other is in its softmax: an item of up to 128
 // rows gives each tile every other chunk (own accumulator, own references,
 // joined at the item's end), a larger one gives each tile half of its rows and
@@ -84,7 +84,7 @@ __device__ __forceinline__ void multiply_rows(const TreeArgs& a, uint8_t* gb, Sy
   int pieces_over = 0;         // pieces that both warpgroups are done with
   uint64_t t0 = 0;
   auto test = [&](uint32_t bar, int parity) { return __all_sync(FULL, dev::mbar_test(bar, parity & 1)) != 0; };
-  const uint32_t id_s = idesc<T>(kKeys, false) | (a.negate << 13), id_o = idesc<typename L::VT>(D, true);
+  const uint32_t id_s = idesc<T>(kKeys, false) | (a.negate << 13), id_o = idesc<T>(D, true);
   // The ring items of the next scores and the next O: slot, and parity of its fill.
   int ks = 0, kf = 0, vs = 1, vf = 0;
   auto advance = [](int& slot, int& fill) {
@@ -395,7 +395,7 @@ __device__ __forceinline__ void write_row(const TreeArgs& a, const Row& x, const
 // K's scales go on the scores and V's, once l has summed the weights, on them;
 // only that product is rounded.  References go by its maximum: it is taken against
 // them as they are, and again where it turns out to have outgrown one.
-template <typename L>
+template <typename T, typename L>
 __device__ __forceinline__ void soften(const TreeArgs& a, const Row& x, const uint8_t* gb, const Piece& p, int piece,
                                        Pair& ra, Pair& rb, const uint8_t* scales, bool masked, int j0, int tile_row,
                                        float sl2) {
@@ -406,7 +406,7 @@ __device__ __forceinline__ void soften(const TreeArgs& a, const Row& x, const ui
   for (int h = 0; h < 2; ++h) {
     const uint32_t sc = x.s + (static_cast<uint32_t>(16 * h) << 16);
     float2 ls0, ls1;
-    uint32_t pk[32];
+    uint32_t pk[32], low[L::SPLIT ? 32 : 1];
     bool settle = __any_sync(FULL, (ra.has0 && !ra.seen0) || (ra.has1 && !ra.seen1));
 #pragma unroll 1
     for (;; settle = true) {
@@ -481,13 +481,15 @@ __device__ __forceinline__ void soften(const TreeArgs& a, const Row& x, const ui
           ls0 = add2(ls0, w);
           t0 = max3(t0, fabsf(y.x), fabsf(y.y));
         }
-        pk[i] = dev::pack2<typename L::VT>(y.x, y.y);
+        pk[i] = dev::pack2<T>(y.x, y.y);
+        if constexpr (L::SPLIT) low[i] = low_half(y, pk[i]);
       }
       if (settle || !__any_sync(FULL, (ra.has0 && t0 > kMost) || (ra.has1 && t1 > kMost))) break;
     }
     ra.l0 += ls0.x + ls0.y;
     ra.l1 += ls1.x + ls1.y;
     tmem_st_frag(sc, pk);
+    if constexpr (L::SPLIT) tmem_st_frag(sc + 64, low);
     const Pair other = rb;  // the other 16 rows' turn (and back)
     rb = ra;
     ra = other;
@@ -496,12 +498,11 @@ __device__ __forceinline__ void soften(const TreeArgs& a, const Row& x, const ui
 }
 
 template <typename KT, typename T, int D>
-__global__ void __launch_bounds__(Lay<KT, D, true>::THREADS, 1)
+__global__ void __launch_bounds__(Lay<KT, T, D, true>::THREADS, 1)
     tree_rows(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
               const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ TreeArgs a) {
   using namespace tcg;
-  using L = Lay<KT, D, true>;
-  using VT = typename L::VT;
+  using L = Lay<KT, T, D, true>;
   constexpr bool Q8 = L::Q8;
   constexpr int NS = L::NS;
   extern __shared__ __align__(1024) uint8_t gb[];
@@ -592,7 +593,7 @@ __global__ void __launch_bounds__(Lay<KT, D, true>::THREADS, 1)
             named_bar(2 + t, 128);
           }
           if (x.live)
-            soften<L>(a, x, gb, p, k.i, ra, rb, gb + L::SCALES + (((k.it0 >> 1) + c) & 7) * 1024, masked,
+            soften<T, L>(a, x, gb, p, k.i, ra, rb, gb + L::SCALES + (((k.it0 >> 1) + c) & 7) * 1024, masked,
                          key0 - shift, row - x.r, sl2);
         } else if (x.live) {
           float f[kKeys];
@@ -632,16 +633,16 @@ __global__ void __launch_bounds__(Lay<KT, D, true>::THREADS, 1)
               const float2 e1 = fma2(make_float2(f[i + 2], f[i + 3]), make_float2(sl2, sl2), make_float2(-ref, -ref));
               const float2 w0 = make_float2(dev::ex2(e0.x), dev::ex2(e0.y));
               const float2 w1 = make_float2(dev::ex2(e1.x), dev::ex2(e1.y));
-              pk[j] = dev::pack2<VT>(w0.x, w0.y);
-              pk[j + 1] = dev::pack2<VT>(w1.x, w1.y);
+              pk[j] = dev::pack2<T>(w0.x, w0.y);
+              pk[j + 1] = dev::pack2<T>(w1.x, w1.y);
               if constexpr (L::SPLIT) {
                 low[j] = low_half(w0, pk[j]);
                 low[j + 1] = low_half(w1, pk[j + 1]);
                 ls = add2(ls, w0);
                 ls1 = add2(ls1, w1);
               } else {
-                add16x2<VT>(ls, pk[j]);  // l sums the rounded weights
-                add16x2<VT>(ls1, pk[j + 1]);
+                add16x2<T>(ls, pk[j]);  // l sums the rounded weights
+                add16x2<T>(ls1, pk[j + 1]);
               }
             }
             tmem_st16(x.s + 16 * h, pk);
@@ -653,7 +654,7 @@ __global__ void __launch_bounds__(Lay<KT, D, true>::THREADS, 1)
         if (masked) {
           const int vi = k.it0 + 2 * c + 1, vs = vi % NS;
           if (ok) ok = __all_sync(FULL, wait_issued(sy.issued(), vi)) && wait_warp(sy.ready(vs), (vi / NS) & 1);
-          guard_rows<VT, L>(x, gb, gb + L::RING + vs * L::SLOT, (p.c0 + c) & 1, k.both, key0 + r - shift, p.n,
+          guard_rows<T, L>(x, gb, gb + L::RING + vs * L::SLOT, (p.c0 + c) & 1, k.both, key0 + r - shift, p.n,
                            c == c_first);
         }
         fence_before();

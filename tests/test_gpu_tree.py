@@ -332,14 +332,14 @@ def exact_scores(w):
 
 
 def check_weights(w, u):
-    """Float32 outputs, weights of half a step u: the scores in octaves are below 64,
-    off by 2^-24 of that (a weight by 2^-18), exponentials by 2^-22; a part's reference
-    and the merge as much again: 2^-17.  f16 products are at least 2^7 at a row's
+    """Float32 outputs, weights of half a step u: the scores in octaves are below 64 (at
+    a scale of 0.25), off by 2^-24 of that (a weight by 2^-18), exponentials by 2^-22; a
+    part's reference and the merge as much again: 2^-17.  f16 products are at least 2^7 at a row's
     largest (as above).  The product's float32 sum goes on 16 keys at a time, 2^-23 each."""
     want, spread, _ = oracle(w)
     steps = np.repeat(-(-w.lens // 16), w.sizes)[:, None, None]
-    tol = spread * (u + 2.0 ** -17 + steps * 2.0 ** -23)
-    if w.k_scale is not None:
+    tol = spread * (u + 2.0 ** -17 * max(1.0, w.scale / 0.25) + steps * 2.0 ** -23)
+    if w.k_scale is not None and w.q.dtype == torch.float16:
         most = O.tree_largest(np_exact(w.q), w.q_start, w.mask, np_exact(w.k), w.tables, w.lens, w.scale,
                               w.k_scale.numpy(), w.v_scale.numpy())[..., None]
         tol = tol + np.repeat(w.lens, w.sizes)[:, None, None] * 2.0 ** -32 * {"fp8": 448, "int8": 127}[w.kind] * most
@@ -348,13 +348,15 @@ def check_weights(w, u):
 
 
 @pytest.mark.parametrize("kind", ["fp8", "int8"])
-@pytest.mark.parametrize("G,sizes", [(2, [9, 20, 3]), (8, [12, 16, 3])])
-def test_weights_over_one_byte_caches_have_11_bits(kind, G, sizes):
-    """With bf16 queries as with f16 ones."""
-    for qdt in (torch.float16, torch.bfloat16):
-        w = TreeBatch(38, 2 * G, 2, 128, kind, sizes, [700, 40, 3], q_dtype=qdt)
-        exact_scores(w)
-        check_weights(w, 2.0 ** -11)
+@pytest.mark.parametrize("qdt,u", [(torch.float16, 2.0 ** -11), (torch.bfloat16, 2.0 ** -16)])
+@pytest.mark.parametrize("G,sizes", [(1, [9, 0, 3]), (2, [9, 20, 3]), (8, [12, 16, 3])])
+@pytest.mark.parametrize("scale", [0.25, 4.0])
+def test_weights_over_one_byte_caches(kind, qdt, u, G, sizes, scale):
+    """11 bits with f16 queries; with bf16 ones 16 bits, down to the smallest weights."""
+    w = TreeBatch(38, 2 * G, 2, 128, kind, sizes, [700, 40, 3], q_dtype=qdt, masks="any")
+    exact_scores(w)
+    w.scale = scale
+    check_weights(w, u)
 
 
 @pytest.mark.parametrize("D", [64, 128])
