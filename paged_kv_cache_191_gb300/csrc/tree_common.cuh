@@ -118,11 +118,13 @@ struct Lay {
   static constexpr int BYTES = MASK + (WORDS ? 1024 : 0);
   static constexpr int THREADS = Q8 ? 512 : 384;
   // log2 of how far below its row's maximum a reference is set, and of how far that
-  // maximum may outgrow it.  1-byte caches: the maximum is of weight x V scale, which
-  // is what the product takes in 16 bits, so whatever the scales are a row's largest is
-  // 2^7 .. 2^15 in f16: finite, and as far above what f16 drops as it goes.  (The
-  // weight itself is float32: 2^95 with scales of 2^-80, which smaller ones count as here.)
-  static constexpr float LIFT = Q8 && !SPLIT ? 7.f : 0.f, MOVE = Q8 && !SPLIT ? 15.f : 8.f;
+  // maximum may outgrow it.  f16 weights: a row's largest is 2^7 .. 2^15, finite and as
+  // far above what f16 drops as it goes, so that one of 2^-21 of it has all its bits.
+  // bf16 drops nothing, and its values may be so large that a lift would overflow their
+  // sum.  (1-byte caches: the maximum is of weight x V scale, which is what is rounded.
+  // The weight itself is float32: 2^95 with scales of 2^-80, which smaller ones count as
+  // here.)
+  static constexpr float LIFT = SPLIT ? 0.f : 7.f, MOVE = SPLIT ? 8.f : 15.f;
   static constexpr int HIGH = Q8 ? 176 : 200, LOW = Q8 ? 80 : 104;  // registers: softmax threads', the others'
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };

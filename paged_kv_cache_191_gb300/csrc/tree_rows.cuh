@@ -614,12 +614,12 @@ __global__ void __launch_bounds__(Lay<KT, T, D, true>::THREADS, 1)
           const float top = max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * sl2;
           const bool move = x.exists && (seen ? top > ref + L::MOVE : top > -INFINITY);
           if (__any_sync(FULL, move && seen)) {  // O and l follow the reference
-            const float alpha = move && seen ? dev::ex2(ref - top) : 1.f;
+            const float alpha = move && seen ? dev::ex2(ref - (top - L::LIFT)) : 1.f;
             l *= alpha;
             rescale<L>(x, alpha);
           }
           if (move) {
-            ref = top;
+            ref = top - L::LIFT;
             seen = true;
           }
           float2 ls = make_float2(0.f, 0.f), ls1 = ls;

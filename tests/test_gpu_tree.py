@@ -385,6 +385,22 @@ def test_a_bf16_chain_is_as_exact_as_chunked_prefill(G):
         assert (np.abs(out.double().numpy() - want) <= spread * 2.0 ** -14).all()
 
 
+@pytest.mark.parametrize("G", [2, 16])
+def test_small_weights_beside_large_ones(G):
+    """In every 128 keys one with value 0; the others, of e^-16 of its weight, which f16
+    would round 6 % off, are the whole output."""
+    w = TreeBatch(42, 2 * G, 2, 128, "f16", [5], [3000])
+    one = torch.where(torch.arange(128) % 3 == 0, 1.0, -1.0).half()
+    i = torch.arange(128)
+    w.q[:], w.k[:] = one, one * torch.where(i < 64, 1.0, -1.0).half()
+    w.scale = 0.25
+    w.v = w.v.abs()
+    blk = torch.from_numpy(w.tables[0][2:-1:8].astype(np.int64))
+    w.k[blk, :, 5] = one * torch.where(i < 96, 1.0, -1.0).half()  # score 64 x 0.25, the others' 0
+    w.v[blk, :, 5] = 0
+    tight(w, 7)
+
+
 def test_a_chain_is_chunked_prefill():
     w = TreeBatch(26, 16, 4, 128, "bf16", [40, 3, 17], [900, 3, 64])
     for b, n in enumerate(w.sizes):
