@@ -63,7 +63,9 @@ __device__ __forceinline__ float2 rotation(int64_t pos, double inv_freq, float f
   turns -= floor(turns);
   const uint64_t frac = static_cast<uint64_t>(turns * 18446744073709551616.0);  // 2^64; saturates
   const int64_t ang = static_cast<int64_t>(static_cast<uint64_t>(pos) * frac);
-  const float half_turns = static_cast<float>(ang) * 0x1p-63f;  // [-1, 1]
+  // [-1, 1].  (An infinite or NaN frequency, whose turns are NaN, has no angle; a
+  // select in place of the product with 0 took 69 us for 65 in the 8192-token prompt.)
+  const float half_turns = fmaf(static_cast<float>(turns), 0.f, static_cast<float>(ang) * 0x1p-63f);
   float s, c;
   sincospif(half_turns, &s, &c);
   return make_float2(c * factor, s * factor);

@@ -586,6 +586,22 @@ def test_rope_far_and_negative_positions():
     assert (np.abs(got.cpu().double().numpy() - want) <= tol).all()
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_rope_frequency_that_is_no_number(bad):
+    """Its pair becomes NaN, the others stay."""
+    qkv, slots, pos, kc, vc, _ = rope_case(11, 9, 2, 1, 64, torch.float32, "f16", 64)
+    f, _ = ops.rope_frequencies(64, device=DEV)
+    call = lambda f: ops.rope_cache_write(qkv[:, :2], qkv[:, 2:3], qkv[:, 3:], dev(pos), f, dev(slots), kc, vc)  # noqa: E731
+    want = call(f)
+    f[5] = bad
+    got = call(f)
+    pair = torch.tensor([5, 37], device=DEV)
+    assert got[..., pair].isnan().all()
+    rest = torch.ones(64, dtype=torch.bool, device=DEV)
+    rest[pair] = False
+    assert torch.equal(got[..., rest], want[..., rest])
+
+
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_rope_in_place_in_a_packed_projection(interleaved):
     qkv, slots, pos, kc, vc, _ = rope_case(8, 40, 8, 2, 128, torch.bfloat16, "bf16", 64)
