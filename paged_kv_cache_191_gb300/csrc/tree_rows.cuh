@@ -399,7 +399,7 @@ template <typename T, typename L>
 __device__ __forceinline__ void soften(const TreeArgs& a, const Row& x, const uint8_t* gb, const Piece& p, int piece,
                                        Pair& ra, Pair& rb, const uint8_t* scales, bool masked, int j0, int tile_row,
                                        float sl2) {
-  constexpr float kMost = static_cast<float>(1 << static_cast<int>(L::MOVE));
+  constexpr float kMost = static_cast<float>(1 << static_cast<int>(L::MOVE)), kHuge = 0x1p101f;
   const int b2 = 2 * (x.lane & 3);
   const float2* ks = reinterpret_cast<const float2*>(scales + b2 * 4);
 #pragma unroll 1
@@ -484,7 +484,10 @@ __device__ __forceinline__ void soften(const TreeArgs& a, const Row& x, const ui
         pk[i] = dev::pack2<T>(y.x, y.y);
         if constexpr (L::SPLIT) low[i] = low_half(y, pk[i]);
       }
-      if (settle || !__any_sync(FULL, (ra.has0 && t0 > kMost) || (ra.has1 && t1 > kMost))) break;
+      // (Beside a V scale of 0 a weight may outgrow float32 unseen by its product.)
+      if (settle || !__any_sync(FULL, (ra.has0 && !(t0 <= kMost && ls0.x + ls0.y <= kHuge)) ||
+                                          (ra.has1 && !(t1 <= kMost && ls1.x + ls1.y <= kHuge))))
+        break;
     }
     ra.l0 += ls0.x + ls0.y;
     ra.l1 += ls1.x + ls1.y;

@@ -316,6 +316,31 @@ def test_value_scales_of_zero_and_below(G):
     assert (np.abs(run(w).double().numpy() - want) <= tol).all()
 
 
+@pytest.mark.parametrize("kind", ["fp8", "int8"])
+@pytest.mark.parametrize("qdt", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("G", [1, 16])
+def test_dominant_keys_with_value_scale_zero(kind, qdt, G):
+    """Two of 140 octaves above the scores before them, in later chunks of a CTA, and
+    one like them with a value: a third of it is the output."""
+    w = TreeBatch(43, 64 * G, 64, 128, kind, [5, 5, 5], [600, 600, 600], q_dtype=qdt)
+    exact_scores(w)
+    w.scale = 1.0
+    w.q[:] = 1
+    w.k[:] = torch.where(torch.arange(128) % 3 > 0, 0x38 if kind == "fp8" else 1,
+                         0xB8 if kind == "fp8" else -1).to(w.k.dtype)  # score 42
+    for b in range(3):
+        for at in (300, 430, 560):
+            blk = w.tables[b][at // 16]
+            w.k[blk, :, at % 16] = 0x38 if kind == "fp8" else 1  # score 128 x 1.1
+            w.k_scale[blk, at % 16] = 1.1
+            if at < 500:
+                w.v_scale[blk, at % 16] = 0
+    want, spread, _ = oracle(w)
+    assert np.abs(want).max() > 1e-2
+    got = run(w).double().numpy()
+    assert (np.abs(got - want) <= spread * (U[qdt] + 2.0 ** -15) + 1e-30).all()
+
+
 def exact_scores(w):
     """Queries and keys of -1, 0 and 1: products that float32 sums exactly, so that
     nothing but exponentials and the rounding of weights is off."""
