@@ -13,16 +13,19 @@
 // read, and their items are up to 128 rows (the stages of codes take the room).
 //
 // A tile's cycle is softmax (~1500 clocks a chunk), P V and the next scores (~600
-// each) and the waits between them (~1000); two tiles in turns keep the MMA warp
-// busy two thirds of it.  P V in two halves, the first issued before the second
+// each) and the waits between them (~1000); two tiles in turns keep the tensor pipe
+// busy 57 % of it (512 rows, by its counter).  P V in two halves, the first issued before the second
 // half's weights exist, was slower (357 us for 334 then), and so were two softmax
 // warpgroups per tile (345 us for 334, and 130 for 110): 104 registers a thread spill.
-//   64 sequences of 8 kv heads, 128 rows, bf16, mean context 2064: 109 us, 5.3
-//   TB/s, 79 % of the copy rate: HBM, and the launch and merge (10 us).
+//   64 sequences of 8 kv heads, 128 rows, bf16, mean context 2064: 120 us, 4.8
+//   TB/s, 71 % of the copy rate: HBM, the launch and merge (10 us), and V's slot of the
+//   ring, which both halves of the weights hold longer (6 us their softmax, 4 us their
+//   product).
 //   8 sequences of 8 kv heads, 512 rows, f16, contexts to 32768: 323 us, 1.27
-//   PFLOP/s, 66 % of the library product's burst rate: the cycle above, and the board's
-//   power limit (1360 W).
-//   8 sequences of 8 kv heads, 96 .. 128 rows, E4M3, contexts to 32768: 132 us,
+//   PFLOP/s, 66 % of the library product's burst rate: the cycle above.  Repeated for
+//   seconds 345 us, 61 % (68 % of the sustained rate): the board's power limit (1370 W,
+//   1.94 GHz of 2.07).
+//   8 sequences of 8 kv heads, 96 .. 128 rows, E4M3, contexts to 32768: 131 us,
 //   3.1 TB/s, 46 % of the copy rate: shared memory, ~83 % of whose cycles are taken
 //   by codes in (32 KB a chunk, read again), their conversion out (64 KB), the
 //   MMAs' operands (96 KB) and the scales (64 KB).
