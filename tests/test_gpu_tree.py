@@ -209,6 +209,30 @@ def test_infinities_reach_the_rows_that_see_them_only(kind, G):
     assert (np.abs(fin - np.delete(want, 5, axis=2)) <= tol).all()
 
 
+@pytest.mark.parametrize("kind,qdt", [("bf16", None), ("fp8", torch.float16), ("fp8", torch.bfloat16)])
+@pytest.mark.parametrize("G", [1, 3, 16])
+@pytest.mark.parametrize("before", [0, 20, 300])
+def test_nan_values_reach_the_rows_that_see_them_only(kind, qdt, G, before):
+    """Nodes with a NaN value in one dim, in the first chunk of a context and later:
+    that dim of the rows that see them is NaN, all the rest is right."""
+    w = TreeBatch(45, 2 * G, 2, 128, kind, [10, 6], [10 + before, 6 + before], q_dtype=qdt, masks="any")
+    bad = [(0, 3), (0, 7), (1, 1)]
+    at = [(w.tables[b][p // 16], p % 16) for b, j in bad for p in [w.lens[b] - w.sizes[b] + j]]
+    for blk, row in at:
+        w.v[blk, :, row, 77] = float("nan") if kind == "bf16" else 127  # (E4M3's NaN code)
+    out = run(w)
+    for blk, row in at:
+        w.v[blk, :, row, 77] = 0
+    hit = torch.tensor([any(b2 == b and O.visible(w.mask[w.q_start[b] + i], w.sizes[b])[j] for b2, j in bad)
+                        for b in range(2) for i in range(w.sizes[b])])
+    assert out[hit][..., 77].isnan().all() and 0 < hit.sum() < len(hit)
+    want, spread, score = oracle(w)
+    fix = hit[:, None] & (torch.arange(128) == 77)[None]
+    got = torch.where(fix[:, None], torch.from_numpy(want), out.double()).numpy()
+    tol = spread * (2 * U[w.q.dtype] + 2.0 ** -15 * score[..., None] + 2.0 ** -18) + 1e-6
+    assert (np.abs(got - want) <= tol).all()
+
+
 @pytest.mark.parametrize("scale", [-0.09, 0.0, 3.0])
 def test_any_scale(scale):
     w = TreeBatch(25, 8, 2, 128, "f16", [9, 70], [200, 300])
