@@ -551,7 +551,8 @@ size_t pa_tree_attention_workspace_size(int32_t num_q_heads, int32_t max_q_len, 
  *     out[q_start[b]+i][h] = sum_t softmax_t(scale * q[q_start[b]+i][h] . K_t) V_t
  * over the keys it sees, kv head g = h / G.  A row that sees no key is zero.
  * The nodes' K/V are in the cache already.  A node's K/V row reaches only the
- * rows that see it, whatever it holds (infinities and NaN included).
+ * rows that see it, whatever it holds (infinities and NaN included).  An infinite
+ * value of the context, which every row sees, makes its dim infinite or NaN.
  *
  * q, q_start, k_scale, v_scale, block_tables, context_lens, max_context_len,
  * out          as pa_chunked_prefill; up to 128 query heads per kv head.

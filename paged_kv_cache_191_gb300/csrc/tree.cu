@@ -46,9 +46,10 @@
 // (1-byte caches: weight x V scale is rounded, and the sum is of the weights before
 // it), so a row that rests on one key returns that key's value.  A bf16 weight would
 // have 8 bits: it is carried as two bf16 halves (off by 2^-17, as in the other
-// attention calls) and V multiplied by both.  With one, 64 sequences of 8 kv heads, 128 rows, took 110 us
-// where this takes 120, 512 rows 321 for 428; its errors were 2^8 times the half's, 1.3
-// times those of an exact softmax in bf16 outputs.  References, l and O are float32.
+// attention calls) and V multiplied by both.  One bf16 took 110 us for 120 (64
+// sequences of 8 kv heads, 128 rows) and 321 for 428 (512 rows), at errors of 2^-9 of a
+// row in float32 outputs, and in bf16 ones of 1.3 times those of an exact softmax.
+// References, l and O are float32.
 //
 // What bounds it: HBM while the rows per kv head stay below ~290 (4 D flops
 // per key and row against 4 D bytes per key at 16 bits), the exponentials and

@@ -12,10 +12,10 @@
 // accumulator and references, and the one that had the last chunk joins the two
 // while the other starts on the next piece.
 //
-// A row's reference is the maximum of the first chunk in which it sees a key,
-// kept in tensor memory beside the scores (read as cheaply as they are, where
-// shared memory, which feeds the MMAs, has no bandwidth to spare); it moves,
-// O^T and l with it, only when an exponent outgrows it by 2^8.
+// A row's reference goes by the maximum of the first chunk in which it sees a key
+// (Lay::LIFT), kept in tensor memory beside the scores (read as cheaply as they are,
+// where shared memory, which feeds the MMAs, has no bandwidth to spare); it moves,
+// O^T and l with it, only when a later maximum outgrows it by 8 octaves.
 //
 // Bound by HBM.  32 sequences of 32 kv heads, 9 .. 26 nodes, f16, mean context
 // 1044: 101 us, 5.5 TB/s, 82 % of the copy rate; what is missing is the launch,
