@@ -87,7 +87,7 @@ typedef enum {
 #define PA_DEVERR_TIMEOUT      0x8u  /* a bounded barrier wait gave up */
 #define PA_DEVERR_QUERY_RANGE  0x10u /* chunked prefill: q_start out of order or range */
 #define PA_DEVERR_GROUP        0x20u /* grouped decode: bad group bounds, or members' shared blocks differ */
-#define PA_DEVERR_TREE         0x40u /* drafted tree: a parent or a path element out of order or range */
+#define PA_DEVERR_TREE         0x40u /* drafted tree: a parent, path element or token out of order or range */
 
 /* Shape of a paged KV cache. */
 typedef struct {
@@ -635,6 +635,141 @@ pa_status pa_tree_commit(void* k_cache, void* v_cache, float* k_scale, float* v_
                          const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
                          const int32_t* q_start, const int32_t* path, int32_t max_path, const int32_t* path_len,
                          int32_t B, int32_t* new_lens, const pa_cache_desc* desc, void* stream);
+
+/*
+ * pa_draft_verify -- pa_tree_accept for a sampled step: drafted tokens are
+ * accepted or refused against the target's probabilities, from given random
+ * numbers, so that accepted tokens and the one drawn behind them are
+ * distributed as the target's own ([LLM-INF] 6.1).  Node 0 is accepted.
+ *
+ * With draft_probs (a chain: parents NULL, node i's child is node i + 1), x the
+ * child's token, p and q the target's and the draft's row of node i: the child
+ * is accepted when u q[x] < p[x]; else the next token is drawn from
+ * max(p - q, 0).  Without draft_probs (a chain, or a tree of any shape; tokens
+ * that were picked, not sampled): the children of an accepted node are tried
+ * from the lowest on, x is accepted when u (1 - S) < p[x], S the sum of the
+ * refused siblings' p (in 64 bits, in order; a token refused once has no
+ * probability left and is refused again); with all of them refused, the next
+ * token is drawn from p without their tokens.  After a node without children,
+ * or the max_path-th, it is drawn from p.
+ * Drawn from weights w: the first v with w[0] + .. + w[v] > u0 (w[0] + .. +
+ * w[V - 1]), u0 node 0's number.  Weights are summed as multiples of 2^-44 in 64
+ * bits: exactly, in any order.  Where nothing is left, w is p; where p has
+ * nothing either, next_token is -1, flagged PA_DEVERR_TREE.
+ *
+ * tokens        device int64 [num_tokens]: the nodes' tokens; q_start, parents,
+ *               max_path, path, path_len, next_token as pa_tree_accept.  A
+ *               token outside 0 .. vocab - 1 is refused and flagged
+ *               PA_DEVERR_TREE (node 0's is not read).
+ * target_probs  device float32, node i's row [vocab] at target_probs +
+ *               (q_start[b] + i) * target_stride: the probabilities after node i.
+ *               Values are taken into 0 .. 1, NaN as 0.
+ * draft_probs   the same for the draft's, or NULL.
+ * vocab         1 .. 2^19; strides at least that.
+ * uniform       device float32 [num_tokens] in [0, 1): node i's number decides
+ *               its acceptance, node 0's the drawn token.  (NaN refuses, and
+ *               draws as 0.)
+ * A sequence of more than 1024 nodes, or with a bad q_start, counts as n_b = 0
+ * and is flagged PA_DEVERR_QUERY_RANGE.
+ * Work: one cluster of CTAs per sequence; each CTA sums its part of the row,
+ * the sums meet in shared memory, and the part that holds the token is read
+ * again.  No workspace.
+ */
+pa_status pa_draft_verify(const int64_t* tokens, const float* target_probs, int64_t target_stride,
+                          const float* draft_probs, int64_t draft_stride, int32_t vocab, const float* uniform,
+                          const int32_t* parents, const int32_t* q_start, int32_t num_tokens, int32_t B,
+                          int32_t max_path, int32_t* path, int32_t* path_len, int64_t* next_token, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Block-scaled caches: E4M3 codes with one scale for every (block, kv head) of
+ * K and of V ([LLM-INF] 5.3 names per-token and per-channel scales; here a
+ * scale belongs to the tile that the kernels load).  k_scale and v_scale are
+ * float32 [num_blocks][num_kv_heads]; codes are laid out as in every cache, and
+ * desc is that of an FP8_E4M3 cache (head_dim 128).  The per-token calls
+ * (pa_cache_write, pa_decode, ...) do not read such a cache, nor these calls a
+ * per-token one.  Block tables, the block manager and the scheduler are the same.
+ * A speculative step: append n_b slots per sequence (pa_append_tokens),
+ * pa_block_scaled_append and pa_block_scaled_attention in every layer,
+ * pa_draft_verify once, and pa_truncate_seq to the accepted length.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * pa_block_scaled_append -- store the new tokens' K/V rows, the last n_b =
+ * q_start[b+1] - q_start[b] of sequence b's context_lens[b] = L_b positions, in
+ * the blocks that its table names there.
+ *
+ * Scales are powers of two: the smallest 2^e (e >= -126) with |x| <= 448 2^e
+ * for the finite new values of the block and head; where rows before the first
+ * new one stay in the block, no less than the scale they have, and if it grows
+ * their codes are rounded to the new one (exact but for values that become
+ * E4M3 subnormals).  A block whose first row is new starts afresh, so rows that a
+ * verification refused leave nothing behind; without any value above 0 it gets
+ * scale 1.  code = E4M3(x / scale), to nearest even; infinities are stored as
+ * +-448, NaN as NaN.  Rows behind the last new one keep what they hold.
+ *
+ * k, v         device, token t's row [num_kv_heads][head_dim] at k + t *
+ *              k_stride elements of in_dtype (F16, BF16, F32): views of one
+ *              packed projection need no copy.  Strides are at least a row and
+ *              a multiple of 16 bytes.
+ * q_start      device int32 [B + 1], as pa_chunked_prefill.
+ * A sequence with a q_start or length out of range (PA_DEVERR_QUERY_RANGE,
+ * PA_DEVERR_CONTEXT_LEN) and a block id outside the pool (PA_DEVERR_BLOCK_RANGE)
+ * store nothing and are flagged.  The blocks written must not be shared between
+ * sequences (pa_append_tokens has named the copies to make), nor occur twice.
+ */
+pa_status pa_block_scaled_append(const void* k, const void* v, int32_t in_dtype, int64_t k_stride, int64_t v_stride,
+                                 const int32_t* q_start, int32_t num_tokens, const int32_t* block_tables,
+                                 int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t B, void* k_cache,
+                                 void* v_cache, float* k_scale, float* v_scale, const pa_cache_desc* desc,
+                                 void* stream);
+
+/*
+ * pa_block_scaled_attention_workspace_size -- bytes of device workspace
+ * pa_block_scaled_attention needs on the current device (0 on an invalid
+ * argument).  It does not grow with the batch or the context.
+ */
+size_t pa_block_scaled_attention_workspace_size(int32_t num_q_heads, const pa_cache_desc* desc);
+
+/*
+ * pa_block_scaled_attention -- attention of the new tokens over their paged
+ * context: token i of sequence b (position L_b - n_b + i) sees the keys 0 ..
+ * L_b - n_b + i:
+ *     out[q_start[b]+i][h] = sum_t softmax_t(scale * q[q_start[b]+i][h] . K_t) V_t,
+ *     K_t, V_t = scale of (block, kv head) x code,   kv head g = h / G.
+ * One token per sequence is a decode step, gamma + 1 a verification, more a
+ * prompt chunk.  A token with no key is a zero row (n_b > L_b, flagged
+ * PA_DEVERR_CONTEXT_LEN).  What a key or value holds (NaN codes included)
+ * reaches only the tokens that see it.
+ *
+ * q            device, token t's row [num_q_heads][head_dim] at q + t * q_stride
+ *              elements of q_dtype (F16 or BF16); a stride of at least a row
+ *              and a multiple of 8.  Up to 32 query heads per kv head.
+ * q_start, block_tables, context_lens, max_context_len, max_q_len, scale, out
+ *              as pa_chunked_prefill (scale of either sign).
+ * workspace    device, >= pa_block_scaled_attention_workspace_size bytes,
+ *              16-byte aligned; scratch.  Calls that may run at the same time
+ *              need one each.
+ * Deterministic: the same inputs give the same bits on the same device.
+ */
+pa_status pa_block_scaled_attention(const void* q, int32_t q_dtype, int64_t q_stride, const int32_t* q_start,
+                                    int32_t num_tokens, int32_t max_q_len, const void* k_cache,
+                                    const void* v_cache, const float* k_scale, const float* v_scale,
+                                    const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                    const int32_t* context_lens, int32_t max_context_len, int32_t B,
+                                    int32_t num_q_heads, float scale, void* out, int32_t out_dtype,
+                                    const pa_cache_desc* desc, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/*
+ * pa_block_scaled_copy -- whole blocks and their scales from one pool to
+ * another, or within one: copy-on-write copies (both pools the cache) and swaps
+ * with a pinned host pool.  Arguments as pa_swap_blocks, scales
+ * [num_blocks][num_kv_heads]; within one pool no dst may repeat or be a src.
+ */
+pa_status pa_block_scaled_copy(void* dst_k, void* dst_v, float* dst_k_scale, float* dst_v_scale,
+                               int32_t dst_num_blocks, const void* src_k, const void* src_v,
+                               const float* src_k_scale, const float* src_v_scale, int32_t src_num_blocks,
+                               const int64_t* pairs, int64_t num_pairs, const pa_cache_desc* desc, void* stream);
 
 /*
  * pa_decode_static_ws -- pa_decode that allocates nothing.  The pages have no

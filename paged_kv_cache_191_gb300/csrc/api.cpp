@@ -758,18 +758,16 @@ pa_status pa_swap_blocks(void* dst_k, void* dst_v, float* dst_k_scale, float* ds
 
 pa_status pa_device_errors(uint32_t* flags, int32_t clear) {
   if (!flags) return fail(PA_ERR_INVALID, "pa_device_errors: flags is NULL");
-  uint32_t a = 0, b = 0, c = 0, t = 0, s = 0;
-  pa_status st = pa::read_errors_decode(&a, clear != 0);
-  if (st != PA_OK) return st;
-  st = pa::read_errors_cache_ops(&b, clear != 0);
-  if (st != PA_OK) return st;
-  st = pa::read_errors_prefill(&c, clear != 0);
-  if (st != PA_OK) return st;
-  st = pa::read_errors_tree(&t, clear != 0);
-  if (st != PA_OK) return st;
-  st = pa::read_errors_tree_step(&s, clear != 0);
-  if (st != PA_OK) return st;
-  *flags = a | b | c | t | s;
+  uint32_t all = 0;
+  for (auto read : {pa::read_errors_decode, pa::read_errors_cache_ops, pa::read_errors_prefill, pa::read_errors_tree,
+                    pa::read_errors_tree_step, pa::read_errors_verify, pa::read_errors_scaled_cache,
+                    pa::read_errors_scaled_attention}) {
+    uint32_t bits = 0;
+    const pa_status st = read(&bits, clear != 0);
+    if (st != PA_OK) return st;
+    all |= bits;
+  }
+  *flags = all;
   return PA_OK;
 }
 

@@ -134,17 +134,18 @@ constexpr int kCopyChunk = 16384;  // bytes of one block copied by one CTA
 struct BlockPool {
   uint8_t* k;
   uint8_t* v;
-  float* ks;  // [num_blocks][16] or null
+  float* ks;  // [num_blocks][scale_row] or null
   float* vs;
   int num_blocks;
 };
 
 // Copy block pairs[i] = (src, dst) from pool `from` to pool `to` (the same
 // pool for copy-on-write, a pinned host pool for swapping).  One CTA per
-// (pair, 16 KB chunk); ids outside either pool are skipped and flagged.
+// (pair, 16 KB chunk); ids outside either pool are skipped and flagged.  A
+// block has scale_row scales: one per token, or per kv head in a block-scaled cache.
 __global__ void __launch_bounds__(kCopyThreads)
     copy_blocks_kernel(BlockPool to, BlockPool from, const int64_t* __restrict__ pairs,
-                       size_t block_bytes) {
+                       size_t block_bytes, int scale_row) {
   const int64_t src = pairs[2 * blockIdx.x], dst = pairs[2 * blockIdx.x + 1];
   if (src < 0 || src >= from.num_blocks || dst < 0 || dst >= to.num_blocks) {
     if (threadIdx.x == 0 && blockIdx.y == 0) atomicOr(&g_cache_err, PA_DEVERR_BLOCK_RANGE);
@@ -161,9 +162,11 @@ __global__ void __launch_bounds__(kCopyThreads)
     kdst[i] = a;
     vdst[i] = b;
   }
-  if (from.ks && blockIdx.y == 0 && threadIdx.x < PA_BLOCK_SIZE) {
-    to.ks[dst * PA_BLOCK_SIZE + threadIdx.x] = from.ks[src * PA_BLOCK_SIZE + threadIdx.x];
-    to.vs[dst * PA_BLOCK_SIZE + threadIdx.x] = from.vs[src * PA_BLOCK_SIZE + threadIdx.x];
+  if (from.ks && blockIdx.y == 0) {
+    for (int i = threadIdx.x; i < scale_row; i += blockDim.x) {
+      to.ks[dst * scale_row + i] = from.ks[src * scale_row + i];
+      to.vs[dst * scale_row + i] = from.vs[src * scale_row + i];
+    }
   }
 }
 
@@ -212,12 +215,13 @@ pa_status launch_cache_write(const void* k, const void* v, int32_t in_dtype, con
 }
 
 static pa_status launch_pool_copy(const BlockPool& to, const BlockPool& from, const int64_t* pairs,
-                                  int64_t n, const pa_cache_desc* d, void* stream, const char* what) {
+                                  int64_t n, const pa_cache_desc* d, void* stream, const char* what,
+                                  int scale_row = PA_BLOCK_SIZE) {
   const size_t block_bytes = static_cast<size_t>(d->num_kv_heads) * PA_BLOCK_SIZE * d->head_dim *
                              dtype_bytes(d->kv_dtype);
   const unsigned chunks = static_cast<unsigned>((block_bytes + kCopyChunk - 1) / kCopyChunk);
   copy_blocks_kernel<<<dim3(static_cast<unsigned>(n), chunks), kCopyThreads, 0,
-                       static_cast<cudaStream_t>(stream)>>>(to, from, pairs, block_bytes);
+                       static_cast<cudaStream_t>(stream)>>>(to, from, pairs, block_bytes, scale_row);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
   return PA_OK;
@@ -236,6 +240,15 @@ pa_status launch_swap_blocks(void* dk, void* dv, float* dks, float* dvs, int32_t
   const BlockPool from{static_cast<uint8_t*>(const_cast<void*>(sk)), static_cast<uint8_t*>(const_cast<void*>(sv)),
                        const_cast<float*>(sks), const_cast<float*>(svs), snb};
   return launch_pool_copy(to, from, pairs, n, d, stream, "pa_swap_blocks");
+}
+
+pa_status launch_scaled_copy(void* dk, void* dv, float* dks, float* dvs, int32_t dnb, const void* sk, const void* sv,
+                             const float* sks, const float* svs, int32_t snb, const int64_t* pairs, int64_t n,
+                             const pa_cache_desc* d, void* stream) {
+  const BlockPool to{static_cast<uint8_t*>(dk), static_cast<uint8_t*>(dv), dks, dvs, dnb};
+  const BlockPool from{static_cast<uint8_t*>(const_cast<void*>(sk)), static_cast<uint8_t*>(const_cast<void*>(sv)),
+                       const_cast<float*>(sks), const_cast<float*>(svs), snb};
+  return launch_pool_copy(to, from, pairs, n, d, stream, "pa_block_scaled_copy", d->num_kv_heads);
 }
 
 pa_status read_errors_cache_ops(uint32_t* flags, bool clear) {

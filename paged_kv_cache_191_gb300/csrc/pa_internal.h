@@ -224,6 +224,67 @@ struct CommitLaunch {
 };
 pa_status launch_tree_commit(const CommitLaunch& a, const pa_cache_desc* d, void* stream);
 
+// Arguments of the sampled verification after host validation.
+struct VerifyLaunch {
+  const int64_t* tokens;
+  const float* target;
+  const float* draft;  // or null
+  int64_t target_stride, draft_stride;
+  int32_t V;
+  const float* uniform;
+  const int32_t* parents;  // null: a chain
+  const int32_t* q_start;
+  int32_t T, B, max_path;
+  int32_t* path;
+  int32_t* path_len;
+  int64_t* next_token;
+};
+pa_status launch_draft_verify(const VerifyLaunch& a, void* stream);
+
+// Block-scaled caches: arguments after host validation.
+struct ScaledAppendLaunch {
+  const void* k;
+  const void* v;
+  int32_t in_dtype;
+  int64_t k_stride, v_stride;  // elements between tokens
+  const int32_t* q_start;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  int32_t T, B, max_blocks;
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+};
+pa_status launch_scaled_append(const ScaledAppendLaunch& a, const pa_cache_desc* d, void* stream);
+
+struct ScaledAttentionLaunch {
+  const void* q;
+  int32_t q_dtype;
+  int64_t q_stride;
+  const int32_t* q_start;
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* block_tables;
+  int32_t max_blocks;
+  const int32_t* context_lens;
+  int32_t max_context_len, max_q_len;
+  int32_t B, T, Hq, Hkv, num_blocks;
+  float scale;
+  void* out;
+  int32_t out_dtype;
+  void* workspace;
+  int32_t n_cta;      // persistent CTAs: one per SM
+  int32_t item_rows;  // query rows that share a stream of K/V
+};
+pa_status launch_scaled_attention(const ScaledAttentionLaunch& a, void* stream);
+
+pa_status launch_scaled_copy(void* dk, void* dv, float* dks, float* dvs, int32_t dnb, const void* sk,
+                             const void* sv, const float* sks, const float* svs, int32_t snb,
+                             const int64_t* pairs, int64_t n, const pa_cache_desc* d, void* stream);
+
 pa_status launch_cache_write(const void* k, const void* v, int32_t in_dtype,
                              const int64_t* slots, int64_t T, void* k_cache, void* v_cache,
                              float* k_scale, float* v_scale, const pa_cache_desc* d,
@@ -266,6 +327,9 @@ pa_status read_errors_cache_ops(uint32_t* flags, bool clear);
 pa_status read_errors_prefill(uint32_t* flags, bool clear);
 pa_status read_errors_tree(uint32_t* flags, bool clear);
 pa_status read_errors_tree_step(uint32_t* flags, bool clear);
+pa_status read_errors_verify(uint32_t* flags, bool clear);
+pa_status read_errors_scaled_cache(uint32_t* flags, bool clear);
+pa_status read_errors_scaled_attention(uint32_t* flags, bool clear);
 
 // Host checks shared by the entry points: a valid, built cache shape; the
 // current device's SM count (148 where there is none to ask).

@@ -85,6 +85,14 @@ SIGNATURES = {
     "pa_tree_commit": (C.c_int, [_P, _P, _P, _P, _P, _I32, _P, _P, _P, _I32, _P, _I32, _P, C.POINTER(CacheDesc),
                                  _P]),
     "pa_truncate_seq": (C.c_int, [_P, _U64, _I64]),
+    "pa_draft_verify": (C.c_int, [_P, _P, _I64, _P, _I64, _I32, _P, _P, _P, _I32, _I32, _I32, _P, _P, _P, _P]),
+    "pa_block_scaled_append": (C.c_int, [_P, _P, _I32, _I64, _I64, _P, _I32, _P, _I32, _P, _I32, _P, _P, _P, _P,
+                                         C.POINTER(CacheDesc), _P]),
+    "pa_block_scaled_attention_workspace_size": (C.c_size_t, [_I32, C.POINTER(CacheDesc)]),
+    "pa_block_scaled_attention": (C.c_int, [_P, _I32, _I64, _P, _I32, _I32, _P, _P, _P, _P, _P, _I32, _P, _I32, _I32,
+                                            _I32, _F, _P, _I32, C.POINTER(CacheDesc), _P, C.c_size_t, _P]),
+    "pa_block_scaled_copy": (C.c_int, [_P, _P, _P, _P, _I32, _P, _P, _P, _P, _I32, _P, _I64, C.POINTER(CacheDesc),
+                                       _P]),
     "pa_decode_workspace_size": (C.c_size_t, [_I32, _I32, _I32, C.POINTER(CacheDesc), _I32]),
     "pa_decode_plan_info": (C.c_int, [_I32, _I32, _I32, C.POINTER(CacheDesc), _I32, _I32P, _I32P, _I32P]),
     "pa_chunked_prefill_plan_info": (C.c_int, [_I32, _I32, _I32, _I32, _I32, C.POINTER(CacheDesc), _I32,
@@ -519,6 +527,166 @@ def tree_commit(k_cache, v_cache, block_tables, context_lens, q_start, path, pat
                                 new_lens.data_ptr(), C.byref(desc), _raw_stream(stream, dev)),
            "pa_tree_commit")
     return new_lens
+
+
+def draft_verify(tokens, target_probs, uniform, q_start, max_path, draft_probs=None, parents=None, stream=None):
+    """tree_accept for a sampled step: (path int32 [B, max_path] padded with
+    -1, path_len int32 [B], next_token int64 [B]) of drafted tokens (int64
+    [T], packed by q_start int32 [B + 1]) against the target's probabilities,
+    float32 [T, vocab], row i those after node i; uniform: float32 [T] in [0, 1),
+    a node's for its acceptance, the first one's for the drawn token.
+
+    draft_probs, float32 [T, vocab]: the distribution that the node behind node i
+    was sampled from (chains).  None: tokens that were picked, in a chain or, with
+    parents int32 [T], a tree.  Rows may be strided views (dense in the
+    vocabulary)."""
+    dev = _operands("tokens uniform q_start parents target_probs draft_probs", (tokens, uniform, q_start, parents),
+                    (target_probs, draft_probs))
+    T, B = tokens.numel(), q_start.numel() - 1
+    if tokens.dtype != torch.int64:
+        raise ValueError("tokens must be int64 [T]")
+    if uniform.dtype != torch.float32 or uniform.numel() != T:
+        raise ValueError("uniform must be float32 [T]")
+    if q_start.dtype != torch.int32 or B < 0:
+        raise ValueError("q_start must be int32 [B + 1]")
+    if parents is not None and (parents.dtype != torch.int32 or parents.numel() != T):
+        raise ValueError("parents must be int32 [T]")
+    if target_probs.dim() != 2:
+        raise ValueError("target_probs must be float32 [T, vocab]")
+    V = target_probs.shape[1]
+    strides = []
+    for t, n in ((target_probs, "target_probs"), (draft_probs, "draft_probs")):
+        if t is None:
+            strides.append(V)
+            continue
+        if t.dtype != torch.float32 or t.shape != (T, V) or (V > 1 and t.stride(1) != 1):
+            raise ValueError(f"{n} must be float32 [T, vocab], dense in the vocabulary")
+        strides.append(t.stride(0) if T > 1 else V)
+    on = q_start.device
+    path = _empty((B, max_path), torch.int32, on, stream)
+    path_len = _empty((B,), torch.int32, on, stream)
+    token = _empty((B,), torch.int64, on, stream)
+    _check(lib().pa_draft_verify(tokens.data_ptr(), target_probs.data_ptr(), strides[0], _addr(draft_probs),
+                                 strides[1], V, uniform.data_ptr(), _addr(parents), q_start.data_ptr(), T, B,
+                                 int(max_path), path.data_ptr(), path_len.data_ptr(), token.data_ptr(),
+                                 _raw_stream(stream, dev)),
+           "pa_draft_verify")
+    return path, path_len, token
+
+
+def _block_scaled(k_cache, v_cache, k_scale, v_scale):
+    """The descriptor of a block-scaled cache (read only: shared between calls)."""
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache differ")
+    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if t.dtype != torch.float32 or t.shape != k_cache.shape[:2]:
+            raise ValueError(f"{n} must be float32 [num_blocks, num_kv_heads]")
+    return _desc_of(k_cache.shape, k_cache.dtype)
+
+
+def _context(q_start, block_tables, context_lens):
+    """Batch size of a call over the sequences' contexts."""
+    B = context_lens.numel()
+    if q_start.dtype != torch.int32 or q_start.numel() != B + 1:
+        raise ValueError("q_start must be int32 [B + 1]")
+    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("block_tables must be int32 [B, max_blocks]")
+    if context_lens.dtype != torch.int32:
+        raise ValueError("context_lens must be int32 [B]")
+    return B
+
+
+def block_scaled_append(k, v, q_start, block_tables, context_lens, k_cache, v_cache, k_scale, v_scale, stream=None):
+    """Store the new tokens' rows k, v [T, Hkv, D] (f16 / bf16 / f32, packed by
+    q_start int32 [B + 1]; views of one packed projection are fine): the last
+    q_start[b+1] - q_start[b] positions of sequence b's context.  k_cache, v_cache
+    hold E4M3 codes [num_blocks, Hkv, 16, D], k_scale, v_scale float32
+    [num_blocks, Hkv]: powers of two, which grow with a block's values."""
+    dev = _operands("q_start block_tables context_lens k_cache v_cache k_scale v_scale k v",
+                    (q_start, block_tables, context_lens, k_cache, v_cache, k_scale, v_scale), (k, v))
+    desc = _block_scaled(k_cache, v_cache, k_scale, v_scale)
+    B = _context(q_start, block_tables, context_lens)
+    D = desc.head_dim
+    ks, vs = _rows(k, "k", D), _rows(v, "v", D)
+    T = k.shape[0]
+    if k.shape != (T, desc.num_kv_heads, D) or v.shape != k.shape:
+        raise ValueError("k, v must be [T, num_kv_heads, head_dim]")
+    if k.dtype != v.dtype or k.dtype not in (torch.float16, torch.bfloat16, torch.float32):
+        raise ValueError("k, v must share dtype f16 / bf16 / f32")
+    _check(lib().pa_block_scaled_append(k.data_ptr(), v.data_ptr(), _TORCH_DT[k.dtype], ks, vs, q_start.data_ptr(), T,
+                                        block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B,
+                                        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                                        v_scale.data_ptr(), C.byref(desc), _raw_stream(stream, dev)),
+           "pa_block_scaled_append")
+
+
+@functools.lru_cache(maxsize=256)
+def _scaled_workspace(dev, num_q_heads, shape, dtype):
+    """Bytes on the current device, `dev` (their number goes by its SMs)."""
+    return int(lib().pa_block_scaled_attention_workspace_size(num_q_heads, C.byref(_desc_of(shape, dtype))))
+
+
+def block_scaled_attention_workspace_size(num_q_heads, k_cache):
+    return int(lib().pa_block_scaled_attention_workspace_size(num_q_heads, C.byref(cache_desc(k_cache))))
+
+
+def block_scaled_attention(q, q_start, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                           max_context_len, max_q_len, scale, out=None, out_dtype=None, workspace=None, stream=None):
+    """Attention of the new tokens q [T, Hq, D] (f16 / bf16, packed by q_start
+    int32 [B + 1], the last of their contexts; a view of a packed projection is
+    fine) over a block-scaled cache, causal among them: a decode step with one
+    token per sequence, a verification or a prompt chunk with more.  Returns out
+    [T, Hq, D] (q dtype, or out_dtype)."""
+    dev = _operands("q_start k_cache v_cache k_scale v_scale block_tables context_lens out workspace q",
+                    (q_start, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, out, workspace), (q,))
+    desc = _block_scaled(k_cache, v_cache, k_scale, v_scale)
+    B = _context(q_start, block_tables, context_lens)
+    qs = _rows(q, "q", desc.head_dim)
+    T, Hq, D = q.shape
+    if D != desc.head_dim:
+        raise ValueError("q head_dim differs from the cache")
+    if out is None:
+        out = _empty((T, Hq, D), out_dtype or q.dtype, q.device, stream)
+    elif out.shape != (T, Hq, D):
+        raise ValueError("out must be [T, Hq, D]")
+    L = lib()
+    if workspace is None:
+        workspace = _empty(_scaled_workspace(dev, Hq, k_cache.shape, k_cache.dtype), torch.uint8, q.device, stream,
+                           result=False)
+    _check(L.pa_block_scaled_attention(q.data_ptr(), _dtype(q, "q"), qs, q_start.data_ptr(), T, int(max_q_len),
+                                       k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                       block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
+                                       int(max_context_len), B, Hq, float(scale), out.data_ptr(), _dtype(out, "out"),
+                                       C.byref(desc), workspace.data_ptr(),
+                                       workspace.numel() * workspace.element_size(), _raw_stream(stream, dev)),
+           "pa_block_scaled_attention")
+    return out
+
+
+def block_scaled_copy(dst_k, dst_v, dst_k_scale, dst_v_scale, src_k, src_v, src_k_scale, src_v_scale, pairs,
+                      stream=None):
+    """Copy blocks pairs[i] = (src, dst) and their scales between two
+    block-scaled pools (swaps; either on the GPU or in pinned host memory), or
+    within one (copy on write); pairs is an int64 [n, 2] tensor on the GPU or pinned."""
+    for t, n in ((dst_k, "dst_k"), (dst_v, "dst_v"), (dst_k_scale, "dst_k_scale"), (dst_v_scale, "dst_v_scale"),
+                 (src_k, "src_k"), (src_v, "src_v"), (src_k_scale, "src_k_scale"), (src_v_scale, "src_v_scale"),
+                 (pairs, "pairs")):
+        if not isinstance(t, torch.Tensor) or not t.is_contiguous():
+            raise ValueError(f"{n} must be a contiguous tensor")
+        if not (t.is_cuda or t.is_pinned()):
+            raise ValueError(f"{n} must be on the GPU or in pinned host memory")
+        if t.is_cuda and t.get_device() != torch.cuda.current_device():
+            raise ValueError(f"{n} is not on the current device")
+    if pairs.dtype != torch.int64 or pairs.dim() != 2 or pairs.shape[1] != 2:
+        raise ValueError("pairs must be int64 [n, 2]")
+    if dst_k.shape[1:] != src_k.shape[1:] or dst_k.dtype != src_k.dtype:
+        raise ValueError("pools differ in shape or dtype")
+    _block_scaled(dst_k, dst_v, dst_k_scale, dst_v_scale)
+    desc = _block_scaled(src_k, src_v, src_k_scale, src_v_scale)
+    _check(lib().pa_block_scaled_copy(_ptr(dst_k), _ptr(dst_v), _ptr(dst_k_scale), _ptr(dst_v_scale), dst_k.shape[0],
+                                      _ptr(src_k), _ptr(src_v), _ptr(src_k_scale), _ptr(src_v_scale), src_k.shape[0],
+                                      _ptr(pairs), pairs.shape[0], C.byref(desc), _stream(stream)),
+           "pa_block_scaled_copy")
 
 
 def decode_plan_info(B, num_q_heads, max_context_len, k_cache, split_tokens=0):
