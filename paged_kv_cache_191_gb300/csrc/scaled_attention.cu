@@ -1,147 +1,541 @@
-// Attention over a block-scaled cache: one CTA per (token, kv head), its warps
-// taking every eighth key, merged at the end.
-#include "device_common.cuh"
+// Attention of new tokens over a block-scaled cache, on tcgen05 (sm_103a).
+//
+// What it computes: token i of the last n of an L-token context sees the keys
+// 0 .. L - n + i,
+//     out_i = sum_t p_it V_t / sum_t p_it,   p_it = exp(scale q_i . K_t),
+// K and V one scale per (block, kv head) times E4M3 codes ("LLM推理引擎深度实战：
+// 从PagedAttention到分布式推理部署", 5.3 and 2.3).
+//
+// The codes are never converted: they go from HBM by TMA to shared memory and from
+// there into tcgen05.mma kind::f8f6f4 as they are.  What meets them, queries and
+// weights, has more bits than an 8-bit type, so each is a sum of four E5M2 terms,
+// which hold an f16 value exactly (scaled_common.cuh), and the terms are four
+// times the columns of one product rather than four products: K and V, the
+// larger operand, are read from shared memory once.  Converting codes to f16 costs a
+// kernel of this shape twice their bytes in shared-memory traffic in each of three
+// steps (landing, conversion, product) where this one has two.
+//
+// The products are transposed as in the tree attention: S^T = K Q^T (M = the
+// chunk's 128 keys, N = 4 terms x rows) and O^T += V^T P^T (M = 128 dims), a
+// softmax thread owning a key, whose scales are its own registers: a block's scale
+// multiplies the score after the product and the weight before it.  Rows, work
+// items, persistent CTAs and the merge of items that span CTAs are the tree
+// attention's too; an item is 8, 16 or 32 rows (a token's heads, up to a power of
+// two, of one kv head), and of a prompt's items each streams only the chunks that
+// its tokens see.
+//
+// Inside a CTA: warp 0 loads K and the scales, warp 2 V, warp 1 issues the
+// products, warp 3 plans the pieces and splits their queries into terms, warps 4-7
+// and 8-11 are two softmax warpgroups on alternate chunks.
+//
+// Values in masked places: a masked exponent is replaced; V rows that no row sees
+// are zeroed in shared memory, and a NaN code in a row that only some see is
+// zeroed and remembered for (dim, row), which end as NaN.
+#include <mutex>
+
+#include "kv_map.h"
 #include "pa_internal.h"
+#include "scaled_common.cuh"
 
 namespace pa {
 namespace {
 
-__device__ uint32_t g_sa_err;
+constexpr int kMaxDevices = 64;
 
-constexpr unsigned FULL = 0xffffffffu;
-constexpr int kWarps = 8, kDim = 128, kHeads = 8;
-
-struct Args {
-  const void* q;
-  int64_t q_stride;
-  const int32_t* q_start;
-  const uint8_t* kc;
-  const uint8_t* vc;
-  const float* ks;
-  const float* vs;
-  const int32_t* block_tables;
-  const int32_t* context_lens;
-  void* out;
-  int32_t B, T, Hq, Hkv, G, max_blocks, num_blocks, max_context_len, max_q_len, q_bf16, out_f32;
-  float scale_log2;
-};
-
-__device__ __forceinline__ float4 codes4(uint32_t w) {
-  uint32_t lo, hi;
-  dev::e4m3x4_to_f16(w, lo, hi);
-  const float2 a = dev::unpack2<__half>(lo), b = dev::unpack2<__half>(hi);
-  return make_float4(a.x, a.y, b.x, b.y);
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc));
+}
+// kind::f8f6f4, f32 accumulate, M = 128, A E4M3, B E5M2; both K-major, or both not.
+__device__ __forceinline__ constexpr uint32_t idesc_f8(int N, bool mn_major) {
+  return (1u << 4) | (1u << 10) | (mn_major ? 3u << 15 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-__global__ void __launch_bounds__(32 * kWarps) scaled_attention_simple(const __grid_constant__ Args a) {
-  __shared__ float part[kWarps][kHeads][kDim + 2];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = blockIdx.y;
-  dev::grid_dependency_wait();
-  // the sequence of row blockIdx.x
-  int b = 0;
-  const int t = blockIdx.x;
-  while (b < a.B && !(t >= a.q_start[b] && t < a.q_start[b + 1])) ++b;
-  if (b == a.B) return;
-  const int n = a.q_start[b + 1] - a.q_start[b], cap = min(a.max_context_len, a.max_blocks * 16);
-  int L = a.context_lens[b];
-  uint32_t err = 0;
-  if (n > a.max_q_len || a.q_start[b] < 0 || a.q_start[b + 1] > a.T) err |= PA_DEVERR_QUERY_RANGE;
-  if (L < 0 || L > cap || n > L) err |= PA_DEVERR_CONTEXT_LEN;
-  if (err && threadIdx.x == 0) atomicOr(&g_sa_err, err);
-  if (err & PA_DEVERR_QUERY_RANGE) return;
-  L = max(0, min(L, cap));
-  const int keys = L - n + (t - a.q_start[b]) + 1;
-  for (int h0 = 0; h0 < a.G; h0 += kHeads) {
-    const int nh = min(kHeads, a.G - h0);
-    float4 q[kHeads], o[kHeads];
-    float m[kHeads], l[kHeads];
+// The MMA warp: S^T of a chunk once K has landed and the score buffer is read, O^T +=
+// V^T P^T once P^T is written and V has landed.
+template <typename L>
+__device__ __forceinline__ void multiply_scaled(uint8_t* gb, Sync<L> sy, uint32_t tmem) {
+  using namespace tcg;
+  constexpr int NS = L::NS;
+  bool ok = true;
+  Cursor<L> s, o;
+  auto same = [&](Cursor<L>& x) {
+    x.live = uniform(x.live);
+    x.nc = uniform(x.nc);
+  };
+  s.start(sy, gb, ok);
+  o.start(sy, gb, ok);
+  same(s);
+  same(o);
+  int ahead = 0, spin = 0;                 // chunks whose S^T is issued and O^T not
+  int ns0 = 0, ns1 = 0, no0 = 0, no1 = 0;  // S^T and O^T issued per tile
+  int pieces_over = 0;                     // pieces that both warpgroups are done with
+  uint64_t t0 = 0;
+  auto test = [&](uint32_t bar, int parity) { return __all_sync(FULL, dev::mbar_test(bar, parity & 1)) != 0; };
+  auto landed = [&](int i) { return test(sy.full(i % NS), i / NS); };
+#pragma unroll 1
+  while (o.live) {
+    bool moved = false;
+    if (ahead > 0) {
+      const int t = o.tile(), i = o.it0 + 2 * o.c + 1;
+      // (a piece's first products wait for the piece that had its accumulators)
+      const int over = o.c < 2 ? o.i - (L::OPAR - 1) : 0;
+      if (pieces_over < over && test(sy.ofree(pieces_over & 1), pieces_over >> 1)) ++pieces_over;
+      if (pieces_over >= over && test(sy.pfull(t), t ? no1 : no0) && landed(i)) {
+        fence_after();
+        const uint32_t id = idesc_f8(L::COLS, true);
+        const uint64_t vd = sdesc(sy.base + L::RING + (i % NS) * L::SLOT, 16, 1024);
+        const uint64_t pd = sdesc(sy.base + L::P0 + t * 16384, 16, 1024);
+        const uint32_t od = tmem + L::COL_O + ((o.i & (L::OPAR - 1)) * 2 + t) * L::COLS;
+        const uint32_t acc = o.c >= 2 ? 1u : 0u;
+        if (elect_one()) {
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h) {
-      o[h] = make_float4(0.f, 0.f, 0.f, 0.f);
-      q[h] = o[h];
-      m[h] = -INFINITY;
-      l[h] = 0.f;
-      if (h < nh) {
-        const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + t * a.q_stride +
-                                                        static_cast<size_t>(g * a.G + h0 + h) * kDim + 4 * lane);
-        const float2 u = a.q_bf16 ? dev::unpack2<__nv_bfloat16>(x.x) : dev::unpack2<__half>(x.x);
-        const float2 v = a.q_bf16 ? dev::unpack2<__nv_bfloat16>(x.y) : dev::unpack2<__half>(x.y);
-        q[h] = make_float4(u.x, u.y, v.x, v.y);
+          for (int kk = 0; kk < 4; ++kk) mma_f8(od, vd + ((kk * 4096) >> 4), pd + ((kk * 4096) >> 4), id, kk > 0 ? 1u : acc);
+          commit(sy.pdone(t));
+          commit(sy.empty(i % NS));
+        }
+        __syncwarp();
+        ++(t ? no1 : no0);
+        --ahead;
+        if (o.next(sy, gb, ok)) same(o);
+        moved = true;
       }
     }
-    for (int k = w; k < keys; k += kWarps) {
-      int blk = a.block_tables[static_cast<size_t>(b) * a.max_blocks + k / 16];
-      if (blk < 0 || blk >= a.num_blocks) {
-        if (lane == 0) atomicOr(&g_sa_err, PA_DEVERR_BLOCK_RANGE);
-        blk = 0;
-      }
-      const size_t tile = static_cast<size_t>(blk) * a.Hkv + g, at = (tile * 16 + k % 16) * kDim + 4 * lane;
-      const float4 K = codes4(*reinterpret_cast<const uint32_t*>(a.kc + at));
-      const float4 V = codes4(*reinterpret_cast<const uint32_t*>(a.vc + at));
-      const float ks = a.ks[tile] * a.scale_log2, vs = a.vs[tile];
+    if (s.live && ahead < 2) {
+      const int t = s.tile(), i = s.it0 + 2 * s.c, qb = s.i & 1, n = t ? ns1 : ns0;
+      if ((n == 0 || test(sy.sfree(t), n - 1)) && (s.c > 0 || test(sy.qfull(qb), s.i >> 1)) && landed(i)) {
+        fence_after();
+        const uint32_t id = idesc_f8(L::COLS, false);
+        const uint64_t kd = sdesc(sy.base + L::RING + (i % NS) * L::SLOT, 16, 1024);
+        const uint64_t qd = sdesc(sy.base + qb * L::QTILE, 16, 1024);
+        const uint32_t sd = tmem + L::COLS * t;
+        if (elect_one()) {
 #pragma unroll
-      for (int h = 0; h < kHeads; ++h) {
-        float s = q[h].x * K.x + q[h].y * K.y + q[h].z * K.z + q[h].w * K.w;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(FULL, s, off);
-        s *= ks;
-        const float mm = fmaxf(m[h], s), f = m[h] == mm ? 1.f : exp2f(m[h] - mm);
-        const float p = s == -INFINITY ? 0.f : exp2f(s - mm), y = p * vs;
-        m[h] = mm;
-        l[h] = l[h] * f + p;
-        o[h] = make_float4(o[h].x * f + y * V.x, o[h].y * f + y * V.y, o[h].z * f + y * V.z, o[h].w * f + y * V.w);
+          for (int kk = 0; kk < 4; ++kk) mma_f8(sd, kd + ((kk * 32) >> 4), qd + ((kk * 32) >> 4), id, kk > 0 ? 1u : 0u);
+          commit(sy.sfull(t));
+          commit(sy.empty(i % NS));
+          if (s.c + 1 == s.nc) commit(sy.qfree(qb));
+        }
+        __syncwarp();
+        ++(t ? ns1 : ns0);
+        ++ahead;
+        if (s.next(sy, gb, ok)) same(s);
+        moved = true;
       }
     }
+    if (moved) {
+      spin = 0;
+    } else if ((++spin & 63) == 0) {
+      const uint64_t t1 = dev::global_timer_ns();
+      if (spin == 64) t0 = t1;
+      if (uniform(t1 - t0 > kLimit)) {
+        ok = false;
+        break;
+      }
+    }
+  }
+  ok = __all_sync(FULL, ok);
+  if (!ok && elect_one()) {
+    flag(PA_DEVERR_TIMEOUT);
+    commit(sy.mdone());  // products in flight complete before their tensor memory is released
+    wait_thread(sy.mdone(), 0);
+  }
+  __syncwarp();
+}
+
+// The four terms' columns of 8 rows, summed (the small ones first).
+__device__ __forceinline__ void load_sum8(uint32_t at, int step, float (&f)[8]) {
+  uint32_t a[8], b[8], c[8], d[8];
+#define PA_X8(r) "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%33];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16,%17,%18,%19,%20,%21,%22,%23}, [%34];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%24,%25,%26,%27,%28,%29,%30,%31}, [%35];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : PA_X8(a), PA_X8(b), PA_X8(c), PA_X8(d)
+      : "r"(at), "r"(at + step), "r"(at + 2 * step), "r"(at + 3 * step)
+      : "memory");
+#undef PA_X8
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h) {
-      *reinterpret_cast<float2*>(&part[w][h][4 * lane]) = make_float2(o[h].x, o[h].y);
-      *reinterpret_cast<float2*>(&part[w][h][4 * lane + 2]) = make_float2(o[h].z, o[h].w);
-      if (lane == 0) {
-        part[w][h][kDim] = m[h];
-        part[w][h][kDim + 1] = l[h];
-      }
-    }
-    __syncthreads();
-    for (int h = w; h < nh; h += kWarps) {
-      float M = -INFINITY, sum = 0.f;
-      for (int i = 0; i < kWarps; ++i) M = fmaxf(M, part[i][h][kDim]);
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int i = 0; i < kWarps; ++i) {
-        const float mi = part[i][h][kDim];
-        if (mi == -INFINITY && part[i][h][kDim + 1] == 0.f) continue;  // (a NaN score leaves NaN in l)
-        const float f = mi == M ? 1.f : exp2f(mi - M);
-        sum += f * part[i][h][kDim + 1];
-        for (int e = 0; e < 4; ++e) acc[e] += f * part[i][h][4 * lane + e];
-      }
-      const size_t at = (static_cast<size_t>(t) * a.Hq + g * a.G + h0 + h) * kDim + 4 * lane;
-      const float inv = keys > 0 ? 1.f / sum : 0.f;
-      for (int e = 0; e < 4; ++e) {
-        const float y = keys > 0 ? acc[e] * inv : 0.f;
-        if (a.out_f32)
-          static_cast<float*>(a.out)[at + e] = y;
-        else if (a.q_bf16)
-          static_cast<__nv_bfloat16*>(a.out)[at + e] = __float2bfloat16(y);
-        else
-          static_cast<__half*>(a.out)[at + e] = __float2half(y);
-      }
-    }
-    __syncthreads();
+  for (int i = 0; i < 8; i += 2) {
+    auto two = [&](const uint32_t(&x)[8]) { return make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])); };
+    const float2 s = add2(add2(add2(two(d), two(c)), two(b)), two(a));
+    f[i] = s.x;
+    f[i + 1] = s.y;
   }
 }
 
-}  // namespace
+// Sum over the warp's lanes of N values a lane: lane j * (32 / N) gets value j's.
+template <int N>
+__device__ __forceinline__ float lane_sums(float (&v)[N], int lane) {
+  int bit = 16;
+#pragma unroll
+  for (int h = N / 2; h > 0; h >>= 1, bit >>= 1) {
+    const bool up = lane & bit;
+#pragma unroll
+    for (int j = 0; j < h; ++j) {
+      const float give = up ? v[j] : v[j + h], keep = up ? v[j + h] : v[j];
+      v[j] = keep + __shfl_xor_sync(FULL, give, bit);
+    }
+  }
+  float x = v[0];
+#pragma unroll
+  for (; bit > 0; bit >>= 1) x += __shfl_xor_sync(FULL, x, bit);
+  return x;
+}
 
-pa_status launch_scaled_attention(const ScaledAttentionLaunch& l, void* stream) {
-  Args a;
+// New references from the scores in tensor memory, where a row has none yet or an
+// exponent outgrew it; O^T moves with them.  alpha: what the rows' l are to be
+// multiplied by, in scratch[5 R ..], if the result's bit 0 is set.  Bit 1: some
+// row still has no reference.
+template <typename L>
+__device__ __forceinline__ int settle_scaled(const KeyLane& x, uint32_t sc, const float* fac, float* refs, float ks, float lv,
+                                             uint32_t vis, uint32_t oc, bool exists, bool& seen, float& ref) {
+  constexpr int R = L::R;
+  const int bar = 2 + x.t;
+  float best = -INFINITY;  // of row `lane`
+#pragma unroll 1
+  for (int j = 0; j < R; j += 8) {
+    float f[8];
+    load_sum8(sc + j, R, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float m = warp_max((vis >> (j + e)) & 1u ? fmaf(f[e] * fac[j + e], ks, lv) : -INFINITY);
+      if (x.lane == j + e) best = m;
+    }
+  }
+  if (x.lane < R) x.scratch[R * x.w4 + x.lane] = best;
+  named_bar(bar, 128);
+  bool rescale = false;
+  if (x.r < R) {
+    const float cm = fmaxf(fmaxf(x.scratch[x.r], x.scratch[R + x.r]), fmaxf(x.scratch[2 * R + x.r], x.scratch[3 * R + x.r]));
+    float alpha = 1.f;
+    if (exists && (seen ? cm > ref + L::MOVE : cm > -INFINITY)) {
+      rescale = seen;
+      if (seen) alpha = dev::ex2(ref - (cm - L::LIFT));
+      ref = cm - L::LIFT;
+      seen = true;
+    }
+    refs[x.r] = exists ? -ref : -INFINITY;  // rows that do not exist get weight 0
+    x.scratch[5 * R + x.r] = alpha;
+  }
+  rescale = bar_or(bar, 128, rescale);
+  if (rescale) {
+#pragma unroll 1
+    for (int j = 0; j < kParts * R; j += 8) {
+      uint32_t o[8];
+      tmem_ld8(oc + j, o);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * x.scratch[5 * R + ((j + e) & (R - 1))]);
+      tmem_st8(oc + j, o);
+    }
+    tcg::wait_st();
+  }
+  const bool unset = bar_or(bar, 128, x.r < R && !seen);
+  return (rescale ? 1 : 0) | (unset ? 2 : 0);
+}
+
+// V rows that not every row sees: those that none does are zeroed, NaN codes in the
+// others too, and noted for the rows (vis) that do see them.  Thread r has key r's.
+template <typename L>
+__device__ __forceinline__ void guard_scaled(const KeyLane& x, uint8_t* vslot, uint32_t* poison, uint32_t vis) {
+  uint8_t* row = vslot + x.r * 128;
+  if (vis == FULL) return;
+#pragma unroll 2
+  for (int ch = 0; ch < 8; ++ch) {  // (in the order that the lanes' banks differ)
+    uint4* at = reinterpret_cast<uint4*>(row + ((ch ^ x.r) & 7) * 16);
+    if (vis == 0u) {
+      *at = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    uint32_t w[4] = {at->x, at->y, at->z, at->w}, bad = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bad |= __vcmpeq4(w[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    if (bad == 0u) continue;
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t sh = 8 * (i & 3);
+      if (((w[i >> 2] >> sh) & 0x7Fu) != 0x7Fu) continue;
+      w[i >> 2] &= ~(0xFFu << sh);
+      atomicOr(poison + 16 * ch + i, vis);  // (chunk ch of the row is at ch ^ its number)
+    }
+    *at = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// The rows of a piece out, by the warpgroup that joins: O^T of both tiles times the
+// rows' weights, a thread a dim.
+template <typename L>
+__device__ __forceinline__ void write_scaled(const ScaledArgs& sa, const KeyLane& x, const Piece& p, const float2* pubs,
+                                             const uint32_t* poison, uint32_t oa, bool exists) {
+  constexpr int R = L::R, D = L::D;
+  const TreeArgs& a = sa.t;
+  const bool direct = p.slot < 0;
+  float* wts = x.scratch;  // [2 accumulators][R]
+  int* place = reinterpret_cast<int*>(x.scratch + 2 * R);
+  if (x.r < R) {
+    const float2 c0 = pubs[x.r], c1 = pubs[R + x.r];
+    const float m = fmaxf(c0.x, c1.x), mz = m == -INFINITY ? 0.f : m;
+    const float w0 = dev::ex2(c0.x - mz), w1 = dev::ex2(c1.x - mz);
+    const float sum = w0 * c0.y + w1 * c1.y;
+    const float inv = direct && m != -INFINITY ? 1.f / sum : 1.f;
+    wts[x.r] = w0 * inv;
+    wts[R + x.r] = w1 * inv;
+    // where the row goes, in rows of out or of the partials
+    const int at = p.row0 + x.r, h = x.r & ((1 << a.gl) - 1);
+    place[x.r] = !exists ? -1 : direct ? (p.qs + (at >> a.gl)) * a.Hq + p.g * a.G + h : p.slot * a.slot_rows + x.r;
+    if (!direct && exists) {
+      a.part_m[place[x.r]] = m;
+      a.part_l[place[x.r]] = sum;
+    }
+  }
+  named_bar(2 + x.t, 128);
+  const uint32_t nan_rows = poison[x.r] | poison[128 + x.r];
+#pragma unroll 1
+  for (int j0 = 0; j0 < p.rows; j0 += 8) {
+    float u[8], v[8];
+    load_sum8(oa + j0, R, u);
+    load_sum8(oa + L::COLS + j0, R, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float w0 = wts[j0 + e], w1 = wts[R + j0 + e];
+      float o = w0 == 0.f ? 0.f : u[e] * w0;
+      if (w1 != 0.f) o = fmaf(v[e], w1, o);
+      if ((nan_rows >> (j0 + e)) & 1u) o = NAN;
+      const int at = place[j0 + e];
+      if (at < 0) continue;
+      const size_t i = static_cast<size_t>(at) * D + x.r;
+      if (!direct)
+        a.part_o[i] = o;
+      else if (a.out_f32)
+        static_cast<float*>(a.out)[i] = o;
+      else if (sa.q_bf16)
+        static_cast<__nv_bfloat16*>(a.out)[i] = __float2bfloat16(o);
+      else
+        static_cast<__half*>(a.out)[i] = __float2half(o);
+    }
+  }
+  __syncwarp();
+}
+
+template <int R_>
+__global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
+    scaled_attention(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const __grid_constant__ ScaledArgs sa) {
+  using namespace tcg;
+  using L = ScaledLay<R_>;
+  constexpr int R = L::R, NS = L::NS;
+  extern __shared__ __align__(1024) uint8_t gb[];
+  const TreeArgs& a = sa.t;
+  const Sync<L> sy{dev::smem_addr(gb)};
+  if (sy.base & 1023u) {  // the swizzled tiles need it; a launch without static shared memory has it
+    if (threadIdx.x == 0) flag(PA_DEVERR_TIMEOUT);
+    return;
+  }
+  const int wid = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  if (threadIdx.x == 64) {
+    for (int i = 0; i < 8; ++i) dev::mbar_init(scales_full(sy, i), 1);
+    for (int i = 0; i < 4; ++i) dev::mbar_init(factors_full(sy, i), 1);
+  }
+  for (int i = static_cast<int>(threadIdx.x); i < 512; i += L::THREADS) reinterpret_cast<uint32_t*>(gb + L::POISON)[i] = 0u;
+  const uint32_t tmem = setup<L>(gb, sy, wid, &tmK, &tmV, &tmK);
+
+  if (wid == 0) {
+    fewer_registers<L>();
+    produce_scaled<L, false>(a, &tmK, gb, sy);
+  } else if (wid == 1) {
+    fewer_registers<L>();
+    multiply_scaled<L>(gb, sy, static_cast<uint32_t>(uniform(static_cast<int>(tmem))));
+  } else if (wid == 2) {
+    fewer_registers<L>();
+    produce_scaled<L, true>(a, &tmV, gb, sy);
+  } else if (wid == 3) {
+    fewer_registers<L>();
+    plan_scaled<L>(sa, gb, sy);
+  } else {
+    // ---- softmax warpgroups: thread r owns key r of a chunk -----------------------------
+    more_registers<L>();
+    KeyLane x;
+    x.t = (wid - 4) >> 2;
+    x.w4 = wid & 3;
+    x.lane = lane;
+    x.r = 32 * x.w4 + lane;
+    x.tl = tmem + (static_cast<uint32_t>(32 * x.w4) << 16);
+    uint8_t* pbuf = gb + L::P0 + x.t * 16384;
+    x.scratch = reinterpret_cast<float*>(pbuf);
+    const int t = x.t, r = x.r, bar = 2 + t;
+    float2* pubs = reinterpret_cast<float2*>(gb + L::PUB);
+    float* refs = reinterpret_cast<float*>(gb + L::REF) + t * R;
+    uint8_t* prow = pbuf + r * 128;  // the key's row of P^T, swizzled by r & 7
+    const uint32_t sc = x.tl + L::COLS * t;
+    bool ok = true;
+    int n = 0;  // chunks of this tile so far
+    Cursor<L> k;
+    k.i = k.it0 = k.ph = 0;
+#pragma unroll 1
+    for (;; k.close()) {
+      k.open(sy, gb, ok);
+      // The barriers inside a piece have no limit, so where one warp has given up a
+      // wait the whole warpgroup leaves, here.  (And every warp has read the sums of l
+      // that the piece before left in the scratch.)
+      ok = !bar_or(bar, 128, !ok);
+      if (!ok || !__all_sync(FULL, k.live)) break;
+      const Piece& p = k.p;
+      const int pp = k.i & 1, shift = p.L - p.n, i0 = p.row0 >> a.gl;  // the piece's first token
+      const uint32_t oc = x.tl + L::COL_O + ((k.i & (L::OPAR - 1)) * 2 + t) * L::COLS;
+      const float* fac = reinterpret_cast<const float*>(gb + L::FAC) + (k.i & 3) * R;
+      uint32_t* poison = reinterpret_cast<uint32_t*>(gb + L::POISON) + 256 * pp;
+      const bool exists = r < p.rows && (r & ((1 << a.gl) - 1)) < a.G;  // row r (r < R)
+      bool seen = !exists, unset = true;  // row r has a reference; some row may have none
+      float ref = 0.f, l[R];
+#pragma unroll
+      for (int j = 0; j < R; ++j) l[j] = 0.f;
+      const int c_first = (t ^ k.ph) & 1;
+      const bool any = c_first < k.nc;
+      if (ok) ok = wait_warp(factors_full(sy, k.i), (k.i >> 2) & 1);
+#pragma unroll 1
+      for (int c = c_first; c < k.nc; c += 2, ++n) {
+        const int chunk = (k.it0 >> 1) + c, key = (p.c0 + c) * kKeys + r;
+        const bool masked = (p.c0 + c + 1) * kKeys > shift + i0 + 1;
+        if (ok) ok = wait_warp(sy.sfull(t), n & 1);
+        if (ok) ok = wait_warp(scales_full(sy, chunk), (chunk >> 3) & 1);
+        fence_after();
+        const float* scales = reinterpret_cast<const float*>(gb + L::SC) + (chunk & 7) * 16;
+        const float ks = scales[r >> 4], vsc = scales[8 + (r >> 4)], lv = log2_scale(vsc);
+        uint32_t vis = FULL;  // the rows that see the key
+        if (masked) {
+          const int first = key - shift - i0;  // the piece's first token that does
+          if (first > 0) vis = first > ((R - 1) >> a.gl) ? 0u : FULL << (first << a.gl);
+          if (key >= p.L) vis = 0u;
+        }
+        float e[R];
+        // Exponents less the references, and their maximum.
+        auto exponents = [&](float& top) {
+          top = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < R; j += 8) {
+            float f[8];
+            load_sum8(sc + j, R, f);
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              const float2 fa = *reinterpret_cast<const float2*>(fac + j + i);
+              const float2 rf = *reinterpret_cast<const float2*>(refs + j + i);
+              const float2 y = fma2(mul2(make_float2(f[i], f[i + 1]), fa), make_float2(ks, ks), rf);
+              e[j + i] = y.x;
+              e[j + i + 1] = y.y;
+            }
+          }
+          if (masked) {  // whatever the key's score and scale are
+#pragma unroll
+            for (int j = 0; j < R; ++j) e[j] = (vis >> j) & 1u ? e[j] : -INFINITY;
+          }
+#pragma unroll
+          for (int j = 0; j < R; j += 2) top = max3(top, e[j], e[j + 1]);
+        };
+        float top;
+        bool moved = unset;
+        if (!moved) {
+          exponents(top);
+          moved = bar_or(bar, 128, top > L::MOVE - lv);
+        }
+        if (moved) {
+          if (ok && n > 0) ok = wait_warp(sy.pdone(t), (n - 1) & 1);  // (P^T free, O^T at rest)
+          fence_after();
+          const int what = settle_scaled<L>(x, sc, fac, refs, ks, lv, vis, oc, exists, seen, ref);
+          unset = what & 2;
+          if (what & 1) {
+#pragma unroll
+            for (int j = 0; j < R; ++j) l[j] *= x.scratch[5 * R + j];
+            named_bar(bar, 128);  // the scratch is read before P^T takes its place
+          }
+          exponents(top);
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sy.sfree(t));  // the scores and scales are read
+        // weights, their sum, and the terms of weight x V scale
+        uint32_t out[kParts][R / 4];
+#pragma unroll
+        for (int j = 0; j < R; j += 4) {
+          uint32_t p0[kParts], p1[kParts];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int i = j + 2 * h;
+            const float2 w = make_float2(dev::ex2(e[i]), dev::ex2(e[i + 1]));
+            const float2 ll = add2(make_float2(l[i], l[i + 1]), w), y = mul2(w, make_float2(vsc, vsc));
+            l[i] = ll.x;
+            l[i + 1] = ll.y;
+            // (a weight of 0 must not meet a NaN scale)
+            terms(dev::pack2<__half>(w.x == 0.f ? 0.f : y.x, w.y == 0.f ? 0.f : y.y), h ? p1 : p0);
+          }
+#pragma unroll
+          for (int q = 0; q < kParts; ++q) out[q][j / 4] = upper(p0[q], p1[q]);
+        }
+        if (ok && n > 0) ok = wait_warp(sy.pdone(t), (n - 1) & 1);  // P^T's buffer is free
+        const uint32_t* flat = &out[0][0];
+#pragma unroll
+        for (int ch = 0; ch < R * kParts / 16; ++ch)
+          *reinterpret_cast<uint4*>(prow + ((ch ^ (r & 7)) << 4)) =
+              make_uint4(flat[4 * ch], flat[4 * ch + 1], flat[4 * ch + 2], flat[4 * ch + 3]);
+        if (masked) {
+          const int vi = k.it0 + 2 * c + 1, vs = vi % NS;
+          if (ok) ok = __all_sync(FULL, wait_issued(sy.issued(), chunk)) && wait_warp(sy.full(vs), (vi / NS) & 1);
+          guard_scaled<L>(x, gb + L::RING + vs * L::SLOT, poison + 128 * t, vis);
+        }
+        dev::fence_proxy_async_smem();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sy.pfull(t));
+      }
+      // ---- the piece's end --------------------------------------------------------------
+      if (p.last) dev::grid_launch_dependents();
+      if (ok && any) ok = wait_warp(sy.pdone(t), (n - 1) & 1);  // O^T final, P^T's buffer free
+      fence_after();
+      if (any) {  // l over the 128 keys' lanes
+        const float sum = lane_sums<R>(l, lane);
+        if (lane % (32 / R) == 0) x.scratch[R * x.w4 + lane / (32 / R)] = sum;
+      }
+      // both warpgroups are done with what the piece before published
+      if (ok && k.i >= 1) ok = wait_warp(sy.ofree(pp ^ 1), ((k.i - 1) >> 1) & 1);
+      named_bar(bar, 128);
+      if (r < R) {
+        const float sum = any ? (x.scratch[r] + x.scratch[R + r]) + (x.scratch[2 * R + r] + x.scratch[3 * R + r]) : 0.f;
+        pubs[R * t + r] = make_float2(any && exists && seen ? ref : sum != sum ? 0.f : -INFINITY, sum);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sy.pub(t));
+      // the warpgroup with the last chunk joins both accumulators
+      if (((k.ph + k.nc - 1) & 1) == t) {
+        if (ok) ok = wait_warp(sy.pub(t ^ 1), k.i & 1);  // (after that tile's last product)
+        named_bar(bar, 128);
+        fence_after();
+        write_scaled<L>(sa, x, p, pubs, poison, x.tl + L::COL_O + (k.i & (L::OPAR - 1)) * 2 * L::COLS, exists);
+        poison[r] = poison[128 + r] = 0u;
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sy.ofree(pp));
+    }
+    if (!ok && lane == 0) flag(PA_DEVERR_TIMEOUT);
+  }
+  teardown(wid, tmem);
+}
+
+template <int R>
+pa_status launch_rows(const ScaledAttentionLaunch& l, cudaStream_t stream) {
+  using L = ScaledLay<R>;
+  const auto kernel = scaled_attention<R>;
+  ScaledArgs sa = {};
+  TreeArgs& a = sa.t;
   a.q = l.q;
-  a.q_stride = l.q_stride;
   a.q_start = l.q_start;
-  a.kc = static_cast<const uint8_t*>(l.k_cache);
-  a.vc = static_cast<const uint8_t*>(l.v_cache);
-  a.ks = l.k_scale;
-  a.vs = l.v_scale;
   a.block_tables = l.block_tables;
   a.context_lens = l.context_lens;
+  a.k_scale = l.k_scale;
+  a.v_scale = l.v_scale;
   a.out = l.out;
   a.B = l.B;
   a.T = l.T;
@@ -152,22 +546,67 @@ pa_status launch_scaled_attention(const ScaledAttentionLaunch& l, void* stream) 
   a.num_blocks = l.num_blocks;
   a.max_context_len = l.max_context_len;
   a.max_q_len = l.max_q_len;
-  a.q_bf16 = l.q_dtype == PA_DTYPE_BF16;
-  a.out_f32 = l.out_dtype == PA_DTYPE_F32;
+  a.n_cta = l.n_cta;
+  while ((1 << a.gl) < a.G) ++a.gl;
   a.scale_log2 = l.scale * 1.4426950408889634f;
-  cudaError_t e = launch_dependent(scaled_attention_simple, dim3(static_cast<unsigned>(a.T), static_cast<unsigned>(a.Hkv)),
-                                   dim3(32 * kWarps), 0, static_cast<cudaStream_t>(stream), a);
+  a.out_f32 = l.out_dtype == PA_DTYPE_F32;
+  a.min_units = 2;
+  a.item_rows = R;
+  a.slot_rows = R;
+  sa.q_stride = l.q_stride;
+  sa.q_bf16 = l.q_dtype == PA_DTYPE_BF16;
+  const size_t rows = static_cast<size_t>(2) * a.n_cta * R;
+  a.part_o = static_cast<float*>(l.workspace);
+  a.part_m = a.part_o + rows * L::D;
+  a.part_l = a.part_m + rows;
+  a.split = reinterpret_cast<int4*>(a.part_l + rows);
+
+  CUtensorMap tmK, tmV;
+  for (int v = 0; v < 2; ++v) {
+    const pa_status st = make_kv_map(v ? &tmV : &tmK, v ? l.v_cache : l.k_cache, l.Hkv, l.num_blocks, L::D, 1,
+                                     CU_TENSOR_MAP_DATA_TYPE_UINT8, "pa_block_scaled_attention");
+    if (st != PA_OK) return st;
+  }
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices)
+    return fail(PA_ERR_CUDA, "pa_block_scaled_attention: no CUDA device");
+  static std::once_flag once[kMaxDevices];
+  static cudaError_t setup[kMaxDevices];
+  std::call_once(once[dev], [dev, kernel] {
+    setup[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+    // the registers that the roles ask for have to be the launch's, or they would wait for them forever
+    constexpr int WANT = 256 * L::HIGH + (L::THREADS - 256) * L::LOW;
+    cudaFuncAttributes fa;
+    if (setup[dev] == cudaSuccess) setup[dev] = cudaFuncGetAttributes(&fa, kernel);
+    if (setup[dev] == cudaSuccess && fa.numRegs * L::THREADS < WANT) setup[dev] = cudaErrorInvalidConfiguration;
+  });
+  if (setup[dev] != cudaSuccess)
+    return fail(PA_ERR_CUDA, "pa_block_scaled_attention: %s", cudaGetErrorString(setup[dev]));
+  cudaError_t e = launch_dependent(kernel, dim3(static_cast<unsigned>(a.n_cta)), dim3(L::THREADS), L::BYTES, stream, tmK,
+                                   tmV, sa);
+  if (e == cudaSuccess && l.max_context_len > kKeys) {
+    const dim3 grid(static_cast<unsigned>(a.n_cta), R / kMergeRows), block(32 * kMergeRows);
+    e = sa.q_bf16 ? launch_dependent(tree_merge<__nv_bfloat16, L::D>, grid, block, 0, stream, a)
+                  : launch_dependent(tree_merge<__half, L::D>, grid, block, 0, stream, a);
+  }
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return fail(PA_ERR_CUDA, "pa_block_scaled_attention launch: %s", cudaGetErrorString(e));
   return PA_OK;
 }
 
+}  // namespace
+
+pa_status launch_scaled_attention(const ScaledAttentionLaunch& l, void* stream) {
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return l.item_rows == 8 ? launch_rows<8>(l, st) : l.item_rows == 16 ? launch_rows<16>(l, st) : launch_rows<32>(l, st);
+}
+
 pa_status read_errors_scaled_attention(uint32_t* flags, bool clear) {
   uint32_t v = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_sa_err, sizeof(v));
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_tree_err, sizeof(v));
   if (e == cudaSuccess && clear) {
     const uint32_t z = 0;
-    e = cudaMemcpyToSymbol(g_sa_err, &z, sizeof(z));
+    e = cudaMemcpyToSymbol(g_tree_err, &z, sizeof(z));
   }
   if (e != cudaSuccess) return fail(PA_ERR_CUDA, "pa_device_errors: %s", cudaGetErrorString(e));
   *flags = v;

@@ -1,0 +1,385 @@
+// Attention over a block-scaled cache: shared memory, the planner and query
+// warp, and the producers.  The ring, the pieces, the waits and tensor memory's
+// access are those of the tree attention.
+#pragma once
+
+#include "tree_merge.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kParts = 4;  // E5M2 terms of a query or a weight
+
+struct ScaledArgs {
+  TreeArgs t;        // (mask and words are not used; scale_log2 has the scale's sign)
+  int64_t q_stride;  // elements between tokens
+  int32_t q_bf16;
+};
+
+// R: rows of an item, 8, 16 or 32.
+template <int R_>
+struct ScaledLay {
+  static constexpr int R = R_, D = 128, HQ = R;
+  static constexpr bool Q8 = false, ROWS = false, WORDS = false;
+  static constexpr int PRODUCERS = 1;           // threads that announce a slot's bytes
+  static constexpr int QTILE = kParts * R * D;  // Q of a piece [term][R][128 B], E5M2
+  static constexpr int SLOT = kKeys * D;        // one K or V chunk of codes
+  static constexpr int P0 = 2 * QTILE;          // P^T [tile][128 keys][128 B: term, row]
+  static constexpr int RING = P0 + 2 * 16384;
+  static constexpr int NS = R == 32 ? 8 : 10;   // even: K's and V's producers own every other slot
+  static constexpr int NL = NS;
+  static constexpr int BAR = RING + NS * SLOT;
+  static constexpr int EXTRA = 2 * NL + 2 * NS + 23;
+  static constexpr int NBAR = EXTRA + 8 + 4;    // scales of a chunk, factors of a piece
+  static constexpr int MISC = (BAR + NBAR * 8 + 15) & ~15;
+  static constexpr int PIECE = MISC + 128;      // Piece [4]
+  static constexpr int PUB = PIECE + 4 * 48;    // float2 [2 tiles][R]
+  static constexpr int SC = PUB + 16 * R;       // float [8 chunks][K 8, V 8]
+  static constexpr int FAC = SC + 8 * 64;       // float [4 pieces][R]
+  static constexpr int REF = FAC + 16 * R;      // float [2 tiles][R]: minus the references
+  static constexpr int POISON = REF + 8 * R;    // uint32 [piece parity][2 tiles][128 dims]: rows that see a NaN there
+  static constexpr int MASK = 0;
+  static constexpr int BYTES = POISON + 2048;
+  static constexpr int THREADS = 384;
+  static constexpr int HIGH = 200, LOW = 104;
+  // tensor memory columns: S^T [tile] x kParts R, O^T [piece parity, where there is room][tile] x kParts R
+  static constexpr int COLS = kParts * R, OPAR = R == 32 ? 1 : 2;
+  static constexpr uint32_t COL_O = 2 * COLS;
+  // log2 of how far below its row's maximum of weight x V scale a reference is set, and
+  // of how far that maximum may outgrow it: E5M2 terms of f16 values go from 2^15.9
+  // down to 2^-16, 2^-27 of the largest.
+  static constexpr float LIFT = 11.f, MOVE = 15.5f;
+  static_assert(BYTES <= 232448, "shared memory of one CTA");
+  static_assert(COL_O + OPAR * 2 * COLS <= static_cast<int>(kTmemCols), "tensor memory");
+};
+
+template <typename L>
+__device__ __forceinline__ uint32_t scales_full(const Sync<L>& sy, int chunk) { return sy.at(L::EXTRA + (chunk & 7)); }
+template <typename L>
+__device__ __forceinline__ uint32_t factors_full(const Sync<L>& sy, int piece) {
+  return sy.at(L::EXTRA + 8 + (piece & 3));
+}
+
+// What the softmax's rare paths share with its loop.
+struct KeyLane {
+  int t, w4, lane, r;  // tile, warp of the tile, lane, key of the chunk
+  uint32_t tl;         // tensor memory at the warp's lanes
+  float* scratch;      // the tile's P^T buffer, between a product's end and the next P^T
+};
+
+// ---- E5M2 terms --------------------------------------------------------------
+// An f16 value is the sum of four E5M2 ones: E5M2 is f16's upper byte, so a term is
+// what is left, cut behind its first three bits (11 bits: 3 + 3 + 3 + 2).  The
+// differences are exact; only below 2^-16, E5M2's smallest, is anything lost.
+// h: two values in, the four terms' pairs out (their upper bytes count).
+__device__ __forceinline__ void terms(uint32_t h, uint32_t (&p)[kParts]) {
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) {
+    p[i] = h;
+    if (i + 1 < kParts) {
+      const uint32_t cut = h & 0xFF00FF00u;
+      const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&cut));
+      h = *reinterpret_cast<const uint32_t*>(&r);
+    }
+  }
+}
+// The upper bytes of two pairs.
+__device__ __forceinline__ uint32_t upper(uint32_t a, uint32_t b) { return dev::prmt(a, b, 0x7531u); }
+
+// ---- the batch's work ----------------------------------------------------------
+// A sequence's items of one kv head, tpi tokens each; item j sees L - n + (j + 1)
+// tpi keys at most, and a chunk beyond is not its work.
+struct Span {
+  int qs, n, L, tiles;
+  int a;  // tokens before the new ones, in items
+};
+// sum of ceil(x / s) over x = 1 .. m
+__device__ __forceinline__ int64_t ceil_sum(int64_t m, int s) {
+  const int64_t q = m / s, r = m - q * s;
+  return s * (q * (q + 1) / 2) + r * (q + 1);
+}
+__device__ __forceinline__ int64_t units_before(const Span& x, int k, int s) {
+  return static_cast<int64_t>(kItem) * k + ceil_sum(x.a + k, s) - ceil_sum(x.a, s);
+}
+__device__ __forceinline__ int64_t units_per_head(const Span& x, int s) {
+  if (x.tiles == 0) return 0;
+  return units_before(x, x.tiles - 1, s) + kItem + max(1, (x.L + kKeys - 1) / kKeys);
+}
+
+// The planner warp: this CTA's pieces and their queries.  Piece i + 1 is published
+// before piece i's queries are loaded, so that the producers see two pieces ahead.
+template <typename L>
+__device__ __forceinline__ void plan_scaled(const ScaledArgs& sa, uint8_t* gb, Sync<L> sy) {
+  constexpr int R = L::R;
+  const TreeArgs& a = sa.t;
+  const int lane = static_cast<int>(threadIdx.x & 31), me = static_cast<int>(blockIdx.x);
+  const int tpi = R >> a.gl, per = kKeys / tpi;
+  Span mine{0, 0, 0, 0, 0};
+  int group = -1;
+  auto read = [&](int g, bool report) {
+    if (g == group) return;
+    group = g;
+    const int b = 32 * g + lane;
+    mine = Span{0, 0, 0, 0, 0};
+    if (b >= a.B) return;
+    const Seq s = seq_of(a, b, report);
+    mine = Span{s.qs, s.n, s.L, s.tiles, (max(0, s.L - s.n) + tpi - 1) / tpi};
+  };
+  auto span = [&](int b) {
+    read(b >> 5, false);
+    return Span{__shfl_sync(FULL, mine.qs, b & 31), __shfl_sync(FULL, mine.n, b & 31), __shfl_sync(FULL, mine.L, b & 31),
+                __shfl_sync(FULL, mine.tiles, b & 31), __shfl_sync(FULL, mine.a, b & 31)};
+  };
+  int64_t sum = 0;
+#pragma unroll 1
+  for (int g = 0; 32 * g < a.B; ++g) {
+    read(g, me == 0);
+    sum += units_per_head(mine, per) * a.Hkv;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(FULL, sum, off);
+  // more than the launch was checked for: q_start has ranges that overlap
+  if (sum > kMaxUnits && me == 0 && lane == 0) flag(PA_DEVERR_QUERY_RANGE);
+  const int total = sum > kMaxUnits ? 0 : static_cast<int>(sum);
+  const int upc = max((total + a.n_cta - 1) / a.n_cta, a.min_units);
+  const int start = static_cast<int>(min(static_cast<int64_t>(me) * upc, static_cast<int64_t>(total)));
+  const int end = min(start + upc, total);
+  int b = 0, ub = 0;  // the sequence of unit `u`, and the units before it
+#pragma unroll 1
+  for (int b0 = 0; start < end; b0 += 32) {
+    read(b0 >> 5, false);
+    const int w = static_cast<int>(units_per_head(mine, per)) * a.Hkv;
+    int inc = w;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(FULL, inc, off);
+      if (lane >= off) inc += y;
+    }
+    const unsigned over = __ballot_sync(FULL, ub + inc > start);
+    if (over) {
+      const int f = __ffs(over) - 1;
+      b = b0 + f;
+      ub += __shfl_sync(FULL, inc - w, f);
+      break;
+    }
+    ub += __shfl_sync(FULL, inc, 31);
+  }
+  Piece* ring = reinterpret_cast<Piece*>(gb + L::PIECE);
+  int u = start;
+  bool ok = true, more = true;
+  int4 sp0 = make_int4(0, 0, 0, 0), sp1 = sp0;
+  auto publish_piece = [&](int i) {
+    if (ok && i >= 4) ok = wait_warp(sy.ofree(i & 1), ((i - 4) >> 1) & 1);
+    Piece p;
+    p.live = 0;
+#pragma unroll 1
+    while (u < end && !p.live) {
+      Span s = span(b);
+      int U = static_cast<int>(units_per_head(s, per));
+#pragma unroll 1
+      while (b < a.B && u >= ub + U * a.Hkv) {
+        ub += U * a.Hkv;
+        s = span(++b);
+        U = static_cast<int>(units_per_head(s, per));
+      }
+      if (b >= a.B) {  // (lengths that changed under the kernel)
+        u = end;
+        break;
+      }
+      const int at = u - ub, g = at / U, rem = at - g * U;
+      int lo = 0, hi = s.tiles;  // the item: the last that starts at or before rem
+#pragma unroll 1
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (units_before(s, mid, per) <= rem)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      const int before = static_cast<int>(units_before(s, lo, per));
+      const int cost = (lo + 1 < s.tiles ? static_cast<int>(units_before(s, lo + 1, per)) : U) - before;
+      const int off = rem - before, stop = min(cost, off + end - u), item_end = u - off + cost;
+      p.c0 = max(0, off - kItem);
+      p.c1 = stop - kItem;
+      u += stop - off;
+      if (p.c1 <= p.c0) continue;  // the range ends before the item's first chunk
+      p.live = 1;
+      p.b = b;
+      p.qs = s.qs;
+      p.n = s.n;
+      p.L = s.L;
+      p.g = g;
+      p.row0 = lo * R;
+      p.rows = min(R, (s.n << a.gl) - p.row0);
+      p.slot = p.c0 == 0 && p.c1 == cost - kItem ? -1 : 2 * me + (i == 0 ? 0 : 1);
+      if (p.c0 == 0 && p.c1 < cost - kItem) {  // the item goes on in the next CTAs: what the merge needs
+        sp0 = make_int4((item_end - 1) / upc - me + 1, p.slot, s.qs, p.row0);
+        sp1 = make_int4(g, p.rows, 1, 0);
+      }
+    }
+    p.last = u >= end;  // (or only an item's start is left)
+    more = p.live;
+    if (lane == 0) {
+      ring[i & 3] = p;
+      mbar_arrive(sy.pieces(i & 3));
+    }
+    __syncwarp();
+  };
+  // Piece i's queries: every row scaled by a power of two to 2^14 .. 2^15 (a row of
+  // small values keeps its bits beside one of large ones), in E5M2 terms; its factor
+  // takes the power back.
+  auto queries = [&](int i) {
+    const Piece p = ring[i & 3];
+    if (ok && i >= 2) ok = wait_warp(sy.qfree(i & 1), ((i - 2) >> 1) & 1);
+    float* fac = reinterpret_cast<float*>(gb + L::FAC) + (i & 3) * R;
+    uint8_t* to = gb + (i & 1) * L::QTILE + (lane & 3) * 4;
+    const int heads = (1 << a.gl) - 1;
+#pragma unroll 1
+    for (int r0 = 0; r0 < R; r0 += 8) {
+      uint2 x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int r = r0 + j, h = r & heads;
+        x[j] = make_uint2(0u, 0u);
+        if (r < p.rows && h < a.G)
+          x[j] = __ldg(reinterpret_cast<const uint2*>(
+              static_cast<const uint16_t*>(a.q) + static_cast<size_t>(p.qs + ((p.row0 + r) >> a.gl)) * sa.q_stride +
+              static_cast<size_t>(p.g * a.G + h) * L::D + 4 * lane));
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int r = r0 + j;
+        const float2 lo = sa.q_bf16 ? dev::unpack2<__nv_bfloat16>(x[j].x) : dev::unpack2<__half>(x[j].x);
+        const float2 hi = sa.q_bf16 ? dev::unpack2<__nv_bfloat16>(x[j].y) : dev::unpack2<__half>(x[j].y);
+        const float f[4] = {lo.x, lo.y, hi.x, hi.y};
+        uint32_t top = 0;  // the largest finite size
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t s = __float_as_uint(f[e]) & 0x7FFFFFFFu;
+          if (s < 0x7F800000u) top = max(top, s);
+        }
+        top = __reduce_max_sync(FULL, top);
+        const int k = min(14 - (static_cast<int>(top >> 23) - 127), 100);
+        const float up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+        uint32_t p0[kParts], p1[kParts];
+        terms(dev::pack2<__half>(f[0] * up, f[1] * up), p0);
+        terms(dev::pack2<__half>(f[2] * up, f[3] * up), p1);
+#pragma unroll
+        for (int e = 0; e < kParts; ++e)
+          *reinterpret_cast<uint32_t*>(to + (e * R + r) * 128 + (((lane >> 2) ^ (r & 7)) << 4)) = upper(p0[e], p1[e]);
+        if (lane == 0) fac[r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+      }
+    }
+    dev::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(sy.qfull(i & 1));
+      mbar_arrive(factors_full(sy, i));
+    }
+  };
+#pragma unroll 1
+  for (int i = 0; more; ++i) {
+    publish_piece(i);
+    if (i > 0) queries(i - 1);
+  }
+  if (lane == 0) {
+    a.split[2 * blockIdx.x] = sp0;
+    a.split[2 * blockIdx.x + 1] = sp1;
+    if (!ok) flag(PA_DEVERR_TIMEOUT);
+  }
+}
+
+// The producer warps, one for K (and both tensors' scales) and one for V: a piece's
+// chunks into their slots of the ring, one 2 KB box per block.
+template <typename L, bool V>
+__device__ __forceinline__ void produce_scaled(const TreeArgs& a, const CUtensorMap* map, uint8_t* gb, Sync<L> sy) {
+  constexpr int NS = L::NS;
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  bool ok = true;
+  int chunk = 0;  // chunks issued
+  // Loads behind a full ring take microseconds, so the ids of the next 32 blocks, and
+  // their scales, are fetched well ahead.
+  auto fetch = [&](const Piece& x, int j0) {  // lane's block id, blocks j0 .. j0 + 31 of the piece
+    const int j = j0 + lane;
+    if (j >= min((x.L + 15) / 16, x.c1 * kBlk)) return 0;
+    int v = a.block_tables[static_cast<size_t>(x.b) * a.max_blocks + j];
+    if (v < 0 || v >= a.num_blocks) {
+      flag(PA_DEVERR_BLOCK_RANGE);  // block 0 is read instead; flagged
+      v = 0;
+    }
+    return v;
+  };
+  Piece p, pn;
+  bool more = sy.piece(gb, 0, p, ok);
+  int ids_next = more ? fetch(p, p.c0 * kBlk) : 0;
+  float2 next = make_float2(0.f, 0.f);  // the scales of the lane's block in ids_next
+  auto scales = [&](int g) {
+    const size_t at = static_cast<size_t>(ids_next) * a.Hkv + g;
+    next = make_float2(__ldg(a.k_scale + at), __ldg(a.v_scale + at));
+  };
+  if (!V && more) scales(p.g);
+#pragma unroll 1
+  for (int i = 1; more; ++i) {
+    const bool more_n = sy.piece(gb, i, pn, ok);
+    p.g = uniform(p.g);
+    p.c0 = uniform(p.c0);
+    p.c1 = uniform(p.c1);
+    const int nblk = uniform((p.L + 15) / 16), ids_n = more_n ? fetch(pn, pn.c0 * kBlk) : 0;
+    int ids = 0;
+    float2 sc = next;
+#pragma unroll 1
+    for (int c = p.c0; c < p.c1; ++c, ++chunk) {
+      const int k4 = (c - p.c0) & 3;
+      if (k4 == 0) {
+        ids = ids_next;
+        sc = next;
+        ids_next = c + 4 < p.c1 ? fetch(p, (c + 4) * kBlk) : ids_n;
+      }
+      int blk[kBlk];  // the chunk's block ids
+#pragma unroll
+      for (int k = 0; k < kBlk; ++k) blk[k] = __shfl_sync(FULL, ids, k4 * kBlk + k);
+      const int live = max(0, min(kBlk, nblk - c * kBlk));  // those that exist
+      const int it = 2 * chunk + (V ? 1 : 0), s = it % NS;
+      if (ok && it >= NS) ok = wait_warp(sy.empty(s), (it / NS - 1) & 1);
+      if (!ok) break;
+      dev::fence_proxy_async_smem();  // the softmax's accesses precede the refill
+      const uint32_t bar = sy.full(s), dst = sy.base + L::RING + s * L::SLOT;
+      if (lane == 0) {
+        dev::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(live * 2048));
+        if (V) publish(sy.issued(), chunk + 1);
+      }
+      __syncwarp();
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < kBlk; ++k) {
+          if (k >= live) break;
+          dev::tma_load_3d(dst + k * 2048, map, bar, 0, p.g * 16, blk[k]);
+        }
+      }
+      __syncwarp();
+      if (!V) {
+        // (a place is free: its chunk's scores were read before those two chunks on were computed)
+        float* to = reinterpret_cast<float*>(gb + L::SC) + (chunk & 7) * 16;
+        if ((lane >> 3) == k4) {
+          to[lane & 7] = sc.x;
+          to[8 + (lane & 7)] = sc.y;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(scales_full(sy, chunk));
+        if (c + 1 == p.c1 ? more_n : k4 == 3) scales(c + 1 == p.c1 ? pn.g : p.g);
+      }
+    }
+    p = pn;
+    more = more_n && ok;
+  }
+  // no copy may still be landing when the CTA exits
+  for (int c = max(0, chunk - NS / 2); c < chunk; ++c) {
+    const int it = 2 * c + (V ? 1 : 0);
+    wait_thread(sy.full(it % NS), (it / NS) & 1);
+  }
+  if (!ok && lane == 0) flag(PA_DEVERR_TIMEOUT);
+  __syncwarp();
+}
+
+}  // namespace
+}  // namespace pa
