@@ -728,7 +728,7 @@ pa_status pa_block_scaled_append(const void* k, const void* v, int32_t in_dtype,
  * pa_block_scaled_attention needs on the current device (0 on an invalid
  * argument).  It does not grow with the batch or the context.
  */
-size_t pa_block_scaled_attention_workspace_size(int32_t num_q_heads, const pa_cache_desc* desc);
+size_t pa_block_scaled_attention_workspace_size(int32_t num_q_heads, int32_t max_q_len, const pa_cache_desc* desc);
 
 /*
  * pa_block_scaled_attention -- attention of the new tokens over their paged

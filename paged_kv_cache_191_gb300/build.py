@@ -24,7 +24,8 @@ SOURCES = ["decode.cu", "decode_static.cu", "prefill.cu", "cache_ops.cu", "api.c
            "serve.cpp", "segments.cpp", "tree.cu", "tree_step.cu", "tree.cpp", "scaled.cpp", "scaled_cache.cu",
            "scaled_attention.cu", "verify.cu"]
 HEADERS = ["device_common.cuh", "tcgen05.cuh", "cache_rows.cuh", "tree_common.cuh", "tree_keys.cuh",
-           "tree_rows.cuh", "tree_merge.cuh", "scaled_common.cuh", "pa_internal.h", "kv_map.h"]
+           "tree_rows.cuh", "tree_merge.cuh", "tree_maps.h", "scaled_common.cuh",
+           "scaled_rows.cuh", "pa_internal.h", "kv_map.h"]
 
 
 def nvcc():

@@ -21,24 +21,32 @@ pa_status check_scaled(const pa_cache_desc* d, const char* fn) {
 
 // Query rows that share a stream of K/V: a token's heads of one kv head take a
 // power of two of them.
-constexpr int32_t kMaxItemRows = 32;
+constexpr int32_t kMaxHeads = 32;
+int32_t item_rows(int32_t num_q_heads, int32_t max_q_len, const pa_cache_desc* d) {
+  int64_t rows = 1;
+  while (rows < num_q_heads / d->num_kv_heads) rows *= 2;
+  rows *= max_q_len;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
+}
 
-pa_status check_attention(int32_t num_q_heads, const pa_cache_desc* desc) {
+pa_status check_attention(int32_t num_q_heads, int32_t max_q_len, const pa_cache_desc* desc) {
   const char* fn = "pa_block_scaled_attention";
   const pa_status st = check_scaled(desc, fn);
   if (st != PA_OK) return st;
   if (num_q_heads <= 0 || num_q_heads % desc->num_kv_heads)
     return fail(PA_ERR_INVALID, "%s: num_q_heads must be a positive multiple of num_kv_heads", fn);
-  if (num_q_heads / desc->num_kv_heads > kMaxItemRows)
-    return fail(PA_ERR_UNSUPPORTED, "%s: more than %d query heads per kv head", fn, kMaxItemRows);
+  if (num_q_heads / desc->num_kv_heads > kMaxHeads)
+    return fail(PA_ERR_UNSUPPORTED, "%s: more than %d query heads per kv head", fn, kMaxHeads);
+  if (max_q_len < 0) return fail(PA_ERR_INVALID, "%s: max_q_len < 0", fn);
+  if (max_q_len > 65535) return fail(PA_ERR_UNSUPPORTED, "%s: max_q_len above 65535", fn);
   return PA_OK;
 }
 
 // Per CTA two sets of partial rows (o, m, l) and 32 bytes on the item it leaves
 // unfinished.
-size_t attention_workspace(const pa_cache_desc* d) {
-  const size_t ctas = static_cast<size_t>(pa::sm_count());
-  return (ctas * (2 * kMaxItemRows * (d->head_dim + 2) * sizeof(float) + 32) + 255) & ~static_cast<size_t>(255);
+size_t attention_workspace(int32_t rows, int32_t sms, const pa_cache_desc* d) {
+  const size_t ctas = static_cast<size_t>(sms);
+  return (ctas * (2 * rows * (d->head_dim + 2) * sizeof(float) + 32) + 255) & ~static_cast<size_t>(255);
 }
 
 }  // namespace
@@ -88,8 +96,9 @@ pa_status pa_block_scaled_append(const void* k, const void* v, int32_t in_dtype,
   return pa::launch_scaled_append(a, desc, stream);
 }
 
-size_t pa_block_scaled_attention_workspace_size(int32_t num_q_heads, const pa_cache_desc* desc) {
-  return check_attention(num_q_heads, desc) == PA_OK ? attention_workspace(desc) : 0;
+size_t pa_block_scaled_attention_workspace_size(int32_t num_q_heads, int32_t max_q_len, const pa_cache_desc* desc) {
+  if (check_attention(num_q_heads, max_q_len, desc) != PA_OK) return 0;
+  return attention_workspace(item_rows(num_q_heads, max_q_len, desc), pa::sm_count(), desc);
 }
 
 pa_status pa_block_scaled_attention(const void* q, int32_t q_dtype, int64_t q_stride, const int32_t* q_start,
@@ -100,16 +109,15 @@ pa_status pa_block_scaled_attention(const void* q, int32_t q_dtype, int64_t q_st
                                     const pa_cache_desc* desc, void* workspace, size_t workspace_bytes,
                                     void* stream) {
   const char* fn = "pa_block_scaled_attention";
-  const pa_status st = check_attention(num_q_heads, desc);
+  const pa_status st = check_attention(num_q_heads, max_q_len, desc);
   if (st != PA_OK) return st;
   if (q_dtype != PA_DTYPE_F16 && q_dtype != PA_DTYPE_BF16)
     return fail(PA_ERR_INVALID, "%s: q_dtype must be F16 or BF16", fn);
   if (out_dtype != q_dtype && out_dtype != PA_DTYPE_F32)
     return fail(PA_ERR_INVALID, "%s: out_dtype must be q_dtype or F32", fn);
-  if (num_tokens < 0 || B < 0 || max_context_len < 0 || max_q_len < 0 || max_blocks_per_seq <= 0)
+  if (num_tokens < 0 || B < 0 || max_context_len < 0 || max_blocks_per_seq <= 0)
     return fail(PA_ERR_INVALID, "%s: negative size or max_blocks_per_seq <= 0", fn);
   if (num_tokens > 0 && max_q_len == 0) return fail(PA_ERR_INVALID, "%s: max_q_len is 0 with tokens", fn);
-  if (max_q_len > 65535) return fail(PA_ERR_UNSUPPORTED, "%s: max_q_len above 65535", fn);
   if (max_blocks_per_seq > INT32_MAX / PA_BLOCK_SIZE) return fail(PA_ERR_UNSUPPORTED, "%s: table too wide", fn);
   if (!std::isfinite(scale)) return fail(PA_ERR_INVALID, "%s: scale is not finite", fn);
   if (q_stride < static_cast<int64_t>(num_q_heads) * desc->head_dim || q_stride % 8)
@@ -123,15 +131,14 @@ pa_status pa_block_scaled_attention(const void* q, int32_t q_dtype, int64_t q_st
   // units of work (128-key chunks of every item, and 4 for its start and end) are counted in 32 bits
   int64_t G = 1;
   while (G < num_q_heads / desc->num_kv_heads) G *= 2;
+  const int32_t item = item_rows(num_q_heads, max_q_len, desc), sms = pa::sm_count();
   const int64_t chunks = static_cast<int64_t>(max_context_len) / 128 + 5;
-  const int64_t rows = static_cast<int64_t>(max_q_len) * G;
-  const int32_t item = rows <= 8 ? 8 : rows <= 16 ? 16 : kMaxItemRows;
   const int64_t items = static_cast<int64_t>(num_tokens) * G / item + B;
   if (items * desc->num_kv_heads > INT32_MAX / 2 / chunks)
     return fail(PA_ERR_UNSUPPORTED, "%s: more than 2^30 units of work", fn);
   if (static_cast<int64_t>(num_tokens) * num_q_heads > INT32_MAX)
     return fail(PA_ERR_UNSUPPORTED, "%s: too many query rows", fn);
-  const size_t need = attention_workspace(desc);
+  const size_t need = attention_workspace(item, sms, desc);
   if (!workspace || !pa::aligned16(workspace) || workspace_bytes < need)
     return fail(PA_ERR_INVALID, "%s: workspace NULL, misaligned or %zu of %zu bytes", fn, workspace_bytes, need);
   pa::ScaledAttentionLaunch a;
@@ -157,7 +164,7 @@ pa_status pa_block_scaled_attention(const void* q, int32_t q_dtype, int64_t q_st
   a.out = out;
   a.out_dtype = out_dtype;
   a.workspace = workspace;
-  a.n_cta = pa::sm_count();
+  a.n_cta = sms;
   a.item_rows = item;
   return pa::launch_scaled_attention(a, stream);
 }

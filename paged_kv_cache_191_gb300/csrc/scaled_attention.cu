@@ -33,9 +33,9 @@
 // zeroed and remembered for (dim, row), which end as NaN.
 #include <mutex>
 
-#include "kv_map.h"
 #include "pa_internal.h"
-#include "scaled_common.cuh"
+#include "scaled_rows.cuh"
+#include "tree_maps.h"
 
 namespace pa {
 namespace {
@@ -103,7 +103,7 @@ __device__ __forceinline__ void multiply_scaled(uint8_t* gb, Sync<L> sy, uint32_
         moved = true;
       }
     }
-    if (s.live && ahead < 2) {
+    if (s.live) {
       const int t = s.tile(), i = s.it0 + 2 * s.c, qb = s.i & 1, n = t ? ns1 : ns0;
       if ((n == 0 || test(sy.sfree(t), n - 1)) && (s.c > 0 || test(sy.qfull(qb), s.i >> 1)) && landed(i)) {
         fence_after();
@@ -145,26 +145,50 @@ __device__ __forceinline__ void multiply_scaled(uint8_t* gb, Sync<L> sy, uint32_
   __syncwarp();
 }
 
-// The four terms' columns of 8 rows, summed (the small ones first).
-__device__ __forceinline__ void load_sum8(uint32_t at, int step, float (&f)[8]) {
+// The four terms' columns of 8 rows: on their way, arrived (no use of the registers
+// moves above the wait), summed (the small ones first).
+struct Terms8 {
   uint32_t a[8], b[8], c[8], d[8];
-#define PA_X8(r) "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+};
+__device__ __forceinline__ void terms_load(uint32_t at, int step, Terms8& x) {
+#define PA_X8(c, r) c(r[0]), c(r[1]), c(r[2]), c(r[3]), c(r[4]), c(r[5]), c(r[6]), c(r[7])
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%32];\n\t"
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%33];\n\t"
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16,%17,%18,%19,%20,%21,%22,%23}, [%34];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%24,%25,%26,%27,%28,%29,%30,%31}, [%35];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : PA_X8(a), PA_X8(b), PA_X8(c), PA_X8(d)
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%24,%25,%26,%27,%28,%29,%30,%31}, [%35];"
+      : PA_X8("=r", x.a), PA_X8("=r", x.b), PA_X8("=r", x.c), PA_X8("=r", x.d)
       : "r"(at), "r"(at + step), "r"(at + 2 * step), "r"(at + 3 * step)
       : "memory");
+}
+__device__ __forceinline__ void terms_wait(Terms8& x) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : PA_X8("+r", x.a), PA_X8("+r", x.b), PA_X8("+r", x.c), PA_X8("+r", x.d)
+               :
+               : "memory");
 #undef PA_X8
+}
+__device__ __forceinline__ void terms_sum(const Terms8& x, float (&f)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; i += 2) {
-    auto two = [&](const uint32_t(&x)[8]) { return make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])); };
-    const float2 s = add2(add2(add2(two(d), two(c)), two(b)), two(a));
+    auto two = [&](const uint32_t(&r)[8]) { return make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])); };
+    const float2 s = add2(add2(add2(two(x.d), two(x.c)), two(x.b)), two(x.a));
     f[i] = s.x;
     f[i + 1] = s.y;
+  }
+}
+// Of N rows 8 at a time, the next ones on their way while f sees these: f(row, sums).
+template <int N, typename F>
+__device__ __forceinline__ void terms_each(uint32_t at, int step, F f) {
+  Terms8 x[2];
+  terms_load(at, step, x[0]);
+#pragma unroll
+  for (int j = 0; j < N; j += 8) {
+    terms_wait(x[(j >> 3) & 1]);
+    if (j + 8 < N) terms_load(at + j + 8, step, x[((j >> 3) & 1) ^ 1]);
+    float v[8];
+    terms_sum(x[(j >> 3) & 1], v);
+    f(j, v);
   }
 }
 
@@ -197,16 +221,13 @@ __device__ __forceinline__ int settle_scaled(const KeyLane& x, uint32_t sc, cons
   constexpr int R = L::R;
   const int bar = 2 + x.t;
   float best = -INFINITY;  // of row `lane`
-#pragma unroll 1
-  for (int j = 0; j < R; j += 8) {
-    float f[8];
-    load_sum8(sc + j, R, f);
+  terms_each<R>(sc, R, [&](int j, const float(&f)[8]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float m = warp_max((vis >> (j + e)) & 1u ? fmaf(f[e] * fac[j + e], ks, lv) : -INFINITY);
       if (x.lane == j + e) best = m;
     }
-  }
+  });
   if (x.lane < R) x.scratch[R * x.w4 + x.lane] = best;
   named_bar(bar, 128);
   bool rescale = false;
@@ -225,12 +246,16 @@ __device__ __forceinline__ int settle_scaled(const KeyLane& x, uint32_t sc, cons
   rescale = bar_or(bar, 128, rescale);
   if (rescale) {
 #pragma unroll 1
-    for (int j = 0; j < kParts * R; j += 8) {
-      uint32_t o[8];
-      tmem_ld8(oc + j, o);
+    for (int j = 0; j < kParts * R; j += 32) {
+      uint32_t o[32];
+      tcg::ld32(oc + j, o);
+      tcg::wait_ld();
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * x.scratch[5 * R + ((j + e) & (R - 1))]);
-      tmem_st8(oc + j, o);
+      for (int e = 0; e < 32; ++e) {
+        asm volatile("" : "+r"(o[e]));  // (no use above the wait)
+        o[e] = __float_as_uint(__uint_as_float(o[e]) * x.scratch[5 * R + ((j + e) & (R - 1))]);
+      }
+      tcg::st32(oc + j, o);
     }
     tcg::wait_st();
   }
@@ -296,9 +321,14 @@ __device__ __forceinline__ void write_scaled(const ScaledArgs& sa, const KeyLane
   const uint32_t nan_rows = poison[x.r] | poison[128 + x.r];
 #pragma unroll 1
   for (int j0 = 0; j0 < p.rows; j0 += 8) {
+    Terms8 tu, tv;
+    terms_load(oa + j0, R, tu);
+    terms_load(oa + L::COLS + j0, R, tv);
+    terms_wait(tu);
+    terms_wait(tv);
     float u[8], v[8];
-    load_sum8(oa + j0, R, u);
-    load_sum8(oa + L::COLS + j0, R, v);
+    terms_sum(tu, u);
+    terms_sum(tv, v);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float w0 = wts[j0 + e], w1 = wts[R + j0 + e];
@@ -323,8 +353,8 @@ __device__ __forceinline__ void write_scaled(const ScaledArgs& sa, const KeyLane
 
 template <int R_>
 __global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
-    scaled_attention(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                     const __grid_constant__ ScaledArgs sa) {
+    scaled_keys(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                const __grid_constant__ ScaledArgs sa) {
   using namespace tcg;
   using L = ScaledLay<R_>;
   constexpr int R = L::R, NS = L::NS;
@@ -415,19 +445,21 @@ __global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
         // Exponents less the references, and their maximum.
         auto exponents = [&](float& top) {
           top = -INFINITY;
+          terms_each<R>(sc, R, [&](int j, const float(&f)[8]) {
 #pragma unroll
-          for (int j = 0; j < R; j += 8) {
-            float f[8];
-            load_sum8(sc + j, R, f);
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              const float2 fa = *reinterpret_cast<const float2*>(fac + j + i);
-              const float2 rf = *reinterpret_cast<const float2*>(refs + j + i);
-              const float2 y = fma2(mul2(make_float2(f[i], f[i + 1]), fa), make_float2(ks, ks), rf);
+            for (int i = 0; i < 8; i += 4) {
+              const float4 fa = *reinterpret_cast<const float4*>(fac + j + i);
+              const float4 rf = *reinterpret_cast<const float4*>(refs + j + i);
+              const float2 y = fma2(mul2(make_float2(f[i], f[i + 1]), make_float2(fa.x, fa.y)), make_float2(ks, ks),
+                                    make_float2(rf.x, rf.y));
+              const float2 z = fma2(mul2(make_float2(f[i + 2], f[i + 3]), make_float2(fa.z, fa.w)), make_float2(ks, ks),
+                                    make_float2(rf.z, rf.w));
               e[j + i] = y.x;
               e[j + i + 1] = y.y;
+              e[j + i + 2] = z.x;
+              e[j + i + 3] = z.y;
             }
-          }
+          });
           if (masked) {  // whatever the key's score and scale are
 #pragma unroll
             for (int j = 0; j < R; ++j) e[j] = (vis >> j) & 1u ? e[j] : -INFINITY;
@@ -468,8 +500,7 @@ __global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
             const float2 ll = add2(make_float2(l[i], l[i + 1]), w), y = mul2(w, make_float2(vsc, vsc));
             l[i] = ll.x;
             l[i + 1] = ll.y;
-            // (a weight of 0 must not meet a NaN scale)
-            terms(dev::pack2<__half>(w.x == 0.f ? 0.f : y.x, w.y == 0.f ? 0.f : y.y), h ? p1 : p0);
+            terms(dev::pack2<__half>(y.x, y.y), h ? p1 : p0);
           }
 #pragma unroll
           for (int q = 0; q < kParts; ++q) out[q][j / 4] = upper(p0[q], p1[q]);
@@ -524,10 +555,10 @@ __global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
   teardown(wid, tmem);
 }
 
-template <int R>
-pa_status launch_rows(const ScaledAttentionLaunch& l, cudaStream_t stream) {
-  using L = ScaledLay<R>;
-  const auto kernel = scaled_attention<R>;
+// L: a kernel's layout; kernel: with a thread per key it has no map of q.
+template <typename L, typename K>
+pa_status launch_kernel(const ScaledAttentionLaunch& l, K kernel, cudaStream_t stream) {
+  const char* fn = "pa_block_scaled_attention";
   ScaledArgs sa = {};
   TreeArgs& a = sa.t;
   a.q = l.q;
@@ -549,27 +580,35 @@ pa_status launch_rows(const ScaledAttentionLaunch& l, cudaStream_t stream) {
   a.n_cta = l.n_cta;
   while ((1 << a.gl) < a.G) ++a.gl;
   a.scale_log2 = l.scale * 1.4426950408889634f;
+  if (L::ROWS && l.scale < 0.f) {  // the products negate Q
+    a.scale_log2 = -a.scale_log2;
+    a.negate = 1;
+  }
   a.out_f32 = l.out_dtype == PA_DTYPE_F32;
   a.min_units = 2;
-  a.item_rows = R;
-  a.slot_rows = R;
+  a.item_rows = L::R;
+  a.slot_rows = L::R;
   sa.q_stride = l.q_stride;
   sa.q_bf16 = l.q_dtype == PA_DTYPE_BF16;
-  const size_t rows = static_cast<size_t>(2) * a.n_cta * R;
+  const size_t rows = static_cast<size_t>(2) * a.n_cta * L::R;
   a.part_o = static_cast<float*>(l.workspace);
   a.part_m = a.part_o + rows * L::D;
   a.part_l = a.part_m + rows;
   a.split = reinterpret_cast<int4*>(a.part_l + rows);
 
-  CUtensorMap tmK, tmV;
+  CUtensorMap tm[3];
   for (int v = 0; v < 2; ++v) {
-    const pa_status st = make_kv_map(v ? &tmV : &tmK, v ? l.v_cache : l.k_cache, l.Hkv, l.num_blocks, L::D, 1,
-                                     CU_TENSOR_MAP_DATA_TYPE_UINT8, "pa_block_scaled_attention");
+    const pa_status st = make_kv_map(&tm[v], v ? l.v_cache : l.k_cache, l.Hkv, l.num_blocks, L::D, 1,
+                                     CU_TENSOR_MAP_DATA_TYPE_UINT8, fn);
+    if (st != PA_OK) return st;
+  }
+  if constexpr (L::ROWS) {
+    const pa_status st = make_q_map(&tm[2], l.q, L::D, l.Hq, l.T, l.q_stride, 1 << a.gl,
+                                    sa.q_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, fn);
     if (st != PA_OK) return st;
   }
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices)
-    return fail(PA_ERR_CUDA, "pa_block_scaled_attention: no CUDA device");
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return fail(PA_ERR_CUDA, "%s: no CUDA device", fn);
   static std::once_flag once[kMaxDevices];
   static cudaError_t setup[kMaxDevices];
   std::call_once(once[dev], [dev, kernel] {
@@ -580,25 +619,37 @@ pa_status launch_rows(const ScaledAttentionLaunch& l, cudaStream_t stream) {
     if (setup[dev] == cudaSuccess) setup[dev] = cudaFuncGetAttributes(&fa, kernel);
     if (setup[dev] == cudaSuccess && fa.numRegs * L::THREADS < WANT) setup[dev] = cudaErrorInvalidConfiguration;
   });
-  if (setup[dev] != cudaSuccess)
-    return fail(PA_ERR_CUDA, "pa_block_scaled_attention: %s", cudaGetErrorString(setup[dev]));
-  cudaError_t e = launch_dependent(kernel, dim3(static_cast<unsigned>(a.n_cta)), dim3(L::THREADS), L::BYTES, stream, tmK,
-                                   tmV, sa);
+  if (setup[dev] != cudaSuccess) return fail(PA_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(setup[dev]));
+  const dim3 grid(static_cast<unsigned>(a.n_cta)), block(L::THREADS);
+  cudaError_t e;
+  if constexpr (L::ROWS)
+    e = launch_dependent(kernel, grid, block, L::BYTES, stream, tm[0], tm[1], tm[2], sa);
+  else
+    e = launch_dependent(kernel, grid, block, L::BYTES, stream, tm[0], tm[1], sa);
   if (e == cudaSuccess && l.max_context_len > kKeys) {
-    const dim3 grid(static_cast<unsigned>(a.n_cta), R / kMergeRows), block(32 * kMergeRows);
-    e = sa.q_bf16 ? launch_dependent(tree_merge<__nv_bfloat16, L::D>, grid, block, 0, stream, a)
-                  : launch_dependent(tree_merge<__half, L::D>, grid, block, 0, stream, a);
+    const dim3 mgrid(static_cast<unsigned>(a.n_cta), L::R / kMergeRows), mblock(32 * kMergeRows);
+    e = sa.q_bf16 ? launch_dependent(tree_merge<__nv_bfloat16, L::D>, mgrid, mblock, 0, stream, a)
+                  : launch_dependent(tree_merge<__half, L::D>, mgrid, mblock, 0, stream, a);
   }
   if (e == cudaSuccess) e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(PA_ERR_CUDA, "pa_block_scaled_attention launch: %s", cudaGetErrorString(e));
+  if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));
   return PA_OK;
 }
 
 }  // namespace
 
+// A thread per key while one kv head's rows fit in 32 columns of four terms, then a
+// thread per row.
 pa_status launch_scaled_attention(const ScaledAttentionLaunch& l, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return l.item_rows == 8 ? launch_rows<8>(l, st) : l.item_rows == 16 ? launch_rows<16>(l, st) : launch_rows<32>(l, st);
+  switch (l.item_rows) {
+    case 8: return launch_kernel<ScaledLay<8>>(l, scaled_keys<8>, st);
+    case 16: return launch_kernel<ScaledLay<16>>(l, scaled_keys<16>, st);
+    case 32: return launch_kernel<ScaledLay<32>>(l, scaled_keys<32>, st);
+    default:
+      return l.q_dtype == PA_DTYPE_BF16 ? launch_kernel<ScaledRowsLay<__nv_bfloat16>>(l, scaled_rows<__nv_bfloat16>, st)
+                                        : launch_kernel<ScaledRowsLay<__half>>(l, scaled_rows<__half>, st);
+  }
 }
 
 pa_status read_errors_scaled_attention(uint32_t* flags, bool clear) {

@@ -47,8 +47,10 @@ struct ScaledLay {
   static constexpr uint32_t COL_O = 2 * COLS;
   // log2 of how far below its row's maximum of weight x V scale a reference is set, and
   // of how far that maximum may outgrow it: E5M2 terms of f16 values go from 2^15.9
-  // down to 2^-16, 2^-27 of the largest.
-  static constexpr float LIFT = 11.f, MOVE = 15.5f;
+  // down to 2^-16, rounded: 2^-27 of the largest is the most that a weight is off by
+  // beyond its f16 rounding.  (Lower references are outgrown less often, higher ones
+  // keep more of small weights.)
+  static constexpr float LIFT = 10.f, MOVE = 15.5f;
   static_assert(BYTES <= 232448, "shared memory of one CTA");
   static_assert(COL_O + OPAR * 2 * COLS <= static_cast<int>(kTmemCols), "tensor memory");
 };
@@ -70,12 +72,13 @@ struct KeyLane {
 // ---- E5M2 terms --------------------------------------------------------------
 // An f16 value is the sum of four E5M2 ones: E5M2 is f16's upper byte, so a term is
 // what is left, cut behind its first three bits (11 bits: 3 + 3 + 3 + 2).  The
-// differences are exact; only below 2^-16, E5M2's smallest, is anything lost.
+// differences are exact; only below 2^-16, E5M2's smallest, is anything lost (the
+// last term is rounded there; to a NaN the first one is what counts).
 // h: two values in, the four terms' pairs out (their upper bytes count).
 __device__ __forceinline__ void terms(uint32_t h, uint32_t (&p)[kParts]) {
 #pragma unroll
   for (int i = 0; i < kParts; ++i) {
-    p[i] = h;
+    p[i] = i + 1 < kParts ? h : h + 0x00800080u;
     if (i + 1 < kParts) {
       const uint32_t cut = h & 0xFF00FF00u;
       const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&cut));
@@ -93,27 +96,94 @@ struct Span {
   int qs, n, L, tiles;
   int a;  // tokens before the new ones, in items
 };
-// sum of ceil(x / s) over x = 1 .. m
+// sum of ceil(x / 2^s) over x = 1 .. m
 __device__ __forceinline__ int64_t ceil_sum(int64_t m, int s) {
-  const int64_t q = m / s, r = m - q * s;
-  return s * (q * (q + 1) / 2) + r * (q + 1);
+  const int64_t q = m >> s, r = m - (q << s);
+  return (q * (q + 1) / 2 << s) + r * (q + 1);
 }
 __device__ __forceinline__ int64_t units_before(const Span& x, int k, int s) {
   return static_cast<int64_t>(kItem) * k + ceil_sum(x.a + k, s) - ceil_sum(x.a, s);
 }
+// chunks of item k
+__device__ __forceinline__ int chunks_of(const Span& x, int k, int s) {
+  return k + 1 < x.tiles ? (x.a + k + (1 << s)) >> s : max(1, (x.L + kKeys - 1) / kKeys);
+}
 __device__ __forceinline__ int64_t units_per_head(const Span& x, int s) {
-  if (x.tiles == 0) return 0;
-  return units_before(x, x.tiles - 1, s) + kItem + max(1, (x.L + kKeys - 1) / kKeys);
+  return x.tiles == 0 ? 0 : units_before(x, x.tiles - 1, s) + kItem + chunks_of(x, x.tiles - 1, s);
 }
 
-// The planner warp: this CTA's pieces and their queries.  Piece i + 1 is published
-// before piece i's queries are loaded, so that the producers see two pieces ahead.
+// Piece i's queries: every row scaled by a power of two to 2^14 .. 2^15 (a row of small
+// values keeps its bits beside one of large ones), in E5M2 terms; its factor takes the
+// power back.
+template <typename L>
+__device__ __forceinline__ void load_queries(const ScaledArgs& sa, uint8_t* gb, const Sync<L>& sy, const Piece& p, int i,
+                                             bool& ok) {
+  constexpr int R = L::R;
+  const TreeArgs& a = sa.t;
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  const int heads = (1 << a.gl) - 1;
+  auto load = [&](int r0, uint2(&x)[8]) {  // rows r0 .. r0 + 7, 8 bytes a lane
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int r = r0 + j, h = r & heads;
+      x[j] = make_uint2(0u, 0u);
+      if (r < p.rows && h < a.G)
+        x[j] = __ldg(reinterpret_cast<const uint2*>(
+            static_cast<const uint16_t*>(a.q) + static_cast<size_t>(p.qs + ((p.row0 + r) >> a.gl)) * sa.q_stride +
+            static_cast<size_t>(p.g * a.G + h) * L::D + 4 * lane));
+    }
+  };
+  uint2 x[8], next[8];
+  load(0, next);
+  if (ok && i >= 2) ok = wait_warp(sy.qfree(i & 1), ((i - 2) >> 1) & 1);
+  float* fac = reinterpret_cast<float*>(gb + L::FAC) + (i & 3) * R;
+  uint8_t* to = gb + (i & 1) * L::QTILE + (lane & 3) * 4;
+#pragma unroll 1
+  for (int r0 = 0; r0 < p.rows; r0 += 8) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = next[j];
+    if (r0 + 8 < p.rows) load(r0 + 8, next);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int r = r0 + j;
+      const float2 lo = sa.q_bf16 ? dev::unpack2<__nv_bfloat16>(x[j].x) : dev::unpack2<__half>(x[j].x);
+      const float2 hi = sa.q_bf16 ? dev::unpack2<__nv_bfloat16>(x[j].y) : dev::unpack2<__half>(x[j].y);
+      const float f[4] = {lo.x, lo.y, hi.x, hi.y};
+      uint32_t top = 0;  // the largest finite size
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t size = __float_as_uint(f[e]) & 0x7FFFFFFFu;
+        if (size < 0x7F800000u) top = max(top, size);
+      }
+      top = __reduce_max_sync(FULL, top);
+      const int k = min(14 - (static_cast<int>(top >> 23) - 127), 100);
+      const float up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+      uint32_t p0[kParts], p1[kParts];
+      terms(dev::pack2<__half>(f[0] * up, f[1] * up), p0);
+      terms(dev::pack2<__half>(f[2] * up, f[3] * up), p1);
+#pragma unroll
+      for (int e = 0; e < kParts; ++e)
+        *reinterpret_cast<uint32_t*>(to + (e * R + r) * 128 + (((lane >> 2) ^ (r & 7)) << 4)) = upper(p0[e], p1[e]);
+      if (lane == 0) fac[r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+    }
+  }
+  dev::fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    mbar_arrive(sy.qfull(i & 1));
+    mbar_arrive(factors_full(sy, i));
+  }
+}
+
+// The planner warp: this CTA's pieces, and with a thread per key their queries.  Piece
+// i + 1 is published before piece i's queries are loaded, so that the producers see
+// two pieces ahead.
 template <typename L>
 __device__ __forceinline__ void plan_scaled(const ScaledArgs& sa, uint8_t* gb, Sync<L> sy) {
   constexpr int R = L::R;
   const TreeArgs& a = sa.t;
   const int lane = static_cast<int>(threadIdx.x & 31), me = static_cast<int>(blockIdx.x);
-  const int tpi = R >> a.gl, per = kKeys / tpi;
+  const int tpi = R >> a.gl, per = 31 - __clz(kKeys / tpi);  // tokens of an item; log2 of the items to a chunk
   Span mine{0, 0, 0, 0, 0};
   int group = -1;
   auto read = [&](int g, bool report) {
@@ -165,7 +235,26 @@ __device__ __forceinline__ void plan_scaled(const ScaledArgs& sa, uint8_t* gb, S
     ub += __shfl_sync(FULL, inc, 31);
   }
   Piece* ring = reinterpret_cast<Piece*>(gb + L::PIECE);
-  int u = start;
+  // the item at unit u: tile `tile` of kv head g of sequence b, which is s; `off` of
+  // its units are gone
+  Span s{0, 0, 0, 0, 0};
+  int u = start, g = 0, tile = 0, off = 0;
+  if (start < end) {
+    s = span(b);
+    const int U = static_cast<int>(units_per_head(s, per)), at = start - ub;
+    g = at / U;
+    const int rem = at - g * U;
+    int hi = s.tiles;  // the last that starts at or before rem
+#pragma unroll 1
+    while (hi - tile > 1) {
+      const int mid = (tile + hi) >> 1;
+      if (units_before(s, mid, per) <= rem)
+        tile = mid;
+      else
+        hi = mid;
+    }
+    off = rem - static_cast<int>(units_before(s, tile, per));
+  }
   bool ok = true, more = true;
   int4 sp0 = make_int4(0, 0, 0, 0), sp1 = sp0;
   auto publish_piece = [&](int i) {
@@ -174,47 +263,33 @@ __device__ __forceinline__ void plan_scaled(const ScaledArgs& sa, uint8_t* gb, S
     p.live = 0;
 #pragma unroll 1
     while (u < end && !p.live) {
-      Span s = span(b);
-      int U = static_cast<int>(units_per_head(s, per));
-#pragma unroll 1
-      while (b < a.B && u >= ub + U * a.Hkv) {
-        ub += U * a.Hkv;
-        s = span(++b);
-        U = static_cast<int>(units_per_head(s, per));
-      }
-      if (b >= a.B) {  // (lengths that changed under the kernel)
-        u = end;
-        break;
-      }
-      const int at = u - ub, g = at / U, rem = at - g * U;
-      int lo = 0, hi = s.tiles;  // the item: the last that starts at or before rem
-#pragma unroll 1
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (units_before(s, mid, per) <= rem)
-          lo = mid;
-        else
-          hi = mid;
-      }
-      const int before = static_cast<int>(units_before(s, lo, per));
-      const int cost = (lo + 1 < s.tiles ? static_cast<int>(units_before(s, lo + 1, per)) : U) - before;
-      const int off = rem - before, stop = min(cost, off + end - u), item_end = u - off + cost;
+      const int nch = chunks_of(s, tile, per), cost = nch + kItem, stop = min(cost, off + end - u);
       p.c0 = max(0, off - kItem);
       p.c1 = stop - kItem;
+      if (p.c1 > p.c0) {  // (else the range ends before the item's first chunk)
+        p.live = 1;
+        p.b = b;
+        p.qs = s.qs;
+        p.n = s.n;
+        p.L = s.L;
+        p.g = g;
+        p.row0 = tile * R;
+        p.rows = min(R, (s.n << a.gl) - p.row0);
+        p.slot = p.c0 == 0 && p.c1 == nch ? -1 : 2 * me + (i == 0 ? 0 : 1);
+        if (p.c0 == 0 && p.c1 < nch) {  // the item goes on in the next CTAs: what the merge needs
+          sp0 = make_int4((u - off + cost - 1) / upc - me + 1, p.slot, s.qs, p.row0);
+          sp1 = make_int4(g, p.rows, 1, 0);
+        }
+      }
       u += stop - off;
-      if (p.c1 <= p.c0) continue;  // the range ends before the item's first chunk
-      p.live = 1;
-      p.b = b;
-      p.qs = s.qs;
-      p.n = s.n;
-      p.L = s.L;
-      p.g = g;
-      p.row0 = lo * R;
-      p.rows = min(R, (s.n << a.gl) - p.row0);
-      p.slot = p.c0 == 0 && p.c1 == cost - kItem ? -1 : 2 * me + (i == 0 ? 0 : 1);
-      if (p.c0 == 0 && p.c1 < cost - kItem) {  // the item goes on in the next CTAs: what the merge needs
-        sp0 = make_int4((item_end - 1) / upc - me + 1, p.slot, s.qs, p.row0);
-        sp1 = make_int4(g, p.rows, 1, 0);
+      off = 0;  // (the item's end, or the range's)
+      if (++tile >= s.tiles) {
+        tile = 0;
+        if (++g >= a.Hkv) {
+          g = 0;
+          do s = span(++b);
+          while (s.tiles == 0 && b + 1 < a.B);
+        }
       }
     }
     p.last = u >= end;  // (or only an item's start is left)
@@ -225,68 +300,26 @@ __device__ __forceinline__ void plan_scaled(const ScaledArgs& sa, uint8_t* gb, S
     }
     __syncwarp();
   };
-  // Piece i's queries: every row scaled by a power of two to 2^14 .. 2^15 (a row of
-  // small values keeps its bits beside one of large ones), in E5M2 terms; its factor
-  // takes the power back.
-  auto queries = [&](int i) {
-    const Piece p = ring[i & 3];
-    if (ok && i >= 2) ok = wait_warp(sy.qfree(i & 1), ((i - 2) >> 1) & 1);
-    float* fac = reinterpret_cast<float*>(gb + L::FAC) + (i & 3) * R;
-    uint8_t* to = gb + (i & 1) * L::QTILE + (lane & 3) * 4;
-    const int heads = (1 << a.gl) - 1;
-#pragma unroll 1
-    for (int r0 = 0; r0 < R; r0 += 8) {
-      uint2 x[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int r = r0 + j, h = r & heads;
-        x[j] = make_uint2(0u, 0u);
-        if (r < p.rows && h < a.G)
-          x[j] = __ldg(reinterpret_cast<const uint2*>(
-              static_cast<const uint16_t*>(a.q) + static_cast<size_t>(p.qs + ((p.row0 + r) >> a.gl)) * sa.q_stride +
-              static_cast<size_t>(p.g * a.G + h) * L::D + 4 * lane));
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int r = r0 + j;
-        const float2 lo = sa.q_bf16 ? dev::unpack2<__nv_bfloat16>(x[j].x) : dev::unpack2<__half>(x[j].x);
-        const float2 hi = sa.q_bf16 ? dev::unpack2<__nv_bfloat16>(x[j].y) : dev::unpack2<__half>(x[j].y);
-        const float f[4] = {lo.x, lo.y, hi.x, hi.y};
-        uint32_t top = 0;  // the largest finite size
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t s = __float_as_uint(f[e]) & 0x7FFFFFFFu;
-          if (s < 0x7F800000u) top = max(top, s);
-        }
-        top = __reduce_max_sync(FULL, top);
-        const int k = min(14 - (static_cast<int>(top >> 23) - 127), 100);
-        const float up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
-        uint32_t p0[kParts], p1[kParts];
-        terms(dev::pack2<__half>(f[0] * up, f[1] * up), p0);
-        terms(dev::pack2<__half>(f[2] * up, f[3] * up), p1);
-#pragma unroll
-        for (int e = 0; e < kParts; ++e)
-          *reinterpret_cast<uint32_t*>(to + (e * R + r) * 128 + (((lane >> 2) ^ (r & 7)) << 4)) = upper(p0[e], p1[e]);
-        if (lane == 0) fac[r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-      }
-    }
-    dev::fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(sy.qfull(i & 1));
-      mbar_arrive(factors_full(sy, i));
-    }
-  };
 #pragma unroll 1
   for (int i = 0; more; ++i) {
     publish_piece(i);
-    if (i > 0) queries(i - 1);
+    if constexpr (!L::ROWS) {
+      if (i > 0) load_queries<L>(sa, gb, sy, ring[(i - 1) & 3], i - 1, ok);
+    }
   }
   if (lane == 0) {
     a.split[2 * blockIdx.x] = sp0;
     a.split[2 * blockIdx.x + 1] = sp1;
     if (!ok) flag(PA_DEVERR_TIMEOUT);
   }
+}
+
+// A block's scales (K, V) into their places.  A V scale that is no number is to meet no
+// weight but of the tokens that see the block: theirs become NaN by K's.
+__device__ __forceinline__ void put_scales(float* to, float2 s) {
+  const bool fine = fabsf(s.y) < INFINITY;
+  to[0] = fine ? s.x : NAN;
+  to[8] = fine ? s.y : 0.f;
 }
 
 // The producer warps, one for K (and both tensors' scales) and one for V: a piece's
@@ -360,10 +393,7 @@ __device__ __forceinline__ void produce_scaled(const TreeArgs& a, const CUtensor
       if (!V) {
         // (a place is free: its chunk's scores were read before those two chunks on were computed)
         float* to = reinterpret_cast<float*>(gb + L::SC) + (chunk & 7) * 16;
-        if ((lane >> 3) == k4) {
-          to[lane & 7] = sc.x;
-          to[8 + (lane & 7)] = sc.y;
-        }
+        if ((lane >> 3) == k4) put_scales(to + (lane & 7), sc);
         __syncwarp();
         if (lane == 0) mbar_arrive(scales_full(sy, chunk));
         if (c + 1 == p.c1 ? more_n : k4 == 3) scales(c + 1 == p.c1 ? pn.g : p.g);

@@ -61,13 +61,12 @@
 // context's end are zeroed in shared memory, and a node's V row that holds an
 // infinity or NaN (a slot nothing was ever written to) is zeroed too and added
 // to O by hand for the rows that do see it, so it reaches no other row.
-#include <cudaTypedefs.h>
-
 #include <mutex>
 
 #include "kv_map.h"
 #include "pa_internal.h"
 #include "tree_keys.cuh"
+#include "tree_maps.h"
 #include "tree_merge.cuh"
 #include "tree_rows.cuh"
 
@@ -77,44 +76,6 @@ namespace {
 constexpr int kMaxDevices = 64;
 
 // ---- launch ------------------------------------------------------------------
-pa_status encode_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* p, const cuuint64_t* dims,
-                 const cuuint64_t* strides, const cuuint32_t* box) {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  }();
-  if (!fn) return fail(PA_ERR_CUDA, "pa_tree_attention: cuTensorMapEncodeTiled unavailable");
-  const cuuint32_t one[5] = {1, 1, 1, 1, 1};
-  const CUresult r = fn(m, dt, rank, const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS)
-    return fail(PA_ERR_CUDA, "pa_tree_attention: tensor map encode failed (%d)", static_cast<int>(r));
-  return PA_OK;
-}
-// TMA map over a 16-bit cache of head_dim 128 whose box is one (block, kv
-// head) tile, landing as [group of 8 tokens][span of 64 dims][8][128 B]: the
-// 8-row groups of a span are evenly spaced over a run of tiles, as one UMMA
-// operand of many tiles wants them.
-pa_status make_group_map(CUtensorMap* m, const void* cache, int Hkv, int num_blocks, CUtensorMapDataType dt) {
-  const cuuint64_t dims[5] = {64, 8, 2, static_cast<cuuint64_t>(2) * Hkv, static_cast<cuuint64_t>(num_blocks)};
-  const cuuint64_t strides[4] = {256, 128, 2048, static_cast<cuuint64_t>(4096) * Hkv};
-  const cuuint32_t box[5] = {64, 8, 2, 2, 1};
-  return encode_map(m, dt, 5, cache, dims, strides, box);
-}
-// TMA map over q [T][Hq][D] whose box is a 64-dim span of gp heads (a group,
-// padded to a power of two) of as many nodes as make 32 rows.
-pa_status make_q_map(CUtensorMap* m, const void* q, int D, int Hq, int T, int gp, CUtensorMapDataType dt) {
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hq), static_cast<cuuint64_t>(T)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(D) * 2 * Hq};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(gp), static_cast<cuuint32_t>(gp < 32 ? 32 / gp : 1)};
-  return encode_map(m, dt, 3, q, dims, strides, box);
-}
-
 template <typename KT, typename T, int D, bool ROWS>
 pa_status launch_t(const TreeLaunch& l, CUtensorMapDataType dt, cudaStream_t stream) {
   using L = Lay<KT, T, D, ROWS>;
@@ -168,13 +129,14 @@ pa_status launch_t(const TreeLaunch& l, CUtensorMapDataType dt, cudaStream_t str
     CUtensorMap* m = v ? &tmV : &tmK;
     const void* cache = v ? l.v_cache : l.k_cache;
     const pa_status st = D * EB == 256
-                             ? make_group_map(m, cache, l.Hkv, l.num_blocks, dt)
+                             ? make_group_map(m, cache, l.Hkv, l.num_blocks, dt, "pa_tree_attention")
                              : make_kv_map(m, cache, l.Hkv, l.num_blocks, D * EB, EB, dt, "pa_tree_attention");
     if (st != PA_OK) return st;
   }
-  const pa_status sq = make_q_map(&tmQ, l.q, D, l.Hq, l.T, 1 << a.gl,
+  const pa_status sq = make_q_map(&tmQ, l.q, D, l.Hq, l.T, static_cast<int64_t>(l.Hq) * D, 1 << a.gl,
                                   std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                                                 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+                                                                 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                                  "pa_tree_attention");
   if (sq != PA_OK) return sq;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices)

@@ -88,7 +88,7 @@ SIGNATURES = {
     "pa_draft_verify": (C.c_int, [_P, _P, _I64, _P, _I64, _I32, _P, _P, _P, _I32, _I32, _I32, _P, _P, _P, _P]),
     "pa_block_scaled_append": (C.c_int, [_P, _P, _I32, _I64, _I64, _P, _I32, _P, _I32, _P, _I32, _P, _P, _P, _P,
                                          C.POINTER(CacheDesc), _P]),
-    "pa_block_scaled_attention_workspace_size": (C.c_size_t, [_I32, C.POINTER(CacheDesc)]),
+    "pa_block_scaled_attention_workspace_size": (C.c_size_t, [_I32, _I32, C.POINTER(CacheDesc)]),
     "pa_block_scaled_attention": (C.c_int, [_P, _I32, _I64, _P, _I32, _I32, _P, _P, _P, _P, _P, _I32, _P, _I32, _I32,
                                             _I32, _F, _P, _I32, C.POINTER(CacheDesc), _P, C.c_size_t, _P]),
     "pa_block_scaled_copy": (C.c_int, [_P, _P, _P, _P, _I32, _P, _P, _P, _P, _I32, _P, _I64, C.POINTER(CacheDesc),
@@ -621,13 +621,13 @@ def block_scaled_append(k, v, q_start, block_tables, context_lens, k_cache, v_ca
 
 
 @functools.lru_cache(maxsize=256)
-def _scaled_workspace(dev, num_q_heads, shape, dtype):
+def _scaled_workspace(dev, num_q_heads, max_q_len, shape, dtype):
     """Bytes on the current device, `dev` (their number goes by its SMs)."""
-    return int(lib().pa_block_scaled_attention_workspace_size(num_q_heads, C.byref(_desc_of(shape, dtype))))
+    return int(lib().pa_block_scaled_attention_workspace_size(num_q_heads, max_q_len, C.byref(_desc_of(shape, dtype))))
 
 
-def block_scaled_attention_workspace_size(num_q_heads, k_cache):
-    return int(lib().pa_block_scaled_attention_workspace_size(num_q_heads, C.byref(cache_desc(k_cache))))
+def block_scaled_attention_workspace_size(num_q_heads, max_q_len, k_cache):
+    return int(lib().pa_block_scaled_attention_workspace_size(num_q_heads, int(max_q_len), C.byref(cache_desc(k_cache))))
 
 
 def block_scaled_attention(q, q_start, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
@@ -651,8 +651,8 @@ def block_scaled_attention(q, q_start, k_cache, v_cache, k_scale, v_scale, block
         raise ValueError("out must be [T, Hq, D]")
     L = lib()
     if workspace is None:
-        workspace = _empty(_scaled_workspace(dev, Hq, k_cache.shape, k_cache.dtype), torch.uint8, q.device, stream,
-                           result=False)
+        workspace = _empty(_scaled_workspace(dev, Hq, int(max_q_len), k_cache.shape, k_cache.dtype), torch.uint8, q.device,
+                           stream, result=False)
     _check(L.pa_block_scaled_attention(q.data_ptr(), _dtype(q, "q"), qs, q_start.data_ptr(), T, int(max_q_len),
                                        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                        block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),

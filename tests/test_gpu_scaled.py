@@ -142,12 +142,13 @@ def test_append_flags_what_it_cannot_store():
 def attend(w, cs=None, out_dtype=torch.float32, q=None, max_len=None, max_q=None, **kw):
     cs = cs or caches(w)
     q = dev(w.q) if q is None else q
-    need = ops.block_scaled_attention_workspace_size(w.Hq, cs[0])
+    max_q = max_q or max(1, int(w.sizes.max(initial=0)))
+    need = ops.block_scaled_attention_workspace_size(w.Hq, max_q, cs[0])
     ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)  # NaN floats: stale scratch must not leak
     out = torch.full(w.q.shape, float("nan"), dtype=out_dtype, device=DEV)
     ops.block_scaled_attention(q, dev(w.q_start), *cs, dev(w.tables), dev(w.lens),
-                               max_len or max(1, int(w.lens.max(initial=0))),
-                               max_q or max(1, int(w.sizes.max(initial=0))), w.scale, out=out, workspace=ws, **kw)
+                               max_len or max(1, int(w.lens.max(initial=0))), max_q, w.scale, out=out, workspace=ws,
+                               **kw)
     torch.cuda.synchronize()
     return out.cpu()
 

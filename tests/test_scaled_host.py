@@ -147,9 +147,10 @@ def test_attention_refuses(palib, desc_kw, kw, status):
 
 
 def test_attention_workspace_size(palib):
-    assert palib.pa_block_scaled_attention_workspace_size(4, C.byref(_d8())) > 0
-    assert palib.pa_block_scaled_attention_workspace_size(3, C.byref(_d8())) == 0
-    assert palib.pa_block_scaled_attention_workspace_size(4, C.byref(_desc())) == 0
+    size = palib.pa_block_scaled_attention_workspace_size
+    assert 0 < size(4, 1, C.byref(_d8())) < size(4, 8, C.byref(_d8())) < size(4, 100, C.byref(_d8()))
+    assert size(4, 100, C.byref(_d8())) == size(4, 60000, C.byref(_d8()))
+    assert size(3, 1, C.byref(_d8())) == size(4, 1, C.byref(_desc())) == size(4, -1, C.byref(_d8())) == 0
 
 
 def _copy(d, **kw):
