@@ -23,9 +23,10 @@ pa_status check_scaled(const pa_cache_desc* d, const char* fn) {
 // power of two of them.
 constexpr int32_t kMaxHeads = 32;
 int32_t item_rows(int32_t num_q_heads, int32_t max_q_len, const pa_cache_desc* d) {
-  int64_t rows = 1;
-  while (rows < num_q_heads / d->num_kv_heads) rows *= 2;
-  rows *= max_q_len;
+  int64_t heads = 1;
+  while (heads < num_q_heads / d->num_kv_heads) heads *= 2;
+  const int64_t rows = heads * max_q_len;
+  if (rows <= 40 && heads <= 8 && rows > 32) return 40;  // (whole tokens)
   return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
 }
 

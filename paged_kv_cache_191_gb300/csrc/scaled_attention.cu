@@ -60,36 +60,31 @@ __device__ __forceinline__ void multiply_scaled(uint8_t* gb, Sync<L> sy, uint32_
   using namespace tcg;
   constexpr int NS = L::NS;
   bool ok = true;
-  Cursor<L> s, o;
-  auto same = [&](Cursor<L>& x) {
-    x.live = uniform(x.live);
-    x.nc = uniform(x.nc);
-  };
+  Units<L> s, o;  // (a unit a chunk)
   s.start(sy, gb, ok);
   o.start(sy, gb, ok);
-  same(s);
-  same(o);
-  int ahead = 0, spin = 0;                 // chunks whose S^T is issued and O^T not
+  int spin = 0;
   int ns0 = 0, ns1 = 0, no0 = 0, no1 = 0;  // S^T and O^T issued per tile
   int pieces_over = 0;                     // pieces that both warpgroups are done with
   uint64_t t0 = 0;
   auto test = [&](uint32_t bar, int parity) { return __all_sync(FULL, dev::mbar_test(bar, parity & 1)) != 0; };
   auto landed = [&](int i) { return test(sy.full(i % NS), i / NS); };
 #pragma unroll 1
-  while (o.live) {
+  while (o.k.live) {
     bool moved = false;
-    if (ahead > 0) {
-      const int t = o.tile(), i = o.it0 + 2 * o.c + 1;
+    if (ns0 + ns1 > no0 + no1) {
+      const int t = o.tile, i = o.k.it0 + 2 * o.k.c + 1;
       // (a piece's first products wait for the piece that had its accumulators)
-      const int over = o.c < 2 ? o.i - (L::OPAR - 1) : 0;
+      const bool fresh = o.k.c < 2;
+      const int over = fresh ? o.k.i - (L::OPAR - 1) : 0;
       if (pieces_over < over && test(sy.ofree(pieces_over & 1), pieces_over >> 1)) ++pieces_over;
       if (pieces_over >= over && test(sy.pfull(t), t ? no1 : no0) && landed(i)) {
         fence_after();
         const uint32_t id = idesc_f8(L::COLS, true);
         const uint64_t vd = sdesc(sy.base + L::RING + (i % NS) * L::SLOT, 16, 1024);
         const uint64_t pd = sdesc(sy.base + L::P0 + t * 16384, 16, 1024);
-        const uint32_t od = tmem + L::COL_O + ((o.i & (L::OPAR - 1)) * 2 + t) * L::COLS;
-        const uint32_t acc = o.c >= 2 ? 1u : 0u;
+        const uint32_t od = tmem + L::COL_O + ((o.k.i & (L::OPAR - 1)) * 2 + t) * L::COLS;
+        const uint32_t acc = fresh ? 0u : 1u;
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) mma_f8(od, vd + ((kk * 4096) >> 4), pd + ((kk * 4096) >> 4), id, kk > 0 ? 1u : acc);
@@ -98,30 +93,30 @@ __device__ __forceinline__ void multiply_scaled(uint8_t* gb, Sync<L> sy, uint32_
         }
         __syncwarp();
         ++(t ? no1 : no0);
-        --ahead;
-        if (o.next(sy, gb, ok)) same(o);
+        o.next(sy, gb, ok);
         moved = true;
       }
     }
-    if (s.live) {
-      const int t = s.tile(), i = s.it0 + 2 * s.c, qb = s.i & 1, n = t ? ns1 : ns0;
-      if ((n == 0 || test(sy.sfree(t), n - 1)) && (s.c > 0 || test(sy.qfull(qb), s.i >> 1)) && landed(i)) {
+    if (s.k.live) {
+      const int t = s.tile, i = s.k.it0 + 2 * s.k.c, qb = s.k.i & 1, n = t ? ns1 : ns0;
+      if ((n == 0 || test(sy.sfree(t), n - 1)) &&
+          (s.k.c > 0 || test(sy.qfull(qb), s.k.i >> 1)) && landed(i)) {
         fence_after();
         const uint32_t id = idesc_f8(L::COLS, false);
         const uint64_t kd = sdesc(sy.base + L::RING + (i % NS) * L::SLOT, 16, 1024);
         const uint64_t qd = sdesc(sy.base + qb * L::QTILE, 16, 1024);
         const uint32_t sd = tmem + L::COLS * t;
+        const bool over = s.k.c + 1 == s.k.nc;
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) mma_f8(sd, kd + ((kk * 32) >> 4), qd + ((kk * 32) >> 4), id, kk > 0 ? 1u : 0u);
           commit(sy.sfull(t));
           commit(sy.empty(i % NS));
-          if (s.c + 1 == s.nc) commit(sy.qfree(qb));
+          if (over) commit(sy.qfree(qb));
         }
         __syncwarp();
         ++(t ? ns1 : ns0);
-        ++ahead;
-        if (s.next(sy, gb, ok)) same(s);
+        s.next(sy, gb, ok);
         moved = true;
       }
     }
@@ -145,34 +140,29 @@ __device__ __forceinline__ void multiply_scaled(uint8_t* gb, Sync<L> sy, uint32_
   __syncwarp();
 }
 
-// The four terms' columns of 8 rows: on their way, arrived (no use of the registers
-// moves above the wait), summed (the small ones first).
+// The terms' columns of 8 rows: on their way, arrived (no use of the registers moves
+// above the wait), summed (the small ones first).
 struct Terms8 {
-  uint32_t a[8], b[8], c[8], d[8];
+  uint32_t a[8], b[8], c[8];
 };
 __device__ __forceinline__ void terms_load(uint32_t at, int step, Terms8& x) {
 #define PA_X8(c, r) c(r[0]), c(r[1]), c(r[2]), c(r[3]), c(r[4]), c(r[5]), c(r[6]), c(r[7])
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%32];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%33];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16,%17,%18,%19,%20,%21,%22,%23}, [%34];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%24,%25,%26,%27,%28,%29,%30,%31}, [%35];"
-      : PA_X8("=r", x.a), PA_X8("=r", x.b), PA_X8("=r", x.c), PA_X8("=r", x.d)
-      : "r"(at), "r"(at + step), "r"(at + 2 * step), "r"(at + 3 * step)
-      : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%24];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%25];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16,%17,%18,%19,%20,%21,%22,%23}, [%26];"
+      : PA_X8("=r", x.a), PA_X8("=r", x.b), PA_X8("=r", x.c)
+      : "r"(at), "r"(at + step), "r"(at + 2 * step));
 }
 __device__ __forceinline__ void terms_wait(Terms8& x) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : PA_X8("+r", x.a), PA_X8("+r", x.b), PA_X8("+r", x.c), PA_X8("+r", x.d)
-               :
-               : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : PA_X8("+r", x.a), PA_X8("+r", x.b), PA_X8("+r", x.c));
 #undef PA_X8
 }
 __device__ __forceinline__ void terms_sum(const Terms8& x, float (&f)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; i += 2) {
     auto two = [&](const uint32_t(&r)[8]) { return make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])); };
-    const float2 s = add2(add2(add2(two(x.d), two(x.c)), two(x.b)), two(x.a));
+    const float2 s = add2(add2(two(x.c), two(x.b)), two(x.a));
     f[i] = s.x;
     f[i + 1] = s.y;
   }
@@ -192,7 +182,8 @@ __device__ __forceinline__ void terms_each(uint32_t at, int step, F f) {
   }
 }
 
-// Sum over the warp's lanes of N values a lane: lane j * (32 / N) gets value j's.
+// Sum over the warp's lanes of N values a lane, N a power of two: lane j * (32 / N) gets
+// value j's.
 template <int N>
 __device__ __forceinline__ float lane_sums(float (&v)[N], int lane) {
   int bit = 16;
@@ -211,24 +202,23 @@ __device__ __forceinline__ float lane_sums(float (&v)[N], int lane) {
   return x;
 }
 
-// New references from the scores in tensor memory, where a row has none yet or an
-// exponent outgrew it; O^T moves with them.  alpha: what the rows' l are to be
-// multiplied by, in scratch[5 R ..], if the result's bit 0 is set.  Bit 1: some
-// row still has no reference.
+// New references where a row has none yet or an exponent outgrew it; O^T and the
+// exponents e move with them.  alpha: what the rows' l are to be multiplied by, in
+// scratch[5 R ..], if the result's bit 0 is set.  Bit 1: some row still has no reference.
 template <typename L>
-__device__ __forceinline__ int settle_scaled(const KeyLane& x, uint32_t sc, const float* fac, float* refs, float ks, float lv,
-                                             uint32_t vis, uint32_t oc, bool exists, bool& seen, float& ref) {
+__device__ __forceinline__ int settle_scaled(const KeyLane& x, float (&e)[L::R], float* refs, float lv, uint32_t oc,
+                                             bool exists, bool& seen, float& ref) {
   constexpr int R = L::R;
   const int bar = 2 + x.t;
   float best = -INFINITY;  // of row `lane`
-  terms_each<R>(sc, R, [&](int j, const float(&f)[8]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float m = warp_max((vis >> (j + e)) & 1u ? fmaf(f[e] * fac[j + e], ks, lv) : -INFINITY);
-      if (x.lane == j + e) best = m;
-    }
-  });
-  if (x.lane < R) x.scratch[R * x.w4 + x.lane] = best;
+  for (int j = 0; j < R; ++j) {
+    e[j] -= refs[j];  // (back to the scores; a first chunk's are: its references are 0)
+    const float m = warp_max(e[j] + lv);
+    if (x.lane == (j & 31)) best = m;
+    if (j == 31 && R > 32) x.scratch[R * x.w4 + x.lane] = best;
+  }
+  if (x.lane < (R > 32 ? R - 32 : R)) x.scratch[R * x.w4 + (R > 32 ? 32 : 0) + x.lane] = best;
   named_bar(bar, 128);
   bool rescale = false;
   if (x.r < R) {
@@ -240,39 +230,39 @@ __device__ __forceinline__ int settle_scaled(const KeyLane& x, uint32_t sc, cons
       ref = cm - L::LIFT;
       seen = true;
     }
-    refs[x.r] = exists ? -ref : -INFINITY;  // rows that do not exist get weight 0
+    if (exists) refs[x.r] = -ref;
     x.scratch[5 * R + x.r] = alpha;
   }
+  const bool unset = bar_or(bar, 128, x.r < R && !seen);
   rescale = bar_or(bar, 128, rescale);
+#pragma unroll
+  for (int j = 0; j < R; ++j) e[j] += refs[j];
   if (rescale) {
 #pragma unroll 1
-    for (int j = 0; j < kParts * R; j += 32) {
-      uint32_t o[32];
-      tcg::ld32(oc + j, o);
-      tcg::wait_ld();
+    for (int j = 0; j < kParts * R; j += 8) {
+      uint32_t o[8];
+      tmem_ld8(oc + j, o);
+      const float* by = x.scratch + 5 * R + j % R;
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        asm volatile("" : "+r"(o[e]));  // (no use above the wait)
-        o[e] = __float_as_uint(__uint_as_float(o[e]) * x.scratch[5 * R + ((j + e) & (R - 1))]);
-      }
-      tcg::st32(oc + j, o);
+      for (int q = 0; q < 8; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * by[q]);
+      tmem_st8(oc + j, o);
     }
     tcg::wait_st();
   }
-  const bool unset = bar_or(bar, 128, x.r < R && !seen);
   return (rescale ? 1 : 0) | (unset ? 2 : 0);
 }
 
 // V rows that not every row sees: those that none does are zeroed, NaN codes in the
-// others too, and noted for the rows (vis) that do see them.  Thread r has key r's.
+// others too, and noted as the first row that sees one.  Thread r has key r's; the rows
+// from `from` on see it.
 template <typename L>
-__device__ __forceinline__ void guard_scaled(const KeyLane& x, uint8_t* vslot, uint32_t* poison, uint32_t vis) {
+__device__ __forceinline__ void guard_scaled(const KeyLane& x, uint8_t* vslot, int* poison, int from) {
   uint8_t* row = vslot + x.r * 128;
-  if (vis == FULL) return;
-#pragma unroll 2
+  if (from <= 0) return;
+#pragma unroll 1
   for (int ch = 0; ch < 8; ++ch) {  // (in the order that the lanes' banks differ)
     uint4* at = reinterpret_cast<uint4*>(row + ((ch ^ x.r) & 7) * 16);
-    if (vis == 0u) {
+    if (from >= L::R) {
       *at = make_uint4(0, 0, 0, 0);
       continue;
     }
@@ -280,22 +270,24 @@ __device__ __forceinline__ void guard_scaled(const KeyLane& x, uint8_t* vslot, u
 #pragma unroll
     for (int i = 0; i < 4; ++i) bad |= __vcmpeq4(w[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
     if (bad == 0u) continue;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
 #pragma unroll 1
-    for (int i = 0; i < 16; ++i) {
-      const uint32_t sh = 8 * (i & 3);
-      if (((w[i >> 2] >> sh) & 0x7Fu) != 0x7Fu) continue;
-      w[i >> 2] &= ~(0xFFu << sh);
-      atomicOr(poison + 16 * ch + i, vis);  // (chunk ch of the row is at ch ^ its number)
+      for (int sh = 0; sh < 32; sh += 8) {
+        if (((w[i] >> sh) & 0x7Fu) != 0x7Fu) continue;
+        w[i] &= ~(0xFFu << sh);
+        atomicMin(poison + 16 * ch + 4 * i + sh / 8, from);  // (chunk ch of the row is at ch ^ its number)
+      }
     }
     *at = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
-// The rows of a piece out, by the warpgroup that joins: O^T of both tiles times the
-// rows' weights, a thread a dim.
+// The rows of a piece out, by the warpgroup that joins them, a thread a dim: O^T of both
+// tiles times the rows' weights.
 template <typename L>
 __device__ __forceinline__ void write_scaled(const ScaledArgs& sa, const KeyLane& x, const Piece& p, const float2* pubs,
-                                             const uint32_t* poison, uint32_t oa, bool exists) {
+                                             int nan_from, uint32_t oa, bool exists) {
   constexpr int R = L::R, D = L::D;
   const TreeArgs& a = sa.t;
   const bool direct = p.slot < 0;
@@ -310,7 +302,7 @@ __device__ __forceinline__ void write_scaled(const ScaledArgs& sa, const KeyLane
     wts[x.r] = w0 * inv;
     wts[R + x.r] = w1 * inv;
     // where the row goes, in rows of out or of the partials
-    const int at = p.row0 + x.r, h = x.r & ((1 << a.gl) - 1);
+    const int at = p.row0 + x.r, h = at & ((1 << a.gl) - 1);
     place[x.r] = !exists ? -1 : direct ? (p.qs + (at >> a.gl)) * a.Hq + p.g * a.G + h : p.slot * a.slot_rows + x.r;
     if (!direct && exists) {
       a.part_m[place[x.r]] = m;
@@ -318,15 +310,14 @@ __device__ __forceinline__ void write_scaled(const ScaledArgs& sa, const KeyLane
     }
   }
   named_bar(2 + x.t, 128);
-  const uint32_t nan_rows = poison[x.r] | poison[128 + x.r];
 #pragma unroll 1
   for (int j0 = 0; j0 < p.rows; j0 += 8) {
     Terms8 tu, tv;
+    float u[8], v[8];
     terms_load(oa + j0, R, tu);
     terms_load(oa + L::COLS + j0, R, tv);
     terms_wait(tu);
     terms_wait(tv);
-    float u[8], v[8];
     terms_sum(tu, u);
     terms_sum(tv, v);
 #pragma unroll
@@ -334,7 +325,7 @@ __device__ __forceinline__ void write_scaled(const ScaledArgs& sa, const KeyLane
       const float w0 = wts[j0 + e], w1 = wts[R + j0 + e];
       float o = w0 == 0.f ? 0.f : u[e] * w0;
       if (w1 != 0.f) o = fmaf(v[e], w1, o);
-      if ((nan_rows >> (j0 + e)) & 1u) o = NAN;
+      if (j0 + e >= nan_from) o = NAN;
       const int at = place[j0 + e];
       if (at < 0) continue;
       const size_t i = static_cast<size_t>(at) * D + x.r;
@@ -370,7 +361,7 @@ __global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
     for (int i = 0; i < 8; ++i) dev::mbar_init(scales_full(sy, i), 1);
     for (int i = 0; i < 4; ++i) dev::mbar_init(factors_full(sy, i), 1);
   }
-  for (int i = static_cast<int>(threadIdx.x); i < 512; i += L::THREADS) reinterpret_cast<uint32_t*>(gb + L::POISON)[i] = 0u;
+  for (int i = static_cast<int>(threadIdx.x); i < 512; i += L::THREADS) reinterpret_cast<int*>(gb + L::POISON)[i] = R;
   const uint32_t tmem = setup<L>(gb, sy, wid, &tmK, &tmV, &tmK);
 
   if (wid == 0) {
@@ -408,18 +399,19 @@ __global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
 #pragma unroll 1
     for (;; k.close()) {
       k.open(sy, gb, ok);
+      const Piece& p = k.p;
+      const bool exists = r < p.rows && (r & ((1 << a.gl) - 1)) < a.G;  // row r (r < R)
+      if (r < R) refs[r] = exists ? 0.f : -INFINITY;  // (a row that does not exist gets weight 0)
       // The barriers inside a piece have no limit, so where one warp has given up a
       // wait the whole warpgroup leaves, here.  (And every warp has read the sums of l
       // that the piece before left in the scratch.)
       ok = !bar_or(bar, 128, !ok);
       if (!ok || !__all_sync(FULL, k.live)) break;
-      const Piece& p = k.p;
-      const int pp = k.i & 1, shift = p.L - p.n, i0 = p.row0 >> a.gl;  // the piece's first token
+      const int pp = k.i & 1, shift = p.L - p.n, i0 = p.row0 >> a.gl;  // the item's first token
       const uint32_t oc = x.tl + L::COL_O + ((k.i & (L::OPAR - 1)) * 2 + t) * L::COLS;
       const float* fac = reinterpret_cast<const float*>(gb + L::FAC) + (k.i & 3) * R;
-      uint32_t* poison = reinterpret_cast<uint32_t*>(gb + L::POISON) + 256 * pp;
-      const bool exists = r < p.rows && (r & ((1 << a.gl) - 1)) < a.G;  // row r (r < R)
-      bool seen = !exists, unset = true;  // row r has a reference; some row may have none
+      int* poison = reinterpret_cast<int*>(gb + L::POISON) + 256 * pp;
+      bool seen = !exists, unset = true;  // row r has a reference (or does not exist); some row may have none
       float ref = 0.f, l[R];
 #pragma unroll
       for (int j = 0; j < R; ++j) l[j] = 0.f;
@@ -435,16 +427,11 @@ __global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
         fence_after();
         const float* scales = reinterpret_cast<const float*>(gb + L::SC) + (chunk & 7) * 16;
         const float ks = scales[r >> 4], vsc = scales[8 + (r >> 4)], lv = log2_scale(vsc);
-        uint32_t vis = FULL;  // the rows that see the key
-        if (masked) {
-          const int first = key - shift - i0;  // the piece's first token that does
-          if (first > 0) vis = first > ((R - 1) >> a.gl) ? 0u : FULL << (first << a.gl);
-          if (key >= p.L) vis = 0u;
-        }
+        // the first row that sees the key: those of the first token at or behind it
+        const int from = !masked ? 0 : key >= p.L ? R : max(0, min(R, (key - shift - i0) << a.gl));
         float e[R];
-        // Exponents less the references, and their maximum.
-        auto exponents = [&](float& top) {
-          top = -INFINITY;
+        float top = -INFINITY;  // of the exponents, scores less the references
+        {
           terms_each<R>(sc, R, [&](int j, const float(&f)[8]) {
 #pragma unroll
             for (int i = 0; i < 8; i += 4) {
@@ -462,28 +449,21 @@ __global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
           });
           if (masked) {  // whatever the key's score and scale are
 #pragma unroll
-            for (int j = 0; j < R; ++j) e[j] = (vis >> j) & 1u ? e[j] : -INFINITY;
+            for (int j = 0; j < R; ++j) e[j] = j >= from ? e[j] : -INFINITY;
           }
 #pragma unroll
           for (int j = 0; j < R; j += 2) top = max3(top, e[j], e[j + 1]);
-        };
-        float top;
-        bool moved = unset;
-        if (!moved) {
-          exponents(top);
-          moved = bar_or(bar, 128, top > L::MOVE - lv);
         }
-        if (moved) {
+        if (unset || bar_or(bar, 128, top > L::MOVE - lv)) {
           if (ok && n > 0) ok = wait_warp(sy.pdone(t), (n - 1) & 1);  // (P^T free, O^T at rest)
           fence_after();
-          const int what = settle_scaled<L>(x, sc, fac, refs, ks, lv, vis, oc, exists, seen, ref);
+          const int what = settle_scaled<L>(x, e, refs, lv, oc, exists, seen, ref);
           unset = what & 2;
           if (what & 1) {
 #pragma unroll
             for (int j = 0; j < R; ++j) l[j] *= x.scratch[5 * R + j];
             named_bar(bar, 128);  // the scratch is read before P^T takes its place
           }
-          exponents(top);
         }
         fence_before();
         __syncwarp();
@@ -507,14 +487,19 @@ __global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
         }
         if (ok && n > 0) ok = wait_warp(sy.pdone(t), (n - 1) & 1);  // P^T's buffer is free
         const uint32_t* flat = &out[0][0];
+        constexpr int WORDS = kParts * R / 4;
 #pragma unroll
-        for (int ch = 0; ch < R * kParts / 16; ++ch)
-          *reinterpret_cast<uint4*>(prow + ((ch ^ (r & 7)) << 4)) =
-              make_uint4(flat[4 * ch], flat[4 * ch + 1], flat[4 * ch + 2], flat[4 * ch + 3]);
+        for (int ch = 0; 4 * ch < WORDS; ++ch) {
+          uint8_t* to = prow + ((ch ^ (r & 7)) << 4);
+          if (4 * ch + 4 <= WORDS)
+            *reinterpret_cast<uint4*>(to) = make_uint4(flat[4 * ch], flat[4 * ch + 1], flat[4 * ch + 2], flat[4 * ch + 3]);
+          else
+            *reinterpret_cast<uint2*>(to) = make_uint2(flat[4 * ch], flat[4 * ch + 1]);
+        }
         if (masked) {
           const int vi = k.it0 + 2 * c + 1, vs = vi % NS;
           if (ok) ok = __all_sync(FULL, wait_issued(sy.issued(), chunk)) && wait_warp(sy.full(vs), (vi / NS) & 1);
-          guard_scaled<L>(x, gb + L::RING + vs * L::SLOT, poison + 128 * t, vis);
+          guard_scaled<L>(x, gb + L::RING + vs * L::SLOT, poison + 128 * t, from);
         }
         dev::fence_proxy_async_smem();
         fence_before();
@@ -526,8 +511,19 @@ __global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
       if (ok && any) ok = wait_warp(sy.pdone(t), (n - 1) & 1);  // O^T final, P^T's buffer free
       fence_after();
       if (any) {  // l over the 128 keys' lanes
-        const float sum = lane_sums<R>(l, lane);
-        if (lane % (32 / R) == 0) x.scratch[R * x.w4 + lane / (32 / R)] = sum;
+        constexpr int R0 = R > 32 ? 32 : R;
+        float v[R0];
+#pragma unroll
+        for (int j = 0; j < R0; ++j) v[j] = l[j];
+        const float sum = lane_sums<R0>(v, lane);
+        if (lane % (32 / R0) == 0) x.scratch[R * x.w4 + lane / (32 / R0)] = sum;
+        if constexpr (R > 32) {
+          float v2[R - 32];
+#pragma unroll
+          for (int j = 0; j < R - 32; ++j) v2[j] = l[32 + j];
+          const float sum2 = lane_sums<R - 32>(v2, lane);
+          if (lane % (32 / (R - 32)) == 0) x.scratch[R * x.w4 + 32 + lane / (32 / (R - 32))] = sum2;
+        }
       }
       // both warpgroups are done with what the piece before published
       if (ok && k.i >= 1) ok = wait_warp(sy.ofree(pp ^ 1), ((k.i - 1) >> 1) & 1);
@@ -543,8 +539,9 @@ __global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
         if (ok) ok = wait_warp(sy.pub(t ^ 1), k.i & 1);  // (after that tile's last product)
         named_bar(bar, 128);
         fence_after();
-        write_scaled<L>(sa, x, p, pubs, poison, x.tl + L::COL_O + (k.i & (L::OPAR - 1)) * 2 * L::COLS, exists);
-        poison[r] = poison[128 + r] = 0u;
+        const int nan_from = min(poison[r], poison[128 + r]);
+        poison[r] = poison[128 + r] = R;
+        write_scaled<L>(sa, x, p, pubs, nan_from, x.tl + L::COL_O + (k.i & (L::OPAR - 1)) * 2 * L::COLS, exists);
       }
       fence_before();
       __syncwarp();
@@ -586,11 +583,10 @@ pa_status launch_kernel(const ScaledAttentionLaunch& l, K kernel, cudaStream_t s
   }
   a.out_f32 = l.out_dtype == PA_DTYPE_F32;
   a.min_units = 2;
-  a.item_rows = L::R;
-  a.slot_rows = L::R;
+  a.item_rows = a.slot_rows = l.item_rows;
   sa.q_stride = l.q_stride;
   sa.q_bf16 = l.q_dtype == PA_DTYPE_BF16;
-  const size_t rows = static_cast<size_t>(2) * a.n_cta * L::R;
+  const size_t rows = static_cast<size_t>(2) * a.n_cta * a.slot_rows;
   a.part_o = static_cast<float*>(l.workspace);
   a.part_m = a.part_o + rows * L::D;
   a.part_l = a.part_m + rows;
@@ -627,7 +623,7 @@ pa_status launch_kernel(const ScaledAttentionLaunch& l, K kernel, cudaStream_t s
   else
     e = launch_dependent(kernel, grid, block, L::BYTES, stream, tm[0], tm[1], sa);
   if (e == cudaSuccess && l.max_context_len > kKeys) {
-    const dim3 mgrid(static_cast<unsigned>(a.n_cta), L::R / kMergeRows), mblock(32 * kMergeRows);
+    const dim3 mgrid(static_cast<unsigned>(a.n_cta), a.slot_rows / kMergeRows), mblock(32 * kMergeRows);
     e = sa.q_bf16 ? launch_dependent(tree_merge<__nv_bfloat16, L::D>, mgrid, mblock, 0, stream, a)
                   : launch_dependent(tree_merge<__half, L::D>, mgrid, mblock, 0, stream, a);
   }
@@ -638,7 +634,7 @@ pa_status launch_kernel(const ScaledAttentionLaunch& l, K kernel, cudaStream_t s
 
 }  // namespace
 
-// A thread per key while one kv head's rows fit in 32 columns of four terms, then a
+// A thread per key while one kv head's rows fit in 128 columns of three terms, then a
 // thread per row.
 pa_status launch_scaled_attention(const ScaledAttentionLaunch& l, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -646,6 +642,7 @@ pa_status launch_scaled_attention(const ScaledAttentionLaunch& l, void* stream) 
     case 8: return launch_kernel<ScaledLay<8>>(l, scaled_keys<8>, st);
     case 16: return launch_kernel<ScaledLay<16>>(l, scaled_keys<16>, st);
     case 32: return launch_kernel<ScaledLay<32>>(l, scaled_keys<32>, st);
+    case 40: return launch_kernel<ScaledLay<40>>(l, scaled_keys<40>, st);
     default:
       return l.q_dtype == PA_DTYPE_BF16 ? launch_kernel<ScaledRowsLay<__nv_bfloat16>>(l, scaled_rows<__nv_bfloat16>, st)
                                         : launch_kernel<ScaledRowsLay<__half>>(l, scaled_rows<__half>, st);

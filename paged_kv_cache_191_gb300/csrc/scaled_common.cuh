@@ -8,7 +8,7 @@
 namespace pa {
 namespace {
 
-constexpr int kParts = 4;  // E5M2 terms of a query or a weight
+constexpr int kParts = 3;  // E5M2 terms of a query or a weight
 
 struct ScaledArgs {
   TreeArgs t;        // (mask and words are not used; scale_log2 has the scale's sign)
@@ -16,37 +16,39 @@ struct ScaledArgs {
   int32_t q_bf16;
 };
 
-// R: rows of an item, 8, 16 or 32.
+// R: rows of an item, 8, 16, 32 or 40.
 template <int R_>
 struct ScaledLay {
-  static constexpr int R = R_, D = 128, HQ = R;
+  static constexpr int R = R_, D = 128;
+  static constexpr int HQ = INT32_MAX;            // (no piece is split over the tiles)
   static constexpr bool Q8 = false, ROWS = false, WORDS = false;
-  static constexpr int PRODUCERS = 1;           // threads that announce a slot's bytes
-  static constexpr int QTILE = kParts * R * D;  // Q of a piece [term][R][128 B], E5M2
-  static constexpr int SLOT = kKeys * D;        // one K or V chunk of codes
-  static constexpr int P0 = 2 * QTILE;          // P^T [tile][128 keys][128 B: term, row]
+  static constexpr int PRODUCERS = 1;             // threads that announce a slot's bytes
+  static constexpr int COLS = (kParts * R + 15) & ~15;  // columns of a product
+  static constexpr int QTILE = ((COLS * D + 1023) & ~1023);  // Q of a piece [term][R][128 B], E5M2
+  static constexpr int SLOT = kKeys * D;          // one K or V chunk of codes
+  static constexpr int P0 = 2 * QTILE;            // P^T [tile][128 keys][128 B: term, row]
   static constexpr int RING = P0 + 2 * 16384;
-  static constexpr int NS = R == 32 ? 8 : 10;   // even: K's and V's producers own every other slot
+  static constexpr int NS = R > 16 ? 8 : 10;      // even: K's and V's producers own every other slot
   static constexpr int NL = NS;
   static constexpr int BAR = RING + NS * SLOT;
   static constexpr int EXTRA = 2 * NL + 2 * NS + 23;
-  static constexpr int NBAR = EXTRA + 8 + 4;    // scales of a chunk, factors of a piece
+  static constexpr int NBAR = EXTRA + 8 + 4;      // scales of a chunk, factors of a piece
   static constexpr int MISC = (BAR + NBAR * 8 + 15) & ~15;
-  static constexpr int PIECE = MISC + 128;      // Piece [4]
-  static constexpr int PUB = PIECE + 4 * 48;    // float2 [2 tiles][R]
-  static constexpr int SC = PUB + 16 * R;       // float [8 chunks][K 8, V 8]
-  static constexpr int FAC = SC + 8 * 64;       // float [4 pieces][R]
-  static constexpr int REF = FAC + 16 * R;      // float [2 tiles][R]: minus the references
-  static constexpr int POISON = REF + 8 * R;    // uint32 [piece parity][2 tiles][128 dims]: rows that see a NaN there
+  static constexpr int PIECE = MISC + 128;        // Piece [4]
+  static constexpr int PUB = PIECE + 4 * 48;      // float2 [2 tiles][R]
+  static constexpr int SC = PUB + 16 * R;         // float [8 chunks][K 8, V 8]
+  static constexpr int FAC = SC + 8 * 64;         // float [4 pieces][R]
+  static constexpr int REF = FAC + 16 * R;        // float [2 tiles][R]: minus the references
+  static constexpr int POISON = REF + 8 * R;      // int [piece parity][2 tiles][128 dims]: first row that sees a NaN there
   static constexpr int MASK = 0;
   static constexpr int BYTES = POISON + 2048;
   static constexpr int THREADS = 384;
   static constexpr int HIGH = 200, LOW = 104;
-  // tensor memory columns: S^T [tile] x kParts R, O^T [piece parity, where there is room][tile] x kParts R
-  static constexpr int COLS = kParts * R, OPAR = R == 32 ? 1 : 2;
+  // tensor memory columns: S^T [tile] x COLS, O^T [piece parity, where there is room][tile] x COLS
+  static constexpr int OPAR = R > 16 ? 1 : 2;
   static constexpr uint32_t COL_O = 2 * COLS;
   // log2 of how far below its row's maximum of weight x V scale a reference is set, and
-  // of how far that maximum may outgrow it: E5M2 terms of f16 values go from 2^15.9
+  // of how far that maximum may outgrow it: E5M2 terms of f16 values go from 2^15.8
   // down to 2^-16, rounded: 2^-27 of the largest is the most that a weight is off by
   // beyond its f16 rounding.  (Lower references are outgrown less often, higher ones
   // keep more of small weights.)
@@ -70,18 +72,19 @@ struct KeyLane {
 };
 
 // ---- E5M2 terms --------------------------------------------------------------
-// An f16 value is the sum of four E5M2 ones: E5M2 is f16's upper byte, so a term is
-// what is left, cut behind its first three bits (11 bits: 3 + 3 + 3 + 2).  The
-// differences are exact; only below 2^-16, E5M2's smallest, is anything lost (the
-// last term is rounded there; to a NaN the first one is what counts).
-// h: two values in, the four terms' pairs out (their upper bytes count).
+// An f16 value is the sum of three E5M2 ones: E5M2 is f16's upper byte, so a term is
+// what is left, rounded to its first three bits.  Of 11 bits a term leaves a rest of
+// at most half a step, 2^7 units, the next one 2^3, which the last holds: exact, but
+// below 2^-16, E5M2's smallest, where it is rounded.  (Differences are exact.  A NaN
+// does not come through: a query's goes by its row's factor, a weight's by its row's sum.)
+// h: two values in, the terms' pairs out (their upper bytes count).
 __device__ __forceinline__ void terms(uint32_t h, uint32_t (&p)[kParts]) {
 #pragma unroll
   for (int i = 0; i < kParts; ++i) {
-    p[i] = i + 1 < kParts ? h : h + 0x00800080u;
+    p[i] = h + 0x00800080u;
     if (i + 1 < kParts) {
-      const uint32_t cut = h & 0xFF00FF00u;
-      const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&cut));
+      const uint32_t t = p[i] & 0xFF00FF00u;
+      const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&t));
       h = *reinterpret_cast<const uint32_t*>(&r);
     }
   }
@@ -96,20 +99,26 @@ struct Span {
   int qs, n, L, tiles;
   int a;  // tokens before the new ones, in items
 };
-// sum of ceil(x / 2^s) over x = 1 .. m
-__device__ __forceinline__ int64_t ceil_sum(int64_t m, int s) {
-  const int64_t q = m >> s, r = m - (q << s);
-  return (q * (q + 1) / 2 << s) + r * (q + 1);
+// sum of ceil(x / 2^s) over x = 1 .. m.  (In 32 bits it may wrap; differences, which are
+// within what the launch was checked for, are right all the same.)
+template <typename U>
+__device__ __forceinline__ U ceil_sum(U m, int s) {
+  const U q = m >> s, r = m - (q << s);
+  return (((q & 1 ? q : q + 1) * (q & 1 ? (q + 1) >> 1 : q >> 1)) << s) + r * (q + 1);
 }
-__device__ __forceinline__ int64_t units_before(const Span& x, int k, int s) {
-  return static_cast<int64_t>(kItem) * k + ceil_sum(x.a + k, s) - ceil_sum(x.a, s);
+// units of the items before item k of a kv head
+template <typename U>
+__device__ __forceinline__ U units_before(const Span& x, int k, int s) {
+  return static_cast<U>(kItem) * static_cast<U>(k) + ceil_sum(static_cast<U>(x.a + k), s) -
+         ceil_sum(static_cast<U>(x.a), s);
 }
 // chunks of item k
 __device__ __forceinline__ int chunks_of(const Span& x, int k, int s) {
   return k + 1 < x.tiles ? (x.a + k + (1 << s)) >> s : max(1, (x.L + kKeys - 1) / kKeys);
 }
-__device__ __forceinline__ int64_t units_per_head(const Span& x, int s) {
-  return x.tiles == 0 ? 0 : units_before(x, x.tiles - 1, s) + kItem + chunks_of(x, x.tiles - 1, s);
+template <typename U>
+__device__ __forceinline__ U units_per_head(const Span& x, int s) {
+  return x.tiles == 0 ? 0 : units_before<U>(x, x.tiles - 1, s) + kItem + chunks_of(x, x.tiles - 1, s);
 }
 
 // Piece i's queries: every row scaled by a power of two to 2^14 .. 2^15 (a row of small
@@ -122,9 +131,9 @@ __device__ __forceinline__ void load_queries(const ScaledArgs& sa, uint8_t* gb, 
   const TreeArgs& a = sa.t;
   const int lane = static_cast<int>(threadIdx.x & 31);
   const int heads = (1 << a.gl) - 1;
-  auto load = [&](int r0, uint2(&x)[8]) {  // rows r0 .. r0 + 7, 8 bytes a lane
+  auto load = [&](int r0, uint2(&x)[4]) {  // rows r0 .. r0 + 3, 8 bytes a lane
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 4; ++j) {
       const int r = r0 + j, h = r & heads;
       x[j] = make_uint2(0u, 0u);
       if (r < p.rows && h < a.G)
@@ -133,29 +142,27 @@ __device__ __forceinline__ void load_queries(const ScaledArgs& sa, uint8_t* gb, 
             static_cast<size_t>(p.g * a.G + h) * L::D + 4 * lane));
     }
   };
-  uint2 x[8], next[8];
+  uint2 x[4], next[4];
   load(0, next);
   if (ok && i >= 2) ok = wait_warp(sy.qfree(i & 1), ((i - 2) >> 1) & 1);
   float* fac = reinterpret_cast<float*>(gb + L::FAC) + (i & 3) * R;
   uint8_t* to = gb + (i & 1) * L::QTILE + (lane & 3) * 4;
 #pragma unroll 1
-  for (int r0 = 0; r0 < p.rows; r0 += 8) {
+  for (int r0 = 0; r0 < p.rows; r0 += 4) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = next[j];
-    if (r0 + 8 < p.rows) load(r0 + 8, next);
+    for (int j = 0; j < 4; ++j) x[j] = next[j];
+    if (r0 + 4 < p.rows) load(r0 + 4, next);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 4; ++j) {
       const int r = r0 + j;
       const float2 lo = sa.q_bf16 ? dev::unpack2<__nv_bfloat16>(x[j].x) : dev::unpack2<__half>(x[j].x);
       const float2 hi = sa.q_bf16 ? dev::unpack2<__nv_bfloat16>(x[j].y) : dev::unpack2<__half>(x[j].y);
       const float f[4] = {lo.x, lo.y, hi.x, hi.y};
-      uint32_t top = 0;  // the largest finite size
+      uint32_t top = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t size = __float_as_uint(f[e]) & 0x7FFFFFFFu;
-        if (size < 0x7F800000u) top = max(top, size);
-      }
+      for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(f[e]) & 0x7FFFFFFFu);
       top = __reduce_max_sync(FULL, top);
+      const bool fine = top < 0x7F800000u;  // (else the row's factor is NaN, and so is the row)
       const int k = min(14 - (static_cast<int>(top >> 23) - 127), 100);
       const float up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
       uint32_t p0[kParts], p1[kParts];
@@ -164,7 +171,7 @@ __device__ __forceinline__ void load_queries(const ScaledArgs& sa, uint8_t* gb, 
 #pragma unroll
       for (int e = 0; e < kParts; ++e)
         *reinterpret_cast<uint32_t*>(to + (e * R + r) * 128 + (((lane >> 2) ^ (r & 7)) << 4)) = upper(p0[e], p1[e]);
-      if (lane == 0) fac[r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+      if (lane == 0) fac[r] = fine ? a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23) : NAN;
     }
   }
   dev::fence_proxy_async_smem();
@@ -175,15 +182,16 @@ __device__ __forceinline__ void load_queries(const ScaledArgs& sa, uint8_t* gb, 
   }
 }
 
-// The planner warp: this CTA's pieces, and with a thread per key their queries.  Piece
-// i + 1 is published before piece i's queries are loaded, so that the producers see
-// two pieces ahead.
+// The planner warp: this CTA's pieces, and with a thread per key their queries.  But
+// for the first, piece i + 1 is published before piece i's queries are loaded, so that
+// the producers see two pieces ahead.
 template <typename L>
 __device__ __forceinline__ void plan_scaled(const ScaledArgs& sa, uint8_t* gb, Sync<L> sy) {
-  constexpr int R = L::R;
   const TreeArgs& a = sa.t;
   const int lane = static_cast<int>(threadIdx.x & 31), me = static_cast<int>(blockIdx.x);
-  const int tpi = R >> a.gl, per = 31 - __clz(kKeys / tpi);  // tokens of an item; log2 of the items to a chunk
+  const int tpi = a.item_rows >> a.gl, per = 31 - __clz(kKeys / tpi);  // tokens of an item; log2 of the items to a chunk
+  // Sequences are read 32 at a time, a lane each.  (The code is kept small, one place for
+  // each step: what a CTA runs once should not push the loops out of the caches.)
   Span mine{0, 0, 0, 0, 0};
   int group = -1;
   auto read = [&](int g, bool report) {
@@ -195,30 +203,32 @@ __device__ __forceinline__ void plan_scaled(const ScaledArgs& sa, uint8_t* gb, S
     const Seq s = seq_of(a, b, report);
     mine = Span{s.qs, s.n, s.L, s.tiles, (max(0, s.L - s.n) + tpi - 1) / tpi};
   };
-  auto span = [&](int b) {
-    read(b >> 5, false);
-    return Span{__shfl_sync(FULL, mine.qs, b & 31), __shfl_sync(FULL, mine.n, b & 31), __shfl_sync(FULL, mine.L, b & 31),
-                __shfl_sync(FULL, mine.tiles, b & 31), __shfl_sync(FULL, mine.a, b & 31)};
-  };
+  // First all units are summed, then the sequence of this CTA's first one is found.
   int64_t sum = 0;
+  int upc = 0, start = 0, end = 0, b = 0, ub = 0;  // units before sequence b: ub
 #pragma unroll 1
-  for (int g = 0; 32 * g < a.B; ++g) {
-    read(g, me == 0);
-    sum += units_per_head(mine, per) * a.Hkv;
-  }
+  for (int g = 0, find = 0;; ++g) {
+    if (32 * g >= a.B) {
+      if (find) break;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(FULL, sum, off);
-  // more than the launch was checked for: q_start has ranges that overlap
-  if (sum > kMaxUnits && me == 0 && lane == 0) flag(PA_DEVERR_QUERY_RANGE);
-  const int total = sum > kMaxUnits ? 0 : static_cast<int>(sum);
-  const int upc = max((total + a.n_cta - 1) / a.n_cta, a.min_units);
-  const int start = static_cast<int>(min(static_cast<int64_t>(me) * upc, static_cast<int64_t>(total)));
-  const int end = min(start + upc, total);
-  int b = 0, ub = 0;  // the sequence of unit `u`, and the units before it
-#pragma unroll 1
-  for (int b0 = 0; start < end; b0 += 32) {
-    read(b0 >> 5, false);
-    const int w = static_cast<int>(units_per_head(mine, per)) * a.Hkv;
+      for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(FULL, sum, off);
+      // more than the launch was checked for: q_start has ranges that overlap
+      if (sum > kMaxUnits && me == 0 && lane == 0) flag(PA_DEVERR_QUERY_RANGE);
+      const int total = sum > kMaxUnits ? 0 : static_cast<int>(sum);
+      upc = max((total + a.n_cta - 1) / a.n_cta, a.min_units);
+      start = static_cast<int>(min(static_cast<int64_t>(me) * upc, static_cast<int64_t>(total)));
+      end = min(start + upc, total);
+      if (start >= end) break;
+      find = 1;
+      g = 0;
+    }
+    read(g, me == 0);
+    const int64_t units = units_per_head<int64_t>(mine, per) * a.Hkv;
+    if (!find) {
+      sum += units;
+      continue;
+    }
+    const int w = static_cast<int>(units);
     int inc = w;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -226,35 +236,18 @@ __device__ __forceinline__ void plan_scaled(const ScaledArgs& sa, uint8_t* gb, S
       if (lane >= off) inc += y;
     }
     const unsigned over = __ballot_sync(FULL, ub + inc > start);
+    const int f = over ? __ffs(over) - 1 : 31;
+    ub += __shfl_sync(FULL, over ? inc - w : inc, f);
     if (over) {
-      const int f = __ffs(over) - 1;
-      b = b0 + f;
-      ub += __shfl_sync(FULL, inc - w, f);
+      b = 32 * g + f;
       break;
     }
-    ub += __shfl_sync(FULL, inc, 31);
   }
   Piece* ring = reinterpret_cast<Piece*>(gb + L::PIECE);
   // the item at unit u: tile `tile` of kv head g of sequence b, which is s; `off` of
   // its units are gone
   Span s{0, 0, 0, 0, 0};
-  int u = start, g = 0, tile = 0, off = 0;
-  if (start < end) {
-    s = span(b);
-    const int U = static_cast<int>(units_per_head(s, per)), at = start - ub;
-    g = at / U;
-    const int rem = at - g * U;
-    int hi = s.tiles;  // the last that starts at or before rem
-#pragma unroll 1
-    while (hi - tile > 1) {
-      const int mid = (tile + hi) >> 1;
-      if (units_before(s, mid, per) <= rem)
-        tile = mid;
-      else
-        hi = mid;
-    }
-    off = rem - static_cast<int>(units_before(s, tile, per));
-  }
+  int u = start, g = 0, tile = 0, off = 0, seq = -1;
   bool ok = true, more = true;
   int4 sp0 = make_int4(0, 0, 0, 0), sp1 = sp0;
   auto publish_piece = [&](int i) {
@@ -263,6 +256,32 @@ __device__ __forceinline__ void plan_scaled(const ScaledArgs& sa, uint8_t* gb, S
     p.live = 0;
 #pragma unroll 1
     while (u < end && !p.live) {
+      if (seq != b) {  // (b stays below B: its units cover those of the range)
+        const int from = b & 31;
+        read(b >> 5, false);
+        s = Span{__shfl_sync(FULL, mine.qs, from), __shfl_sync(FULL, mine.n, from), __shfl_sync(FULL, mine.L, from),
+                 __shfl_sync(FULL, mine.tiles, from), __shfl_sync(FULL, mine.a, from)};
+        if (s.tiles == 0 && b + 1 < a.B) {
+          ++b;
+          continue;
+        }
+        if (seq < 0) {  // the CTA's first item
+          const int U = max(1, static_cast<int>(units_per_head<uint32_t>(s, per))), at = start - ub;
+          g = at / U;
+          off = at - g * U;
+          int hi = s.tiles;  // the last that starts at or before it
+#pragma unroll 1
+          while (hi - tile > 1) {
+            const int mid = (tile + hi) >> 1;
+            if (static_cast<int>(units_before<uint32_t>(s, mid, per)) <= off)
+              tile = mid;
+            else
+              hi = mid;
+          }
+          off -= static_cast<int>(units_before<uint32_t>(s, tile, per));
+        }
+        seq = b;
+      }
       const int nch = chunks_of(s, tile, per), cost = nch + kItem, stop = min(cost, off + end - u);
       p.c0 = max(0, off - kItem);
       p.c1 = stop - kItem;
@@ -273,8 +292,8 @@ __device__ __forceinline__ void plan_scaled(const ScaledArgs& sa, uint8_t* gb, S
         p.n = s.n;
         p.L = s.L;
         p.g = g;
-        p.row0 = tile * R;
-        p.rows = min(R, (s.n << a.gl) - p.row0);
+        p.row0 = tile * a.item_rows;
+        p.rows = min(a.item_rows, (s.n << a.gl) - p.row0);
         p.slot = p.c0 == 0 && p.c1 == nch ? -1 : 2 * me + (i == 0 ? 0 : 1);
         if (p.c0 == 0 && p.c1 < nch) {  // the item goes on in the next CTAs: what the merge needs
           sp0 = make_int4((u - off + cost - 1) / upc - me + 1, p.slot, s.qs, p.row0);
@@ -287,8 +306,7 @@ __device__ __forceinline__ void plan_scaled(const ScaledArgs& sa, uint8_t* gb, S
         tile = 0;
         if (++g >= a.Hkv) {
           g = 0;
-          do s = span(++b);
-          while (s.tiles == 0 && b + 1 < a.B);
+          ++b;
         }
       }
     }
@@ -304,7 +322,8 @@ __device__ __forceinline__ void plan_scaled(const ScaledArgs& sa, uint8_t* gb, S
   for (int i = 0; more; ++i) {
     publish_piece(i);
     if constexpr (!L::ROWS) {
-      if (i > 0) load_queries<L>(sa, gb, sy, ring[(i - 1) & 3], i - 1, ok);
+      const int q = max(i - 1, 0);
+      if (i != 1 && (i > 0 || more)) load_queries<L>(sa, gb, sy, ring[q & 3], q, ok);
     }
   }
   if (lane == 0) {
@@ -343,7 +362,7 @@ __device__ __forceinline__ void produce_scaled(const TreeArgs& a, const CUtensor
     return v;
   };
   Piece p, pn;
-  bool more = sy.piece(gb, 0, p, ok);
+  bool more = sy.piece(gb, 0, p, ok), more_n = false;
   int ids_next = more ? fetch(p, p.c0 * kBlk) : 0;
   float2 next = make_float2(0.f, 0.f);  // the scales of the lane's block in ids_next
   auto scales = [&](int g) {
@@ -353,11 +372,10 @@ __device__ __forceinline__ void produce_scaled(const TreeArgs& a, const CUtensor
   if (!V && more) scales(p.g);
 #pragma unroll 1
   for (int i = 1; more; ++i) {
-    const bool more_n = sy.piece(gb, i, pn, ok);
     p.g = uniform(p.g);
     p.c0 = uniform(p.c0);
     p.c1 = uniform(p.c1);
-    const int nblk = uniform((p.L + 15) / 16), ids_n = more_n ? fetch(pn, pn.c0 * kBlk) : 0;
+    const int nblk = uniform((p.L + 15) / 16);
     int ids = 0;
     float2 sc = next;
 #pragma unroll 1
@@ -366,7 +384,7 @@ __device__ __forceinline__ void produce_scaled(const TreeArgs& a, const CUtensor
       if (k4 == 0) {
         ids = ids_next;
         sc = next;
-        ids_next = c + 4 < p.c1 ? fetch(p, (c + 4) * kBlk) : ids_n;
+        if (c + 4 < p.c1) ids_next = fetch(p, (c + 4) * kBlk);
       }
       int blk[kBlk];  // the chunk's block ids
 #pragma unroll
@@ -396,8 +414,14 @@ __device__ __forceinline__ void produce_scaled(const TreeArgs& a, const CUtensor
         if ((lane >> 3) == k4) put_scales(to + (lane & 7), sc);
         __syncwarp();
         if (lane == 0) mbar_arrive(scales_full(sy, chunk));
-        if (c + 1 == p.c1 ? more_n : k4 == 3) scales(c + 1 == p.c1 ? pn.g : p.g);
       }
+      // what comes behind these 32 blocks: more of the piece, or the next one's first (asked
+      // for once this chunk is on its way: its plan may still be made)
+      if (k4 == 0 && c + 4 >= p.c1) {
+        more_n = sy.piece(gb, i, pn, ok);
+        if (more_n) ids_next = fetch(pn, pn.c0 * kBlk);
+      }
+      if (!V && (c + 1 == p.c1 ? more_n : k4 == 3)) scales(c + 1 == p.c1 ? pn.g : p.g);
     }
     p = pn;
     more = more_n && ok;

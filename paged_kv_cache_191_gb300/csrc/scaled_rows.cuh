@@ -79,7 +79,7 @@ __device__ __forceinline__ void produce_rows(const TreeArgs& a, const CUtensorMa
     __syncwarp();
   };
   Piece p, pn;
-  bool more = sy.piece(gb, 0, p, ok);
+  bool more = sy.piece(gb, 0, p, ok), more_n = false;
   int ids_next = more ? fetch(p, p.c0 * kBlk) : 0;
   float2 next = make_float2(0.f, 0.f);  // the scales of the lane's block in ids_next
   auto scales = [&](int g) {
@@ -89,11 +89,10 @@ __device__ __forceinline__ void produce_rows(const TreeArgs& a, const CUtensorMa
   if (more) scales(p.g);
 #pragma unroll 1
   for (int i = 1; more; ++i) {
-    const bool more_n = sy.piece(gb, i, pn, ok);
     p.g = uniform(p.g);
     p.c0 = uniform(p.c0);
     p.c1 = uniform(p.c1);
-    const int nblk = uniform((p.L + 15) / 16), ids_n = more_n ? fetch(pn, pn.c0 * kBlk) : 0;
+    const int nblk = uniform((p.L + 15) / 16);
     int ids = 0;
     float2 sc = next;
 #pragma unroll 1
@@ -102,7 +101,7 @@ __device__ __forceinline__ void produce_rows(const TreeArgs& a, const CUtensorMa
       if (k4 == 0) {
         ids = ids_next;
         sc = next;
-        ids_next = c + 4 < p.c1 ? fetch(p, (c + 4) * kBlk) : ids_n;
+        if (c + 4 < p.c1) ids_next = fetch(p, (c + 4) * kBlk);
       }
       int blk[kBlk];  // the chunk's block ids
 #pragma unroll
@@ -132,8 +131,13 @@ __device__ __forceinline__ void produce_rows(const TreeArgs& a, const CUtensorMa
       __syncwarp();
       if (lane == 0) mbar_arrive(scales_full(sy, chunk));
       ++chunk;
-      if (c + 1 == p.c1 ? more_n : k4 == 3) scales(c + 1 == p.c1 ? pn.g : p.g);
       if (c == p.c0) load_q(p, i - 1);  // (the first chunk goes ahead of the wait for Q's place)
+      // what comes behind these 32 blocks: more of the piece, or the next one's first
+      if (k4 == 0 && c + 4 >= p.c1) {
+        more_n = sy.piece(gb, i, pn, ok);
+        if (more_n) ids_next = fetch(pn, pn.c0 * kBlk);
+      }
+      if (c + 1 == p.c1 ? more_n : k4 == 3) scales(c + 1 == p.c1 ? pn.g : p.g);
     }
     p = pn;
     more = more_n && ok;
