@@ -97,7 +97,9 @@ __device__ __forceinline__ void multiply_scaled(uint8_t* gb, Sync<L> sy, uint32_
         moved = true;
       }
     }
-    if (s.k.live) {
+    // (Scores two pieces ahead of the products at most: the next piece's plan, which
+    // s.next waits for, may wait for the last but three to be over.)
+    if (s.k.live && s.k.i - o.k.i <= 2) {
       const int t = s.tile, i = s.k.it0 + 2 * s.k.c, qb = s.k.i & 1, n = t ? ns1 : ns0;
       if ((n == 0 || test(sy.sfree(t), n - 1)) &&
           (s.k.c > 0 || test(sy.qfull(qb), s.k.i >> 1)) && landed(i)) {
@@ -359,7 +361,10 @@ __global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
   const int wid = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   if (threadIdx.x == 64) {
     for (int i = 0; i < 8; ++i) dev::mbar_init(scales_full(sy, i), 1);
-    for (int i = 0; i < 4; ++i) dev::mbar_init(factors_full(sy, i), 1);
+    for (int i = 0; i < 4; ++i) {
+      dev::mbar_init(piece_over(sy, i), 8);
+      dev::mbar_init(factors_full(sy, i), 1);
+    }
   }
   for (int i = static_cast<int>(threadIdx.x); i < 512; i += L::THREADS) reinterpret_cast<int*>(gb + L::POISON)[i] = R;
   const uint32_t tmem = setup<L>(gb, sy, wid, &tmK, &tmV, &tmK);
@@ -375,7 +380,10 @@ __global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
     produce_scaled<L, true>(a, &tmV, gb, sy);
   } else if (wid == 3) {
     fewer_registers<L>();
-    plan_scaled<L>(sa, gb, sy);
+    plan_scaled<L>(a, gb, sy);
+  } else if (wid >= 12) {
+    fewer_registers<L>();
+    load_queries<L>(sa, gb, sy);
   } else {
     // ---- softmax warpgroups: thread r owns key r of a chunk -----------------------------
     more_registers<L>();
@@ -545,7 +553,10 @@ __global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
       }
       fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(sy.ofree(pp));
+      if (lane == 0) {
+        mbar_arrive(sy.ofree(pp));
+        mbar_arrive(piece_over(sy, k.i));
+      }
     }
     if (!ok && lane == 0) flag(PA_DEVERR_TIMEOUT);
   }

@@ -32,7 +32,7 @@ struct ScaledLay {
   static constexpr int NL = NS;
   static constexpr int BAR = RING + NS * SLOT;
   static constexpr int EXTRA = 2 * NL + 2 * NS + 23;
-  static constexpr int NBAR = EXTRA + 8 + 4;      // scales of a chunk, factors of a piece
+  static constexpr int NBAR = EXTRA + 16;         // scales of a chunk, pieces over, factors of a piece
   static constexpr int MISC = (BAR + NBAR * 8 + 15) & ~15;
   static constexpr int PIECE = MISC + 128;        // Piece [4]
   static constexpr int PUB = PIECE + 4 * 48;      // float2 [2 tiles][R]
@@ -42,8 +42,8 @@ struct ScaledLay {
   static constexpr int POISON = REF + 8 * R;      // int [piece parity][2 tiles][128 dims]: first row that sees a NaN there
   static constexpr int MASK = 0;
   static constexpr int BYTES = POISON + 2048;
-  static constexpr int THREADS = 384;
-  static constexpr int HIGH = 200, LOW = 104;
+  static constexpr int THREADS = 512;
+  static constexpr int HIGH = 176, LOW = 80;
   // tensor memory columns: S^T [tile] x COLS, O^T [piece parity, where there is room][tile] x COLS
   static constexpr int OPAR = R > 16 ? 1 : 2;
   static constexpr uint32_t COL_O = 2 * COLS;
@@ -59,9 +59,14 @@ struct ScaledLay {
 
 template <typename L>
 __device__ __forceinline__ uint32_t scales_full(const Sync<L>& sy, int chunk) { return sy.at(L::EXTRA + (chunk & 7)); }
+// Both warpgroups are done with the piece.  (Of four pieces each its own: the planner, who
+// waits for the last but three, may be more than two behind, and ofree's two would then
+// have gone round.)
+template <typename L>
+__device__ __forceinline__ uint32_t piece_over(const Sync<L>& sy, int piece) { return sy.at(L::EXTRA + 8 + (piece & 3)); }
 template <typename L>
 __device__ __forceinline__ uint32_t factors_full(const Sync<L>& sy, int piece) {
-  return sy.at(L::EXTRA + 8 + (piece & 3));
+  return sy.at(L::EXTRA + 12 + (piece & 3));
 }
 
 // What the softmax's rare paths share with its loop.
@@ -121,73 +126,79 @@ __device__ __forceinline__ U units_per_head(const Span& x, int s) {
   return x.tiles == 0 ? 0 : units_before<U>(x, x.tiles - 1, s) + kItem + chunks_of(x, x.tiles - 1, s);
 }
 
-// Piece i's queries: every row scaled by a power of two to 2^14 .. 2^15 (a row of small
-// values keeps its bits beside one of large ones), in E5M2 terms; its factor takes the
-// power back.
+// The query warpgroup: every row of a piece scaled by a power of two to 2^14 .. 2^15 (a
+// row of small values keeps its bits beside one of large ones), in E5M2 terms; its
+// factor takes the power back.  A warp has a quarter of the rows.
 template <typename L>
-__device__ __forceinline__ void load_queries(const ScaledArgs& sa, uint8_t* gb, const Sync<L>& sy, const Piece& p, int i,
-                                             bool& ok) {
-  constexpr int R = L::R;
+__device__ __forceinline__ void load_queries(const ScaledArgs& sa, uint8_t* gb, Sync<L> sy) {
+  constexpr int R = L::R, EACH = R / 4, BATCH = EACH % 4 == 0 ? 4 : 2;
   const TreeArgs& a = sa.t;
-  const int lane = static_cast<int>(threadIdx.x & 31);
+  const int lane = static_cast<int>(threadIdx.x & 31), w4 = static_cast<int>(threadIdx.x >> 5) & 3;
   const int heads = (1 << a.gl) - 1;
-  auto load = [&](int r0, uint2(&x)[4]) {  // rows r0 .. r0 + 3, 8 bytes a lane
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = r0 + j, h = r & heads;
-      x[j] = make_uint2(0u, 0u);
-      if (r < p.rows && h < a.G)
-        x[j] = __ldg(reinterpret_cast<const uint2*>(
-            static_cast<const uint16_t*>(a.q) + static_cast<size_t>(p.qs + ((p.row0 + r) >> a.gl)) * sa.q_stride +
-            static_cast<size_t>(p.g * a.G + h) * L::D + 4 * lane));
-    }
-  };
-  uint2 x[4], next[4];
-  load(0, next);
-  if (ok && i >= 2) ok = wait_warp(sy.qfree(i & 1), ((i - 2) >> 1) & 1);
-  float* fac = reinterpret_cast<float*>(gb + L::FAC) + (i & 3) * R;
-  uint8_t* to = gb + (i & 1) * L::QTILE + (lane & 3) * 4;
+  bool ok = true;
+  Piece p;
 #pragma unroll 1
-  for (int r0 = 0; r0 < p.rows; r0 += 4) {
+  for (int i = 0;; ++i) {
+    const bool live = sy.piece(gb, i, p, ok);
+    ok = !bar_or(4, 128, !ok);  // (where a warp has given up a wait, the warpgroup leaves as a whole)
+    if (!ok || !live) break;
+    auto load = [&](int r0, uint2(&x)[BATCH]) {  // 8 bytes a lane and row
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = next[j];
-    if (r0 + 4 < p.rows) load(r0 + 4, next);
+      for (int j = 0; j < BATCH; ++j) {
+        const int r = r0 + j, h = r & heads;
+        x[j] = make_uint2(0u, 0u);
+        if (r < p.rows && h < a.G)
+          x[j] = __ldg(reinterpret_cast<const uint2*>(
+              static_cast<const uint16_t*>(a.q) + static_cast<size_t>(p.qs + ((p.row0 + r) >> a.gl)) * sa.q_stride +
+              static_cast<size_t>(p.g * a.G + h) * L::D + 4 * lane));
+      }
+    };
+    uint2 x[BATCH], next[BATCH];
+    load(EACH * w4, next);
+    if (ok && i >= 2) ok = wait_warp(sy.qfree(i & 1), ((i - 2) >> 1) & 1);
+    float* fac = reinterpret_cast<float*>(gb + L::FAC) + (i & 3) * R;
+    uint8_t* to = gb + (i & 1) * L::QTILE + (lane & 3) * 4;
+#pragma unroll 1
+    for (int r0 = EACH * w4; r0 < EACH * (w4 + 1); r0 += BATCH) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = r0 + j;
-      const float2 lo = sa.q_bf16 ? dev::unpack2<__nv_bfloat16>(x[j].x) : dev::unpack2<__half>(x[j].x);
-      const float2 hi = sa.q_bf16 ? dev::unpack2<__nv_bfloat16>(x[j].y) : dev::unpack2<__half>(x[j].y);
-      const float f[4] = {lo.x, lo.y, hi.x, hi.y};
-      uint32_t top = 0;
+      for (int j = 0; j < BATCH; ++j) x[j] = next[j];
+      if (r0 + BATCH < EACH * (w4 + 1)) load(r0 + BATCH, next);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(f[e]) & 0x7FFFFFFFu);
-      top = __reduce_max_sync(FULL, top);
-      const bool fine = top < 0x7F800000u;  // (else the row's factor is NaN, and so is the row)
-      const int k = min(14 - (static_cast<int>(top >> 23) - 127), 100);
-      const float up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
-      uint32_t p0[kParts], p1[kParts];
-      terms(dev::pack2<__half>(f[0] * up, f[1] * up), p0);
-      terms(dev::pack2<__half>(f[2] * up, f[3] * up), p1);
+      for (int j = 0; j < BATCH; ++j) {
+        const int r = r0 + j;
+        const float2 lo = sa.q_bf16 ? dev::unpack2<__nv_bfloat16>(x[j].x) : dev::unpack2<__half>(x[j].x);
+        const float2 hi = sa.q_bf16 ? dev::unpack2<__nv_bfloat16>(x[j].y) : dev::unpack2<__half>(x[j].y);
+        const float f[4] = {lo.x, lo.y, hi.x, hi.y};
+        uint32_t top = 0;
 #pragma unroll
-      for (int e = 0; e < kParts; ++e)
-        *reinterpret_cast<uint32_t*>(to + (e * R + r) * 128 + (((lane >> 2) ^ (r & 7)) << 4)) = upper(p0[e], p1[e]);
-      if (lane == 0) fac[r] = fine ? a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23) : NAN;
+        for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(f[e]) & 0x7FFFFFFFu);
+        top = __reduce_max_sync(FULL, top);
+        const bool fine = top < 0x7F800000u;  // (else the row's factor is NaN, and so is the row)
+        const int k = min(14 - (static_cast<int>(top >> 23) - 127), 100);
+        const float up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+        uint32_t p0[kParts], p1[kParts];
+        terms(dev::pack2<__half>(f[0] * up, f[1] * up), p0);
+        terms(dev::pack2<__half>(f[2] * up, f[3] * up), p1);
+#pragma unroll
+        for (int e = 0; e < kParts; ++e)
+          *reinterpret_cast<uint32_t*>(to + (e * R + r) * 128 + (((lane >> 2) ^ (r & 7)) << 4)) = upper(p0[e], p1[e]);
+        if (lane == 0) fac[r] = fine ? a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23) : NAN;
+      }
     }
+    dev::fence_proxy_async_smem();
+    named_bar(4, 128);
+    if (w4 == 0 && lane == 0) {
+      mbar_arrive(sy.qfull(i & 1));
+      mbar_arrive(factors_full(sy, i));
+    }
+    __syncwarp();
   }
-  dev::fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    mbar_arrive(sy.qfull(i & 1));
-    mbar_arrive(factors_full(sy, i));
-  }
+  if (!ok && lane == 0) flag(PA_DEVERR_TIMEOUT);
 }
 
-// The planner warp: this CTA's pieces, and with a thread per key their queries.  But
-// for the first, piece i + 1 is published before piece i's queries are loaded, so that
-// the producers see two pieces ahead.
+// The planner warp: this CTA's pieces, published up to four ahead.
 template <typename L>
-__device__ __forceinline__ void plan_scaled(const ScaledArgs& sa, uint8_t* gb, Sync<L> sy) {
-  const TreeArgs& a = sa.t;
+__device__ __forceinline__ void plan_scaled(const TreeArgs& a, uint8_t* gb, Sync<L> sy) {
   const int lane = static_cast<int>(threadIdx.x & 31), me = static_cast<int>(blockIdx.x);
   const int tpi = a.item_rows >> a.gl, per = 31 - __clz(kKeys / tpi);  // tokens of an item; log2 of the items to a chunk
   // Sequences are read 32 at a time, a lane each.  (The code is kept small, one place for
@@ -250,8 +261,10 @@ __device__ __forceinline__ void plan_scaled(const ScaledArgs& sa, uint8_t* gb, S
   int u = start, g = 0, tile = 0, off = 0, seq = -1;
   bool ok = true, more = true;
   int4 sp0 = make_int4(0, 0, 0, 0), sp1 = sp0;
-  auto publish_piece = [&](int i) {
-    if (ok && i >= 4) ok = wait_warp(sy.ofree(i & 1), ((i - 4) >> 1) & 1);
+#pragma unroll 1
+  for (int i = 0; more; ++i) {
+    if (i >= 4) ok = wait_warp(piece_over(sy, i), ((i - 4) >> 2) & 1);
+    if (!ok) break;  // (what is still read is not written over: the others' waits run out in turn)
     Piece p;
     p.live = 0;
 #pragma unroll 1
@@ -317,14 +330,6 @@ __device__ __forceinline__ void plan_scaled(const ScaledArgs& sa, uint8_t* gb, S
       mbar_arrive(sy.pieces(i & 3));
     }
     __syncwarp();
-  };
-#pragma unroll 1
-  for (int i = 0; more; ++i) {
-    publish_piece(i);
-    if constexpr (!L::ROWS) {
-      const int q = max(i - 1, 0);
-      if (i != 1 && (i > 0 || more)) load_queries<L>(sa, gb, sy, ring[q & 3], q, ok);
-    }
   }
   if (lane == 0) {
     a.split[2 * blockIdx.x] = sp0;

@@ -29,7 +29,7 @@ struct ScaledRowsLay {
   static constexpr int STAGE = RING + NS * SLOT;
   static constexpr int BAR = STAGE + NL * kKeys * D;
   static constexpr int EXTRA = 2 * NL + 2 * NS + 23;
-  static constexpr int NBAR = EXTRA + 8;              // scales of a chunk
+  static constexpr int NBAR = EXTRA + 12;             // scales of a chunk, pieces over
   static constexpr int MISC = (BAR + NBAR * 8 + 15) & ~15;
   static constexpr int PIECE = MISC + 128;            // Piece [4]
   static constexpr int PUB = PIECE + 4 * 48;          // float2 [2 tiles][HQ]
@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(ScaledRowsLay<T>::THREADS, 1)
   const int wid = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   if (threadIdx.x == 64) {
     for (int i = 0; i < 8; ++i) dev::mbar_init(scales_full(sy, i), 1);
+    for (int i = 0; i < 4; ++i) dev::mbar_init(piece_over(sy, i), 8);
   }
   const uint32_t tmem = setup<L>(gb, sy, wid, &tmK, &tmV, &tmQ);
 
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(ScaledRowsLay<T>::THREADS, 1)
     fewer_registers<L>();
   } else if (wid == 3) {
     fewer_registers<L>();
-    plan_scaled<L>(sa, gb, sy);
+    plan_scaled<L>(a, gb, sy);
   } else if (wid < 12) {
     // ---- softmax warpgroups: thread r owns row r of every other chunk ------------------------
     more_registers<L>();
@@ -330,7 +331,10 @@ __global__ void __launch_bounds__(ScaledRowsLay<T>::THREADS, 1)
       }
       fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(sy.ofree(pp));
+      if (lane == 0) {
+        mbar_arrive(sy.ofree(pp));
+        mbar_arrive(piece_over(sy, k.i));
+      }
     }
     if (!ok && lane == 0) flag(PA_DEVERR_TIMEOUT);
   } else {
