@@ -653,8 +653,8 @@ pa_status pa_tree_commit(void* k_cache, void* v_cache, float* k_scale, float* v_
  * token is drawn from p without their tokens.  After a node without children,
  * or the max_path-th, it is drawn from p.
  * Drawn from weights w: the first v with w[0] + .. + w[v] > u0 (w[0] + .. +
- * w[V - 1]), u0 node 0's number.  Weights are summed as multiples of 2^-44 in 64
- * bits: exactly, in any order.  Where nothing is left, w is p; where p has
+ * w[V - 1]), u0 node 0's number.  p and q are taken as multiples of 2^-44 (to
+ * nearest even), and weights summed in 64 bits: exactly, in any order.  Where nothing is left, w is p; where p has
  * nothing either, next_token is -1, flagged PA_DEVERR_TREE.
  *
  * tokens        device int64 [num_tokens]: the nodes' tokens; q_start, parents,

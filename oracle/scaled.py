@@ -11,7 +11,7 @@ verifies drafted tokens in one pass.  Readings where the pages are silent:
   new starts afresh, with scale 1 if it has no value above 0;
 * a token at position t sees the keys 0 .. t;
 * refused siblings' tokens have nothing left; weights are whole multiples of
-  2^-44, rounded down.
+  2^-44, to nearest even.
 """
 import math
 
@@ -93,9 +93,9 @@ def attention(q, q_start, k_cache, v_cache, k_scale, v_scale, tables, lens, scal
 
 
 def fixed(p):
-    """Probabilities as whole multiples of 2^-44, rounded down."""
+    """Probabilities as whole multiples of 2^-44, to nearest even."""
     p = np.asarray(p, dtype=np.float64)
-    return np.floor(np.clip(np.where(np.isnan(p), 0.0, p), 0.0, 1.0) * 2.0 ** 44).astype(object)
+    return np.rint(np.clip(np.where(np.isnan(p), 0.0, p), 0.0, 1.0) * 2.0 ** 44).astype(object)
 
 
 def verify(tokens, target, uniform, q_start, max_path, draft=None, parents=None):

@@ -9,13 +9,14 @@
 // for those that become subnormal, where a scale of amax / 448 would round every
 // code again with every growth.
 //
-// One warp owns a (block, head) tile of K or of V: 16 rows of 128 values, 8
-// values a lane and row, so that all of a tile's rows are in flight at once and
-// the maximum is one reduction over the warp; nothing is read twice.  Tiles are
-// found from q_start alone: sequence b may touch at most n_b / 16 + 2 blocks, so
-// its tiles are grid columns q_start[b] / 16 + 2 b .., and a warp finds its
-// sequence by a search 32 ways at a time.  No column is longer than the batch
-// is, however uneven the sequences are.
+// One warp owns a (block, head): its tile of K and that of V, 16 rows of 128 values
+// each, 8 values a lane and row, so that all rows of a tile (16-bit input: of both) are
+// in flight at once and a maximum is one reduction over the warp; nothing is read
+// twice.  Tiles are found from q_start alone: sequence b may touch at most n_b / 16 + 2
+// blocks, so its tiles are grid columns q_start[b] / 16 + 2 b .., and a warp finds its
+// sequence by a search 32 ways at a time.  No column is longer than the batch is,
+// however uneven the sequences are.  The chain of loads before the rows (q_start,
+// length, table) is what both tiles share.
 #include "cache_rows.cuh"
 #include "device_common.cuh"
 #include "pa_internal.h"
@@ -66,6 +67,70 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
   return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 
+// A lane's values of a tile as they came: 8 of each of 8 rows.
+template <int IN>
+struct Rows {
+  uint4 w[8];
+  __device__ __forceinline__ void load(int i, const void* src, size_t at, bool live) {
+    w[i] = live ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src) + at) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ void get(int i, float (&y)[8]) const {
+    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = IN == PA_DTYPE_F16 ? dev::unpack2<__half>(u[e]) : dev::unpack2<__nv_bfloat16>(u[e]);
+      y[2 * e] = f.x;
+      y[2 * e + 1] = f.y;
+    }
+  }
+  // The largest size over the warp's values (finite: of those that are), as a float32's
+  // bits; sizes order like their bits, infinities and NaN above all.
+  __device__ __forceinline__ uint32_t largest(bool finite) const {
+    constexpr uint32_t INF = IN == PA_DTYPE_F16 ? 0x7C00u : 0x7F80u;
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t size = u[e] & 0x7FFF7FFFu;
+        if (finite) size &= ~__vcmpgeu2(size, INF * 0x10001u);
+        top = __vmaxu2(top, size);
+      }
+    }
+    top = __reduce_max_sync(FULL, max(top & 0xFFFFu, top >> 16));
+    const float2 f = IN == PA_DTYPE_F16 ? dev::unpack2<__half>(top) : dev::unpack2<__nv_bfloat16>(top);
+    return __float_as_uint(f.x) & 0x7FFFFFFFu;
+  }
+};
+template <>
+struct Rows<PA_DTYPE_F32> {
+  float x[8][8];
+  __device__ __forceinline__ void load(int i, const void* src, size_t at, bool live) {
+    if (live) {
+      dev::load8<PA_DTYPE_F32>(src, at, x[i]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
+    }
+  }
+  __device__ __forceinline__ void get(int i, float (&y)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = x[i][e];
+  }
+  __device__ __forceinline__ uint32_t largest(bool finite) const {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t u = __float_as_uint(x[i][e]) & 0x7FFFFFFFu;
+        if (!finite || u < 0x7F800000u) top = max(top, u);
+      }
+    return __reduce_max_sync(FULL, top);
+  }
+};
+
 template <int IN>
 __global__ void __launch_bounds__(32 * kWarps) scaled_append(const __grid_constant__ AppendArgs a) {
   const int lane = static_cast<int>(threadIdx.x & 31), col = static_cast<int>(blockIdx.x);
@@ -79,8 +144,8 @@ __global__ void __launch_bounds__(32 * kWarps) scaled_append(const __grid_consta
     }
     if (bits) atomicOr(&g_scaled_err, bits);
   }
-  const int tile = static_cast<int>(blockIdx.y) * kWarps + static_cast<int>(threadIdx.x >> 5);
-  if (tile >= 2 * a.Hkv) return;
+  const int g = static_cast<int>(blockIdx.y) * kWarps + static_cast<int>(threadIdx.x >> 5);
+  if (g >= a.Hkv) return;
   // the last sequence whose columns start at or before this one
   int lo = 0, hi = a.B;
   while (hi - lo > 1) {
@@ -99,80 +164,65 @@ __global__ void __launch_bounds__(32 * kWarps) scaled_append(const __grid_consta
     if (lane == 0) atomicOr(&g_scaled_err, PA_DEVERR_BLOCK_RANGE);
     return;
   }
-  const bool is_v = tile >= a.Hkv;
-  const int g = is_v ? tile - a.Hkv : tile;
-  const void* src = is_v ? a.v : a.k;
-  const int64_t stride = is_v ? a.v_stride : a.k_stride;
-  float* scale = (is_v ? a.vs : a.ks) + blk * a.Hkv + g;
-  uint8_t* dst = (is_v ? a.vc : a.kc) + (blk * a.Hkv + g) * (PA_BLOCK_SIZE * kDim);
+  const size_t tile = blk * a.Hkv + g;
   // rows r0 .. r1 - 1 of the block are new; a half warp takes every other one
   const int r0 = max(0, first - j * PA_BLOCK_SIZE), r1 = min(PA_BLOCK_SIZE, L - j * PA_BLOCK_SIZE);
   const int half = lane >> 4, c = 8 * (lane & 15);
-  const float old = r0 > 0 ? *scale : 0.f;
-  float x[8][8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = 2 * i + half;
-    if (r >= r0 && r < r1) {
-      const size_t t = static_cast<size_t>(qs) + (j * PA_BLOCK_SIZE + r - first);
-      dev::load8<IN>(src, t * stride + static_cast<size_t>(g) * kDim + c, x[i]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
-    }
-  }
-  // |x| as integers: they order like the values, infinities and NaN above all
-  constexpr uint32_t INF = 0x7F800000u;
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[i][e]) & 0x7FFFFFFFu);
-  top = __reduce_max_sync(FULL, top);
-  if (top >= INF) {  // the largest finite one
-    top = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t u = __float_as_uint(x[i][e]) & 0x7FFFFFFFu;
-        if (u < INF) top = max(top, u);
-      }
-    top = __reduce_max_sync(FULL, top);
-  }
-  // 448 = 1.75 x 2^8: the exponent less 8, one more for fractions above 1.75
-  float want = 0.f;
-  if (top > 0) {
-    const int e = max(-126, static_cast<int>(top >> 23) - 127 - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0));
-    want = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-  }
-  float s = fmaxf(want, old);  // (a NaN that stands there counts as none)
-  if (!(s > 0.f)) s = 1.f;
-  const float inv = 1.f / s;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = 2 * i + half;
-    if (r >= r0 && r < r1) *reinterpret_cast<uint2*>(dst + r * kDim + c) = encode8(x[i], inv);
-  }
-  if (r0 > 0 && s > old) {
+  const float old[2] = {r0 > 0 ? a.ks[tile] : 0.f, r0 > 0 ? a.vs[tile] : 0.f};
+  Rows<IN> x[2];
+  auto load = [&](int v) {
+    const int64_t stride = v ? a.v_stride : a.k_stride;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int r = 2 * i + half;
-      if (r >= r0) continue;
-      uint2* at = reinterpret_cast<uint2*>(dst + r * kDim + c);
-      const uint2 w = *at;
-      float y[8];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = dev::unpack2<__half>(
-            dev::e4m3x2_to<__half>(static_cast<uint16_t>((e < 2 ? w.x : w.y) >> (16 * (e & 1)))));
-        y[2 * e] = f.x;
-        y[2 * e + 1] = f.y;
-      }
-      *at = encode8(y, old * inv);
+      const size_t t = static_cast<size_t>(qs) + (j * PA_BLOCK_SIZE + r - first);
+      x[v].load(i, v ? a.v : a.k, t * stride + static_cast<size_t>(g) * kDim + c, r >= r0 && r < r1);
     }
+  };
+  load(0);
+  if constexpr (IN != PA_DTYPE_F32) load(1);
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    if constexpr (IN == PA_DTYPE_F32) {
+      if (v == 1) load(1);
+    }
+    uint32_t top = x[v].largest(false);
+    if (top >= 0x7F800000u) top = x[v].largest(true);  // of the finite ones
+    // 448 = 1.75 x 2^8: the exponent less 8, one more for fractions above 1.75
+    float want = 0.f;
+    if (top > 0) {
+      const int e = max(-126, static_cast<int>(top >> 23) - 127 - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0));
+      want = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+    }
+    float s = fmaxf(want, old[v]);  // (a NaN that stands there counts as none)
+    if (!(s > 0.f)) s = 1.f;
+    const float inv = 1.f / s;
+    uint8_t* dst = (v ? a.vc : a.kc) + tile * (PA_BLOCK_SIZE * kDim) + c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 2 * i + half;
+      float y[8];
+      x[v].get(i, y);
+      if (r >= r0 && r < r1) *reinterpret_cast<uint2*>(dst + r * kDim) = encode8(y, inv);
+    }
+    if (r0 > 0 && s > old[v]) {  // the rows that stay, under a larger scale
+#pragma unroll 1
+      for (int r = half; r < r0; r += 2) {
+        uint2* at = reinterpret_cast<uint2*>(dst + r * kDim);
+        const uint2 w = *at;
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = dev::unpack2<__half>(
+              dev::e4m3x2_to<__half>(static_cast<uint16_t>((e < 2 ? w.x : w.y) >> (16 * (e & 1)))));
+          y[2 * e] = f.x;
+          y[2 * e + 1] = f.y;
+        }
+        *at = encode8(y, old[v] * inv);
+      }
+    }
+    if (lane == 0) (v ? a.vs : a.ks)[tile] = s;
   }
-  if (lane == 0) *scale = s;
 }
 
 }  // namespace
@@ -198,7 +248,7 @@ pa_status launch_scaled_append(const ScaledAppendLaunch& l, const pa_cache_desc*
   const auto kernel = l.in_dtype == PA_DTYPE_F16    ? scaled_append<PA_DTYPE_F16>
                       : l.in_dtype == PA_DTYPE_BF16 ? scaled_append<PA_DTYPE_BF16>
                                                     : scaled_append<PA_DTYPE_F32>;
-  const dim3 grid(static_cast<unsigned>(l.T / PA_BLOCK_SIZE + 2 * l.B), static_cast<unsigned>((2 * a.Hkv + kWarps - 1) / kWarps));
+  const dim3 grid(static_cast<unsigned>(l.T / PA_BLOCK_SIZE + 2 * l.B), static_cast<unsigned>((a.Hkv + kWarps - 1) / kWarps));
   cudaError_t e = launch_dependent(kernel, grid, dim3(32 * kWarps), 0, static_cast<cudaStream_t>(stream), a);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return fail(PA_ERR_CUDA, "pa_block_scaled_append launch: %s", cudaGetErrorString(e));
