@@ -31,6 +31,7 @@
 // Values in masked places: a masked exponent is replaced; V rows that no row sees
 // are zeroed in shared memory, and a NaN code in a row that only some see is
 // zeroed and remembered for (dim, row), which end as NaN.
+#include <atomic>
 #include <mutex>
 
 #include "pa_internal.h"
@@ -65,7 +66,7 @@ __device__ __forceinline__ void multiply_scaled(uint8_t* gb, Sync<L> sy, uint32_
   o.start(sy, gb, ok);
   int spin = 0;
   int ns0 = 0, ns1 = 0, no0 = 0, no1 = 0;  // S^T and O^T issued per tile
-  int pieces_over = 0;                     // pieces that both warpgroups are done with
+  int pieces_over = 0;                     // pieces whose accumulators are read
   uint64_t t0 = 0;
   auto test = [&](uint32_t bar, int parity) { return __all_sync(FULL, dev::mbar_test(bar, parity & 1)) != 0; };
   auto landed = [&](int i) { return test(sy.full(i % NS), i / NS); };
@@ -77,7 +78,7 @@ __device__ __forceinline__ void multiply_scaled(uint8_t* gb, Sync<L> sy, uint32_
       // (a piece's first products wait for the piece that had its accumulators)
       const bool fresh = o.k.c < 2;
       const int over = fresh ? o.k.i - (L::OPAR - 1) : 0;
-      if (pieces_over < over && test(sy.ofree(pieces_over & 1), pieces_over >> 1)) ++pieces_over;
+      if (pieces_over < over && test(out_free(sy, pieces_over), pieces_over >> 1)) ++pieces_over;
       if (pieces_over >= over && test(sy.pfull(t), t ? no1 : no0) && landed(i)) {
         fence_after();
         const uint32_t id = idesc_f8(L::COLS, true);
@@ -90,6 +91,7 @@ __device__ __forceinline__ void multiply_scaled(uint8_t* gb, Sync<L> sy, uint32_
           for (int kk = 0; kk < 4; ++kk) mma_f8(od, vd + ((kk * 4096) >> 4), pd + ((kk * 4096) >> 4), id, kk > 0 ? 1u : acc);
           commit(sy.pdone(t));
           commit(sy.empty(i % NS));
+          if (o.k.c + 1 == o.k.nc) commit(out_full(sy, o.k.i));
         }
         __syncwarp();
         ++(t ? no1 : no0);
@@ -285,63 +287,176 @@ __device__ __forceinline__ void guard_scaled(const KeyLane& x, uint8_t* vslot, i
   }
 }
 
-// The rows of a piece out, by the warpgroup that joins them, a thread a dim: O^T of both
-// tiles times the rows' weights.
+// The outputs' warpgroup: each piece's queries two pieces ahead, and its rows out once
+// both tiles' products have ended: O^T of both times the rows' weights, a thread a dim.
+// (The softmax warpgroups go on with the next piece meanwhile: what they did at a
+// piece's end themselves took as long as four chunks of 8 rows.)  Of an item that other
+// CTAs have parts of, the last to be written is joined with the others by its
+// warpgroup, a warp a row, in the order of the parts.
 template <typename L>
-__device__ __forceinline__ void write_scaled(const ScaledArgs& sa, const KeyLane& x, const Piece& p, const float2* pubs,
-                                             int nan_from, uint32_t oa, bool exists) {
+__device__ __forceinline__ void outputs(const ScaledArgs& sa, uint8_t* gb, Sync<L> sy, uint32_t tmem) {
   constexpr int R = L::R, D = L::D;
   const TreeArgs& a = sa.t;
-  const bool direct = p.slot < 0;
-  float* wts = x.scratch;  // [2 accumulators][R]
-  int* place = reinterpret_cast<int*>(x.scratch + 2 * R);
-  if (x.r < R) {
-    const float2 c0 = pubs[x.r], c1 = pubs[R + x.r];
-    const float m = fmaxf(c0.x, c1.x), mz = m == -INFINITY ? 0.f : m;
-    const float w0 = dev::ex2(c0.x - mz), w1 = dev::ex2(c1.x - mz);
-    const float sum = w0 * c0.y + w1 * c1.y;
-    const float inv = direct && m != -INFINITY ? 1.f / sum : 1.f;
-    wts[x.r] = w0 * inv;
-    wts[R + x.r] = w1 * inv;
-    // where the row goes, in rows of out or of the partials
-    const int at = p.row0 + x.r, h = at & ((1 << a.gl) - 1);
-    place[x.r] = !exists ? -1 : direct ? (p.qs + (at >> a.gl)) * a.Hq + p.g * a.G + h : p.slot * a.slot_rows + x.r;
-    if (!direct && exists) {
-      a.part_m[place[x.r]] = m;
-      a.part_l[place[x.r]] = sum;
-    }
-  }
-  named_bar(2 + x.t, 128);
+  const int lane = static_cast<int>(threadIdx.x & 31), w4 = static_cast<int>(threadIdx.x >> 5) & 3, r = 32 * w4 + lane;
+  const uint32_t tl = tmem + (static_cast<uint32_t>(32 * w4) << 16);
+  float* wts = reinterpret_cast<float*>(gb + L::OUT);
+  int* place = reinterpret_cast<int*>(wts + 2 * R);
+  bool ok = true;
+  Piece p, next[2];  // of this step; and the two whose queries are loaded
+  // (sy.piece tells a lane; the warpgroup goes on, or leaves, as a whole)
+  auto open = [&](int i, Piece& x) {
+    const bool live = sy.piece(gb, i, x, ok);
+    ok = !bar_or(4, 128, !ok);
+    return ok && live;
+  };
+  auto store = [&](int at, int d, float o) {
+    const size_t i = static_cast<size_t>(at) * D + d;
+    if (a.out_f32)
+      static_cast<float*>(a.out)[i] = o;
+    else if (sa.q_bf16)
+      static_cast<__nv_bfloat16*>(a.out)[i] = __float2bfloat16(o);
+    else
+      static_cast<__half*>(a.out)[i] = __float2half(o);
+  };
+  int loaded = 0;  // pieces whose queries are
+  bool more = true;
 #pragma unroll 1
-  for (int j0 = 0; j0 < p.rows; j0 += 8) {
-    Terms8 tu, tv;
-    float u[8], v[8];
-    terms_load(oa + j0, R, tu);
-    terms_load(oa + L::COLS + j0, R, tv);
-    terms_wait(tu);
-    terms_wait(tv);
-    terms_sum(tu, u);
-    terms_sum(tv, v);
+  for (int i = 0;; ++i) {
+#pragma unroll 1
+    for (; more && loaded < i + 2; ++loaded) {
+      Piece x;
+      more = open(loaded, x);
+      if (!more) break;
+      load_queries<L>(sa, gb, sy, x, loaded, ok);
+      next[0] = next[1];
+      next[1] = x;
+    }
+    if (i >= loaded) break;
+    p = loaded == i + 2 ? next[0] : next[1];
+    const int pp = i & 1;
+    const int2 part = reinterpret_cast<const int2*>(gb + L::PARTS)[i & 3];
+    if (ok) ok = wait_warp(sums_full(sy, i, 0), (i >> 1) & 1) && wait_warp(sums_full(sy, i, 1), (i >> 1) & 1);
+    if (ok) ok = wait_warp(out_full(sy, i), (i >> 1) & 1);
+    ok = !bar_or(4, 128, !ok);
+    if (!ok) break;
+    tcg::fence_after();
+    const bool direct = p.slot < 0;
+    const int h = r & ((1 << a.gl) - 1);
+    if (r < R) {
+      const float* top = reinterpret_cast<const float*>(gb + L::TOP) + 2 * R * pp + r;
+      const float* sums = reinterpret_cast<const float*>(gb + L::SUM) + 8 * R * pp + r;
+      const float l0 = (sums[0] + sums[R]) + (sums[2 * R] + sums[3 * R]);
+      const float l1 = (sums[4 * R] + sums[5 * R]) + (sums[6 * R] + sums[7 * R]);
+      // (a row that saw only NaN scores has no reference and a sum of NaN)
+      const float m0 = top[0] == -INFINITY && l0 != l0 ? 0.f : top[0], m1 = top[R] == -INFINITY && l1 != l1 ? 0.f : top[R];
+      const float m = fmaxf(m0, m1), mz = m == -INFINITY ? 0.f : m;
+      const float w0 = dev::ex2(m0 - mz), w1 = dev::ex2(m1 - mz), sum = w0 * l0 + w1 * l1;
+      const float inv = direct && m != -INFINITY ? 1.f / sum : 1.f;
+      wts[r] = w0 * inv;
+      wts[R + r] = w1 * inv;
+      // where the row goes, in rows of out or of the partials
+      const bool exists = r < p.rows && h < a.G;
+      const int at = p.row0 + r;
+      place[r] = !exists ? -1 : direct ? (p.qs + (at >> a.gl)) * a.Hq + p.g * a.G + h : p.slot * R + r;
+      if (!direct && exists) {
+        a.part_m[place[r]] = m;
+        a.part_l[place[r]] = sum;
+      }
+    }
+    int* poison = reinterpret_cast<int*>(gb + L::POISON) + 256 * pp;
+    const int nan_from = min(poison[r], poison[128 + r]);
+    poison[r] = poison[128 + r] = R;
+    named_bar(4, 128);
+    const uint32_t oa = tl + L::COL_O + (i & (L::OPAR - 1)) * 2 * L::COLS;
+#pragma unroll 1
+    for (int j0 = 0; j0 < p.rows; j0 += 8) {
+      Terms8 tu, tv;
+      float u[8], v[8];
+      terms_load(oa + j0, R, tu);
+      terms_load(oa + L::COLS + j0, R, tv);
+      terms_wait(tu);
+      terms_wait(tv);
+      terms_sum(tu, u);
+      terms_sum(tv, v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float w0 = wts[j0 + e], w1 = wts[R + j0 + e];
-      float o = w0 == 0.f ? 0.f : u[e] * w0;
-      if (w1 != 0.f) o = fmaf(v[e], w1, o);
-      if (j0 + e >= nan_from) o = NAN;
-      const int at = place[j0 + e];
-      if (at < 0) continue;
-      const size_t i = static_cast<size_t>(at) * D + x.r;
-      if (!direct)
-        a.part_o[i] = o;
-      else if (a.out_f32)
-        static_cast<float*>(a.out)[i] = o;
-      else if (sa.q_bf16)
-        static_cast<__nv_bfloat16*>(a.out)[i] = __float2bfloat16(o);
-      else
-        static_cast<__half*>(a.out)[i] = __float2half(o);
+      for (int e = 0; e < 8; ++e) {
+        const float w0 = wts[j0 + e], w1 = wts[R + j0 + e];
+        float o = w0 == 0.f ? 0.f : u[e] * w0;
+        if (w1 != 0.f) o = fmaf(v[e], w1, o);
+        if (j0 + e >= nan_from) o = NAN;
+        const int at = place[j0 + e];
+        if (at < 0) continue;
+        if (direct)
+          store(at, r, o);
+        else
+          a.part_o[static_cast<size_t>(at) * D + r] = o;
+      }
+    }
+    tcg::fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(out_free(sy, i));
+      mbar_arrive(piece_over(sy, i));
+    }
+    if (direct) continue;
+    // ---- the item's parts -----------------------------------------------------------
+    __threadfence();
+    named_bar(4, 128);
+    if (r == 0) {
+      uint64_t* ticket = sa.tickets + part.x;
+      uint64_t seen = *reinterpret_cast<volatile uint64_t*>(ticket), was;
+      do {
+        was = seen;
+        const uint64_t now = (was >> 16 == sa.stamp ? was : sa.stamp << 16) + 1;
+        seen = atomicCAS(reinterpret_cast<unsigned long long*>(ticket), was, static_cast<int>(now & 0xFFFF) == part.y ? 0ull : now);
+        place[0] = static_cast<int>(now & 0xFFFF) == part.y;
+      } while (seen != was);
+      __threadfence();
+    }
+    named_bar(4, 128);
+    const bool last = place[0] != 0;
+    named_bar(4, 128);  // (place is written again)
+    if (!last) continue;
+#pragma unroll 1
+    for (int j = w4; j < p.rows; j += 4) {
+      const int head = j & ((1 << a.gl) - 1);
+      if (head >= a.G) continue;
+      auto row_of = [&](int q) { return static_cast<size_t>(q == 0 ? 2 * part.x + 1 : 2 * (part.x + q)) * R + j; };
+      float M = -INFINITY;
+#pragma unroll 1
+      for (int q0 = 0; q0 < part.y; q0 += 32)
+        M = fmaxf(M, warp_max(q0 + lane < part.y ? __ldcg(a.part_m + row_of(q0 + lane)) : -INFINITY));
+      const float mz = M == -INFINITY ? 0.f : M;
+      float ls = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int q0 = 0; q0 < part.y; q0 += 4) {
+        float4 o[4];
+        float m[4], l[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const size_t at = row_of(min(q0 + q, part.y - 1));
+          o[q] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D) + lane);
+          m[q] = __ldcg(a.part_m + at);
+          l[q] = __ldcg(a.part_l + at);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (q0 + q >= part.y) continue;
+          const float w = dev::ex2(m[q] - mz);
+          ls = fmaf(w, l[q], ls);
+          acc = make_float4(fmaf(w, o[q].x, acc.x), fmaf(w, o[q].y, acc.y), fmaf(w, o[q].z, acc.z), fmaf(w, o[q].w, acc.w));
+        }
+      }
+      const float inv = M == -INFINITY ? 0.f : 1.f / ls;
+      const int at = (p.qs + ((p.row0 + j) >> a.gl)) * a.Hq + p.g * a.G + head;
+      store(at, 4 * lane, acc.x * inv);
+      store(at, 4 * lane + 1, acc.y * inv);
+      store(at, 4 * lane + 2, acc.z * inv);
+      store(at, 4 * lane + 3, acc.w * inv);
     }
   }
-  __syncwarp();
+  if (!ok && lane == 0) flag(PA_DEVERR_TIMEOUT);
 }
 
 template <int R_>
@@ -362,8 +477,13 @@ __global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
   if (threadIdx.x == 64) {
     for (int i = 0; i < 8; ++i) dev::mbar_init(scales_full(sy, i), 1);
     for (int i = 0; i < 4; ++i) {
-      dev::mbar_init(piece_over(sy, i), 8);
+      dev::mbar_init(piece_over(sy, i), 4);
       dev::mbar_init(factors_full(sy, i), 1);
+      dev::mbar_init(sums_full(sy, i >> 1, i & 1), 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      dev::mbar_init(out_full(sy, i), 1);
+      dev::mbar_init(out_free(sy, i), 4);
     }
   }
   for (int i = static_cast<int>(threadIdx.x); i < 512; i += L::THREADS) reinterpret_cast<int*>(gb + L::POISON)[i] = R;
@@ -383,7 +503,7 @@ __global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
     plan_scaled<L>(a, gb, sy);
   } else if (wid >= 12) {
     fewer_registers<L>();
-    load_queries<L>(sa, gb, sy);
+    outputs<L>(sa, gb, sy, tmem);
   } else {
     // ---- softmax warpgroups: thread r owns key r of a chunk -----------------------------
     more_registers<L>();
@@ -396,8 +516,6 @@ __global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
     uint8_t* pbuf = gb + L::P0 + x.t * 16384;
     x.scratch = reinterpret_cast<float*>(pbuf);
     const int t = x.t, r = x.r, bar = 2 + t;
-    float2* pubs = reinterpret_cast<float2*>(gb + L::PUB);
-    float* refs = reinterpret_cast<float*>(gb + L::REF) + t * R;
     uint8_t* prow = pbuf + r * 128;  // the key's row of P^T, swizzled by r & 7
     const uint32_t sc = x.tl + L::COLS * t;
     bool ok = true;
@@ -409,13 +527,14 @@ __global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
       k.open(sy, gb, ok);
       const Piece& p = k.p;
       const bool exists = r < p.rows && (r & ((1 << a.gl) - 1)) < a.G;  // row r (r < R)
+      const int pp = k.i & 1;
+      float* refs = reinterpret_cast<float*>(gb + L::REF) + (2 * pp + t) * R;
       if (r < R) refs[r] = exists ? 0.f : -INFINITY;  // (a row that does not exist gets weight 0)
       // The barriers inside a piece have no limit, so where one warp has given up a
-      // wait the whole warpgroup leaves, here.  (And every warp has read the sums of l
-      // that the piece before left in the scratch.)
+      // wait the whole warpgroup leaves, here.
       ok = !bar_or(bar, 128, !ok);
       if (!ok || !__all_sync(FULL, k.live)) break;
-      const int pp = k.i & 1, shift = p.L - p.n, i0 = p.row0 >> a.gl;  // the item's first token
+      const int shift = p.L - p.n, i0 = p.row0 >> a.gl;  // the item's first token
       const uint32_t oc = x.tl + L::COL_O + ((k.i & (L::OPAR - 1)) * 2 + t) * L::COLS;
       const float* fac = reinterpret_cast<const float*>(gb + L::FAC) + (k.i & 3) * R;
       int* poison = reinterpret_cast<int*>(gb + L::POISON) + 256 * pp;
@@ -424,8 +543,9 @@ __global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
 #pragma unroll
       for (int j = 0; j < R; ++j) l[j] = 0.f;
       const int c_first = (t ^ k.ph) & 1;
-      const bool any = c_first < k.nc;
       if (ok) ok = wait_warp(factors_full(sy, k.i), (k.i >> 2) & 1);
+      // (what the piece notes for the outputs' warpgroup takes the place of the last but one's)
+      if (ok && k.i >= 2) ok = wait_warp(out_free(sy, k.i), ((k.i - 2) >> 1) & 1);
 #pragma unroll 1
       for (int c = c_first; c < k.nc; c += 2, ++n) {
         const int chunk = (k.it0 >> 1) + c, key = (p.c0 + c) * kKeys + r;
@@ -516,47 +636,24 @@ __global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
       }
       // ---- the piece's end --------------------------------------------------------------
       if (p.last) dev::grid_launch_dependents();
-      if (ok && any) ok = wait_warp(sy.pdone(t), (n - 1) & 1);  // O^T final, P^T's buffer free
-      fence_after();
-      if (any) {  // l over the 128 keys' lanes
-        constexpr int R0 = R > 32 ? 32 : R;
-        float v[R0];
+      // l over the 128 keys' lanes, and the references, for the outputs' warpgroup
+      float* sums = reinterpret_cast<float*>(gb + L::SUM) + ((2 * pp + t) * 4 + x.w4) * R;
+      constexpr int R0 = R > 32 ? 32 : R;
+      float v[R0];
 #pragma unroll
-        for (int j = 0; j < R0; ++j) v[j] = l[j];
-        const float sum = lane_sums<R0>(v, lane);
-        if (lane % (32 / R0) == 0) x.scratch[R * x.w4 + lane / (32 / R0)] = sum;
-        if constexpr (R > 32) {
-          float v2[R - 32];
+      for (int j = 0; j < R0; ++j) v[j] = l[j];
+      const float sum = lane_sums<R0>(v, lane);
+      if (lane % (32 / R0) == 0) sums[lane / (32 / R0)] = sum;
+      if constexpr (R > 32) {
+        float v2[R - 32];
 #pragma unroll
-          for (int j = 0; j < R - 32; ++j) v2[j] = l[32 + j];
-          const float sum2 = lane_sums<R - 32>(v2, lane);
-          if (lane % (32 / (R - 32)) == 0) x.scratch[R * x.w4 + 32 + lane / (32 / (R - 32))] = sum2;
-        }
+        for (int j = 0; j < R - 32; ++j) v2[j] = l[32 + j];
+        const float sum2 = lane_sums<R - 32>(v2, lane);
+        if (lane % (32 / (R - 32)) == 0) sums[32 + lane / (32 / (R - 32))] = sum2;
       }
-      // both warpgroups are done with what the piece before published
-      if (ok && k.i >= 1) ok = wait_warp(sy.ofree(pp ^ 1), ((k.i - 1) >> 1) & 1);
-      named_bar(bar, 128);
-      if (r < R) {
-        const float sum = any ? (x.scratch[r] + x.scratch[R + r]) + (x.scratch[2 * R + r] + x.scratch[3 * R + r]) : 0.f;
-        pubs[R * t + r] = make_float2(any && exists && seen ? ref : sum != sum ? 0.f : -INFINITY, sum);
-      }
+      if (r < R) reinterpret_cast<float*>(gb + L::TOP)[(2 * pp + t) * R + r] = exists && seen ? ref : -INFINITY;
       __syncwarp();
-      if (lane == 0) mbar_arrive(sy.pub(t));
-      // the warpgroup with the last chunk joins both accumulators
-      if (((k.ph + k.nc - 1) & 1) == t) {
-        if (ok) ok = wait_warp(sy.pub(t ^ 1), k.i & 1);  // (after that tile's last product)
-        named_bar(bar, 128);
-        fence_after();
-        const int nan_from = min(poison[r], poison[128 + r]);
-        poison[r] = poison[128 + r] = R;
-        write_scaled<L>(sa, x, p, pubs, nan_from, x.tl + L::COL_O + (k.i & (L::OPAR - 1)) * 2 * L::COLS, exists);
-      }
-      fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(sy.ofree(pp));
-        mbar_arrive(piece_over(sy, k.i));
-      }
+      if (lane == 0) mbar_arrive(sums_full(sy, k.i, t));
     }
     if (!ok && lane == 0) flag(PA_DEVERR_TIMEOUT);
   }
@@ -602,6 +699,9 @@ pa_status launch_kernel(const ScaledAttentionLaunch& l, K kernel, cudaStream_t s
   a.part_m = a.part_o + rows * L::D;
   a.part_l = a.part_m + rows;
   a.split = reinterpret_cast<int4*>(a.part_l + rows);
+  sa.tickets = reinterpret_cast<uint64_t*>(a.part_l + rows);
+  static std::atomic<uint64_t> launches{0x5CA1ED00ull};
+  sa.stamp = ++launches & 0xFFFFFFFFFFFFull;
 
   CUtensorMap tm[3];
   for (int v = 0; v < 2; ++v) {
@@ -633,10 +733,12 @@ pa_status launch_kernel(const ScaledAttentionLaunch& l, K kernel, cudaStream_t s
     e = launch_dependent(kernel, grid, block, L::BYTES, stream, tm[0], tm[1], tm[2], sa);
   else
     e = launch_dependent(kernel, grid, block, L::BYTES, stream, tm[0], tm[1], sa);
-  if (e == cudaSuccess && l.max_context_len > kKeys) {
-    const dim3 mgrid(static_cast<unsigned>(a.n_cta), a.slot_rows / kMergeRows), mblock(32 * kMergeRows);
-    e = sa.q_bf16 ? launch_dependent(tree_merge<__nv_bfloat16, L::D>, mgrid, mblock, 0, stream, a)
-                  : launch_dependent(tree_merge<__half, L::D>, mgrid, mblock, 0, stream, a);
+  if constexpr (L::ROWS) {
+    if (e == cudaSuccess && l.max_context_len > kKeys) {
+      const dim3 mgrid(static_cast<unsigned>(a.n_cta), a.slot_rows / kMergeRows), mblock(32 * kMergeRows);
+      e = sa.q_bf16 ? launch_dependent(tree_merge<__nv_bfloat16, L::D>, mgrid, mblock, 0, stream, a)
+                    : launch_dependent(tree_merge<__half, L::D>, mgrid, mblock, 0, stream, a);
+    }
   }
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));

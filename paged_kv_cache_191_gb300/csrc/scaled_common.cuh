@@ -14,6 +14,8 @@ struct ScaledArgs {
   TreeArgs t;        // (mask and words are not used; scale_log2 has the scale's sign)
   int64_t q_stride;  // elements between tokens
   int32_t q_bf16;
+  uint64_t* tickets;  // [CTAs]: parts of the item that CTA k begins and leaves, that are written
+  uint64_t stamp;     // of this launch: a ticket without it counts as 0, whatever it holds
 };
 
 // R: rows of an item, 8, 16, 32 or 40.
@@ -32,14 +34,18 @@ struct ScaledLay {
   static constexpr int NL = NS;
   static constexpr int BAR = RING + NS * SLOT;
   static constexpr int EXTRA = 2 * NL + 2 * NS + 23;
-  static constexpr int NBAR = EXTRA + 16;         // scales of a chunk, pieces over, factors of a piece
+  // scales of a chunk, pieces over, factors of a piece, sums published, O^T at rest, O^T read
+  static constexpr int NBAR = EXTRA + 24;
   static constexpr int MISC = (BAR + NBAR * 8 + 15) & ~15;
   static constexpr int PIECE = MISC + 128;        // Piece [4]
-  static constexpr int PUB = PIECE + 4 * 48;      // float2 [2 tiles][R]
-  static constexpr int SC = PUB + 16 * R;         // float [8 chunks][K 8, V 8]
+  static constexpr int PARTS = PIECE + 4 * 48;    // int2 [4 pieces]: the CTA that has the item's first part, its parts
+  static constexpr int SC = PARTS + 4 * 8;        // float [8 chunks][K 8, V 8]
   static constexpr int FAC = SC + 8 * 64;         // float [4 pieces][R]
-  static constexpr int REF = FAC + 16 * R;        // float [2 tiles][R]: minus the references
-  static constexpr int POISON = REF + 8 * R;      // int [piece parity][2 tiles][128 dims]: first row that sees a NaN there
+  static constexpr int REF = FAC + 16 * R;        // float [piece parity][2 tiles][R]: minus the references
+  static constexpr int SUM = REF + 16 * R;        // float [piece parity][2 tiles][4 warps][R]: l
+  static constexpr int TOP = SUM + 64 * R;        // float [piece parity][2 tiles][R]: the references (-inf: none)
+  static constexpr int OUT = TOP + 16 * R;        // the outputs' weights, float [2 tiles][R], and places, int [R]
+  static constexpr int POISON = OUT + 12 * R;     // int [piece parity][2 tiles][128 dims]: first row that sees a NaN there
   static constexpr int MASK = 0;
   static constexpr int BYTES = POISON + 2048;
   static constexpr int THREADS = 512;
@@ -68,6 +74,16 @@ template <typename L>
 __device__ __forceinline__ uint32_t factors_full(const Sync<L>& sy, int piece) {
   return sy.at(L::EXTRA + 12 + (piece & 3));
 }
+// A tile's sums and references of the piece are written; its products have ended; its
+// accumulators and sums are read.
+template <typename L>
+__device__ __forceinline__ uint32_t sums_full(const Sync<L>& sy, int piece, int tile) {
+  return sy.at(L::EXTRA + 16 + 2 * (piece & 1) + tile);
+}
+template <typename L>
+__device__ __forceinline__ uint32_t out_full(const Sync<L>& sy, int piece) { return sy.at(L::EXTRA + 20 + (piece & 1)); }
+template <typename L>
+__device__ __forceinline__ uint32_t out_free(const Sync<L>& sy, int piece) { return sy.at(L::EXTRA + 22 + (piece & 1)); }
 
 // What the softmax's rare paths share with its loop.
 struct KeyLane {
@@ -126,74 +142,65 @@ __device__ __forceinline__ U units_per_head(const Span& x, int s) {
   return x.tiles == 0 ? 0 : units_before<U>(x, x.tiles - 1, s) + kItem + chunks_of(x, x.tiles - 1, s);
 }
 
-// The query warpgroup: every row of a piece scaled by a power of two to 2^14 .. 2^15 (a
-// row of small values keeps its bits beside one of large ones), in E5M2 terms; its
-// factor takes the power back.  A warp has a quarter of the rows.
+// A piece's queries, by the outputs' warpgroup: every row scaled by a power of two to
+// 2^14 .. 2^15 (a row of small values keeps its bits beside one of large ones), in E5M2
+// terms; its factor takes the power back.  A warp has a quarter of the rows.
 template <typename L>
-__device__ __forceinline__ void load_queries(const ScaledArgs& sa, uint8_t* gb, Sync<L> sy) {
+__device__ __forceinline__ void load_queries(const ScaledArgs& sa, uint8_t* gb, Sync<L> sy, const Piece& p, int i, bool& ok) {
   constexpr int R = L::R, EACH = R / 4, BATCH = EACH % 4 == 0 ? 4 : 2;
   const TreeArgs& a = sa.t;
   const int lane = static_cast<int>(threadIdx.x & 31), w4 = static_cast<int>(threadIdx.x >> 5) & 3;
   const int heads = (1 << a.gl) - 1;
-  bool ok = true;
-  Piece p;
-#pragma unroll 1
-  for (int i = 0;; ++i) {
-    const bool live = sy.piece(gb, i, p, ok);
-    ok = !bar_or(4, 128, !ok);  // (where a warp has given up a wait, the warpgroup leaves as a whole)
-    if (!ok || !live) break;
-    auto load = [&](int r0, uint2(&x)[BATCH]) {  // 8 bytes a lane and row
+  auto load = [&](int r0, uint2(&x)[BATCH]) {  // 8 bytes a lane and row
 #pragma unroll
-      for (int j = 0; j < BATCH; ++j) {
-        const int r = r0 + j, h = r & heads;
-        x[j] = make_uint2(0u, 0u);
-        if (r < p.rows && h < a.G)
-          x[j] = __ldg(reinterpret_cast<const uint2*>(
-              static_cast<const uint16_t*>(a.q) + static_cast<size_t>(p.qs + ((p.row0 + r) >> a.gl)) * sa.q_stride +
-              static_cast<size_t>(p.g * a.G + h) * L::D + 4 * lane));
-      }
-    };
-    uint2 x[BATCH], next[BATCH];
-    load(EACH * w4, next);
-    if (ok && i >= 2) ok = wait_warp(sy.qfree(i & 1), ((i - 2) >> 1) & 1);
-    float* fac = reinterpret_cast<float*>(gb + L::FAC) + (i & 3) * R;
-    uint8_t* to = gb + (i & 1) * L::QTILE + (lane & 3) * 4;
-#pragma unroll 1
-    for (int r0 = EACH * w4; r0 < EACH * (w4 + 1); r0 += BATCH) {
-#pragma unroll
-      for (int j = 0; j < BATCH; ++j) x[j] = next[j];
-      if (r0 + BATCH < EACH * (w4 + 1)) load(r0 + BATCH, next);
-#pragma unroll
-      for (int j = 0; j < BATCH; ++j) {
-        const int r = r0 + j;
-        const float2 lo = sa.q_bf16 ? dev::unpack2<__nv_bfloat16>(x[j].x) : dev::unpack2<__half>(x[j].x);
-        const float2 hi = sa.q_bf16 ? dev::unpack2<__nv_bfloat16>(x[j].y) : dev::unpack2<__half>(x[j].y);
-        const float f[4] = {lo.x, lo.y, hi.x, hi.y};
-        uint32_t top = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(f[e]) & 0x7FFFFFFFu);
-        top = __reduce_max_sync(FULL, top);
-        const bool fine = top < 0x7F800000u;  // (else the row's factor is NaN, and so is the row)
-        const int k = min(14 - (static_cast<int>(top >> 23) - 127), 100);
-        const float up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
-        uint32_t p0[kParts], p1[kParts];
-        terms(dev::pack2<__half>(f[0] * up, f[1] * up), p0);
-        terms(dev::pack2<__half>(f[2] * up, f[3] * up), p1);
-#pragma unroll
-        for (int e = 0; e < kParts; ++e)
-          *reinterpret_cast<uint32_t*>(to + (e * R + r) * 128 + (((lane >> 2) ^ (r & 7)) << 4)) = upper(p0[e], p1[e]);
-        if (lane == 0) fac[r] = fine ? a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23) : NAN;
-      }
+    for (int j = 0; j < BATCH; ++j) {
+      const int r = r0 + j, h = r & heads;
+      x[j] = make_uint2(0u, 0u);
+      if (r < p.rows && h < a.G)
+        x[j] = __ldg(reinterpret_cast<const uint2*>(
+            static_cast<const uint16_t*>(a.q) + static_cast<size_t>(p.qs + ((p.row0 + r) >> a.gl)) * sa.q_stride +
+            static_cast<size_t>(p.g * a.G + h) * L::D + 4 * lane));
     }
-    dev::fence_proxy_async_smem();
-    named_bar(4, 128);
-    if (w4 == 0 && lane == 0) {
-      mbar_arrive(sy.qfull(i & 1));
-      mbar_arrive(factors_full(sy, i));
+  };
+  uint2 x[BATCH], next[BATCH];
+  load(EACH * w4, next);
+  if (ok && i >= 2) ok = wait_warp(sy.qfree(i & 1), ((i - 2) >> 1) & 1);
+  float* fac = reinterpret_cast<float*>(gb + L::FAC) + (i & 3) * R;
+  uint8_t* to = gb + (i & 1) * L::QTILE + (lane & 3) * 4;
+#pragma unroll 1
+  for (int r0 = EACH * w4; r0 < EACH * (w4 + 1); r0 += BATCH) {
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j) x[j] = next[j];
+    if (r0 + BATCH < EACH * (w4 + 1)) load(r0 + BATCH, next);
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j) {
+      const int r = r0 + j;
+      const float2 lo = sa.q_bf16 ? dev::unpack2<__nv_bfloat16>(x[j].x) : dev::unpack2<__half>(x[j].x);
+      const float2 hi = sa.q_bf16 ? dev::unpack2<__nv_bfloat16>(x[j].y) : dev::unpack2<__half>(x[j].y);
+      const float f[4] = {lo.x, lo.y, hi.x, hi.y};
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(f[e]) & 0x7FFFFFFFu);
+      top = __reduce_max_sync(FULL, top);
+      const bool fine = top < 0x7F800000u;  // (else the row's factor is NaN, and so is the row)
+      const int k = min(14 - (static_cast<int>(top >> 23) - 127), 100);
+      const float up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+      uint32_t p0[kParts], p1[kParts];
+      terms(dev::pack2<__half>(f[0] * up, f[1] * up), p0);
+      terms(dev::pack2<__half>(f[2] * up, f[3] * up), p1);
+#pragma unroll
+      for (int e = 0; e < kParts; ++e)
+        *reinterpret_cast<uint32_t*>(to + (e * R + r) * 128 + (((lane >> 2) ^ (r & 7)) << 4)) = upper(p0[e], p1[e]);
+      if (lane == 0) fac[r] = fine ? a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23) : NAN;
     }
-    __syncwarp();
   }
-  if (!ok && lane == 0) flag(PA_DEVERR_TIMEOUT);
+  dev::fence_proxy_async_smem();
+  named_bar(4, 128);
+  if (w4 == 0 && lane == 0) {
+    mbar_arrive(sy.qfull(i & 1));
+    mbar_arrive(factors_full(sy, i));
+  }
+  __syncwarp();
 }
 
 // The planner warp: this CTA's pieces, published up to four ahead.
@@ -307,9 +314,13 @@ __device__ __forceinline__ void plan_scaled(const TreeArgs& a, uint8_t* gb, Sync
         p.g = g;
         p.row0 = tile * a.item_rows;
         p.rows = min(a.item_rows, (s.n << a.gl) - p.row0);
-        p.slot = p.c0 == 0 && p.c1 == nch ? -1 : 2 * me + (i == 0 ? 0 : 1);
-        if (p.c0 == 0 && p.c1 < nch) {  // the item goes on in the next CTAs: what the merge needs
-          sp0 = make_int4((u - off + cost - 1) / upc - me + 1, p.slot, s.qs, p.row0);
+        // partial rows: an item's first part has the CTA's second set, a later one the first
+        p.slot = p.c0 == 0 && p.c1 == nch ? -1 : 2 * me + (p.c0 == 0 ? 1 : 0);
+        const int owner = (u - off + kItem) / upc, parts = (u - off + cost - 1) / upc - owner + 1;
+        if constexpr (!L::ROWS) {
+          if (lane == 0) reinterpret_cast<int2*>(gb + L::PARTS)[i & 3] = make_int2(owner, parts);
+        } else if (p.c0 == 0 && p.c1 < nch) {  // the item goes on in the next CTAs: what the merge needs
+          sp0 = make_int4(parts, p.slot, s.qs, p.row0);
           sp1 = make_int4(g, p.rows, 1, 0);
         }
       }
@@ -332,8 +343,10 @@ __device__ __forceinline__ void plan_scaled(const TreeArgs& a, uint8_t* gb, Sync
     __syncwarp();
   }
   if (lane == 0) {
-    a.split[2 * blockIdx.x] = sp0;
-    a.split[2 * blockIdx.x + 1] = sp1;
+    if constexpr (L::ROWS) {
+      a.split[2 * blockIdx.x] = sp0;
+      a.split[2 * blockIdx.x + 1] = sp1;
+    }
     if (!ok) flag(PA_DEVERR_TIMEOUT);
   }
 }
