@@ -14,8 +14,8 @@ struct ScaledArgs {
   TreeArgs t;        // (mask and words are not used; scale_log2 has the scale's sign)
   int64_t q_stride;  // elements between tokens
   int32_t q_bf16;
-  uint64_t* tickets;  // [CTAs]: parts of the item that CTA k begins and leaves, that are written
-  uint64_t stamp;     // of this launch: a ticket without it counts as 0, whatever it holds
+  uint64_t* written;  // [CTAs][2]: the stamp, where that set of partial rows is written
+  uint64_t stamp;     // of this launch
 };
 
 // R: rows of an item, 8, 16, 32 or 40.
@@ -223,6 +223,7 @@ __device__ __forceinline__ void plan_scaled(const TreeArgs& a, uint8_t* gb, Sync
   };
   // First all units are summed, then the sequence of this CTA's first one is found.
   int64_t sum = 0;
+  int most = 0;  // units of the largest item
   int upc = 0, start = 0, end = 0, b = 0, ub = 0;  // units before sequence b: ub
 #pragma unroll 1
   for (int g = 0, find = 0;; ++g) {
@@ -230,10 +231,15 @@ __device__ __forceinline__ void plan_scaled(const TreeArgs& a, uint8_t* gb, Sync
       if (find) break;
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(FULL, sum, off);
+      most = __reduce_max_sync(FULL, most);
       // more than the launch was checked for: q_start has ranges that overlap
       if (sum > kMaxUnits && me == 0 && lane == 0) flag(PA_DEVERR_QUERY_RANGE);
       const int total = sum > kMaxUnits ? 0 : static_cast<int>(sum);
-      upc = max((total + a.n_cta - 1) / a.n_cta, a.min_units);
+      // Few units: equal parts of the largest item, of min_units at least.  (Joining parts takes
+      // 2 us and more: a sequence of 600 tokens 9.3 us whole, 11.1 in parts of 2 units; one of
+      // 32768 with one kv head 37 us in parts of 2, 21 in parts of 6.)
+      upc = (total + a.n_cta - 1) / a.n_cta;
+      if (upc < a.min_units) upc = max(a.min_units, (most + max(1, most / a.min_units) - 1) / max(1, most / a.min_units));
       start = static_cast<int>(min(static_cast<int64_t>(me) * upc, static_cast<int64_t>(total)));
       end = min(start + upc, total);
       if (start >= end) break;
@@ -244,6 +250,7 @@ __device__ __forceinline__ void plan_scaled(const TreeArgs& a, uint8_t* gb, Sync
     const int64_t units = units_per_head<int64_t>(mine, per) * a.Hkv;
     if (!find) {
       sum += units;
+      if (mine.tiles > 0) most = max(most, kItem + chunks_of(mine, mine.tiles - 1, per));
       continue;
     }
     const int w = static_cast<int>(units);
