@@ -8,29 +8,47 @@
 //
 // The codes are never converted: they go from HBM by TMA to shared memory and from
 // there into tcgen05.mma kind::f8f6f4 as they are.  What meets them, queries and
-// weights, has more bits than an 8-bit type, so each is a sum of four E5M2 terms,
-// which hold an f16 value exactly (scaled_common.cuh), and the terms are four
-// times the columns of one product rather than four products: K and V, the
-// larger operand, are read from shared memory once.  Converting codes to f16 costs a
-// kernel of this shape twice their bytes in shared-memory traffic in each of three
-// steps (landing, conversion, product) where this one has two.
+// weights, has more bits than an 8-bit type, so each is a sum of three E5M2 terms,
+// which hold an f16 value exactly (scaled_common.cuh), and the terms are three times the
+// columns of one product rather than three products: K and V, the larger operand, are
+// read from shared memory once.  (Converting them to f16 there, as the calls over
+// per-token scales do, moves a code's byte in, and out again as two, before the product
+// reads those: at 8 rows that kernel's shape is bound by shared memory at half of HBM's
+// rate.)  Above 40 rows per (sequence, kv head) the terms' columns outgrow tensor memory,
+// and another kernel takes over (scaled_rows.cuh).
 //
 // The products are transposed as in the tree attention: S^T = K Q^T (M = the
-// chunk's 128 keys, N = 4 terms x rows) and O^T += V^T P^T (M = 128 dims), a
+// chunk's 128 keys, N = 3 terms x rows) and O^T += V^T P^T (M = 128 dims), a
 // softmax thread owning a key, whose scales are its own registers: a block's scale
-// multiplies the score after the product and the weight before it.  Rows, work
-// items, persistent CTAs and the merge of items that span CTAs are the tree
-// attention's too; an item is 8, 16 or 32 rows (a token's heads, up to a power of
-// two, of one kv head), and of a prompt's items each streams only the chunks that
-// its tokens see.
+// multiplies the score after the product and the weight before it.  An item is 8, 16,
+// 32 or 40 rows (tokens x heads of one kv head, the heads up to a power of two) and
+// streams its context in chunks of 128 keys; of a prompt's items each only the chunks
+// that its tokens see.  One persistent CTA per SM takes an equal run of the batch's
+// chunks, planned on the device from the lengths; the parts of an item that spans CTAs
+// are joined by whichever CTA writes the last one, in the order of the parts.
 //
-// Inside a CTA: warp 0 loads K and the scales, warp 2 V, warp 1 issues the
-// products, warp 3 plans the pieces and splits their queries into terms, warps 4-7
-// and 8-11 are two softmax warpgroups on alternate chunks.
+// Inside a CTA: warp 0 loads K and the scales, warp 2 V, warp 1 issues the products,
+// warp 3 plans the pieces; warps 4-7 and 8-11 are two softmax warpgroups on alternate
+// chunks, each with its scores, accumulators and references; warps 12-15 split the
+// queries of the pieces to come into terms and write the rows of those that are over.
+//
+// What bounds it: HBM while a kv head has few rows, and what a CTA does besides.  8
+// sequences of 8 kv heads, 4 rows, contexts to 32768: 71 us, 84 % of the copy rate; the
+// chunks go by at 96 % of it, and the start (launch, lengths, block ids, scales, first
+// chunk: 5 us) and the last joined rows (3 us) are the rest.  64 sequences of 8 kv heads,
+// 8 rows, mean context 2064: 56 us, 72 %.  32 sequences of 32 kv heads, one row, mean
+// context 1024: 57 us, 69 %: items of 8 chunks, whose first needs new references (700
+// clocks) and a barrier.  The same 64 with chains of 2 to 5 tokens: 100 us, 41 %: the
+// softmax warpgroups, 2250 clocks a chunk where HBM takes 1420; a chunk's exponents take
+// a warp 1000 clocks at 40 rows, the terms of its weights 900.
+// The code that runs once per piece is kept small: 136 KB of it took 78 us where 78 KB
+// take 65 (the instruction caches; 32 kv heads).  Skipping 8 rows at a time that a short
+// chain has not was slower (114 us for 100): it cuts the straight line of exponents.
 //
 // Values in masked places: a masked exponent is replaced; V rows that no row sees
 // are zeroed in shared memory, and a NaN code in a row that only some see is
-// zeroed and remembered for (dim, row), which end as NaN.
+// zeroed and remembered for (dim, row), which end as NaN.  A NaN score or query comes
+// out by the row's sum.
 #include <atomic>
 #include <mutex>
 

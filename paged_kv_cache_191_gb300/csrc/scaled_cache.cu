@@ -16,7 +16,9 @@
 // blocks, so its tiles are grid columns q_start[b] / 16 + 2 b .., and a warp finds its
 // sequence by a search 32 ways at a time.  No column is longer than the batch is,
 // however uneven the sequences are.  The chain of loads before the rows (q_start,
-// length, table) is what both tiles share.
+// length, table) is what both tiles share.  Nine chunks of up to 2043 tokens, 32 heads,
+// f16: 39 us, 86 % of the copy rate (47 us with a warp per tile); one token 2.8 us, 64
+// of 8 heads 3.4 us: the launch.
 #include "cache_rows.cuh"
 #include "device_common.cuh"
 #include "pa_internal.h"

@@ -1,5 +1,5 @@
-// Attention over a block-scaled cache: shared memory, the planner and query
-// warp, and the producers.  The ring, the pieces, the waits and tensor memory's
+// Attention over a block-scaled cache: shared memory, the E5M2 terms, the planner, the
+// queries and the producers.  The ring, the pieces, the waits and tensor memory's
 // access are those of the tree attention.
 #pragma once
 
@@ -65,9 +65,9 @@ struct ScaledLay {
 
 template <typename L>
 __device__ __forceinline__ uint32_t scales_full(const Sync<L>& sy, int chunk) { return sy.at(L::EXTRA + (chunk & 7)); }
-// Both warpgroups are done with the piece.  (Of four pieces each its own: the planner, who
-// waits for the last but three, may be more than two behind, and ofree's two would then
-// have gone round.)
+// The piece is over.  (Of four pieces each its own: the planner, who waits for the last but
+// three, may be more than two behind, and a barrier of every second piece would then have
+// gone round.)
 template <typename L>
 __device__ __forceinline__ uint32_t piece_over(const Sync<L>& sy, int piece) { return sy.at(L::EXTRA + 8 + (piece & 3)); }
 template <typename L>

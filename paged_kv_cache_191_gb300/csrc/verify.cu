@@ -23,7 +23,11 @@
 // Every CTA finds the accepted path by itself (a few gathers, from L2 for all
 // but the first), then sums its share of the row; after one cluster barrier
 // each knows where the threshold lies, and the warp whose share holds it reads one
-// batch of 256 values again, whose sum it had kept.
+// batch of 256 values again, whose sum it had kept.  (A scan of its whole share took
+// longer than the sums: 106 us for 55 in the batch below.)
+// 256 chains over 128000 tokens, two tables: 53 us, 73 % of the copy rate; 48 trees of 9
+// to 26 nodes over 65521: 13 us; one chain of 5 over 32000: 9 us, which are the launch
+// of a cluster and the gathers, path, sums and scan one after another.
 #include <cooperative_groups.h>
 
 #include <algorithm>
