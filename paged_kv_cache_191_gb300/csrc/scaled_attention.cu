@@ -691,6 +691,8 @@ __global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
   teardown(wid, tmem);
 }
 
+std::atomic<uint64_t> g_launches{0};  // of every kernel and device: workspaces may go from one to another
+
 // L: a kernel's layout; kernel: with a thread per key it has no map of q.
 template <typename L, typename K>
 pa_status launch_kernel(const ScaledAttentionLaunch& l, K kernel, cudaStream_t stream) {
@@ -731,8 +733,7 @@ pa_status launch_kernel(const ScaledAttentionLaunch& l, K kernel, cudaStream_t s
   a.part_l = a.part_m + rows;
   a.split = reinterpret_cast<int4*>(a.part_l + rows);
   sa.written = reinterpret_cast<uint64_t*>(a.part_l + rows);
-  static std::atomic<uint64_t> launches{0};
-  sa.stamp = 0x9E3779B97F4A7C15ull * ++launches;  // (odd multiples: no two alike, none 0, no number that memory is full of)
+  sa.stamp = 0x9E3779B97F4A7C15ull * ++g_launches;  // (odd multiples: no two alike, none 0, no number that memory is full of)
 
   CUtensorMap tm[3];
   for (int v = 0; v < 2; ++v) {
