@@ -344,9 +344,9 @@ def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_c
 
 
 def _rows(t, name, heads_dim):
-    """Token stride of [T, H, D] rows whose last two dims are dense."""
+    """Token stride of [T, H, D] rows whose last two dims are dense (without rows, of any strides)."""
     shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or stride[2] != 1 or (shape[1] > 1 and stride[1] != heads_dim):
+    if len(shape) != 3 or (t.numel() and (stride[2] != 1 or (shape[1] > 1 and stride[1] != heads_dim))):
         raise ValueError(f"{name} must be [T, heads, head_dim] with dense heads")
     return stride[0] if shape[0] > 1 else shape[1] * shape[2]
 
@@ -559,7 +559,7 @@ def draft_verify(tokens, target_probs, uniform, q_start, max_path, draft_probs=N
         if t is None:
             strides.append(V)
             continue
-        if t.dtype != torch.float32 or t.shape != (T, V) or (V > 1 and t.stride(1) != 1):
+        if t.dtype != torch.float32 or t.shape != (T, V) or (T > 0 and V > 1 and t.stride(1) != 1):
             raise ValueError(f"{n} must be float32 [T, vocab], dense in the vocabulary")
         strides.append(t.stride(0) if T > 1 else V)
     on = q_start.device

@@ -6,8 +6,8 @@ Codes, scales, paths and drawn tokens are equal to the oracle's.  Attention's
 tolerance, u = 2^-11 (weights x V scale are rounded to f16, the sum of weights
 is not):
 * every product of a weight is off by u relative: u sum w |V|;
-* below 2^-16 of a unit nothing of it is left, a row's largest is at least 2^11
-  units: L keys of at most 448 are off by L 448 2^-27 of the largest V scale;
+* weights are multiples of 2^-16 units, rounded: off by 2^-17, and a row's largest is
+  at least 2^10 units: L keys of at most 448 are off by L 448 2^-27 of the largest V scale;
 * scores: a float32 sum of D products is off by at most D 2^-23 sum |q K|
   scale; q's values go down to 2^-31 of the row's largest.  A score moves its
   weight and the sum of weights by that much relative;
@@ -399,6 +399,98 @@ def test_verification_on_another_stream(monkeypatch):
         monkeypatch, ops, lambda st: list(ops.draft_verify(*a, 5, draft_probs=dr, stream=st)))
     for x, y in zip(plain, other):
         assert torch.equal(x, y)
+
+
+# (query heads, tokens) over one kv head: 8, 16, 32 and 40 rows of an item, a thread per row
+KERNELS = [(8, 1), (16, 1), (8, 4), (8, 5), (32, 9)]
+
+
+def test_kernels_take_turns_in_one_workspace():
+    """One long item each, cut over most CTAs, in a workspace that holds what the
+    call before left there."""
+    ws = torch.full((64 << 20,), 255, dtype=torch.uint8, device=DEV)
+    first = {}
+    for turn in range(3):
+        for i, (Hq, n) in enumerate(KERNELS):
+            w = ScaledBatch(70 + i, Hq, 1, [n], [9000 + 1111 * i])
+            cs = caches(w)
+            out = ops.block_scaled_attention(dev(w.q), dev(w.q_start), *cs, dev(w.tables), dev(w.lens),
+                                             int(w.lens[0]), n, w.scale, out_dtype=torch.float32, workspace=ws).cpu()
+            if turn == 0:
+                check(out, w, what=f"{Hq} heads, {n} tokens")
+            assert torch.equal(first.setdefault(i, out), out)
+
+
+def test_graphs_share_a_workspace():
+    ws = torch.full((64 << 20,), 255, dtype=torch.uint8, device=DEV)
+    runs = []
+    for i, (Hq, n) in enumerate(KERNELS):
+        w = ScaledBatch(80 + i, Hq, 1, [n, n], [5000, 700])
+        a = [dev(w.q), dev(w.q_start), *caches(w), dev(w.tables), dev(w.lens)]
+        want = ops.block_scaled_attention(*a, 5000, n, w.scale, workspace=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = ops.block_scaled_attention(*a, 5000, n, w.scale, workspace=ws)
+        runs.append((g, got, want, a))  # (a graph reads its operands where they were)
+    for order in (range(5), (4, 0, 3, 3, 1, 0, 2), range(4, -1, -1)):
+        for i in order:
+            runs[i][1].fill_(float("nan"))
+            runs[i][0].replay()
+        for i in order:
+            assert torch.equal(runs[i][1], runs[i][2])
+
+
+def test_blocks_beyond_32_bits():
+    """Blocks at the end of pools of 2^31 bytes and more hold and give what they do at the start."""
+    w = ScaledBatch(48, 16, 16, [3, 18], [100, 50])
+    cs, n = caches(w), len(w.k)
+    far = 2 ** 31 // (16 * 2048) + 4000
+    big = [torch.zeros((far + n, *c.shape[1:]), dtype=torch.uint8 if c.dtype == F8 else c.dtype, device=DEV) for c in cs]
+    big = [b.view(F8) if c.dtype == F8 else b for b, c in zip(big, cs)]
+    ops.block_scaled_copy(*big, *cs, dev(np.array([[i, far + i] for i in range(n)], dtype=np.int64)))
+    append(w, cs)
+    want = attend(w, cs)
+    w.tables = np.where(w.tables >= 0, w.tables + far, w.tables).astype(np.int32)
+    append(w, big)
+    assert torch.equal(attend(w, big), want)
+    same([b[far:] for b in big], as_np(cs))
+
+
+@pytest.mark.parametrize("Hq,n", [(8, 1), (8, 5), (32, 9)])
+def test_no_tokens(Hq, n):
+    """Sequences without new tokens, and tensors without elements."""
+    w = ScaledBatch(49, Hq, 2, [0, 0], [40, 3])
+    for t in (w.q, w.new_k, w.new_v):
+        assert t.numel() == 0
+    cs = caches(w)
+    same(append(w, cs), [w.k, w.v, w.k_scale, w.v_scale])
+    assert attend(w, cs, max_q=n).shape == (0, Hq, 128)
+    e = ScaledBatch(49, Hq, 2, [n], [40])
+    e.q_start, e.tables, e.lens = e.q_start[:1], e.tables[:0], e.lens[:0]
+    same(append(e, cs), [w.k, w.v, w.k_scale, w.v_scale])
+    assert torch.isnan(attend(e, cs, max_len=40, max_q=n)).all()
+    d = Drafts(49, [0, 0], 30, "sampled")
+    path, k, tok = verify(d, 3)
+    assert (path == -1).all() and (k == 0).all() and (tok == -1).all()
+
+
+def test_append_and_copy_on_another_stream():
+    w = ScaledBatch(45, 8, 2, [3, 2], [40, 300])
+    cs, want = caches(w), append_oracle(w)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    pairs = dev(np.array([[0, len(w.k) - 1]], dtype=np.int64))
+    k, v, a = dev(w.new_k), dev(w.new_v), [dev(x) for x in (w.q_start, w.tables, w.lens)]
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+    ops.block_scaled_append(k, v, *a, *cs, stream=s)
+    assert not s.query()
+    ops.block_scaled_copy(*cs, *cs, pairs, stream=s)
+    s.synchronize()
+    for x in want:
+        x[-1] = x[0]
+    same(cs, want)
 
 
 # ---- copies --------------------------------------------------------------------
