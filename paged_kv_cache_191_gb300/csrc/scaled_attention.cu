@@ -317,8 +317,7 @@ __device__ __forceinline__ void outputs(const ScaledArgs& sa, uint8_t* gb, Sync<
   const TreeArgs& a = sa.t;
   const int lane = static_cast<int>(threadIdx.x & 31), w4 = static_cast<int>(threadIdx.x >> 5) & 3, r = 32 * w4 + lane;
   const uint32_t tl = tmem + (static_cast<uint32_t>(32 * w4) << 16);
-  float* wts = reinterpret_cast<float*>(gb + L::OUT);
-  int* place = reinterpret_cast<int*>(wts + 2 * R);
+  float4* rows = reinterpret_cast<float4*>(gb + L::OUT);  // the weights of a row's two tiles, and where it goes
   bool ok = true;
   Piece p, next[2];  // of this step; and the two whose queries are loaded
   // (sy.piece tells a lane; the warpgroup goes on, or leaves, as a whole)
@@ -327,17 +326,116 @@ __device__ __forceinline__ void outputs(const ScaledArgs& sa, uint8_t* gb, Sync<
     ok = !bar_or(4, 128, !ok);
     return ok && live;
   };
-  auto store = [&](int at, int d, float o) {
-    const size_t i = static_cast<size_t>(at) * D + d;
-    if (a.out_f32)
-      static_cast<float*>(a.out)[i] = o;
-    else if (sa.q_bf16)
-      static_cast<__nv_bfloat16*>(a.out)[i] = __float2bfloat16(o);
-    else
-      static_cast<__half*>(a.out)[i] = __float2half(o);
+  auto bits16 = [&](float o) {
+    return sa.q_bf16 ? __bfloat16_as_ushort(__float2bfloat16(o)) : __half_as_ushort(__float2half(o));
+  };
+  // A piece of an item that has more: its rows are written; the item's are joined, if all are.
+  // A part's word holds the launch's stamp once its rows are written.  Who then finds all
+  // of the item's words stamped joins the parts: the last to write does, and where
+  // another does too, both write the same.  Words are cleared behind it, for a graph that
+  // runs the launch again.  (No counter: 150 CTAs that count one up took 70 us.)
+  auto join = [&](const Piece& p, int2 part) {
+    auto slot_of = [&](int q) { return q == 0 ? 2 * part.x + 1 : 2 * (part.x + q); };
+    volatile uint64_t* words = sa.written;
+    int* all_written = reinterpret_cast<int*>(rows);
+    named_bar(4, 128);
+    if (w4 == 0) {
+      if (lane == 0) {
+        __threadfence();  // (of the whole warpgroup's rows)
+        words[p.slot] = sa.stamp;
+      }
+      __syncwarp();
+      asm volatile("fence.sc.gpu;" ::: "memory");  // own word before the others'
+      bool all = true;
+      for (int q = lane; q < part.y; q += 32) all &= words[slot_of(q)] == sa.stamp;
+      all = __all_sync(FULL, all);
+      if (all) __threadfence();
+      if (lane == 0) *all_written = all;
+    }
+    named_bar(4, 128);
+    const bool last = *all_written != 0;
+    named_bar(4, 128);  // (the rows' weights take its place)
+    if (!last) return;
+    // a warp takes every fourth row, NB of them at a time, two parts of each on their way
+    // (3 and 4 rows need more registers than the warps have: 90 and 96 us for 91 in chains, 56 and 58 for 55 elsewhere)
+    constexpr int NB = 2;
+#pragma unroll 1
+    for (int j0 = w4; j0 < p.rows; j0 += 4 * NB) {
+      auto row_of = [&](int q, int e) { return static_cast<size_t>(slot_of(q)) * R + min(j0 + 4 * e, p.rows - 1); };
+      float M[NB], ls[NB], w[NB];
+      float4 acc[NB];
+#pragma unroll
+      for (int e = 0; e < NB; ++e) {
+        M[e] = -INFINITY;
+        ls[e] = 0.f;
+        acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll 1
+      for (int q0 = 0; q0 < part.y; q0 += 32) {  // lane i has part q0 + i's maximum and sum
+        const int n = min(32, part.y - q0);
+        float4 o[NB][2];
+        auto load = [&](int q) {
+#pragma unroll
+          for (int e = 0; e < NB; ++e)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              o[e][k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + row_of(q0 + min(q + k, n - 1), e) * D) + lane);
+        };
+        float m[NB], l[NB];
+#pragma unroll
+        for (int e = 0; e < NB; ++e) {
+          m[e] = lane < n ? __ldcg(a.part_m + row_of(q0 + lane, e)) : -INFINITY;
+          l[e] = lane < n ? __ldcg(a.part_l + row_of(q0 + lane, e)) : 0.f;
+        }
+        load(0);
+#pragma unroll
+        for (int e = 0; e < NB; ++e) {
+          const float top = fmaxf(M[e], warp_max(m[e])), mz = top == -INFINITY ? 0.f : top, again = dev::ex2(M[e] - mz);
+          // (a part without a key has no row that counts, but NaN sums have 0 for a maximum)
+          w[e] = dev::ex2(m[e] - mz);
+          float wl = w[e] * l[e];
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) wl += __shfl_xor_sync(FULL, wl, off);
+          M[e] = top;
+          ls[e] = ls[e] * again + wl;
+          acc[e] = make_float4(acc[e].x * again, acc[e].y * again, acc[e].z * again, acc[e].w * again);
+        }
+#pragma unroll 1
+        for (int q = 0;;) {
+#pragma unroll
+          for (int e = 0; e < NB; ++e)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float we = __shfl_sync(FULL, w[e], min(q + k, 31));
+              if (q + k >= n) continue;
+              acc[e] = make_float4(fmaf(we, o[e][k].x, acc[e].x), fmaf(we, o[e][k].y, acc[e].y),
+                                   fmaf(we, o[e][k].z, acc[e].z), fmaf(we, o[e][k].w, acc[e].w));
+            }
+          q += 2;
+          if (q >= n) break;
+          load(q);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < NB; ++e) {
+        const int j = j0 + 4 * e, head = j & ((1 << a.gl) - 1);
+        if (j >= p.rows || head >= a.G) continue;
+        const float inv = M[e] == -INFINITY ? 0.f : 1.f / ls[e];
+        const size_t at = (static_cast<size_t>((p.qs + ((p.row0 + j) >> a.gl)) * a.Hq + p.g * a.G + head) * D) / 4 + lane;
+        const float4 y = make_float4(acc[e].x * inv, acc[e].y * inv, acc[e].z * inv, acc[e].w * inv);
+        if (a.out_f32)
+          static_cast<float4*>(a.out)[at] = y;
+        else
+          static_cast<uint2*>(a.out)[at] = make_uint2(bits16(y.x) | static_cast<uint32_t>(bits16(y.y)) << 16,
+                                                      bits16(y.z) | static_cast<uint32_t>(bits16(y.w)) << 16);
+      }
+    }
+    named_bar(4, 128);
+    for (int q = r; q < part.y; q += 128) words[slot_of(q)] = 0ull;
   };
   int loaded = 0;  // pieces whose queries are
-  bool more = true;
+  bool more = true, pending = false;  // pending: the piece before has to be joined
+  int2 part = make_int2(0, 0);
 #pragma unroll 1
   for (int i = 0;; ++i) {
 #pragma unroll 1
@@ -349,10 +447,13 @@ __device__ __forceinline__ void outputs(const ScaledArgs& sa, uint8_t* gb, Sync<
       next[0] = next[1];
       next[1] = x;
     }
+    // (Not before the next queries are on their way: rows take a while to arrive where others
+    // see them, up to 12000 clocks while the ring fills.)
+    if (pending) join(p, part);
     if (i >= loaded) break;
     p = loaded == i + 2 ? next[0] : next[1];
     const int pp = i & 1;
-    const int2 part = reinterpret_cast<const int2*>(gb + L::PARTS)[i & 3];
+    part = reinterpret_cast<const int2*>(gb + L::PARTS)[i & 3];
     if (ok) ok = wait_warp(sums_full(sy, i, 0), (i >> 1) & 1) && wait_warp(sums_full(sy, i, 1), (i >> 1) & 1);
     if (ok) ok = wait_warp(out_full(sy, i), (i >> 1) & 1);
     ok = !bar_or(4, 128, !ok);
@@ -370,15 +471,14 @@ __device__ __forceinline__ void outputs(const ScaledArgs& sa, uint8_t* gb, Sync<
       const float m = fmaxf(m0, m1), mz = m == -INFINITY ? 0.f : m;
       const float w0 = dev::ex2(m0 - mz), w1 = dev::ex2(m1 - mz), sum = w0 * l0 + w1 * l1;
       const float inv = direct && m != -INFINITY ? 1.f / sum : 1.f;
-      wts[r] = w0 * inv;
-      wts[R + r] = w1 * inv;
       // where the row goes, in rows of out or of the partials
       const bool exists = r < p.rows && h < a.G;
       const int at = p.row0 + r;
-      place[r] = !exists ? -1 : direct ? (p.qs + (at >> a.gl)) * a.Hq + p.g * a.G + h : p.slot * R + r;
+      const int place = !exists ? -1 : direct ? (p.qs + (at >> a.gl)) * a.Hq + p.g * a.G + h : p.slot * R + r;
+      rows[r] = make_float4(w0 * inv, w1 * inv, __int_as_float(place), 0.f);
       if (!direct && exists) {
-        a.part_m[place[r]] = m;
-        a.part_l[place[r]] = sum;
+        a.part_m[place] = m;
+        a.part_l[place] = sum;
       }
     }
     int* poison = reinterpret_cast<int*>(gb + L::POISON) + 256 * pp;
@@ -386,6 +486,7 @@ __device__ __forceinline__ void outputs(const ScaledArgs& sa, uint8_t* gb, Sync<
     poison[r] = poison[128 + r] = R;
     named_bar(4, 128);
     const uint32_t oa = tl + L::COL_O + (i & (L::OPAR - 1)) * 2 * L::COLS;
+    float* f32 = !direct ? a.part_o : a.out_f32 ? static_cast<float*>(a.out) : nullptr;
 #pragma unroll 1
     for (int j0 = 0; j0 < p.rows; j0 += 8) {
       Terms8 tu, tv;
@@ -396,18 +497,23 @@ __device__ __forceinline__ void outputs(const ScaledArgs& sa, uint8_t* gb, Sync<
       terms_wait(tv);
       terms_sum(tu, u);
       terms_sum(tv, v);
+      int at[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float w0 = wts[j0 + e], w1 = wts[R + j0 + e];
-        float o = w0 == 0.f ? 0.f : u[e] * w0;
-        if (w1 != 0.f) o = fmaf(v[e], w1, o);
-        if (j0 + e >= nan_from) o = NAN;
-        const int at = place[j0 + e];
-        if (at < 0) continue;
-        if (direct)
-          store(at, r, o);
-        else
-          a.part_o[static_cast<size_t>(at) * D + r] = o;
+        const float4 row = rows[j0 + e];
+        float o = row.x == 0.f ? 0.f : u[e] * row.x;
+        if (row.y != 0.f) o = fmaf(v[e], row.y, o);
+        u[e] = j0 + e >= nan_from ? NAN : o;
+        at[e] = __float_as_int(row.z);
+      }
+      if (f32) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (at[e] >= 0) f32[static_cast<size_t>(at[e]) * D + r] = u[e];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (at[e] >= 0) static_cast<uint16_t*>(a.out)[static_cast<size_t>(at[e]) * D + r] = bits16(u[e]);
       }
     }
     tcg::fence_before();
@@ -416,76 +522,7 @@ __device__ __forceinline__ void outputs(const ScaledArgs& sa, uint8_t* gb, Sync<
       mbar_arrive(out_free(sy, i));
       mbar_arrive(piece_over(sy, i));
     }
-    if (direct) continue;
-    // ---- the item's parts -----------------------------------------------------------
-    // A part's word holds the launch's stamp once its rows are written.  Who then finds all
-    // of the item's words stamped joins the parts: the last to write does, and where
-    // another does too, both write the same.  Words are cleared behind it, for a graph that
-    // runs the launch again.  (No counter: 150 CTAs that count one up took 70 us.)
-    auto slot_of = [&](int q) { return q == 0 ? 2 * part.x + 1 : 2 * (part.x + q); };
-    volatile uint64_t* words = sa.written;
-    __threadfence();
-    named_bar(4, 128);
-    if (w4 == 0) {
-      if (lane == 0) words[p.slot] = sa.stamp;
-      asm volatile("fence.sc.gpu;" ::: "memory");
-      __syncwarp();
-      asm volatile("fence.sc.gpu;" ::: "memory");
-      bool all = true;
-      for (int q = lane; q < part.y; q += 32) all &= words[slot_of(q)] == sa.stamp;
-      all = __all_sync(FULL, all);
-      if (lane == 0) place[0] = all;
-    }
-    named_bar(4, 128);
-    const bool last = place[0] != 0;
-    named_bar(4, 128);  // (place is written again)
-    if (!last) continue;
-    __threadfence();
-#pragma unroll 1
-    for (int j = w4; j < p.rows; j += 4) {
-      const int head = j & ((1 << a.gl) - 1);
-      if (head >= a.G) continue;
-      auto row_of = [&](int q) { return static_cast<size_t>(slot_of(q)) * R + j; };
-      float M = -INFINITY, ls = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-      for (int q0 = 0; q0 < part.y; q0 += 32) {  // lane i has part q0 + i's maximum and sum
-        const int n = min(32, part.y - q0);
-        const float m = lane < n ? __ldcg(a.part_m + row_of(q0 + lane)) : -INFINITY;
-        const float l = lane < n ? __ldcg(a.part_l + row_of(q0 + lane)) : 0.f;
-        const float top = fmaxf(M, warp_max(m)), mz = top == -INFINITY ? 0.f : top, again = dev::ex2(M - mz);
-        // (a part without a key has no row that counts, but NaN sums have 0 for a maximum)
-        const float w = dev::ex2(m - mz);
-        float wl = w * l;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) wl += __shfl_xor_sync(FULL, wl, off);
-        M = top;
-        ls = ls * again + wl;
-        acc = make_float4(acc.x * again, acc.y * again, acc.z * again, acc.w * again);
-#pragma unroll 1
-        for (int q = 0; q < n; q += 4) {  // four parts' rows on their way at a time
-          float4 o[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            o[e] = __ldcg(reinterpret_cast<const float4*>(a.part_o + row_of(q0 + min(q + e, n - 1)) * D) + lane);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float we = __shfl_sync(FULL, w, min(q + e, 31));
-            if (q + e >= n) continue;
-            acc = make_float4(fmaf(we, o[e].x, acc.x), fmaf(we, o[e].y, acc.y), fmaf(we, o[e].z, acc.z),
-                              fmaf(we, o[e].w, acc.w));
-          }
-        }
-      }
-      const float inv = M == -INFINITY ? 0.f : 1.f / ls;
-      const int at = (p.qs + ((p.row0 + j) >> a.gl)) * a.Hq + p.g * a.G + head;
-      store(at, 4 * lane, acc.x * inv);
-      store(at, 4 * lane + 1, acc.y * inv);
-      store(at, 4 * lane + 2, acc.z * inv);
-      store(at, 4 * lane + 3, acc.w * inv);
-    }
-    named_bar(4, 128);
-    for (int q = r; q < part.y; q += 128) words[slot_of(q)] = 0ull;
+    pending = !direct;
   }
   if (!ok && lane == 0) flag(PA_DEVERR_TIMEOUT);
 }

@@ -44,8 +44,8 @@ struct ScaledLay {
   static constexpr int REF = FAC + 16 * R;        // float [piece parity][2 tiles][R]: minus the references
   static constexpr int SUM = REF + 16 * R;        // float [piece parity][2 tiles][4 warps][R]: l
   static constexpr int TOP = SUM + 64 * R;        // float [piece parity][2 tiles][R]: the references (-inf: none)
-  static constexpr int OUT = TOP + 16 * R;        // the outputs' weights, float [2 tiles][R], and places, int [R]
-  static constexpr int POISON = OUT + 12 * R;     // int [piece parity][2 tiles][128 dims]: first row that sees a NaN there
+  static constexpr int OUT = TOP + 16 * R;        // the outputs' rows: weights of the two tiles, place
+  static constexpr int POISON = OUT + 16 * R;     // int [piece parity][2 tiles][128 dims]: first row that sees a NaN there
   static constexpr int MASK = 0;
   static constexpr int BYTES = POISON + 2048;
   static constexpr int THREADS = 512;
@@ -147,52 +147,43 @@ __device__ __forceinline__ U units_per_head(const Span& x, int s) {
 // terms; its factor takes the power back.  A warp has a quarter of the rows.
 template <typename L>
 __device__ __forceinline__ void load_queries(const ScaledArgs& sa, uint8_t* gb, Sync<L> sy, const Piece& p, int i, bool& ok) {
-  constexpr int R = L::R, EACH = R / 4, BATCH = EACH % 4 == 0 ? 4 : 2;
+  constexpr int R = L::R, EACH = R / 4;
   const TreeArgs& a = sa.t;
   const int lane = static_cast<int>(threadIdx.x & 31), w4 = static_cast<int>(threadIdx.x >> 5) & 3;
   const int heads = (1 << a.gl) - 1;
-  auto load = [&](int r0, uint2(&x)[BATCH]) {  // 8 bytes a lane and row
+  uint2 x[EACH];  // all of a warp's rows on their way at once: a lane's 4 values of each
 #pragma unroll
-    for (int j = 0; j < BATCH; ++j) {
-      const int r = r0 + j, h = r & heads;
-      x[j] = make_uint2(0u, 0u);
-      if (r < p.rows && h < a.G)
-        x[j] = __ldg(reinterpret_cast<const uint2*>(
-            static_cast<const uint16_t*>(a.q) + static_cast<size_t>(p.qs + ((p.row0 + r) >> a.gl)) * sa.q_stride +
-            static_cast<size_t>(p.g * a.G + h) * L::D + 4 * lane));
-    }
-  };
-  uint2 x[BATCH], next[BATCH];
-  load(EACH * w4, next);
+  for (int j = 0; j < EACH; ++j) {
+    const int r = EACH * w4 + j, h = r & heads;
+    x[j] = make_uint2(0u, 0u);
+    if (r < p.rows && h < a.G)
+      x[j] = __ldg(reinterpret_cast<const uint2*>(
+          static_cast<const uint16_t*>(a.q) + static_cast<size_t>(p.qs + ((p.row0 + r) >> a.gl)) * sa.q_stride +
+          static_cast<size_t>(p.g * a.G + h) * L::D + 4 * lane));
+  }
   if (ok && i >= 2) ok = wait_warp(sy.qfree(i & 1), ((i - 2) >> 1) & 1);
   float* fac = reinterpret_cast<float*>(gb + L::FAC) + (i & 3) * R;
   uint8_t* to = gb + (i & 1) * L::QTILE + (lane & 3) * 4;
-#pragma unroll 1
-  for (int r0 = EACH * w4; r0 < EACH * (w4 + 1); r0 += BATCH) {
 #pragma unroll
-    for (int j = 0; j < BATCH; ++j) x[j] = next[j];
-    if (r0 + BATCH < EACH * (w4 + 1)) load(r0 + BATCH, next);
+  for (int j = 0; j < EACH; ++j) {
+    const int r = EACH * w4 + j;
+    const float2 lo = sa.q_bf16 ? dev::unpack2<__nv_bfloat16>(x[j].x) : dev::unpack2<__half>(x[j].x);
+    const float2 hi = sa.q_bf16 ? dev::unpack2<__nv_bfloat16>(x[j].y) : dev::unpack2<__half>(x[j].y);
+    const float f[4] = {lo.x, lo.y, hi.x, hi.y};
+    uint32_t top = 0;
 #pragma unroll
-    for (int j = 0; j < BATCH; ++j) {
-      const int r = r0 + j;
-      const float2 lo = sa.q_bf16 ? dev::unpack2<__nv_bfloat16>(x[j].x) : dev::unpack2<__half>(x[j].x);
-      const float2 hi = sa.q_bf16 ? dev::unpack2<__nv_bfloat16>(x[j].y) : dev::unpack2<__half>(x[j].y);
-      const float f[4] = {lo.x, lo.y, hi.x, hi.y};
-      uint32_t top = 0;
+    for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(f[e]) & 0x7FFFFFFFu);
+    top = __reduce_max_sync(FULL, top);
+    const bool fine = top < 0x7F800000u;  // (else the row's factor is NaN, and so is the row)
+    const int k = min(14 - (static_cast<int>(top >> 23) - 127), 100);
+    const float up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+    uint32_t p0[kParts], p1[kParts];
+    terms(dev::pack2<__half>(f[0] * up, f[1] * up), p0);
+    terms(dev::pack2<__half>(f[2] * up, f[3] * up), p1);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(f[e]) & 0x7FFFFFFFu);
-      top = __reduce_max_sync(FULL, top);
-      const bool fine = top < 0x7F800000u;  // (else the row's factor is NaN, and so is the row)
-      const int k = min(14 - (static_cast<int>(top >> 23) - 127), 100);
-      const float up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
-      uint32_t p0[kParts], p1[kParts];
-      terms(dev::pack2<__half>(f[0] * up, f[1] * up), p0);
-      terms(dev::pack2<__half>(f[2] * up, f[3] * up), p1);
-#pragma unroll
-      for (int e = 0; e < kParts; ++e)
-        *reinterpret_cast<uint32_t*>(to + (e * R + r) * 128 + (((lane >> 2) ^ (r & 7)) << 4)) = upper(p0[e], p1[e]);
-      if (lane == 0) fac[r] = fine ? a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23) : NAN;
-    }
+    for (int e = 0; e < kParts; ++e)
+      *reinterpret_cast<uint32_t*>(to + (e * R + r) * 128 + (((lane >> 2) ^ (r & 7)) << 4)) = upper(p0[e], p1[e]);
+    if (lane == 0) fac[r] = fine ? a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23) : NAN;
   }
   dev::fence_proxy_async_smem();
   named_bar(4, 128);
