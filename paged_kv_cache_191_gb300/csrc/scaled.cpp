@@ -129,13 +129,14 @@ pa_status pa_block_scaled_attention(const void* q, int32_t q_dtype, int64_t q_st
   if (mis(q, 16) || mis(k_cache, 16) || mis(v_cache, 16) || mis(out, 16) || mis(q_start, 4) || mis(block_tables, 4) ||
       mis(context_lens, 4) || mis(k_scale, 4) || mis(v_scale, 4))
     return fail(PA_ERR_INVALID, "%s: misaligned pointer", fn);
-  // units of work (128-key chunks of every item, and 4 for its start and end) are counted in 32 bits
+  // units of work (two for every 128-key chunk of an item, ten for its start and end at most)
+  // are counted in 32 bits
   int64_t G = 1;
   while (G < num_q_heads / desc->num_kv_heads) G *= 2;
   const int32_t item = item_rows(num_q_heads, max_q_len, desc), sms = pa::sm_count();
-  const int64_t chunks = static_cast<int64_t>(max_context_len) / 128 + 5;
+  const int64_t units = 2 * (static_cast<int64_t>(max_context_len) / 128 + 1) + 10;
   const int64_t items = static_cast<int64_t>(num_tokens) * G / item + B;
-  if (items * desc->num_kv_heads > INT32_MAX / 2 / chunks)
+  if (items * desc->num_kv_heads > INT32_MAX / 2 / units)
     return fail(PA_ERR_UNSUPPORTED, "%s: more than 2^30 units of work", fn);
   if (static_cast<int64_t>(num_tokens) * num_q_heads > INT32_MAX)
     return fail(PA_ERR_UNSUPPORTED, "%s: too many query rows", fn);

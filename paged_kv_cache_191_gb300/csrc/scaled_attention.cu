@@ -760,7 +760,7 @@ pa_status launch_kernel(const ScaledAttentionLaunch& l, K kernel, cudaStream_t s
     a.negate = 1;
   }
   a.out_f32 = l.out_dtype == PA_DTYPE_F32;
-  a.min_units = 6;
+  a.min_units = 6 * L::CHUNK;
   a.item_rows = a.slot_rows = l.item_rows;
   sa.q_stride = l.q_stride;
   sa.q_bf16 = l.q_dtype == PA_DTYPE_BF16;

@@ -50,6 +50,11 @@ struct ScaledLay {
   static constexpr int BYTES = POISON + 2048;
   static constexpr int THREADS = 512;
   static constexpr int HIGH = 176, LOW = 80;
+  // Units of work: a chunk; an item's start and end; an item at least, whose chunks wait for
+  // each other.  (ITEM 2, 5, 8, 12: 8 rows, 32 kv heads 57, 55, 57, 58 us, 16 rows 53, 54, 54,
+  // 55, 32 rows 75, 70, 67, 67, 40 rows 102, 96, 92, 91.  Without LEAST one short
+  // sequence is cut in two, 14 us for 9.)
+  static constexpr int CHUNK = 2, ITEM = R > 16 ? 10 : 5, LEAST = 12;
   // tensor memory columns: S^T [tile] x COLS, O^T [piece parity, where there is room][tile] x COLS
   static constexpr int OPAR = R > 16 ? 1 : 2;
   static constexpr uint32_t COL_O = 2 * COLS;
@@ -137,9 +142,14 @@ __device__ __forceinline__ U units_before(const Span& x, int k, int s) {
 __device__ __forceinline__ int chunks_of(const Span& x, int k, int s) {
   return k + 1 < x.tiles ? (x.a + k + (1 << s)) >> s : max(1, (x.L + kKeys - 1) / kKeys);
 }
-template <typename U>
+// units of an item of so many chunks
+template <typename L>
+__device__ __forceinline__ int item_units(int chunks) {
+  return max(L::CHUNK * chunks + L::ITEM, L::LEAST);
+}
+template <typename L, typename U>
 __device__ __forceinline__ U units_per_head(const Span& x, int s) {
-  return x.tiles == 0 ? 0 : units_before<U>(x, x.tiles - 1, s) + kItem + chunks_of(x, x.tiles - 1, s);
+  return x.tiles == 0 ? 0 : units_before<U>(x, x.tiles - 1, s) + item_units<L>(chunks_of(x, x.tiles - 1, s));
 }
 
 // A piece's queries, by the outputs' warpgroup: every row scaled by a power of two to
@@ -238,10 +248,10 @@ __device__ __forceinline__ void plan_scaled(const TreeArgs& a, uint8_t* gb, Sync
       g = 0;
     }
     read(g, me == 0);
-    const int64_t units = units_per_head<int64_t>(mine, per) * a.Hkv;
+    const int64_t units = units_per_head<L, int64_t>(mine, per) * a.Hkv;
     if (!find) {
       sum += units;
-      if (mine.tiles > 0) most = max(most, kItem + chunks_of(mine, mine.tiles - 1, per));
+      if (mine.tiles > 0) most = max(most, item_units<L>(chunks_of(mine, mine.tiles - 1, per)));
       continue;
     }
     const int w = static_cast<int>(units);
@@ -284,7 +294,7 @@ __device__ __forceinline__ void plan_scaled(const TreeArgs& a, uint8_t* gb, Sync
           continue;
         }
         if (seq < 0) {  // the CTA's first item
-          const int U = max(1, static_cast<int>(units_per_head<uint32_t>(s, per))), at = start - ub;
+          const int U = max(1, static_cast<int>(units_per_head<L, uint32_t>(s, per))), at = start - ub;
           g = at / U;
           off = at - g * U;
           int hi = s.tiles;  // the last that starts at or before it
@@ -300,9 +310,11 @@ __device__ __forceinline__ void plan_scaled(const TreeArgs& a, uint8_t* gb, Sync
         }
         seq = b;
       }
-      const int nch = chunks_of(s, tile, per), cost = nch + kItem, stop = min(cost, off + end - u);
-      p.c0 = max(0, off - kItem);
-      p.c1 = stop - kItem;
+      // a chunk is whose range its first unit lies in
+      const int nch = chunks_of(s, tile, per), cost = item_units<L>(nch), stop = min(cost, off + end - u);
+      const int first = cost - L::CHUNK * nch;
+      p.c0 = max(0, off - first + L::CHUNK - 1) / L::CHUNK;
+      p.c1 = max(0, stop - first + L::CHUNK - 1) / L::CHUNK;
       if (p.c1 > p.c0) {  // (else the range ends before the item's first chunk)
         p.live = 1;
         p.b = b;
@@ -314,7 +326,7 @@ __device__ __forceinline__ void plan_scaled(const TreeArgs& a, uint8_t* gb, Sync
         p.rows = min(a.item_rows, (s.n << a.gl) - p.row0);
         // partial rows: an item's first part has the CTA's second set, a later one the first
         p.slot = p.c0 == 0 && p.c1 == nch ? -1 : 2 * me + (p.c0 == 0 ? 1 : 0);
-        const int owner = (u - off + kItem) / upc, parts = (u - off + cost - 1) / upc - owner + 1;
+        const int owner = (u - off + first) / upc, parts = (u - off + cost - L::CHUNK) / upc - owner + 1;
         if constexpr (!L::ROWS) {
           if (lane == 0) reinterpret_cast<int2*>(gb + L::PARTS)[i & 3] = make_int2(owner, parts);
         } else if (p.c0 == 0 && p.c1 < nch) {  // the item goes on in the next CTAs: what the merge needs

@@ -47,6 +47,7 @@ struct ScaledRowsLay {
   // as in the tree attention's Lay
   static constexpr float LIFT = SPLIT ? 0.f : 7.f, MOVE = SPLIT ? 8.f : 15.f;
   static constexpr int HIGH = 176, LOW = 80;
+  static constexpr int CHUNK = 1, ITEM = kItem, LEAST = 0;  // of units: a chunk, an item's start and end, an item at least
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
 
