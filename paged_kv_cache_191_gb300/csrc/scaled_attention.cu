@@ -227,9 +227,10 @@ __device__ __forceinline__ float lane_sums(float (&v)[N], int lane) {
 // New references where a row has none yet or an exponent outgrew it; O^T and the
 // exponents e move with them.  alpha: what the rows' l are to be multiplied by, in
 // scratch[5 R ..], if the result's bit 0 is set.  Bit 1: some row still has no reference.
-template <typename L>
+// (rest: waits until O^T is at rest.)
+template <typename L, typename F>
 __device__ __forceinline__ int settle_scaled(const KeyLane& x, float (&e)[L::R], float* refs, float lv, uint32_t oc,
-                                             bool exists, bool& seen, float& ref) {
+                                             bool exists, bool& seen, float& ref, F rest) {
   constexpr int R = L::R;
   const int bar = 2 + x.t;
   float best = -INFINITY;  // of row `lane`
@@ -260,6 +261,7 @@ __device__ __forceinline__ int settle_scaled(const KeyLane& x, float (&e)[L::R],
 #pragma unroll
   for (int j = 0; j < R; ++j) e[j] += refs[j];
   if (rescale) {
+    rest();
 #pragma unroll 1
     for (int j = 0; j < kParts * R; j += 8) {
       uint32_t o[8];
@@ -582,7 +584,7 @@ __global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
     x.r = 32 * x.w4 + lane;
     x.tl = tmem + (static_cast<uint32_t>(32 * x.w4) << 16);
     uint8_t* pbuf = gb + L::P0 + x.t * 16384;
-    x.scratch = reinterpret_cast<float*>(pbuf);
+    x.scratch = reinterpret_cast<float*>(gb + L::SCRATCH) + 6 * R * x.t;
     const int t = x.t, r = x.r, bar = 2 + t;
     uint8_t* prow = pbuf + r * 128;  // the key's row of P^T, swizzled by r & 7
     const uint32_t sc = x.tl + L::COLS * t;
@@ -651,14 +653,14 @@ __global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
           for (int j = 0; j < R; j += 2) top = max3(top, e[j], e[j + 1]);
         }
         if (unset || bar_or(bar, 128, top > L::MOVE - lv)) {
-          if (ok && n > 0) ok = wait_warp(sy.pdone(t), (n - 1) & 1);  // (P^T free, O^T at rest)
-          fence_after();
-          const int what = settle_scaled<L>(x, e, refs, lv, oc, exists, seen, ref);
+          const int what = settle_scaled<L>(x, e, refs, lv, oc, exists, seen, ref, [&] {
+            if (ok && n > 0) ok = wait_warp(sy.pdone(t), (n - 1) & 1);
+            fence_after();
+          });
           unset = what & 2;
           if (what & 1) {
 #pragma unroll
             for (int j = 0; j < R; ++j) l[j] *= x.scratch[5 * R + j];
-            named_bar(bar, 128);  // the scratch is read before P^T takes its place
           }
         }
         fence_before();

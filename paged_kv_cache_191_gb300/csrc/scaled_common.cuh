@@ -47,7 +47,8 @@ struct ScaledLay {
   static constexpr int OUT = TOP + 16 * R;        // the outputs' rows: weights of the two tiles, place
   static constexpr int POISON = OUT + 16 * R;     // int [piece parity][2 tiles][128 dims]: first row that sees a NaN there
   static constexpr int MASK = 0;
-  static constexpr int BYTES = POISON + 2048;
+  static constexpr int SCRATCH = POISON + 2048;   // float [2 tiles][6][R]: maxima of warps, factors of moved references
+  static constexpr int BYTES = SCRATCH + 48 * R;
   static constexpr int THREADS = 512;
   static constexpr int HIGH = 176, LOW = 80;
   // Units of work: a chunk; an item's start and end; an item at least, whose chunks wait for
@@ -94,7 +95,7 @@ __device__ __forceinline__ uint32_t out_free(const Sync<L>& sy, int piece) { ret
 struct KeyLane {
   int t, w4, lane, r;  // tile, warp of the tile, lane, key of the chunk
   uint32_t tl;         // tensor memory at the warp's lanes
-  float* scratch;      // the tile's P^T buffer, between a product's end and the next P^T
+  float* scratch;      // the tile's
 };
 
 // ---- E5M2 terms --------------------------------------------------------------
