@@ -189,18 +189,35 @@ __device__ __forceinline__ void terms_sum(const Terms8& x, float (&f)[8]) {
     f[i + 1] = s.y;
   }
 }
-// Of N rows 8 at a time, the next ones on their way while f sees these: f(row, sums).
+// Of N rows 8 W at a time, the next ones on their way while f sees these: f(row, sums of 8).
 template <int N, typename F>
 __device__ __forceinline__ void terms_each(uint32_t at, int step, F f) {
-  Terms8 x[2];
-  terms_load(at, step, x[0]);
+  // (16 rows at a time: 32 rows 64 us for 66, 40 rows, which have no registers for the next
+  // ones too, 92 for 93)
+  constexpr int W = N < 32 ? 1 : 2;
+  constexpr bool AHEAD = N <= 32;
+  Terms8 x[AHEAD ? 2 : 1][W];
+  auto load = [&](int j, Terms8(&y)[W]) {
 #pragma unroll
-  for (int j = 0; j < N; j += 8) {
-    terms_wait(x[(j >> 3) & 1]);
-    if (j + 8 < N) terms_load(at + j + 8, step, x[((j >> 3) & 1) ^ 1]);
-    float v[8];
-    terms_sum(x[(j >> 3) & 1], v);
-    f(j, v);
+    for (int i = 0; i < W; ++i)
+      if (j + 8 * i < N) terms_load(at + j + 8 * i, step, y[i]);
+  };
+  load(0, x[0]);
+#pragma unroll
+  for (int j = 0; j < N; j += 8 * W) {
+    Terms8(&now)[W] = x[AHEAD ? (j / (8 * W)) & 1 : 0];
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      if (j + 8 * i < N) terms_wait(now[i]);
+    if (AHEAD && j + 8 * W < N) load(j + 8 * W, x[((j / (8 * W)) & 1) ^ 1]);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      if (j + 8 * i >= N) continue;
+      float v[8];
+      terms_sum(now[i], v);
+      f(j + 8 * i, v);
+    }
+    if (!AHEAD && j + 8 * W < N) load(j + 8 * W, x[0]);
   }
 }
 
