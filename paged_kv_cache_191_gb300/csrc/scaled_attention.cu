@@ -33,17 +33,20 @@
 // queries of the pieces to come into terms and write the rows of those that are over.
 //
 // What bounds it: HBM while a kv head has few rows, and what a CTA does besides.  8
-// sequences of 8 kv heads, 4 rows, contexts to 32768: 71 us, 84 % of the copy rate; the
+// sequences of 8 kv heads, 4 rows, contexts to 32768: 70 us, 85 % of the copy rate; the
 // chunks go by at 96 % of it, and the start (launch, lengths, block ids, scales, first
 // chunk: 5 us) and the last joined rows (3 us) are the rest.  64 sequences of 8 kv heads,
-// 8 rows, mean context 2064: 56 us, 72 %.  32 sequences of 32 kv heads, one row, mean
-// context 1024: 57 us, 69 %: items of 8 chunks, whose first needs new references (700
-// clocks) and a barrier.  The same 64 with chains of 2 to 5 tokens: 100 us, 41 %: the
-// softmax warpgroups, 2250 clocks a chunk where HBM takes 1420; a chunk's exponents take
-// a warp 1000 clocks at 40 rows, the terms of its weights 900.
-// The code that runs once per piece is kept small: 136 KB of it took 78 us where 78 KB
-// take 65 (the instruction caches; 32 kv heads).  Skipping 8 rows at a time that a short
-// chain has not was slower (114 us for 100): it cuts the straight line of exponents.
+// 8 rows, mean context 2064: 54 us, 75 %.  32 sequences of 32 kv heads, one row, mean
+// context 1024: 55 us, 72 %: items of 8 chunks, whose first needs new references (700
+// clocks) and a barrier.  The same 64 with chains of 2 to 5 tokens: 92 us, 44 %: the
+// softmax warpgroups, 2200 clocks a chunk where HBM takes 1420; a chunk's exponents take
+// a warp 1000 clocks at 40 rows, the terms of its weights 900, one after the other.
+// Code that runs once per piece is kept small where it costs no latency: a planner of
+// many copies, 136 KB in all, took 78 us where 78 KB took 65 (the instruction caches; 32
+// kv heads).  Not kept, since no faster: 8 rows at a time skipped that a short chain has
+// not (114 us for 100: it cuts the straight line of exponents); scores of one row's three
+// terms side by side along K, so that the product sums them (105 for 100); a fixed order
+// of products in the middle of a piece (106 for 100).
 //
 // Values in masked places: a masked exponent is replaced; V rows that no row sees
 // are zeroed in shared memory, and a NaN code in a row that only some see is

@@ -162,7 +162,9 @@ __device__ __forceinline__ void load_queries(const ScaledArgs& sa, uint8_t* gb, 
   const TreeArgs& a = sa.t;
   const int lane = static_cast<int>(threadIdx.x & 31), w4 = static_cast<int>(threadIdx.x >> 5) & 3;
   const int heads = (1 << a.gl) - 1;
-  uint2 x[EACH];  // all of a warp's rows on their way at once: a lane's 4 values of each
+  // all of a warp's rows on their way at once, a lane's 4 values of each (32 rows: 64 us, in halves
+  // 68; a warp waits for each flight up to 3 us while the ring fills)
+  uint2 x[EACH];
 #pragma unroll
   for (int j = 0; j < EACH; ++j) {
     const int r = EACH * w4 + j, h = r & heads;

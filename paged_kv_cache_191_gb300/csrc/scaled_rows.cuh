@@ -10,12 +10,14 @@
 // maximum, reference and sum need no other lane.
 //
 // Prompt chunks of 300 to 1024 tokens behind contexts to 4096, 4 sequences of 32 heads,
-// 8 kv heads, f16: 126 us, 0.91 PFLOP/s, 48 % of the library product's rate, where the
+// 8 kv heads, f16: 127 us, 0.90 PFLOP/s, 48 % of the library product's rate, where the
 // kernel with a thread per key took 571.  Bound by shared memory: a chunk's 32 KB of
 // codes in and out again, 64 KB of values, 96 KB of operands are 1750 clocks of the 2200
-// that a chunk takes.  (Items of 256 rows would halve the first two per row; Q's second
-// place does not fit beside the ring.)  At 40 rows, bf16, from HBM: 190 us where the
-// thread per key takes 100.
+// that a chunk takes.  Items of 256 rows, half of them each tile's, halve the first
+// two per row and were no faster: 130 us for 127 here, 74 for 68 at 33 to 60 tokens, 204
+// for 221 in bf16.  Nor is it the exponentials' unit: with every eighth pair by a
+// polynomial instead 135 us.)  At 40 rows, bf16, from HBM: 190 us where the thread per key
+// takes 92.
 #pragma once
 
 #include "scaled_common.cuh"
