@@ -13,10 +13,10 @@
 // 8 kv heads, f16: 127 us, 0.90 PFLOP/s, 48 % of the library product's rate, where the
 // kernel with a thread per key took 571.  Bound by shared memory: a chunk's 32 KB of
 // codes in and out again, 64 KB of values, 96 KB of operands are 1750 clocks of the 2200
-// that a chunk takes.  Items of 256 rows, half of them each tile's, halve the first
+// that a chunk takes.  (Items of 256 rows, half of them each tile's, halve the first
 // two per row and were no faster: 130 us for 127 here, 74 for 68 at 33 to 60 tokens, 204
 // for 221 in bf16.  Nor is it the exponentials' unit: with every eighth pair by a
-// polynomial instead 135 us.)  At 40 rows, bf16, from HBM: 190 us where the thread per key
+// polynomial those 130 us were 135.)  At 40 rows, bf16, from HBM: 190 us where the thread per key
 // takes 92.
 #pragma once
 
