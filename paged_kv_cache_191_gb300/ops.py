@@ -529,6 +529,16 @@ def tree_commit(k_cache, v_cache, block_tables, context_lens, q_start, path, pat
     return new_lens
 
 
+def _prob_rows(t, name, T, V):
+    """Row stride of float32 [T, vocab] probabilities."""
+    if t.dtype != torch.float32 or t.shape != (T, V):
+        raise ValueError(f"{name} must be float32 [T, vocab], dense in the vocabulary")
+    row, one = t.stride()
+    if one != 1 and T > 0 and V > 1:
+        raise ValueError(f"{name} must be float32 [T, vocab], dense in the vocabulary")
+    return row if T > 1 else V
+
+
 def draft_verify(tokens, target_probs, uniform, q_start, max_path, draft_probs=None, parents=None, stream=None):
     """tree_accept for a sampled step: (path int32 [B, max_path] padded with
     -1, path_len int32 [B], next_token int64 [B]) of drafted tokens (int64
@@ -554,21 +564,14 @@ def draft_verify(tokens, target_probs, uniform, q_start, max_path, draft_probs=N
     if target_probs.dim() != 2:
         raise ValueError("target_probs must be float32 [T, vocab]")
     V = target_probs.shape[1]
-    strides = []
-    for t, n in ((target_probs, "target_probs"), (draft_probs, "draft_probs")):
-        if t is None:
-            strides.append(V)
-            continue
-        if t.dtype != torch.float32 or t.shape != (T, V) or (T > 0 and V > 1 and t.stride(1) != 1):
-            raise ValueError(f"{n} must be float32 [T, vocab], dense in the vocabulary")
-        strides.append(t.stride(0) if T > 1 else V)
-    on = q_start.device
+    ts = _prob_rows(target_probs, "target_probs", T, V)
+    ds = V if draft_probs is None else _prob_rows(draft_probs, "draft_probs", T, V)
+    on, max_path = q_start.device, int(max_path)
     path = _empty((B, max_path), torch.int32, on, stream)
     path_len = _empty((B,), torch.int32, on, stream)
     token = _empty((B,), torch.int64, on, stream)
-    _check(lib().pa_draft_verify(tokens.data_ptr(), target_probs.data_ptr(), strides[0], _addr(draft_probs),
-                                 strides[1], V, uniform.data_ptr(), _addr(parents), q_start.data_ptr(), T, B,
-                                 int(max_path), path.data_ptr(), path_len.data_ptr(), token.data_ptr(),
+    _check(lib().pa_draft_verify(tokens.data_ptr(), target_probs.data_ptr(), ts, _addr(draft_probs), ds, V,
+                                 uniform.data_ptr(), _addr(parents), q_start.data_ptr(), T, B, max_path, path.data_ptr(), path_len.data_ptr(), token.data_ptr(),
                                  _raw_stream(stream, dev)),
            "pa_draft_verify")
     return path, path_len, token
@@ -576,12 +579,13 @@ def draft_verify(tokens, target_probs, uniform, q_start, max_path, draft_probs=N
 
 def _block_scaled(k_cache, v_cache, k_scale, v_scale):
     """The descriptor of a block-scaled cache (read only: shared between calls)."""
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+    shape, dtype = k_cache.shape, k_cache.dtype
+    if v_cache.shape != shape or v_cache.dtype != dtype:
         raise ValueError("k_cache and v_cache differ")
-    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if t.dtype != torch.float32 or t.shape != k_cache.shape[:2]:
-            raise ValueError(f"{n} must be float32 [num_blocks, num_kv_heads]")
-    return _desc_of(k_cache.shape, k_cache.dtype)
+    tiles = shape[:2]
+    if k_scale.shape != tiles or v_scale.shape != tiles or k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+        raise ValueError("k_scale and v_scale must be float32 [num_blocks, num_kv_heads]")
+    return _desc_of(shape, dtype)
 
 
 def _context(q_start, block_tables, context_lens):
@@ -642,23 +646,25 @@ def block_scaled_attention(q, q_start, k_cache, v_cache, k_scale, v_scale, block
     desc = _block_scaled(k_cache, v_cache, k_scale, v_scale)
     B = _context(q_start, block_tables, context_lens)
     qs = _rows(q, "q", desc.head_dim)
-    T, Hq, D = q.shape
+    shape, max_q_len = q.shape, int(max_q_len)
+    T, Hq, D = shape
     if D != desc.head_dim:
         raise ValueError("q head_dim differs from the cache")
     if out is None:
-        out = _empty((T, Hq, D), out_dtype or q.dtype, q.device, stream)
-    elif out.shape != (T, Hq, D):
+        out = _empty(shape, out_dtype or q.dtype, q.device, stream)
+    elif out.shape != shape:
         raise ValueError("out must be [T, Hq, D]")
-    L = lib()
     if workspace is None:
-        workspace = _empty(_scaled_workspace(dev, Hq, int(max_q_len), k_cache.shape, k_cache.dtype), torch.uint8, q.device,
-                           stream, result=False)
-    _check(L.pa_block_scaled_attention(q.data_ptr(), _dtype(q, "q"), qs, q_start.data_ptr(), T, int(max_q_len),
-                                       k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                                       block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
-                                       int(max_context_len), B, Hq, float(scale), out.data_ptr(), _dtype(out, "out"),
-                                       C.byref(desc), workspace.data_ptr(),
-                                       workspace.numel() * workspace.element_size(), _raw_stream(stream, dev)),
+        room = _scaled_workspace(dev, Hq, max_q_len, k_cache.shape, k_cache.dtype)
+        workspace = _empty(room, torch.uint8, q.device, stream, result=False)
+    else:
+        room = workspace.numel() * workspace.element_size()
+    _check(lib().pa_block_scaled_attention(q.data_ptr(), _dtype(q, "q"), qs, q_start.data_ptr(), T, max_q_len,
+                                           k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                                           v_scale.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
+                                           context_lens.data_ptr(), int(max_context_len), B, Hq, float(scale),
+                                           out.data_ptr(), _dtype(out, "out"), C.byref(desc), workspace.data_ptr(), room,
+                                           _raw_stream(stream, dev)),
            "pa_block_scaled_attention")
     return out
 
