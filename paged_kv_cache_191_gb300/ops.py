@@ -571,8 +571,8 @@ def draft_verify(tokens, target_probs, uniform, q_start, max_path, draft_probs=N
     path_len = _empty((B,), torch.int32, on, stream)
     token = _empty((B,), torch.int64, on, stream)
     _check(lib().pa_draft_verify(tokens.data_ptr(), target_probs.data_ptr(), ts, _addr(draft_probs), ds, V,
-                                 uniform.data_ptr(), _addr(parents), q_start.data_ptr(), T, B, max_path, path.data_ptr(), path_len.data_ptr(), token.data_ptr(),
-                                 _raw_stream(stream, dev)),
+                                 uniform.data_ptr(), _addr(parents), q_start.data_ptr(), T, B, max_path,
+                                 path.data_ptr(), path_len.data_ptr(), token.data_ptr(), _raw_stream(stream, dev)),
            "pa_draft_verify")
     return path, path_len, token
 

@@ -516,6 +516,23 @@ def test_copy_within_and_between_pools(Hkv):
     same(cs, want)
 
 
+def test_two_calls_at_once():
+    """Calls on two streams, each with the workspace that it allocates."""
+    runs, streams = [], [torch.cuda.Stream() for _ in range(2)]
+    for i, (Hq, n) in enumerate([(8, 1), (8, 5), (32, 9)]):
+        w = ScaledBatch(90 + i, Hq, 1, [n, n, n], [5000, 700, 129])
+        a = [dev(w.q), dev(w.q_start), *caches(w), dev(w.tables), dev(w.lens), 5000, n, w.scale]
+        runs.append((a, ops.block_scaled_attention(*a)))
+    torch.cuda.synchronize()
+    got = []
+    for turn in range(12):
+        a, want = runs[turn % 3]
+        got += [(ops.block_scaled_attention(*a, stream=st), want) for st in streams]
+    torch.cuda.synchronize()
+    for x, want in got:
+        assert torch.equal(x, want)
+
+
 # ---- verification --------------------------------------------------------------
 def verify(d, max_path, strided=False):
     t, q = dev(d.target), None if d.draft is None else dev(d.draft)
@@ -554,6 +571,34 @@ def test_verify_of_many_children(kind):
     if kind == "tree":
         d.parents[1:600] = 0
     check_verify(verify(d, 50), d, 50)
+
+
+def test_verify_of_many_sequences():
+    """More sequences than the SMs have warps for."""
+    d = Drafts(11, [2, 1, 3, 0, 1] * 1400, 300, "sampled")
+    check_verify(verify(d, 3), d, 3)
+
+
+def test_verify_of_the_largest_vocabulary():
+    V = 1 << 19
+    d = Drafts(12, [2, 3], V, "sampled")
+    d.uniform[0], d.uniform[2] = 1.0 - 2.0 ** -24, 0.5
+    check_verify(verify(d, 3), d, 3)
+    d.draft = None
+    check_verify(verify(d, 3), d, 3)
+
+
+def test_verify_refuses_what_it_cannot_read():
+    d = Drafts(13, [2, 3], 100, "sampled")
+    tok, p, u, qs = (dev(x) for x in (d.tokens, d.target, d.uniform, d.q_start))
+    bad = [dict(target_probs=p[:1].expand(5, 100)), dict(target_probs=p.double()), dict(target_probs=p.t()),
+           dict(target_probs=torch.empty(5, 0, device=DEV)), dict(draft_probs=p[:, :99]), dict(tokens=tok.int()),
+           dict(uniform=u[:4]), dict(parents=torch.zeros(5, dtype=torch.int64, device=DEV)),
+           dict(parents=torch.zeros(5, dtype=torch.int32, device=DEV), draft_probs=p),
+           dict(target_probs=torch.empty(5, (1 << 19) + 1, device=DEV)), dict(max_path=0)]
+    for kw in bad:
+        with pytest.raises((ValueError, RuntimeError)):
+            ops.draft_verify(**(dict(tokens=tok, target_probs=p, uniform=u, q_start=qs, max_path=3) | kw))
 
 
 def test_verify_edges_of_the_draw():
