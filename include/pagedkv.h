@@ -750,7 +750,7 @@ size_t pa_block_scaled_attention_workspace_size(int32_t num_q_heads, int32_t max
  *              16-byte aligned; scratch.  Calls that may run at the same time
  *              need one each.
  * Scores, sums and outputs are accumulated in float32; weight x V scale is rounded to
- * f16 (2^-11 of it, and 2^-27 of the row's largest: keys whose blocks have a V scale far
+ * f16 whatever q's type (2^-11 of it, and 2^-27 of the row's largest: keys whose blocks have a V scale far
  * below another's that the row sees keep fewer bits, as do V scales below 2^-80).
  * Deterministic: the same inputs give the same bits on the same device.
  */

@@ -2,21 +2,26 @@
 //
 // S = Q K^T (M = 128 rows, N = the chunk's keys) and O += P V with P in tensor memory,
 // as in the tree attention's kernel of this kind, whose MMA warp, converters and
-// outputs it shares: a warpgroup converts the codes to the queries' 16-bit type in
-// shared memory, which at 128 rows costs less than three E5M2 terms of Q and P would
-// (products of 128 rows: 1074 clocks a chunk in f16, 1608 in terms).  Two tiles take
-// turns over the chunks.  A block's scale is the same for every row, so that a thread
+// outputs it shares: a warpgroup converts the codes to f16 in shared memory, which at 128
+// rows costs less than three E5M2 terms of Q and P would (products of 128 rows: 1074
+// clocks a chunk in f16, 1608 in terms).  bf16 queries become f16 too, a piece's at a
+// time, each row by a power of two: with K, V and P in bf16, P as two halves, 4
+// sequences of 608 tokens behind 1440 took 192 us where they take 121 (f16: 104), with only
+// Q and K in bf16 140 (codes reach bf16 by way of f16 and float32).  Two tiles take turns over
+// the chunks.  A block's scale is the same for every row, so that a thread
 // with its row's 128 scores in registers multiplies 16 of them by one number, and its
 // maximum, reference and sum need no other lane.
 //
-// Prompt chunks of 300 to 1024 tokens behind contexts to 4096, 4 sequences of 32 heads,
-// 8 kv heads, f16: 127 us, 0.90 PFLOP/s, 48 % of the library product's rate, where the
-// kernel with a thread per key took 571.  Bound by shared memory: a chunk's 32 KB of
-// codes in and out again, 64 KB of values, 96 KB of operands are 1750 clocks of the 2200
-// that a chunk takes.  (Items of 256 rows, half of them each tile's, halve the first
-// two per row and were no faster: 130 us for 127 here, 74 for 68 at 33 to 60 tokens, 204
-// for 221 in bf16.  Nor is it the exponentials' unit: with every eighth pair by a
-// polynomial those 130 us were 135.)  At 40 rows, bf16, from HBM: 190 us where the thread per key
+// Prompt chunks of 300 to 1024 tokens in contexts to 4096, 4 sequences of 32 heads,
+// 8 kv heads, f16: 117 to 143 us by which chunk stands in which context, 0.67 to 0.72
+// PFLOP/s, 36 to 38 % of the library product's rate (the kernel with a thread per key took
+// 4 times that).  Over many sizes that is 2470 clocks a chunk, 11900 an item and 14 us a call.
+// A chunk is bound by shared memory: 32 KB of codes in and out again, 64 KB of values, 96 KB
+// of operands are 1750 clocks.  An item's are one turn of each tile with nothing beside
+// it, its rows' way out and the next one's first references; O has no tensor memory for
+// two items.  (Items of 256 rows, half of them each tile's, halve the codes and values per
+// row and were no faster: 130 us for 127, 74 for 68 at 33 to 60 tokens.  Nor is it the
+// exponentials' unit: with every eighth pair by a polynomial those 130 us were 135.)  At 40 rows, bf16, from HBM: 190 us where the thread per key
 // takes 92.
 #pragma once
 
@@ -29,7 +34,7 @@ namespace {
 template <typename T>
 struct ScaledRowsLay {
   static constexpr bool Q8 = true, ROWS = true, WORDS = false;
-  static constexpr bool SPLIT = std::is_same<T, __nv_bfloat16>::value;  // weights as two bf16 halves
+  static constexpr bool SPLIT = false;                // (weights are f16)
   static constexpr int D = 128, SPANS = 2, HQ = 128, QP = 1, R = HQ;
   static constexpr int QTILE = HQ * D * 2;
   static constexpr int SLOT = kKeys * D * 2;          // one K or V chunk, 16-bit
@@ -39,15 +44,19 @@ struct ScaledRowsLay {
   static constexpr int STAGE = RING + NS * SLOT;
   static constexpr int BAR = STAGE + NL * kKeys * D;
   static constexpr int EXTRA = 2 * NL + 2 * NS + 23;
-  static constexpr int NBAR = EXTRA + 12;             // scales of a chunk, pieces over
+  // bf16 queries are made f16, as the codes are: barriers of four pieces' (f16 ones are as they land)
+  static constexpr bool QCONV = std::is_same<T, __nv_bfloat16>::value;
+  static constexpr int QREADY = QCONV ? EXTRA + 12 : 0;
+  static constexpr int NBAR = EXTRA + 16;             // scales of a chunk, pieces over, queries ready
   static constexpr int MISC = (BAR + NBAR * 8 + 15) & ~15;
   static constexpr int PIECE = MISC + 128;            // Piece [4]
   static constexpr int PUB = PIECE + 4 * 48;          // float2 [2 tiles][HQ]
   static constexpr int SC = PUB + 16 * HQ;            // float [8 chunks][K 8, V 8]
-  static constexpr int BYTES = SC + 8 * 64;
+  static constexpr int FAC = SC + 8 * 64;             // float [4 pieces][HQ]: takes back the power of a row of queries
+  static constexpr int BYTES = FAC + 16 * HQ;
   static constexpr int THREADS = 512;
   // as in the tree attention's Lay
-  static constexpr float LIFT = SPLIT ? 0.f : 7.f, MOVE = SPLIT ? 8.f : 15.f;
+  static constexpr float LIFT = 7.f, MOVE = 15.f;
   static constexpr int HIGH = 176, LOW = 80;
   static constexpr int CHUNK = 1, ITEM = kItem, LEAST = 0;  // of units: a chunk, an item's start and end, an item at least
   static_assert(BYTES <= 232448, "shared memory of one CTA");
@@ -160,6 +169,48 @@ __device__ __forceinline__ void produce_rows(const TreeArgs& a, const CUtensorMa
   __syncwarp();
 }
 
+// A piece's bf16 queries as f16, in their place, by the converters, a thread a row: scaled by
+// a power of two to 2^14 .. 2^15, so that a row of any size keeps its 8 bits.
+template <typename L>
+struct HalfQueries {
+  uint8_t* gb;
+  Sync<L> sy;
+  __device__ __forceinline__ void operator()(const Piece& p, int i, bool& ok) const {
+    const int r = static_cast<int>(threadIdx.x) - 384;
+    if (ok) ok = wait_warp(sy.qfull(i & 1), (i >> 1) & 1);
+    if (r < p.rows) {
+      auto at = [&](int ch) {
+        return reinterpret_cast<uint4*>(gb + ((ch >> 3) * L::HQ + r) * 128 + (((ch ^ r) & 7) << 4));
+      };
+      uint32_t top = 0;
+#pragma unroll 4
+      for (int ch = 0; ch < 8 * L::SPANS; ++ch) {
+        const uint4 w = *at(ch);
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                     __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
+      }
+      top = max(top & 0xFFFFu, top >> 16);
+      const bool fine = top < 0x7F80u;  // (else the row's factor is NaN, and so is the row)
+      const int k = min(14 - (static_cast<int>(top >> 7) - 127), 100);
+      const float up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+      auto half = [&](uint32_t u) {
+        const float2 f = dev::unpack2<__nv_bfloat16>(u);
+        return dev::pack2<__half>(f.x * up, f.y * up);
+      };
+#pragma unroll 4
+      for (int ch = 0; ch < 8 * L::SPANS; ++ch) {
+        const uint4 w = *at(ch);
+        *at(ch) = make_uint4(half(w.x), half(w.y), half(w.z), half(w.w));
+      }
+      reinterpret_cast<float*>(gb + L::FAC)[(i & 3) * L::HQ + r] =
+          fine ? __uint_as_float(static_cast<uint32_t>(127 - k) << 23) : NAN;
+    }
+    dev::fence_proxy_async_smem();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(factors_full(sy, i));
+  }
+};
+
 template <typename T>
 __global__ void __launch_bounds__(ScaledRowsLay<T>::THREADS, 1)
     scaled_rows(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -178,6 +229,7 @@ __global__ void __launch_bounds__(ScaledRowsLay<T>::THREADS, 1)
   if (threadIdx.x == 64) {
     for (int i = 0; i < 8; ++i) dev::mbar_init(scales_full(sy, i), 1);
     for (int i = 0; i < 4; ++i) dev::mbar_init(piece_over(sy, i), 8);
+    for (int i = 0; i < 4; ++i) dev::mbar_init(factors_full(sy, i), 4);
   }
   const uint32_t tmem = setup<L>(gb, sy, wid, &tmK, &tmV, &tmQ);
 
@@ -186,7 +238,7 @@ __global__ void __launch_bounds__(ScaledRowsLay<T>::THREADS, 1)
     produce_rows<L>(a, &tmK, &tmV, &tmQ, gb, sy);
   } else if (wid == 1) {
     fewer_registers<L>();
-    multiply_rows<T, L>(a, gb, sy, static_cast<uint32_t>(uniform(static_cast<int>(tmem))));
+    multiply_rows<__half, L>(a, gb, sy, static_cast<uint32_t>(uniform(static_cast<int>(tmem))));
   } else if (wid == 2) {
     fewer_registers<L>();
   } else if (wid == 3) {
@@ -205,7 +257,7 @@ __global__ void __launch_bounds__(ScaledRowsLay<T>::THREADS, 1)
     x.o = tl + kRowO + 128 * x.t;
     const int t = x.t, r = x.r;
     float2* pubs = reinterpret_cast<float2*>(gb + L::PUB);
-    const float sl2 = a.scale_log2;
+    float sl2 = a.scale_log2;
     bool ok = true;
     int n = 0;  // chunks of this tile so far
     Cursor<L> k;
@@ -232,6 +284,12 @@ __global__ void __launch_bounds__(ScaledRowsLay<T>::THREADS, 1)
         const bool masked = key0 + kKeys > shift + (p.row0 >> a.gl) + 1;
         if (ok) ok = wait_warp(sy.sfull(t), n & 1);  // (the tile's products before it have ended too)
         if (ok) ok = wait_warp(scales_full(sy, chunk), (chunk >> 3) & 1);
+        if constexpr (L::QCONV) {
+          if (c == c_first) {
+            if (ok) ok = wait_warp(factors_full(sy, k.i), (k.i >> 2) & 1);
+            sl2 = a.scale_log2 * reinterpret_cast<const float*>(gb + L::FAC)[(k.i & 3) * L::HQ + r];
+          }
+        }
         fence_after();
         if (x.live) {
           const float4* sc = reinterpret_cast<const float4*>(gb + L::SC + (chunk & 7) * 64);
@@ -280,7 +338,7 @@ __global__ void __launch_bounds__(ScaledRowsLay<T>::THREADS, 1)
           float2 ls = make_float2(0.f, 0.f), ls1 = ls;
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
-            uint32_t pk[16], low[L::SPLIT ? 16 : 1];
+            uint32_t pk[16];
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
               const int i = 32 * h + 2 * j;
@@ -292,15 +350,10 @@ __global__ void __launch_bounds__(ScaledRowsLay<T>::THREADS, 1)
               ls = add2(ls, w0);
               ls1 = add2(ls1, w1);
               const float2 y0 = mul2(w0, v2), y1 = mul2(w1, v2);
-              pk[j] = dev::pack2<T>(y0.x, y0.y);
-              pk[j + 1] = dev::pack2<T>(y1.x, y1.y);
-              if constexpr (L::SPLIT) {
-                low[j] = low_half(y0, pk[j]);
-                low[j + 1] = low_half(y1, pk[j + 1]);
-              }
+              pk[j] = dev::pack2<__half>(y0.x, y0.y);
+              pk[j + 1] = dev::pack2<__half>(y1.x, y1.y);
             }
             tmem_st16(x.s + 16 * h, pk);
-            if constexpr (L::SPLIT) tmem_st16(x.s + 64 + 16 * h, low);
           }
           l += (ls.x + ls.y) + (ls1.x + ls1.y);
           wait_st();
@@ -308,7 +361,7 @@ __global__ void __launch_bounds__(ScaledRowsLay<T>::THREADS, 1)
         if (masked) {
           const int vi = k.it0 + 2 * c + 1, vs = vi % NS;
           if (ok) ok = __all_sync(FULL, wait_issued(sy.issued(), vi)) && wait_warp(sy.ready(vs), (vi / NS) & 1);
-          guard_rows<T, L>(x, gb, gb + L::RING + vs * L::SLOT, (p.c0 + c) & 1, false, key0 + r - shift, p.n,
+          guard_rows<__half, L>(x, gb, gb + L::RING + vs * L::SLOT, (p.c0 + c) & 1, false, key0 + r - shift, p.n,
                            c == c_first);
         }
         fence_before();
@@ -350,7 +403,10 @@ __global__ void __launch_bounds__(ScaledRowsLay<T>::THREADS, 1)
     if (!ok && lane == 0) flag(PA_DEVERR_TIMEOUT);
   } else {
     fewer_registers<L>();
-    convert<uint8_t, T, L>(gb, sy);
+    if constexpr (L::QCONV)
+      convert<uint8_t, __half, L>(gb, sy, HalfQueries<L>{gb, sy});
+    else
+      convert<uint8_t, __half, L>(gb, sy);
   }
   teardown(wid, tmem);
 }

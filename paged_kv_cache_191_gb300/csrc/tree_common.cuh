@@ -125,6 +125,7 @@ struct Lay {
   // The weight itself is float32: 2^95 with scales of 2^-80, which smaller ones count as
   // here.)
   static constexpr float LIFT = SPLIT ? 0.f : 7.f, MOVE = SPLIT ? 8.f : 15.f;
+  static constexpr int QREADY = 0;  // (Q is ready once it has landed)
   static constexpr int HIGH = Q8 ? 176 : 200, LOW = Q8 ? 80 : 104;  // registers: softmax threads', the others'
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
@@ -679,9 +680,13 @@ struct Cursor {
 };
 
 // The converter warpgroup (1-byte caches): codes of a landed chunk -> 16-bit
-// values in its slot of the ring, in the layout the MMAs read.
-template <typename KT, typename T, typename L>
-__device__ __forceinline__ void convert(uint8_t* gb, Sync<L> sy) {
+// values in its slot of the ring, in the layout the MMAs read.  queries: what it does
+// besides for a piece, behind the first chunk's codes.
+struct AsLanded {
+  __device__ __forceinline__ void operator()(const Piece&, int, bool&) const {}
+};
+template <typename KT, typename T, typename L, typename F = AsLanded>
+__device__ __forceinline__ void convert(uint8_t* gb, Sync<L> sy, F queries = F{}) {
   constexpr int NS = L::NS, NL = L::NL;
   const int lane = static_cast<int>(threadIdx.x & 31), i0 = static_cast<int>(threadIdx.x) - 384;
   bool ok = true;
@@ -724,6 +729,7 @@ __device__ __forceinline__ void convert(uint8_t* gb, Sync<L> sy) {
       dev::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(sy.conv(to));
+      if (k == 1) queries(p, i, ok);
     }
   }
   if (!ok && lane == 0) flag(PA_DEVERR_TIMEOUT);

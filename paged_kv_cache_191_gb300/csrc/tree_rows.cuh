@@ -164,8 +164,13 @@ __device__ __forceinline__ void multiply_rows(const TreeArgs& a, uint8_t* gb, Sy
     }
     // Scores first: a tile's follow its product without a look at the other tile.
     // What a step needs besides its turn is tested ahead of it, while idle.
-    if (s.k.live && !k_ok)
-      k_ok = s.j > 0 || ((s.k.c > 0 || test(sy.qfull(s.k.i & 1), s.k.i >> 1)) && test(sy.ready(ks), kf));
+    auto q_ready = [&](int i) {
+      if constexpr (L::QREADY > 0)
+        return test(sy.at(L::QREADY + (i & 3)), i >> 2);
+      else
+        return test(sy.qfull(i & 1), i >> 1);
+    };
+    if (s.k.live && !k_ok) k_ok = s.j > 0 || ((s.k.c > 0 || q_ready(s.k.i)) && test(sy.ready(ks), kf));
     if (k_ok && ahead < 2) {
       fence_after();
       const bool last = s.ends_chunk(), over = s.ends_piece();

@@ -321,6 +321,41 @@ def test_a_nan_query_stays_in_its_row():
     assert torch.isnan(got[0, 2]).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=str)
+def test_many_short_items_of_a_row_a_thread(dtype):
+    """96 rows a kv head, one and two chunks, more than a dozen items in every CTA."""
+    lens = [int(x) for x in W.rng_for(47).integers(12, 257, 100)]
+    w = ScaledBatch(47, 128, 16, [12] * 100, lens, dtype=dtype)
+    first = attend(w)
+    check(first, w)
+    for _ in range(9):
+        assert torch.equal(attend(w), first)
+
+
+def test_bf16_queries_of_any_size_in_a_prompt():
+    """Rows of large, small and no values, and of no numbers, beside each other."""
+    w = ScaledBatch(48, 8, 1, [20, 45], [100, 260], dtype=torch.bfloat16)
+    w.k_scale[:] = 2.0 ** -7
+    w.q[3, 1] *= 2.0 ** -30
+    w.q[5, 3] *= 2.0 ** -100
+    w.q[5, 4] *= 2.0 ** -126
+    w.q[30, 2] = 0.0
+    w.q[40, 0, :3] *= 2.0 ** 3
+    ref = attention_oracle(w)
+    check(attend(w), w, ref)
+    rows = np.ones(w.q.shape[:2], bool)
+    w.q[0, 0] *= 2.0 ** 60  # (its scores differ by more than a float32 product is exact to)
+    w.q[7, 2, 9], w.q[33, 5, 0] = float("nan"), float("inf")
+    rows[0, 0] = rows[7, 2] = rows[33, 5] = False
+    got = attend(w)
+    kept = torch.from_numpy(rows)
+    assert torch.isnan(got[7, 2]).all() and torch.isnan(got[33, 5]).all()
+    w.q[0, 0], w.q[7, 2], w.q[33, 5] = 1.0, 1.0, 1.0
+    again = attend(w)
+    check(again, w)
+    assert torch.equal(again[kept], got[kept])
+
+
 def test_attention_flags_and_clamps():
     w = ScaledBatch(41, 8, 2, [2, 1, 3], [40, 20, 33])
     ref = attention_oracle(w)
