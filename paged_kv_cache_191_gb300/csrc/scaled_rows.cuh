@@ -21,8 +21,8 @@
 // it, its rows' way out and the next one's first references; O has no tensor memory for
 // two items.  (Items of 256 rows, half of them each tile's, halve the codes and values per
 // row and were no faster: 130 us for 127, 74 for 68 at 33 to 60 tokens.  Nor is it the
-// exponentials' unit: with every eighth pair by a polynomial those 130 us were 135.)  At 40 rows, bf16, from HBM: 190 us where the thread per key
-// takes 92.
+// exponentials' unit: with every eighth pair by a polynomial those 130 us were 135.)  At 40 rows,
+// from HBM: f16 103 us, bf16 121, where the thread per key takes 89 and 90.
 #pragma once
 
 #include "scaled_common.cuh"
@@ -257,7 +257,6 @@ __global__ void __launch_bounds__(ScaledRowsLay<T>::THREADS, 1)
     x.o = tl + kRowO + 128 * x.t;
     const int t = x.t, r = x.r;
     float2* pubs = reinterpret_cast<float2*>(gb + L::PUB);
-    float sl2 = a.scale_log2;
     bool ok = true;
     int n = 0;  // chunks of this tile so far
     Cursor<L> k;
@@ -285,10 +284,7 @@ __global__ void __launch_bounds__(ScaledRowsLay<T>::THREADS, 1)
         if (ok) ok = wait_warp(sy.sfull(t), n & 1);  // (the tile's products before it have ended too)
         if (ok) ok = wait_warp(scales_full(sy, chunk), (chunk >> 3) & 1);
         if constexpr (L::QCONV) {
-          if (c == c_first) {
-            if (ok) ok = wait_warp(factors_full(sy, k.i), (k.i >> 2) & 1);
-            sl2 = a.scale_log2 * reinterpret_cast<const float*>(gb + L::FAC)[(k.i & 3) * L::HQ + r];
-          }
+          if (ok && c == c_first) ok = wait_warp(factors_full(sy, k.i), (k.i >> 2) & 1);
         }
         fence_after();
         if (x.live) {
@@ -296,6 +292,8 @@ __global__ void __launch_bounds__(ScaledRowsLay<T>::THREADS, 1)
           const float4 s4[4] = {sc[0], sc[1], sc[2], sc[3]};
           const float ks[8] = {s4[0].x, s4[0].y, s4[0].z, s4[0].w, s4[1].x, s4[1].y, s4[1].z, s4[1].w};
           const float vs[8] = {s4[2].x, s4[2].y, s4[2].z, s4[2].w, s4[3].x, s4[3].y, s4[3].z, s4[3].w};
+          float sl2 = a.scale_log2;
+          if constexpr (L::QCONV) sl2 *= reinterpret_cast<const float*>(gb + L::FAC)[(k.i & 3) * L::HQ + r];
           float f[kKeys];
           load_scores(x.s, f);
 #pragma unroll
