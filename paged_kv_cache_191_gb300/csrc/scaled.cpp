@@ -20,7 +20,8 @@ pa_status check_scaled(const pa_cache_desc* d, const char* fn) {
 }
 
 // Query rows that share a stream of K/V: a token's heads of one kv head take a
-// power of two of them.
+// power of two of them.  Below 128 they hold a whole sequence's, which the planner
+// relies on: it has one item per (sequence, kv head) there.
 constexpr int32_t kMaxHeads = 32;
 int32_t item_rows(int32_t num_q_heads, int32_t max_q_len, const pa_cache_desc* d) {
   int64_t heads = 1;

@@ -133,11 +133,17 @@ __device__ __forceinline__ U ceil_sum(U m, int s) {
   const U q = m >> s, r = m - (q << s);
   return (((q & 1 ? q : q + 1) * (q & 1 ? (q + 1) >> 1 : q >> 1)) << s) + r * (q + 1);
 }
-// units of the items before item k of a kv head
-template <typename U>
+// units of the items before item k of a kv head.  With a thread per key there is none before
+// another: a sequence's tokens, max_q_len at most, are one item (item_rows of the call).
+template <typename L, typename U>
 __device__ __forceinline__ U units_before(const Span& x, int k, int s) {
-  return static_cast<U>(kItem) * static_cast<U>(k) + ceil_sum(static_cast<U>(x.a + k), s) -
-         ceil_sum(static_cast<U>(x.a), s);
+  if constexpr (!L::ROWS) {
+    return 0;
+  } else {
+    static_assert(L::LEAST == 0, "the sum has no least units of an item");
+    return static_cast<U>(L::ITEM) * static_cast<U>(k) +
+           static_cast<U>(L::CHUNK) * (ceil_sum(static_cast<U>(x.a + k), s) - ceil_sum(static_cast<U>(x.a), s));
+  }
 }
 // chunks of item k
 __device__ __forceinline__ int chunks_of(const Span& x, int k, int s) {
@@ -150,7 +156,7 @@ __device__ __forceinline__ int item_units(int chunks) {
 }
 template <typename L, typename U>
 __device__ __forceinline__ U units_per_head(const Span& x, int s) {
-  return x.tiles == 0 ? 0 : units_before<U>(x, x.tiles - 1, s) + item_units<L>(chunks_of(x, x.tiles - 1, s));
+  return x.tiles == 0 ? 0 : units_before<L, U>(x, x.tiles - 1, s) + item_units<L>(chunks_of(x, x.tiles - 1, s));
 }
 
 // A piece's queries, by the outputs' warpgroup: every row scaled by a power of two to
@@ -211,7 +217,8 @@ __device__ __forceinline__ void load_queries(const ScaledArgs& sa, uint8_t* gb, 
 template <typename L>
 __device__ __forceinline__ void plan_scaled(const TreeArgs& a, uint8_t* gb, Sync<L> sy) {
   const int lane = static_cast<int>(threadIdx.x & 31), me = static_cast<int>(blockIdx.x);
-  const int tpi = a.item_rows >> a.gl, per = 31 - __clz(kKeys / tpi);  // tokens of an item; log2 of the items to a chunk
+  // tokens of an item; log2 of the items to a chunk (exactly as many of the 128-row ones, whose chunks go by it)
+  const int tpi = a.item_rows >> a.gl, per = 31 - __clz(kKeys / tpi);
   // Sequences are read 32 at a time, a lane each.  (The code is kept small, one place for
   // each step: what a CTA runs once should not push the loops out of the caches.)
   Span mine{0, 0, 0, 0, 0};
@@ -300,16 +307,18 @@ __device__ __forceinline__ void plan_scaled(const TreeArgs& a, uint8_t* gb, Sync
           const int U = max(1, static_cast<int>(units_per_head<L, uint32_t>(s, per))), at = start - ub;
           g = at / U;
           off = at - g * U;
-          int hi = s.tiles;  // the last that starts at or before it
+          if constexpr (L::ROWS) {
+            int hi = s.tiles;  // the last that starts at or before it
 #pragma unroll 1
-          while (hi - tile > 1) {
-            const int mid = (tile + hi) >> 1;
-            if (static_cast<int>(units_before<uint32_t>(s, mid, per)) <= off)
-              tile = mid;
-            else
-              hi = mid;
+            while (hi - tile > 1) {
+              const int mid = (tile + hi) >> 1;
+              if (static_cast<int>(units_before<L, uint32_t>(s, mid, per)) <= off)
+                tile = mid;
+              else
+                hi = mid;
+            }
+            off -= static_cast<int>(units_before<L, uint32_t>(s, tile, per));
           }
-          off -= static_cast<int>(units_before<uint32_t>(s, tile, per));
         }
         seq = b;
       }

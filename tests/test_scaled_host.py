@@ -153,6 +153,18 @@ def test_attention_workspace_size(palib):
     assert size(3, 1, C.byref(_d8())) == size(4, 1, C.byref(_desc())) == size(4, -1, C.byref(_d8())) == 0
 
 
+def test_items_below_128_rows_hold_a_whole_sequence(palib):
+    """What the planner of the thread-per-key kernels relies on.  The rows of an item come out of the workspace: two
+    sets of rows of D + 2 floats a CTA, and 32 bytes."""
+    size = palib.pa_block_scaled_attention_workspace_size
+    sms = next(n for n in range(1, 1000) if abs(size(1, 1, C.byref(_d8(num_kv_heads=1))) - n * (2 * 8 * 130 * 4 + 32)) < 256)
+    for G in range(1, 33):
+        heads = 1 << (G - 1).bit_length()
+        for n in range(1, 200):
+            rows = round((size(G, n, C.byref(_d8(num_kv_heads=1))) / sms - 32) / (2 * 130 * 4))
+            assert rows == 128 or (rows in (8, 16, 32, 40) and heads * n <= rows and rows % heads == 0)
+
+
 def _copy(d, **kw):
     a = dict(dk=FAKE, dv=FAKE, dks=FAKE, dvs=FAKE, dn=8, sk=FAKE, sv=FAKE, sks=FAKE, svs=FAKE, sn=8, p=FAKE, n=2)
     a.update(kw)
