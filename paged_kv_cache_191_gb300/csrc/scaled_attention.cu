@@ -825,7 +825,7 @@ pa_status launch_kernel(const ScaledAttentionLaunch& l, K kernel, cudaStream_t s
   else
     e = launch_dependent(kernel, grid, block, L::BYTES, stream, tm[0], tm[1], sa);
   if constexpr (L::ROWS) {
-    if (e == cudaSuccess && l.max_context_len > kKeys) {
+    if (e == cudaSuccess && l.max_context_len > kKeys) {  // (no item of one chunk is cut)
       const dim3 mgrid(static_cast<unsigned>(a.n_cta), a.slot_rows / kMergeRows), mblock(32 * kMergeRows);
       e = sa.q_bf16 ? launch_dependent(tree_merge<__nv_bfloat16, L::D>, mgrid, mblock, 0, stream, a)
                     : launch_dependent(tree_merge<__half, L::D>, mgrid, mblock, 0, stream, a);

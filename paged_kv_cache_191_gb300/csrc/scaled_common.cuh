@@ -121,11 +121,14 @@ __device__ __forceinline__ uint32_t upper(uint32_t a, uint32_t b) { return dev::
 
 // ---- the batch's work ----------------------------------------------------------
 // A sequence's items of one kv head, tpi tokens each; item j sees L - n + (j + 1)
-// tpi keys at most, and a chunk beyond is not its work.
+// tpi keys at most, and a chunk beyond is not its work.  (Nor one behind the context:
+// where the tokens are more than the keys, n > L, the first of them see none.  So a
+// context of one chunk has no item that is cut, and needs no merge.)
 struct Span {
   int qs, n, L, tiles;
   int a;  // tokens before the new ones, in items
 };
+__device__ __forceinline__ int context_chunks(const Span& x) { return max(1, (x.L + kKeys - 1) / kKeys); }
 // sum of ceil(x / 2^s) over x = 1 .. m.  (In 32 bits it may wrap; differences, which are
 // within what the launch was checked for, are right all the same.)
 template <typename U>
@@ -133,21 +136,25 @@ __device__ __forceinline__ U ceil_sum(U m, int s) {
   const U q = m >> s, r = m - (q << s);
   return (((q & 1 ? q : q + 1) * (q & 1 ? (q + 1) >> 1 : q >> 1)) << s) + r * (q + 1);
 }
-// units of the items before item k of a kv head.  With a thread per key there is none before
-// another: a sequence's tokens, max_q_len at most, are one item (item_rows of the call).
+// units of the items before item k of a kv head; those that have the whole context are at the
+// end.  With a thread per key there is none before another: a sequence's tokens, max_q_len
+// at most, are one item (item_rows of the call).
 template <typename L, typename U>
 __device__ __forceinline__ U units_before(const Span& x, int k, int s) {
   if constexpr (!L::ROWS) {
     return 0;
   } else {
     static_assert(L::LEAST == 0, "the sum has no least units of an item");
+    const U all = static_cast<U>(context_chunks(x)), from = static_cast<U>(x.a), to = static_cast<U>(x.a + k);
+    const U part = min(to, all << s);  // (from is below that: a context holds the tokens before the new ones)
     return static_cast<U>(L::ITEM) * static_cast<U>(k) +
-           static_cast<U>(L::CHUNK) * (ceil_sum(static_cast<U>(x.a + k), s) - ceil_sum(static_cast<U>(x.a), s));
+           static_cast<U>(L::CHUNK) * (ceil_sum(part, s) - ceil_sum(from, s) + (to - part) * all);
   }
 }
 // chunks of item k
 __device__ __forceinline__ int chunks_of(const Span& x, int k, int s) {
-  return k + 1 < x.tiles ? (x.a + k + (1 << s)) >> s : max(1, (x.L + kKeys - 1) / kKeys);
+  const int all = context_chunks(x);
+  return k + 1 < x.tiles ? min((x.a + k + (1 << s)) >> s, all) : all;
 }
 // units of an item of so many chunks
 template <typename L>

@@ -377,6 +377,19 @@ def test_attention_flags_and_clamps():
     assert (out[:2] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("n,L", [(300, 100), (1024, 100), (700, 300)])
+def test_a_prompt_of_more_tokens_than_keys(n, L, dtype):
+    """Above 40 rows a kv head: the tokens without a key are zero rows, and no other row stays unwritten."""
+    w = ScaledBatch(100, 32, 8, [n, 3], [L, 60], dtype=dtype)
+    ref = attention_oracle(w)
+    for out_dtype in (torch.float32, dtype):
+        out = attend(w, out_dtype=out_dtype)
+        assert ops.device_errors(clear=True) == ops.DEVERR_CONTEXT_LEN
+        check(out, w, ref)
+        assert (out[:n - L] == 0).all()
+
+
 def test_rows_behind_the_last_sequence_stay():
     w = ScaledBatch(43, 8, 2, [2, 1], [40, 20])
     want = attend(w)
