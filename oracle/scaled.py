@@ -14,6 +14,7 @@ verifies drafted tokens in one pass.  Readings where the pages are silent:
   2^-44, to nearest even.
 """
 import math
+from fractions import Fraction
 
 import numpy as np
 
@@ -95,7 +96,7 @@ def attention(q, q_start, k_cache, v_cache, k_scale, v_scale, tables, lens, scal
 def fixed(p):
     """Probabilities as whole multiples of 2^-44, to nearest even."""
     p = np.asarray(p, dtype=np.float64)
-    return np.rint(np.clip(np.where(np.isnan(p), 0.0, p), 0.0, 1.0) * 2.0 ** 44).astype(object)
+    return np.rint(np.clip(np.where(np.isnan(p), 0.0, p), 0.0, 1.0) * 2.0 ** 44).astype(np.int64).astype(object)
 
 
 def verify(tokens, target, uniform, q_start, max_path, draft=None, parents=None):
@@ -144,6 +145,6 @@ def verify(tokens, target, uniform, q_start, max_path, draft=None, parents=None)
             nexts.append(-1)
             continue
         u = float(uniform[lo])
-        t = min(int(min(u, 1.0) * float(total)) if u > 0 else 0, total - 1)
+        t = min(math.floor(Fraction(min(u, 1.0)) * total) if u > 0 else 0, total - 1)
         nexts.append(int(np.argmax(np.cumsum(w) > t)))
     return paths, nexts

@@ -90,6 +90,20 @@ __device__ __forceinline__ uint64_t weight44(float p, float q) {
   return join44(ph - qh, pl - ql);
 }
 
+// floor(u total) exactly, total - 1 at most, 0 for a u that is no number or not above 0:
+// a whole sum is above u total where it is above that.  (A float64 product, 53 bits of the 24
+// + 45 and more, can reach the next whole number.)  u = m 2^-s, s >= 24 as u < 1.
+__device__ __forceinline__ uint64_t threshold(float u, uint64_t total) {
+  if (!(u > 0.f)) return 0ull;
+  if (u >= 1.f) return total - 1;
+  const uint32_t bits = __float_as_uint(u), e = max(bits >> 23, 1u);
+  const uint64_t m = (bits & 0x7FFFFFu) | (bits >> 23 ? 0x800000u : 0u);
+  const int s = 150 - static_cast<int>(e);
+  const uint64_t hi = __umul64hi(total, m), lo = total * m;  // (2^87 at most)
+  if (s < 64) return hi << (64 - s) | lo >> s;
+  return s < 128 ? hi >> (s - 64) : 0ull;
+}
+
 __global__ void __launch_bounds__(kThreads) draft_verify(const __grid_constant__ VerifyArgs a) {
   __shared__ float node_p[kNodes], node_u[kNodes];
   __shared__ int32_t node_parent[kNodes];
@@ -293,9 +307,7 @@ __global__ void __launch_bounds__(kThreads) draft_verify(const __grid_constant__
     }
     return;
   }
-  const float u0 = node_u[0];
-  t = u0 > 0.f ? static_cast<uint64_t>(static_cast<double>(fminf(u0, 1.f)) * static_cast<double>(total)) : 0ull;
-  if (t >= total) t = total - 1;
+  t = threshold(node_u[0], total);
   for (int w = 0; w < wid; ++w) before += warp_sum[w];
   if (t < before || t - before >= warp_sum[wid]) return;
   // the warp that holds it: the batch, its row of 32, the value

@@ -660,6 +660,24 @@ def test_verify_edges_of_the_draw():
     assert verify(d, 2)[2].tolist() == [2] * 8
 
 
+def test_verify_draws_from_the_exact_sum():
+    """u0 times the sum lies just below a whole number that is also a cumulated sum, nearer than a float64 product
+    tells; and a sum of 2^54 - 1, which float64 has not."""
+    d = Drafts(14, [1, 1], 1026, "picked")
+    d.target[:] = 0.0
+    # 8393261 2^20 = u0 x sum + 1866 2^-24, in units of 2^-44
+    m, first, rest = 11191015, 8393261 << 20, 4393167093978
+    assert m * (first + rest) == (first << 24) - 1866
+    d.target[0, :3] = np.array([first, rest >> 20 << 20, rest & 0xFFFFF], dtype=np.float64) * 2.0 ** -44
+    d.target[1, :1023], d.target[1, 1023], d.target[1, 1024] = 1.0, 1.0 - 2.0 ** -24, (2 ** 20 - 1) * 2.0 ** -44
+    d.uniform[:] = [m * 2.0 ** -24, 0.5]
+    assert sum(int(x * 2.0 ** 44) for x in d.target[0].astype(np.float64)) == first + rest
+    assert sum(int(x * 2.0 ** 44) for x in d.target[1].astype(np.float64)) == 2 ** 54 - 1
+    got = verify(d, 2)
+    assert got[2].tolist() == [0, 511]
+    check_verify(got, d, 2)
+
+
 def test_verify_where_nothing_is_left():
     d = Drafts(5, [2, 2, 1], 50, "sampled")
     d.draft[:] = 1.0  # takes everything: the target's own row

@@ -84,6 +84,18 @@ def test_verify_by_hand():
     assert O.verify([0], zero, [.5], [0, 1], 3) == ([[0]], [-1])
 
 
+def test_draws_compare_whole_sums():
+    """u0 times the sum lies 1866 2^-24 below a whole number that is a cumulated sum too, and half of 2^54 - 1 half
+    below one: the token there is the first above."""
+    m, first, rest = 11191015, 8393261 << 20, 4393167093978
+    assert m * (first + rest) == (first << 24) - 1866
+    p = np.zeros((2, 1025), dtype=np.float32)
+    p[0, :3] = np.array([first, rest >> 20 << 20, rest & 0xFFFFF]) * 2.0 ** -44
+    p[1, :1023], p[1, 1023], p[1, 1024] = 1.0, 1.0 - 2.0 ** -24, (2 ** 20 - 1) * 2.0 ** -44
+    assert [int(O.fixed(x).sum()) for x in p] == [first + rest, 2 ** 54 - 1]
+    assert O.verify([0, 0], p, [m * 2.0 ** -24, 0.5], [0, 1, 2], 2)[1] == [0, 511]
+
+
 @pytest.mark.parametrize("kind", ["sampled", "picked", "tree"])
 def test_verified_tokens_are_distributed_as_the_target(kind):
     """The first token behind node 0, over many draws: each token's share is
