@@ -575,6 +575,7 @@ __global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
       dev::mbar_init(out_full(sy, i), 1);
       dev::mbar_init(out_free(sy, i), 4);
     }
+    dev::fence_barrier_init();  // (the products' commits arrive on out_full)
   }
   for (int i = static_cast<int>(threadIdx.x); i < 512; i += L::THREADS) reinterpret_cast<int*>(gb + L::POISON)[i] = R;
   const uint32_t tmem = setup<L>(gb, sy, wid, &tmK, &tmV, &tmK);

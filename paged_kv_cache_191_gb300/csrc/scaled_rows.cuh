@@ -230,6 +230,7 @@ __global__ void __launch_bounds__(ScaledRowsLay<T>::THREADS, 1)
     for (int i = 0; i < 8; ++i) dev::mbar_init(scales_full(sy, i), 1);
     for (int i = 0; i < 4; ++i) dev::mbar_init(piece_over(sy, i), 8);
     for (int i = 0; i < 4; ++i) dev::mbar_init(factors_full(sy, i), 4);
+    dev::fence_barrier_init();
   }
   const uint32_t tmem = setup<L>(gb, sy, wid, &tmK, &tmV, &tmQ);
 
