@@ -589,12 +589,12 @@ __global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
   } else if (wid == 2) {
     fewer_registers<L>();
     produce_scaled<L, true>(a, &tmV, gb, sy);
+  } else if (wid >= 12) {  // (ahead of the planner: chains of 40 rows 91 us, behind it 93)
+    fewer_registers<L>();
+    outputs<L>(sa, gb, sy, tmem);
   } else if (wid == 3) {
     fewer_registers<L>();
     plan_scaled<L>(a, gb, sy);
-  } else if (wid >= 12) {
-    fewer_registers<L>();
-    outputs<L>(sa, gb, sy, tmem);
   } else {
     // ---- softmax warpgroups: thread r owns key r of a chunk -----------------------------
     more_registers<L>();

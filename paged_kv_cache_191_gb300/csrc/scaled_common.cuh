@@ -151,9 +151,11 @@ __device__ __forceinline__ U units_before(const Span& x, int k, int s) {
            static_cast<U>(L::CHUNK) * (ceil_sum(part, s) - ceil_sum(from, s) + (to - part) * all);
   }
 }
-// chunks of item k
+// chunks of item k; with a thread per key it is the sequence's only one
+template <typename L>
 __device__ __forceinline__ int chunks_of(const Span& x, int k, int s) {
   const int all = context_chunks(x);
+  if constexpr (!L::ROWS) return all;
   return k + 1 < x.tiles ? min((x.a + k + (1 << s)) >> s, all) : all;
 }
 // units of an item of so many chunks
@@ -163,7 +165,7 @@ __device__ __forceinline__ int item_units(int chunks) {
 }
 template <typename L, typename U>
 __device__ __forceinline__ U units_per_head(const Span& x, int s) {
-  return x.tiles == 0 ? 0 : units_before<L, U>(x, x.tiles - 1, s) + item_units<L>(chunks_of(x, x.tiles - 1, s));
+  return x.tiles == 0 ? 0 : units_before<L, U>(x, x.tiles - 1, s) + item_units<L>(chunks_of<L>(x, x.tiles - 1, s));
 }
 
 // A piece's queries, by the outputs' warpgroup: every row scaled by a power of two to
@@ -268,7 +270,7 @@ __device__ __forceinline__ void plan_scaled(const TreeArgs& a, uint8_t* gb, Sync
     const int64_t units = units_per_head<L, int64_t>(mine, per) * a.Hkv;
     if (!find) {
       sum += units;
-      if (mine.tiles > 0) most = max(most, item_units<L>(chunks_of(mine, mine.tiles - 1, per)));
+      if (mine.tiles > 0) most = max(most, item_units<L>(chunks_of<L>(mine, mine.tiles - 1, per)));
       continue;
     }
     const int w = static_cast<int>(units);
@@ -330,7 +332,7 @@ __device__ __forceinline__ void plan_scaled(const TreeArgs& a, uint8_t* gb, Sync
         seq = b;
       }
       // a chunk is whose range its first unit lies in
-      const int nch = chunks_of(s, tile, per), cost = item_units<L>(nch), stop = min(cost, off + end - u);
+      const int nch = chunks_of<L>(s, tile, per), cost = item_units<L>(nch), stop = min(cost, off + end - u);
       const int first = cost - L::CHUNK * nch;
       p.c0 = max(0, off - first + L::CHUNK - 1) / L::CHUNK;
       p.c1 = max(0, stop - first + L::CHUNK - 1) / L::CHUNK;
