@@ -702,10 +702,17 @@ pa_status pa_draft_verify(const int64_t* tokens, const float* target_probs, int6
  * for the finite new values of the block and head; where rows before the first
  * new one stay in the block, no less than the scale they have, and if it grows
  * their codes are rounded to the new one (exact but for values that become
- * E4M3 subnormals).  A block whose first row is new starts afresh, so rows that a
- * verification refused leave nothing behind; without any value above 0 it gets
- * scale 1.  code = E4M3(x / scale), to nearest even; infinities are stored as
- * +-448, NaN as NaN.  Rows behind the last new one keep what they hold.
+ * E4M3 subnormals).  A block whose first row is new starts afresh; without any
+ * value above 0 it gets scale 1.  code = E4M3(x / scale), to nearest even;
+ * infinities are stored as +-448, NaN as NaN.  Rows behind the last new one keep
+ * their codes, under the block's scale.
+ * Rows that a verification refused leave nothing in a block that starts afresh
+ * behind them.  In one where rows before them stay (most chains begin inside a
+ * block) a large refused row leaves its scale, which does not shrink before the
+ * block is started again, and the rounding that the rows before it, and
+ * those that come after it, get by that scale: 2^-4 of a value as ever, but 2^-10 of
+ * the scale where that is more.  What is attended then depends, within that, on
+ * drafts that were refused.
  *
  * k, v         device, token t's row [num_kv_heads][head_dim] at k + t *
  *              k_stride elements of in_dtype (F16, BF16, F32): views of one
@@ -738,8 +745,9 @@ size_t pa_block_scaled_attention_workspace_size(int32_t num_q_heads, int32_t max
  *     K_t, V_t = scale of (block, kv head) x code,   kv head g = h / G.
  * One token per sequence is a decode step, gamma + 1 a verification, more a
  * prompt chunk.  A token with no key is a zero row (n_b > L_b, flagged
- * PA_DEVERR_CONTEXT_LEN).  What a key or value holds (NaN codes included)
- * reaches only the tokens that see it.
+ * PA_DEVERR_CONTEXT_LEN).  What a key's or value's codes are (NaN included)
+ * reaches only the tokens that see it; its block's scale, which its size may have
+ * raised when it was appended, is that of all rows there.
  *
  * q            device, token t's row [num_q_heads][head_dim] at q + t * q_stride
  *              elements of q_dtype (F16 or BF16); a stride of at least a row

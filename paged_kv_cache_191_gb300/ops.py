@@ -605,7 +605,8 @@ def block_scaled_append(k, v, q_start, block_tables, context_lens, k_cache, v_ca
     q_start int32 [B + 1]; views of one packed projection are fine): the last
     q_start[b+1] - q_start[b] positions of sequence b's context.  k_cache, v_cache
     hold E4M3 codes [num_blocks, Hkv, 16, D], k_scale, v_scale float32
-    [num_blocks, Hkv]: powers of two, which grow with a block's values."""
+    [num_blocks, Hkv]: powers of two, which grow with a block's values, and do not
+    shrink while rows stay there (not behind rows that were refused, either)."""
     dev = _operands("q_start block_tables context_lens k_cache v_cache k_scale v_scale k v",
                     (q_start, block_tables, context_lens, k_cache, v_cache, k_scale, v_scale), (k, v))
     desc = _block_scaled(k_cache, v_cache, k_scale, v_scale)

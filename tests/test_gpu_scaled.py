@@ -117,6 +117,43 @@ def test_append_leaves_everything_else():
         assert np.array_equal(got[i].transpose(0, 2, 1, 3)[rows], before[i].transpose(0, 2, 1, 3)[rows])
 
 
+@pytest.mark.parametrize("kept", [9, 16])
+def test_what_refused_rows_leave(kept):
+    """Rows stay, two with large values are appended, refused and written over.  Behind a full block nothing of them is
+    left; inside one the block keeps the scale that they raised, and the rows before them are rounded by it."""
+    w = ScaledBatch(112, 2, 2, [kept + 2], [kept + 2])
+    w.new_k[kept:, :, 3] = 3000.0
+    k, v, tables = dev(w.new_k), dev(w.new_v), dev(w.tables)
+    cs, clean = caches(w), caches(w)
+    state = [w.k, w.v, w.k_scale, w.v_scale]
+
+    def step(to, lo, n, kk, vv):
+        q, L = dev(np.array([0, n], dtype=np.int32)), dev(np.array([lo + n], dtype=np.int32))
+        ops.block_scaled_append(kk, vv, q, tables, L, *to)
+        return O.append(*state, kk.cpu().double().numpy(), vv.cpu().double().numpy(), [0, n], w.tables, [lo + n])
+
+    small = k[:1] * 0.5
+    for to in (cs, clean):
+        state = [w.k, w.v, w.k_scale, w.v_scale]
+        state = step(to, 0, kept, k[:kept], v[:kept])
+        if to is cs:
+            state = step(to, kept, 2, k[kept:], v[kept:])
+            same(to, state)
+        state = step(to, kept, 1, small, v[:1])
+        same(to, state)
+    a, b = as_np(cs), as_np(clean)
+    first, last = w.tables[0][0], w.tables[0][kept // 16]
+    if kept == 16:
+        rows = np.s_[:, :1]  # the row that took the refused ones' place
+        assert all(np.array_equal(x[first], y[first]) for x, y in zip(a, b))
+        assert all(np.array_equal(x[last][rows], y[last][rows]) for x, y in zip(a[:2], b[:2]))
+        assert all(np.array_equal(x[last], y[last]) for x, y in zip(a[2:], b[2:]))
+    else:
+        assert (a[2][first] == 2.0 ** 3).all() and (b[2][first] < 2.0 ** -5).all()
+        x, y = (O.gather(c[0], c[2], w.tables[0], kept, 0) for c in (a, b))
+        assert (x != y).any() and (np.abs(x - y) <= np.maximum(np.abs(y) * 2.0 ** -4, 2.0 ** -10 * 2.0 ** 3)).all()
+
+
 def test_append_flags_what_it_cannot_store():
     w = ScaledBatch(10, 2, 2, [2, 3, 4], [20, 35, 18])
     good = append_oracle(w)
