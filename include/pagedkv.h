@@ -721,7 +721,9 @@ pa_status pa_draft_verify(const int64_t* tokens, const float* target_probs, int6
  * q_start      device int32 [B + 1], as pa_chunked_prefill.
  * A sequence with a q_start or length out of range (PA_DEVERR_QUERY_RANGE,
  * PA_DEVERR_CONTEXT_LEN) and a block id outside the pool (PA_DEVERR_BLOCK_RANGE)
- * store nothing and are flagged.  The blocks written must not be shared between
+ * store nothing and are flagged.  (A warp finds its sequence by q_start: where that
+ * is out of order, flagged, rows of the sequences around it may stay unstored as
+ * well; nothing else is written.)  The blocks written must not be shared between
  * sequences (pa_append_tokens has named the copies to make), nor occur twice.
  */
 pa_status pa_block_scaled_append(const void* k, const void* v, int32_t in_dtype, int64_t k_stride, int64_t v_stride,

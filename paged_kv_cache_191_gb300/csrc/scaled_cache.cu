@@ -153,7 +153,9 @@ __global__ void __launch_bounds__(32 * kWarps) scaled_append(const __grid_consta
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32, b = lo + lane * step;
     const unsigned m = __ballot_sync(FULL, b < hi && column_of(a, b) <= col);
-    if (m == 0) return;  // (q_start out of order)
+    // (q_start out of order.  A tile may then have another sequence's column, or none: it is not
+    // stored, and the sequence that is out of order is flagged.  No tile has two.)
+    if (m == 0) return;
     lo += (31 - __clz(m)) * step;
     hi = min(lo + step, hi);
   }

@@ -175,6 +175,23 @@ def test_append_flags_what_it_cannot_store():
                     assert np.array_equal(g[ids], y[ids])
 
 
+def test_append_of_a_q_start_out_of_order():
+    """Flagged; what is stored of the batch's other sequences is theirs, and no other row or block is written."""
+    w = ScaledBatch(11, 2, 2, [100, 3, 50], [120, 35, 70])
+    good = append_oracle(w)
+    x = ScaledBatch(11, 2, 2, [100, 3, 50], [120, 35, 70])
+    before = [x.k.copy(), x.v.copy(), x.k_scale.copy(), x.v_scale.copy()]
+    x.q_start = np.array([50, 150, 0, 50], dtype=np.int32)
+    for t, o in ((x.new_k, w.new_k), (x.new_v, w.new_v)):
+        t[50:150], t[:50] = o[:100], o[103:]
+    got = as_np(append(x, caches(x)))
+    assert ops.device_errors(clear=True) == ops.DEVERR_QUERY_RANGE
+    for b in range(len(w.k)):
+        for g, old, new in zip(got, before, good):
+            mine = any(b in w.tables[s][:-(-w.lens[s] // 16)] for s in (0, 2))
+            assert np.array_equal(g[b], old[b]) or (mine and np.array_equal(g[b], new[b]))
+
+
 # ---- attention -----------------------------------------------------------------
 def attend(w, cs=None, out_dtype=torch.float32, q=None, max_len=None, max_q=None, **kw):
     cs = cs or caches(w)
