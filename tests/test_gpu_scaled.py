@@ -444,6 +444,89 @@ def test_a_prompt_of_more_tokens_than_keys(n, L, dtype):
         assert (out[:n - L] == 0).all()
 
 
+# ---- the thread-per-row kernel (above 40 rows of a kv head) where the values are unusual ----
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("scale", [0.0, -0.3, 4.0])
+def test_scales_of_a_prompts_scores(scale, dtype):
+    w = ScaledBatch(101, 8, 2, [30, 11], [40, 300], dtype=dtype)
+    w.scale = scale
+    check(attend(w), w)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("vs", [2.0 ** -60, 2.0 ** -14, 2.0 ** 10])
+def test_v_scales_of_any_size_in_a_prompt(vs, dtype):
+    w = ScaledBatch(102, 8, 2, [25, 45], [400, 700], dtype=dtype)
+    w.v_scale[:] = vs * np.where(W.rng_for(3).random(w.v_scale.shape) < 0.3, 0.25, 1.0)
+    check(attend(w), w)
+
+
+def test_a_tail_of_many_small_weights_in_a_prompt():
+    w = ScaledBatch(103, 4, 1, [20], [20000])
+    w.k[:], w.k_scale[:] = 0, 1.0
+    w.q[:] = 1.0
+    w.k[w.tables[0][3], 0, 5] = 0x38
+    for top in (4.0, 8.0, 11.0):
+        w.scale = top / 128
+        check(attend(w), w, what=f"{top}")
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=str)
+def test_maxima_that_keep_growing_in_a_prompt(dtype):
+    w = ScaledBatch(104, 8, 1, [20, 90], [3000, 1500], dtype=dtype)
+    w.q[:] = 1.0
+    for b, L in enumerate(w.lens):
+        for j, blk in enumerate(w.tables[b][:-(-L // 16)]):
+            w.k[blk], w.k_scale[blk] = 0x38, 2.0 ** -2 * (1 + j)
+    w.scale = 0.02
+    check(attend(w), w)
+
+
+def test_a_nan_query_stays_in_its_row_of_a_prompt():
+    w = ScaledBatch(105, 8, 2, [40], [90])
+    ref = attention_oracle(w)
+    w.q[0, 2, 7], w.q[31, 5, 0] = float("nan"), float("nan")
+    got = attend(w)
+    rows = np.ones(w.q.shape[:2], bool)
+    rows[0, 2] = rows[31, 5] = False
+    check(got, w, ref, rows=rows)
+    assert torch.isnan(got[0, 2]).all() and torch.isnan(got[31, 5]).all()
+
+
+def test_a_nan_value_reaches_its_dim_only_in_a_prompt():
+    w = ScaledBatch(106, 8, 2, [40], [50])
+    ref = attention_oracle(w)
+    blk = w.tables[0][2]
+    w.v[blk, 1, 47 - 32, 9] = 0x7F  # position 47, token 37
+    got = attend(w)
+    nan = torch.isnan(got).numpy()
+    want = np.zeros_like(nan)
+    want[37:, 4:, 9] = True
+    assert np.array_equal(nan, want)
+    got[torch.from_numpy(nan)] = torch.from_numpy(ref[0])[torch.from_numpy(nan)].float()
+    check(got, w, ref)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=str)
+def test_a_prompt_reads_a_packed_projection_and_leaves_the_rows_behind(dtype):
+    w = ScaledBatch(107, 8, 2, [33, 1], [40, 200], dtype=dtype)
+    want = attend(w)
+    q = torch.cat([dev(w.q), dev(w.q)[:, :4]], 1)[:, :8]
+    assert not q.is_contiguous() and torch.equal(attend(w, q=q), want)
+    w.q = torch.cat([w.q, w.q])
+    got = attend(w)
+    assert torch.equal(got[:34], want) and torch.isnan(got[34:]).all()
+
+
+def test_decode_steps_in_a_call_for_prompts():
+    """Single tokens beside one prompt, and alone in a call that allows prompts."""
+    w = ScaledBatch(109, 32, 8, [1] * 12 + [90, 0, 1], [1, 15, 16, 17, 128, 129, 300, 511, 700, 1030, 64, 2, 400, 33, 256])
+    check(attend(w), w)
+    x = ScaledBatch(110, 32, 8, [1] * 6, [1, 16, 129, 300, 700, 1030])
+    check(attend(x, max_q=500), x)
+
+
+# ---- both kernels, and the calls in graphs and on streams ----
 def test_rows_behind_the_last_sequence_stay():
     w = ScaledBatch(43, 8, 2, [2, 1], [40, 20])
     want = attend(w)
