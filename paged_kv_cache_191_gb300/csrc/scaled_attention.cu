@@ -656,9 +656,11 @@ __global__ void __launch_bounds__(ScaledLay<R_>::THREADS, 1)
             for (int i = 0; i < 8; i += 4) {
               const float4 fa = *reinterpret_cast<const float4*>(fac + j + i);
               const float4 rf = *reinterpret_cast<const float4*>(refs + j + i);
-              const float2 y = fma2(mul2(make_float2(f[i], f[i + 1]), make_float2(fa.x, fa.y)), make_float2(ks, ks),
+              // (the factors first: a large row's sum times its own is beyond float32 before a small
+              // scale takes it back)
+              const float2 y = fma2(make_float2(f[i], f[i + 1]), mul2(make_float2(fa.x, fa.y), make_float2(ks, ks)),
                                     make_float2(rf.x, rf.y));
-              const float2 z = fma2(mul2(make_float2(f[i + 2], f[i + 3]), make_float2(fa.z, fa.w)), make_float2(ks, ks),
+              const float2 z = fma2(make_float2(f[i + 2], f[i + 3]), mul2(make_float2(fa.z, fa.w), make_float2(ks, ks)),
                                     make_float2(rf.z, rf.w));
               e[j + i] = y.x;
               e[j + i + 1] = y.y;

@@ -291,6 +291,17 @@ def test_large_and_small_queries():
     check(attend(w), w, ref, rows=rows)
 
 
+@pytest.mark.parametrize("n", [1, 4, 5, 20])
+def test_large_queries_over_small_keys(n):
+    """bf16 queries near 2^124 and K scales near 2^-124: their products are of the usual size, though a query's sum
+    with the codes alone is beyond float32."""
+    w = ScaledBatch(113, 8, 1, [n, n], [100, 260], dtype=torch.bfloat16)
+    w.q *= 2.0 ** 124
+    w.k_scale *= 2.0 ** -117
+    w.scale *= 0.5
+    check(attend(w), w)
+
+
 @pytest.mark.parametrize("vs", [2.0 ** -60, 2.0 ** -14, 2.0 ** 10])
 def test_v_scales_of_any_size(vs):
     w = ScaledBatch(35, 8, 2, [1, 5], [400, 700])
