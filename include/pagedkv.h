@@ -760,8 +760,12 @@ size_t pa_block_scaled_attention_workspace_size(int32_t num_q_heads, int32_t max
  *              16-byte aligned; scratch.  Calls that may run at the same time
  *              need one each.
  * Scores, sums and outputs are accumulated in float32; weight x V scale is rounded to
- * f16 whatever q's type (2^-11 of it, and 2^-27 of the row's largest: keys whose blocks have a V scale far
- * below another's that the row sees keep fewer bits, as do V scales below 2^-80).
+ * f16 whatever q's and out's types (2^-11 of it, and 2^-27 of the row's largest: keys whose
+ * blocks have a V scale far below another's that the row sees keep fewer bits, as do V
+ * scales below 2^-80), and a query's elements by 2^-31 of its row's largest, or
+ * 2^-117 where that is more.
+ * One kernel serves the whole call, by max_q_len: single tokens beside a prompt take
+ * longer than in a call of their own.
  * Deterministic: the same inputs give the same bits on the same device.
  */
 pa_status pa_block_scaled_attention(const void* q, int32_t q_dtype, int64_t q_stride, const int32_t* q_start,

@@ -36,9 +36,10 @@
 // sequences of 8 kv heads, 4 rows, contexts to 32768: 70 us, 85 % of the copy rate; the
 // chunks go by at 96 % of it, and the start (launch, lengths, block ids, scales, first
 // chunk: 5 us) and the last joined rows (3 us) are the rest.  64 sequences of 8 kv heads,
-// 8 rows, mean context 2064: 54 us, 75 %.  32 sequences of 32 kv heads, one row, mean
-// context 1024: 55 us, 72 %: items of 8 chunks, whose first needs new references (700
-// clocks) and a barrier.  The same 64 with chains of 2 to 5 tokens: 92 us, 44 %: the
+// 8 rows, mean context 2064: 54 us, 74 %.  32 sequences of 32 kv heads, one row, mean
+// context 1024: 56 us, 71 %: items of 8 chunks, whose first needs new references (700
+// clocks) and a barrier.  The same 64 with chains of 2 tokens (16 rows) 57 us, 71 %, of
+// 4 (32 rows) 80 us, 51 %, of 2 to 5 (40 rows) 91 us, 45 %: the
 // softmax warpgroups, 2200 clocks a chunk where HBM takes 1420; a chunk's exponents take
 // a warp 1000 clocks at 40 rows, the terms of its weights 900, one after the other.
 // Code that runs once per piece is kept small where it costs no latency: a planner of

@@ -17,7 +17,8 @@
 // sequence by a search 32 ways at a time.  No column is longer than the batch is,
 // however uneven the sequences are.  The chain of loads before the rows (q_start,
 // length, table) is what both tiles share.  Nine chunks of up to 2043 tokens, 32 heads,
-// f16: 39 us, 86 % of the copy rate (47 us with a warp per tile); one token 2.8 us, 64
+// f16: 39 us, 86 % of the copy rate (47 us with a warp per tile); float32, whose K and V
+// tiles do not fit a warp's registers together, 80 us, 70 %; one token 2.8 us, 64
 // of 8 heads 3.4 us: the launch.
 #include "cache_rows.cuh"
 #include "device_common.cuh"

@@ -256,7 +256,7 @@ __device__ __forceinline__ void plan_scaled(const TreeArgs& a, uint8_t* gb, Sync
       if (sum > kMaxUnits && me == 0 && lane == 0) flag(PA_DEVERR_QUERY_RANGE);
       const int total = sum > kMaxUnits ? 0 : static_cast<int>(sum);
       // Few units: equal parts of the largest item, of min_units at least.  (Joining parts takes
-      // 2 us and more: a sequence of 600 tokens 9.3 us whole, 11.1 in parts of 2 units; one of
+      // 2 us and more: a sequence of 600 tokens 8.9 us whole, 11.1 in parts of 2 units; one of
       // 32768 with one kv head 37 us in parts of 2, 21 in parts of 6.)
       upc = (total + a.n_cta - 1) / a.n_cta;
       if (upc < a.min_units) upc = max(a.min_units, (most + max(1, most / a.min_units) - 1) / max(1, most / a.min_units));
